@@ -61,7 +61,8 @@ typedef enum {
     NVFP4_ERR_LAUNCH = 6,    /* the HIP runtime rejected a launch               */
     NVFP4_ERR_DEVICE = 7,    /* the current device is not a gfx950 GPU          */
     NVFP4_ERR_WORKSPACE = 8, /* a required workspace is NULL or too small       */
-    NVFP4_ERR_SCRATCH = 9    /* beyond the fixed scratch of nvfp4_gemv_ws_static */
+    NVFP4_ERR_SCRATCH = 9,   /* beyond the fixed scratch of nvfp4_gemv_ws_static */
+    NVFP4_ERR_OVERLAP = 10   /* an output overlaps another argument             */
 } nvfp4_status;
 
 /* Largest number of tokens one launch covers (the decode batch of the pages:
@@ -285,6 +286,118 @@ int nvfp4_gemm(const uint8_t *Wq, const uint8_t *Wscale, float gscale,
  * Pure host function; returns a status. */
 int nvfp4_gemm_geometry(int n, int N, int K, int *rows_per_workgroup,
                         int *tokens_per_workgroup, int *grid_x, int *grid_y);
+
+/* ---- fused operators ------------------------------------------------------
+ *
+ * The projection with its epilogue, the gated feed-forward block and the
+ * product the other way through the weight, with the gradients of a frozen
+ * NVFP4 weight (to the activations, the biases and the residual).  Conventions
+ * as above, and for all of them:
+ *   - matrices are row-major with a row stride in elements (>= the columns);
+ *     X and dY rows are 16-byte aligned (stride a multiple of 8, at most 2^22);
+ *   - n = 0 is a valid call that launches nothing (but zeroes bias gradients);
+ *   - sums, biases, activations and products are fp32, rounded once when
+ *     stored;
+ *   - outputs may not overlap other arguments (OVERLAP), except that the
+ *     residual may be the output itself (same address, stride and type);
+ *   - for n <= 16 each token's result depends only on (N, K), for n > 16 on
+ *     the same order of sums whatever n: results do not vary from run to run. */
+
+/* Activations: z; max(z, 0); z / (1 + exp(-z)); z Phi(z) (erf form);
+ * 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))). */
+#define NVFP4_ACT_NONE 0
+#define NVFP4_ACT_RELU 1
+#define NVFP4_ACT_SILU 2
+#define NVFP4_ACT_GELU 3
+#define NVFP4_ACT_GELU_TANH 4
+
+typedef struct nvfp4_epilogue {
+    const void *bias;        /* [N], added before the activation (gated: of the gate), or NULL */
+    const void *up_bias;     /* gated only: [F], of the up projection, or NULL */
+    const void *residual;    /* linear only: [n][ldr], added after the activation, or NULL */
+    uint16_t *preact;        /* receives the bf16 pre-activations for the backward pass, or NULL:
+                                [n][ldp], ldp a multiple of 8, 16-byte aligned; linear: N columns;
+                                gated: nvfp4_gated_rows(F) columns in the gated weight's row order
+                                (columns of rows that do not exist are left as they were) */
+    int64_t ldr, ldp;
+    int32_t activation;      /* NVFP4_ACT_* */
+    int32_t bias_dtype;      /* of bias and up_bias: NVFP4_DTYPE_* */
+    int32_t residual_dtype;
+    int32_t out_dtype;       /* of Y or H */
+} nvfp4_epilogue;
+
+/* Y = act(gscale X dequant(W)^T + bias) + residual for any n up to
+ * NVFP4_MAX_GEMM_TOKENS, Wq / Wscale packed (nvfp4_pack).  Up to 16 tokens run
+ * the decode product (K parts beyond K = 8192, which need a workspace of
+ * nvfp4_linear_workspace_bytes(n, N, K) bytes, 16-byte aligned; calls that
+ * share one on different streams race), more run a token-tiled product.
+ * Errors: NULL, RANGE (n, N, K, strides, activation, types; up_bias set),
+ * SHAPE (K % 16, K > 262144, strides), ALIGN, OVERLAP, WORKSPACE, DEVICE,
+ * LAUNCH. */
+int nvfp4_linear(const uint8_t *Wq, const uint8_t *Wscale, float gscale, const uint16_t *X, int64_t ldx,
+                 void *Y, int64_t ldy, int n, int N, int K, const nvfp4_epilogue *epilogue,
+                 void *workspace, size_t workspace_bytes, void *stream);
+size_t nvfp4_linear_workspace_bytes(int n, int N, int K);
+
+/* Rows of the packed weight of a gated block with F outputs: its 16-row groups
+ * alternate gate, up, so gate row r is row (r / 16) * 32 + r % 16 and up row r
+ * lies 16 further; F is padded to 16.  0 if F < 1. */
+size_t nvfp4_gated_rows(int F);
+
+/* The gated weight from the packed gate and up weights (F x K each): codes /
+ * scales receive nvfp4_packed_*_bytes(nvfp4_gated_rows(F), K) bytes.  Once, at
+ * load time.  Errors: NULL, RANGE, SHAPE, ALIGN (16), OVERLAP, DEVICE, LAUNCH. */
+int nvfp4_pack_gated(const uint8_t *gate_codes, const uint8_t *gate_scales, const uint8_t *up_codes,
+                     const uint8_t *up_scales, int F, int K, uint8_t *codes, uint8_t *scales, void *stream);
+
+/* H = act(gate_gscale X Wg^T + bias) * (up_gscale X Wu^T + up_bias): both
+ * projections, the activation and the product in one launch on the gated
+ * weight of nvfp4_pack_gated.  n, workspace and errors as nvfp4_linear
+ * (residual set: RANGE). */
+int nvfp4_gated(const uint8_t *Wq, const uint8_t *Wscale, float gate_gscale, float up_gscale,
+                const uint16_t *X, int64_t ldx, void *H, int64_t ldh, int n, int F, int K,
+                const nvfp4_epilogue *epilogue, void *workspace, size_t workspace_bytes, void *stream);
+size_t nvfp4_gated_workspace_bytes(int n, int F, int K);
+
+/* The transposed copy of a packed weight, which nvfp4_gemm_t reads: tiles of
+ * 16 columns x 128 rows (rows padded with zero codes), codes in the lane order
+ * of the packed layout, and beside each tile the scales of its 128 rows.
+ * Another 9/16 byte a weight, made once, kept only where gradients are wanted. */
+size_t nvfp4_transposed_codes_bytes(int N, int K);
+size_t nvfp4_transposed_scales_bytes(int N, int K);
+int nvfp4_pack_transposed(const uint8_t *codes_packed, const uint8_t *scales_packed, int N, int K,
+                          uint8_t *codes_t, uint8_t *scales_t, void *stream);
+
+/* dX[n][K] = gscale dY[n][N] . dequant(W), bf16: the gradient of a projection
+ * with respect to its input.  Where N is not a multiple of 8, the elements up
+ * to the next multiple are read from each dY row and must be zero.
+ * Errors: NULL, RANGE, SHAPE, ALIGN, OVERLAP, DEVICE, LAUNCH. */
+int nvfp4_gemm_t(const uint8_t *codes_t, const uint8_t *scales_t, float gscale, const uint16_t *dY, int64_t ldy,
+                 uint16_t *dX, int64_t ldx, int n, int N, int K, void *stream);
+
+/* The elementwise half of nvfp4_linear's gradient: dZ = dY * act'(Z) in bf16
+ * with columns N .. next multiple of 8 zero (ready for nvfp4_gemm_t; ldz a
+ * multiple of 8, 16-byte aligned; NULL: not wanted) and dbias = column sums
+ * (NULL: not wanted) of the unrounded values, in a fixed order.  dY: any
+ * stride and alignment.  preact: as nvfp4_linear stored it (NULL with
+ * NVFP4_ACT_NONE).  Bias gradients need nvfp4_grad_workspace_bytes(n, N, 0)
+ * bytes of workspace.  The residual's gradient is dY itself.  Errors: NULL,
+ * RANGE, SHAPE, ALIGN, OVERLAP, WORKSPACE, DEVICE, LAUNCH. */
+int nvfp4_linear_grad(const void *dY, int dy_dtype, int64_t ldy, const uint16_t *preact, int64_t ldp,
+                      int activation, uint16_t *dZ, int64_t ldz, void *dbias, int bias_dtype, int n, int N,
+                      void *workspace, size_t workspace_bytes, void *stream);
+
+/* The same for nvfp4_gated: dZ [n][nvfp4_gated_rows(F)] holds, in the gated
+ * weight's row order, gate_gscale * dH * U * act'(G) and up_gscale * dH *
+ * act(G), zeros where no row exists, so that nvfp4_gemm_t with gscale 1 and N =
+ * nvfp4_gated_rows(F) on the transposed gated weight gives dX; the bias
+ * gradients are sums of the unscaled values.  Workspace:
+ * nvfp4_grad_workspace_bytes(n, F, 1). */
+int nvfp4_gated_grad(const void *dH, int dh_dtype, int64_t ldh, const uint16_t *preact, int64_t ldp,
+                     int activation, float gate_gscale, float up_gscale, uint16_t *dZ, int64_t ldz,
+                     void *dgate_bias, void *dup_bias, int bias_dtype, int n, int F, void *workspace,
+                     size_t workspace_bytes, void *stream);
+size_t nvfp4_grad_workspace_bytes(int n, int N, int gated);
 
 /* Human-readable name of a status code (static storage). */
 const char *nvfp4_strerror(int status);

@@ -25,7 +25,8 @@ MAX_TOKENS = 16
 
 STATUS = {0: "NVFP4_OK", 1: "NVFP4_ERR_NULL", 2: "NVFP4_ERR_RANGE", 3: "NVFP4_ERR_ALIGN",
           4: "NVFP4_ERR_SHAPE", 5: "NVFP4_ERR_SCHEDULE", 6: "NVFP4_ERR_LAUNCH",
-          7: "NVFP4_ERR_DEVICE", 8: "NVFP4_ERR_WORKSPACE", 9: "NVFP4_ERR_SCRATCH"}
+          7: "NVFP4_ERR_DEVICE", 8: "NVFP4_ERR_WORKSPACE", 9: "NVFP4_ERR_SCRATCH",
+          10: "NVFP4_ERR_OVERLAP"}
 
 
 class Nvfp4Error(RuntimeError):
@@ -264,6 +265,10 @@ class PackedWeight:
         gscale = float(ts[0].item())          # one host read at load time
         return cls(cp, sp, gscale, W.shape[0], W.shape[1])
 
+    def transpose(self, stream=None) -> "TransposedWeight":
+        """The transposed copy that gradients of this weight's products go through."""
+        return transpose(self, stream)
+
 
 # ---- the GEMV --------------------------------------------------------------
 
@@ -395,3 +400,7 @@ def gemv_qkv(w: PackedWeight, X: torch.Tensor, rows, out_off, ldy: int,
                                 _stream(stream, w.codes, w.scales, X, Y)),
            "nvfp4_gemv_qkv")
     return Y
+
+
+from .fused import (ACTIVATIONS, GatedWeight, TransposedWeight, gated, gated_backward, gated_rows, gemm_t,  # noqa: E402
+                    linear, linear_backward, preact_columns, transpose)

@@ -48,7 +48,8 @@ def llvm_tool(name: str) -> str:
 
 
 def disassemble(lib: str, arch: str = "gfx950") -> str:
-    """Disassembly of the `arch` code object bundled in the shared library `lib`."""
+    """Disassembly of the `arch` code objects (one a source) bundled in the
+    shared library `lib`."""
     objdump = llvm_tool("llvm-objdump")
     with tempfile.TemporaryDirectory() as tmp:
         copy = os.path.join(tmp, "lib.so")
@@ -56,11 +57,11 @@ def disassemble(lib: str, arch: str = "gfx950") -> str:
         subprocess.run([objdump, "--offloading", copy], cwd=tmp, check=True,
                        stdout=subprocess.DEVNULL, stderr=subprocess.DEVNULL)
         objs = [f for f in os.listdir(tmp) if f.endswith("--" + arch)]
-        if len(objs) != 1:
-            raise RuntimeError("no single %s code object in %s (found %s)" % (arch, lib, objs))
-        res = subprocess.run([objdump, "-d", "--mcpu=" + arch, os.path.join(tmp, objs[0])],
-                             check=True, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)
-        return res.stdout
+        if not objs:
+            raise RuntimeError("no %s code object in %s" % (arch, lib))
+        return "".join(subprocess.run([objdump, "-d", "--mcpu=" + arch, os.path.join(tmp, f)], check=True,
+                                      stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True).stdout
+                       for f in sorted(objs))
 
 
 def parse(text: str) -> dict:
@@ -217,7 +218,7 @@ def check_function(instrs: list, stats: dict = None) -> list:
     return [(a,) + violations[a] for a in sorted(violations)]
 
 
-def check_library(lib: str, pattern: str = r"nvfp4_gem[mv]_kernel") -> dict:
+def check_library(lib: str, pattern: str = r"nvfp4_(fused_)?gem[mv]_kernel") -> dict:
     """{kernel: violations} for every function of `lib` whose name matches
     `pattern`; raises if no function matches."""
     funcs = parse(disassemble(lib))

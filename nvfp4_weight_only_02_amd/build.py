@@ -10,6 +10,7 @@ before the wait that covers the load (asmcheck.py).
 """
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import re
 import shutil
@@ -21,7 +22,9 @@ ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libnvfp4.so")
 PROBES_LIB = os.path.join(PKG, "libnvfp4_probes.so")
 # (library, its sources)
-TARGETS = [(LIB, [os.path.join(PKG, "csrc", "nvfp4.hip")]),
+TARGETS = [(LIB, [os.path.join(PKG, "csrc", f) for f in
+                  ("nvfp4.hip", "fused.hip", "fused_gemm.hip", "fused_gemv_linear.hip",
+                   "fused_gemv_gated.hip", "fused_gemv_partial.hip")]),
            (PROBES_LIB, [os.path.join(PKG, "csrc", "probes.hip")])]
 ARCH = "gfx950"
 
@@ -30,7 +33,6 @@ HIPCC_FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     "-Wall",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-I", os.path.join(ROOT, "include"),
@@ -83,10 +85,10 @@ def check_inflight(lib: str) -> None:
         raise RuntimeError("registers of in-flight loads are touched before their wait:\n  " + "\n  ".join(lines))
 
 
-def build_one(lib: str, sources: list, verbose: bool = False) -> str:
-    """Compile one library (always) and return its path."""
-    tmp = lib + ".tmp%d" % os.getpid()
-    cmd = [hipcc()] + HIPCC_FLAGS + ["-Rpass-analysis=kernel-resource-usage"] + sources + ["-o", tmp]
+def compile_one(source: str, obj: str, verbose: bool = False) -> str:
+    """Compile one source to an object; returns what hipcc said beside the
+    resource remarks, which are checked here."""
+    cmd = [hipcc()] + HIPCC_FLAGS + ["-Rpass-analysis=kernel-resource-usage", "-c", source, "-o", obj]
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
@@ -103,16 +105,34 @@ def build_one(lib: str, sources: list, verbose: bool = False) -> str:
         after_remark = False
         kept.append(line)
     out = "\n".join(kept)
+    check_resources("\n".join(lines))
+    if res.returncode != 0:
+        raise RuntimeError("hipcc failed:\n" + out)
+    return out
+
+
+def build_one(lib: str, sources: list, verbose: bool = False) -> str:
+    """Compile one library (always), its sources side by side, and return its path."""
+    tmp = lib + ".tmp%d" % os.getpid()
+    objs = ["%s.%s.o" % (tmp, os.path.basename(s)) for s in sources]
     try:
-        check_resources("\n".join(lines))
+        with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(sources))) as pool:
+            outs = list(pool.map(lambda so: compile_one(so[0], so[1], verbose), zip(sources, objs)))
+        res = subprocess.run([hipcc(), "--offload-arch=" + ARCH, "-fPIC", "-shared"] + objs + ["-o", tmp],
+                             stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
         if res.returncode != 0:
-            raise RuntimeError("hipcc failed:\n" + out)
+            raise RuntimeError("linking failed:\n" + res.stdout)
         if lib == LIB:
             check_inflight(tmp)
     except RuntimeError:
         if os.path.exists(tmp):
             os.remove(tmp)
         raise
+    finally:
+        for o in objs:
+            if os.path.exists(o):
+                os.remove(o)
+    out = "\n".join(o for o in outs if o.strip())
     if verbose and out.strip():
         print(out)
     os.replace(tmp, lib)

@@ -1,0 +1,741 @@
+// The fused operators of include/nvfp4.h: argument checks and dispatch, the
+// layout steps of their weights, the epilogue of K parts and the elementwise
+// half of their gradients.
+#include "epilogue.h"
+#include "fused_gemm.h"
+
+namespace {
+
+// ---- layout steps (once, at load time) -------------------------------------------
+
+// Row groups of two packed weights in turn: gate 0, up 0, gate 1, up 1, ...
+// `per` 16-byte words a row group.
+__global__ void nvfp4_interleave_kernel(const u32x4 *gate, const u32x4 *up, long long per, long long words, u32x4 *out)
+{
+    const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    if (idx >= words)
+        return;
+    const long long rg = idx / per;
+    out[idx] = (rg & 1 ? up : gate)[(rg >> 1) * per + idx % per];
+}
+
+// Transposed tiles from packed ones.  One thread per 16-byte lane chunk of a
+// transposed tile: lane (i, g) of tile (kb, rt) holds column 16 kb + i at the
+// rows rt*128 + 16 b + 4 g + e (b = 0..7, e = 0..3), the same order in which a
+// packed tile's lane holds columns.
+__global__ void nvfp4_transpose_codes_kernel(const uint8_t *codes, int T, int RG, int TT, long long chunks, u32x4 *out)
+{
+    const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    if (idx >= chunks)
+        return;
+    const int l = (int)(idx & 63);
+    const long long tile = idx >> 6;
+    const int rt = (int)(tile % TT);
+    const int k = (int)(tile / TT) * 16 + (l & 15);
+    const int g = l >> 4;
+    // within a row's tile: lane 16 * (k % 16 / 4) + row % 16, byte and nibble of k
+    const int kt = k / kTileK, kk = k % kTileK;
+    const int byte = 2 * (kk >> 4) + ((kk & 3) >> 1), shift = 4 * (kk & 1);
+    u32 w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int q = 0; q < 32; ++q) {
+        const int r = rt * kTileK + 16 * (q >> 2) + 4 * g + (q & 3);
+        const int rg = r >> 4;
+        if (rg < RG) {
+            const long long src = ((long long)rg * T + kt) * 64 + ((kk & 15) >> 2) * 16 + (r & 15);
+            w[q >> 3] |= (u32)((codes[src * 16 + byte] >> shift) & 15) << (4 * (q & 7));
+        }
+    }
+    out[idx] = u32x4{w[0], w[1], w[2], w[3]};
+}
+
+// One thread per 4 scale bytes: of block column kb, rows rt*128 + 16 b + 4 g + e
+// at byte g*32 + b*4 + e of the tile's 128.
+__global__ void nvfp4_transpose_scales_kernel(const uint8_t *scales, int T, int RG, int TT, long long words, u32 *out)
+{
+    const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    if (idx >= words)
+        return;
+    const int q = (int)(idx & 31);
+    const long long tile = idx >> 5;
+    const int rt = (int)(tile % TT);
+    const int kb = (int)(tile / TT);
+    const int g = q >> 3, b = q & 7;
+    u32 w = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int r = rt * kTileK + 16 * b + 4 * g + e;
+        const int rg = r >> 4;
+        if (rg < RG)
+            w |= (u32)scales[(((long long)rg * T + kb / kBlocksPerTile) * 16 + (r & 15)) * 8 + kb % kBlocksPerTile]
+                 << (8 * e);
+    }
+    out[idx] = w;
+}
+
+// ---- K parts ------------------------------------------------------------------------
+
+// The parts of each output added in part order, then the epilogue.  Grid
+// (ceil(outputs / 256), n).
+template <bool GATED>
+__global__ __launch_bounds__(256) void nvfp4_fused_reduce_kernel(nvfp4_epi_params e, const float *P, int n, int rows, int ks)
+{
+    const int r = blockIdx.x * 256 + threadIdx.x;
+    const int tok = blockIdx.y;
+    if (r >= e.N)
+        return;
+    const long long count = (long long)n * rows;
+    auto total = [&](long long row) {
+        const float *src = P + (long long)tok * rows + row;
+        constexpr int kBatch = 8;   // loads in flight together
+        float s = 0.f;
+        for (int q0 = 0; q0 < ks; q0 += kBatch) {
+            float v[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+                v[j] = q0 + j < ks ? __builtin_nontemporal_load(src + (q0 + j) * count) : 0.f;
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+                if (q0 + j < ks)
+                    s = q0 + j == 0 ? v[j] : s + v[j];
+        }
+        return s;
+    };
+    if constexpr (GATED)
+        gated_out(e, tok, r, total(gated_row(r, 0)), total(gated_row(r, 1)));
+    else
+        linear_out(e, tok, r, total(r));
+}
+
+// ---- the elementwise half of the gradients ---------------------------------------------
+
+struct GradParams {
+    const void *dy;
+    const uint16_t *z;       // bf16 pre-activations, or null (identity)
+    uint16_t *dz;            // bf16, or null
+    float *partial;          // [row blocks][halves][cols] column sums, or null
+    void *db[2];             // bias gradients, or null
+    long long ldy, ldz, lddz;
+    int n, N, cols;          // outputs a token; columns visited (padded with zero gradients)
+    int act, dy_f32, db_f32, vec;
+    int rows_per_block;
+    float gscale[2];
+};
+
+constexpr int kGradCols = 256;   // columns of a block: 32 threads x 8, times 8 rows at once
+
+__device__ __forceinline__ void store_db(const GradParams &p, int half, int col, float v)
+{
+    if (p.db[half] && col < p.N)
+        store_any(p.db[half], col, p.db_f32, v);
+}
+
+// dZ = dY act'(Z) (linear), or of a gate and up row (dH U act'(G), dH act(G))
+// times its tensor scale (gated, so that one product with the gated weight
+// serves both), each rounded to bf16 for that product; and the column sums of
+// the unrounded, unscaled values.  Memory bound: dY and Z in, dZ out, 6 bytes
+// (gated 10) an output.  A block sums 8 * rows_per_block / 8 rows in a fixed
+// order, blocks are added in order: no atomics.
+template <bool GATED>
+__global__ __launch_bounds__(256) void nvfp4_grad_kernel(GradParams p)
+{
+    const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
+    const int c0 = blockIdx.x * kGradCols + cx * 8;
+    const int t1 = min(p.n, (int)(blockIdx.y + 1) * p.rows_per_block);
+    float sum[2][8] = {};
+    if (c0 < p.cols) {
+        for (int t = blockIdx.y * p.rows_per_block + ry; t < t1; t += 8) {
+            float dy[8];
+            const long long at = t * p.ldy + c0;
+            if (p.vec && c0 + 8 <= p.N) {
+                const f32x4 a = load_any4(p.dy, at, p.dy_f32), b = load_any4(p.dy, at + 4, p.dy_f32);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    dy[e] = a[e];
+                    dy[4 + e] = b[e];
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    dy[e] = c0 + e < p.N ? load_any(p.dy, at + e, p.dy_f32) : 0.f;
+            }
+            auto words = [&](long long col) {
+                return *reinterpret_cast<const u32x4 *>(p.z + t * p.ldz + col);
+            };
+            auto value = [](u32x4 w, int e) {
+                return __builtin_bit_cast(float, e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
+            };
+            u32x4 out[2];
+            const u32x4 z0 = p.z ? words(GATED ? gated_row(c0, 0) : c0) : u32x4{0u, 0u, 0u, 0u};
+            const u32x4 z1 = GATED ? words(gated_row(c0, 1)) : z0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float d[2];
+                // past the last output the pre-activations are not defined
+                const bool in = c0 + e < p.N;
+                if constexpr (GATED) {
+                    const float zg = value(z0, e);
+                    d[0] = in ? dy[e] * value(z1, e) * activate_grad(zg, p.act) : 0.f;
+                    d[1] = in ? dy[e] * activate(zg, p.act) : 0.f;
+                } else {
+                    d[0] = in ? (p.act == NVFP4_ACT_NONE ? dy[e] : dy[e] * activate_grad(value(z0, e), p.act)) : 0.f;
+                    d[1] = 0.f;
+                }
+#pragma unroll
+                for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+                    sum[h][e] += d[h];
+                    const u32 b = f32_to_bf16_bits(GATED ? d[h] * p.gscale[h] : d[h]);
+                    out[h][e >> 1] = e & 1 ? out[h][e >> 1] | b << 16 : b;
+                }
+            }
+            if (p.dz) {
+                *reinterpret_cast<u32x4 *>(p.dz + t * p.lddz + (GATED ? gated_row(c0, 0) : c0)) = out[0];
+                if constexpr (GATED)
+                    *reinterpret_cast<u32x4 *>(p.dz + t * p.lddz + gated_row(c0, 1)) = out[1];
+            }
+        }
+    }
+    if (!p.db[0] && !p.db[1])
+        return;
+    __shared__ float part[8][kGradCols + 8];
+#pragma unroll
+    for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            part[ry][cx * 8 + e] = sum[h][e];
+        __syncthreads();
+        float s = 0.f;
+#pragma unroll
+        for (int y = 0; y < 8; ++y)
+            s += part[y][threadIdx.x];
+        const int col = blockIdx.x * kGradCols + threadIdx.x;
+        if (col >= p.cols)
+            continue;
+        if (gridDim.y == 1)
+            store_db(p, h, col, s);
+        else
+            p.partial[((long long)blockIdx.y * (GATED ? 2 : 1) + h) * p.cols + col] = s;
+    }
+}
+
+// Bias gradients from the row blocks' sums, added in block order.
+__global__ __launch_bounds__(256) void nvfp4_grad_sum_kernel(GradParams p, int blocks, int halves)
+{
+    const int col = blockIdx.x * 256 + threadIdx.x;
+    const int h = blockIdx.y;
+    if (col >= p.N)
+        return;
+    float s = 0.f;
+    for (int y = 0; y < blocks; ++y)
+        s += p.partial[((long long)y * halves + h) * p.cols + col];
+    store_db(p, h, col, s);
+}
+
+// ---- host side --------------------------------------------------------------------------
+
+constexpr int kMaxStride = 1 << 22;   // elements between rows: keeps a token tile's offsets within 32 bits
+
+bool is_aligned(const void *p, size_t a)
+{
+    return ((uintptr_t)p % a) == 0;
+}
+
+// Bytes from the first to the last element of an [n][cols] matrix.
+size_t span(long long n, long long ld, long long cols, int size)
+{
+    return n > 0 ? (size_t)((n - 1) * ld + cols) * size : 0;
+}
+
+bool overlap(const void *a, size_t an, const void *b, size_t bn)
+{
+    if (!a || !b || !an || !bn)
+        return false;
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return x < y + bn && y < x + an;
+}
+
+bool valid_dtype(int d)
+{
+    return d == NVFP4_DTYPE_F32 || d == NVFP4_DTYPE_BF16;
+}
+
+int dtype_size(int d)
+{
+    return d == NVFP4_DTYPE_F32 ? 4 : 2;
+}
+
+// Shapes, strides and pointers that linear and gated share.  N: outputs a
+// token; rows: rows of the packed weight.
+int validate_forward(const uint8_t *Wq, const uint8_t *Wscale, const uint16_t *X, int64_t ldx, const void *out,
+                     int64_t ldo, int n, int N, int rows, int K, const nvfp4_epilogue *ep, bool gated)
+{
+    if (!Wq || !Wscale || !ep || (n > 0 && (!X || !out)))
+        return NVFP4_ERR_NULL;
+    if (n < 0 || n > NVFP4_MAX_GEMM_TOKENS || N < 1 || K < 1)
+        return NVFP4_ERR_RANGE;
+    if (K % 16 != 0 || K > kMaxK)
+        return NVFP4_ERR_SHAPE;
+    if (ep->activation < NVFP4_ACT_NONE || ep->activation > NVFP4_ACT_GELU_TANH || !valid_dtype(ep->out_dtype) ||
+        ((ep->bias || ep->up_bias) && !valid_dtype(ep->bias_dtype)) ||
+        (ep->residual && !valid_dtype(ep->residual_dtype)))
+        return NVFP4_ERR_RANGE;
+    if ((gated && ep->residual) || (!gated && ep->up_bias))
+        return NVFP4_ERR_RANGE;
+    const int64_t pre_cols = gated ? rows : N;
+    if (ldx < K || ldo < N || (ep->residual && ep->ldr < N) || (ep->preact && ep->ldp < pre_cols))
+        return NVFP4_ERR_RANGE;
+    if (ldx > kMaxStride || ldo > INT32_MAX || ep->ldr > INT32_MAX || ep->ldp > INT32_MAX)
+        return NVFP4_ERR_SHAPE;
+    const int os = dtype_size(ep->out_dtype);
+    if (!is_aligned(Wq, 16) || !is_aligned(Wscale, 16) || !is_aligned(X, 16) || (n > 1 && ldx % 8 != 0) ||
+        !is_aligned(out, os) || (ep->bias && !is_aligned(ep->bias, dtype_size(ep->bias_dtype))) ||
+        (ep->up_bias && !is_aligned(ep->up_bias, dtype_size(ep->bias_dtype))) ||
+        (ep->residual && !is_aligned(ep->residual, dtype_size(ep->residual_dtype))))
+        return NVFP4_ERR_ALIGN;
+    if (ep->preact && (!is_aligned(ep->preact, 16) || ep->ldp % 8 != 0))
+        return NVFP4_ERR_ALIGN;
+    // Workgroups read what others write unless the outputs lie apart.  The
+    // residual may be the output itself: each element is read by the thread
+    // that then writes it.
+    const size_t on = span(n, ldo, N, os), pn = ep->preact ? span(n, ep->ldp, pre_cols, 2) : 0;
+    const size_t xn = span(n, ldx, K, 2);
+    const size_t bn = (size_t)N * dtype_size(ep->bias_dtype);
+    const size_t wq = nvfp4_packed_codes_bytes(rows, K), ws = nvfp4_packed_scales_bytes(rows, K);
+    const size_t rn = ep->residual ? span(n, ep->ldr, N, dtype_size(ep->residual_dtype)) : 0;
+    const bool in_place = ep->residual == out && ep->ldr == ldo && ep->residual_dtype == ep->out_dtype;
+    if (overlap(out, on, X, xn) || overlap(out, on, Wq, wq) || overlap(out, on, Wscale, ws) ||
+        overlap(out, on, ep->bias, bn) || overlap(out, on, ep->up_bias, bn) || overlap(out, on, ep->preact, pn) ||
+        (!in_place && overlap(out, on, ep->residual, rn)) || overlap(ep->preact, pn, X, xn) ||
+        overlap(ep->preact, pn, Wq, wq) || overlap(ep->preact, pn, Wscale, ws) || overlap(ep->preact, pn, ep->bias, bn) ||
+        overlap(ep->preact, pn, ep->up_bias, bn) || overlap(ep->preact, pn, ep->residual, rn))
+        return NVFP4_ERR_OVERLAP;
+    return NVFP4_OK;
+}
+
+nvfp4_epi_params epi_params(const nvfp4_epilogue *ep, float gscale, float up_gscale, void *out, int64_t ldo, int N,
+                            int64_t pre_cols)
+{
+    nvfp4_epi_params e = {};
+    e.bias = ep->bias;
+    e.up_bias = ep->up_bias;
+    e.residual = ep->residual;
+    e.preact = ep->preact;
+    e.out = out;
+    e.ldr = (int)ep->ldr;
+    e.ldp = (int)ep->ldp;
+    e.ldo = (int)ldo;
+    e.gscale = gscale;
+    e.up_gscale = up_gscale;
+    e.N = N;
+    e.flags = ep->activation | (ep->bias_dtype == NVFP4_DTYPE_F32 ? kEpiBiasF32 : 0) |
+              (ep->residual_dtype == NVFP4_DTYPE_F32 ? kEpiResidualF32 : 0) |
+              (ep->out_dtype == NVFP4_DTYPE_F32 ? kEpiOutF32 : 0);
+    const int bs = 4 * dtype_size(ep->bias_dtype), rs = 4 * dtype_size(ep->residual_dtype);
+    const int os = 4 * dtype_size(ep->out_dtype);
+    const bool vec = ldo % 4 == 0 && is_aligned(out, os) && (!ep->bias || is_aligned(ep->bias, bs)) &&
+            (!ep->up_bias || is_aligned(ep->up_bias, bs)) &&
+            (!ep->residual || (ep->ldr % 4 == 0 && is_aligned(ep->residual, rs)));
+    if (vec)
+        e.flags |= kEpiVec;
+    return e;
+}
+
+// K parts of a fused call: one launch up to 8192 columns and beyond 16 tokens.
+int fused_kparts(int n, int rows, int K)
+{
+    return n <= NVFP4_MAX_TOKENS ? nvfp4_gemv_kparts(rows, K) : 1;
+}
+
+size_t parts_bytes(int n, int rows, int K)
+{
+    const int ks = n > 0 ? fused_kparts(n, rows, K) : 1;
+    return ks > 1 ? (size_t)ks * n * rows * sizeof(float) : 0;
+}
+
+// rows: rows of the packed weight; gated: its row groups alternate gate, up.
+int forward(const uint8_t *Wq, const uint8_t *Wscale, const uint16_t *X, int64_t ldx, int n, int rows, int K,
+            const nvfp4_epi_params &e, bool gated, void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    if (n <= NVFP4_MAX_TOKENS) {
+        const int ks = fused_kparts(n, rows, K);
+        if (ks < 1)
+            return -ks;
+        nvfp4_fused_gemv_args a = {};
+        a.codes = Wq;
+        a.scales = Wscale;
+        a.X = X;
+        a.ldx = (int)ldx;
+        a.n = n;
+        a.K = K;
+        a.rows = rows;
+        a.units = (int)(row_groups(rows) / (gated && ks == 1 ? 2 : 1));
+        a.ks = ks;
+        a.epi = e;
+        if (ks == 1)
+            return gated ? nvfp4_launch_fused_gemv_gated(a, stream) : nvfp4_launch_fused_gemv_linear(a, stream);
+        if (!workspace || workspace_bytes < parts_bytes(n, rows, K))
+            return NVFP4_ERR_WORKSPACE;
+        if (!is_aligned(workspace, 16))
+            return NVFP4_ERR_ALIGN;
+        a.partials = static_cast<float *>(workspace);
+        const int st = nvfp4_launch_fused_gemv_partial(a, stream);
+        if (st != NVFP4_OK)
+            return st;
+        const dim3 grid((unsigned)((e.N + 255) / 256), (unsigned)n);
+        if (gated)
+            hipLaunchKernelGGL(nvfp4_fused_reduce_kernel<true>, grid, dim3(256), 0, stream, e, a.partials, n, rows, ks);
+        else
+            hipLaunchKernelGGL(nvfp4_fused_reduce_kernel<false>, grid, dim3(256), 0, stream, e, a.partials, n, rows, ks);
+        return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
+    }
+    nvfp4_fused_gemm_args a = {};
+    a.mode = gated ? 1 : 0;
+    a.codes = Wq;
+    a.scales = Wscale;
+    a.X = X;
+    a.ldx = ldx;
+    a.n = n;
+    a.K = K;
+    a.row_groups = (int)row_groups(rows);
+    a.epi = e;
+    return nvfp4_launch_fused_gemm(a, stream);
+}
+
+// Rows of the packed weight of a gated block of F outputs.
+long long gated_rows(long long F)
+{
+    return 2 * kRowsPerGroup * row_groups(F);
+}
+
+// Token rows a block of the gradient kernel sums: from the shape alone, so that
+// the order of the sums is.  About 2048 blocks where n allows.
+int grad_rows_per_block(int n, int cols)
+{
+    const long long bx = (cols + kGradCols - 1) / kGradCols;
+    const long long by = (2048 + bx - 1) / bx;
+    return (int)(((n + by - 1) / by + 7) / 8 * 8);
+}
+
+int grad_blocks(int n, int cols)
+{
+    const int rows = n > 0 ? grad_rows_per_block(n, cols) : 8;
+    return n > 0 ? (n + rows - 1) / rows : 1;
+}
+
+size_t grad_bytes(int n, int cols, int halves)
+{
+    const int by = grad_blocks(n, cols);
+    return by > 1 ? (size_t)by * halves * cols * sizeof(float) : 0;
+}
+
+int launch_grad(GradParams p, bool gated, void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    const int halves = gated ? 2 : 1;
+    const bool sums = p.db[0] || p.db[1];
+    if (!sums && (!p.dz || p.n == 0))
+        return NVFP4_OK;
+    const int by = grad_blocks(p.n, p.cols);
+    if (sums && by > 1) {
+        if (!workspace || workspace_bytes < grad_bytes(p.n, p.cols, halves))
+            return NVFP4_ERR_WORKSPACE;
+        if (!is_aligned(workspace, 16))
+            return NVFP4_ERR_ALIGN;
+    }
+    int cus = 0;
+    const int st = nvfp4_device_cus(&cus);
+    if (st != NVFP4_OK)
+        return st;
+    p.partial = static_cast<float *>(workspace);
+    p.rows_per_block = p.n > 0 ? grad_rows_per_block(p.n, p.cols) : 8;
+    const dim3 grid((unsigned)((p.cols + kGradCols - 1) / kGradCols), (unsigned)by);
+    if (gated)
+        hipLaunchKernelGGL(nvfp4_grad_kernel<true>, grid, dim3(256), 0, stream, p);
+    else
+        hipLaunchKernelGGL(nvfp4_grad_kernel<false>, grid, dim3(256), 0, stream, p);
+    if (hipGetLastError() != hipSuccess)
+        return NVFP4_ERR_LAUNCH;
+    if (sums && by > 1) {
+        hipLaunchKernelGGL(nvfp4_grad_sum_kernel, dim3((unsigned)((p.N + 255) / 256), (unsigned)halves), dim3(256), 0,
+                           stream, p, by, halves);
+        if (hipGetLastError() != hipSuccess)
+            return NVFP4_ERR_LAUNCH;
+    }
+    return NVFP4_OK;
+}
+
+int validate_grad(const void *dY, int dy_dtype, int64_t ldy, const uint16_t *preact, int64_t ldp, int activation,
+                  const uint16_t *dZ, int64_t ldz, const void *db0, const void *db1, int db_dtype, int n, int N,
+                  int64_t pre_cols, int64_t dz_cols)
+{
+    if (n > 0 && (!dY || (!preact && activation != NVFP4_ACT_NONE)))
+        return NVFP4_ERR_NULL;
+    if (n < 0 || n > NVFP4_MAX_GEMM_TOKENS || N < 1 || N > (1 << 30))
+        return NVFP4_ERR_RANGE;
+    if (activation < NVFP4_ACT_NONE || activation > NVFP4_ACT_GELU_TANH || !valid_dtype(dy_dtype) ||
+        ((db0 || db1) && !valid_dtype(db_dtype)))
+        return NVFP4_ERR_RANGE;
+    if (ldy < N || (preact && ldp < pre_cols) || (dZ && ldz < dz_cols))
+        return NVFP4_ERR_RANGE;
+    if (ldy > INT32_MAX || ldp > INT32_MAX || ldz > INT32_MAX)
+        return NVFP4_ERR_SHAPE;
+    const int ds = dtype_size(dy_dtype), bs = dtype_size(db_dtype);
+    if (!is_aligned(dY, ds) || (preact && (!is_aligned(preact, 16) || ldp % 8 != 0)) ||
+        (dZ && (!is_aligned(dZ, 16) || ldz % 8 != 0)) || (db0 && !is_aligned(db0, bs)) || (db1 && !is_aligned(db1, bs)))
+        return NVFP4_ERR_ALIGN;
+    const size_t yn = span(n, ldy, N, ds), pn = preact ? span(n, ldp, pre_cols, 2) : 0;
+    const size_t zn = dZ ? span(n, ldz, dz_cols, 2) : 0, bn = (size_t)N * bs;
+    if (overlap(dZ, zn, dY, yn) || overlap(dZ, zn, preact, pn) || overlap(dZ, zn, db0, bn) || overlap(dZ, zn, db1, bn) ||
+        overlap(db0, bn, dY, yn) || overlap(db1, bn, dY, yn) || overlap(db0, bn, preact, pn) ||
+        overlap(db1, bn, preact, pn) || overlap(db0, bn, db1, bn))
+        return NVFP4_ERR_OVERLAP;
+    return NVFP4_OK;
+}
+
+unsigned blocks_of(long long items)
+{
+    return (unsigned)((items + 255) / 256);
+}
+
+}  // namespace
+
+extern "C" {
+
+// ---- weights ----
+
+size_t nvfp4_gated_rows(int F)
+{
+    return F > 0 && F <= (1 << 30) ? (size_t)gated_rows(F) : 0;
+}
+
+int nvfp4_pack_gated(const uint8_t *gate_codes, const uint8_t *gate_scales, const uint8_t *up_codes,
+                     const uint8_t *up_scales, int F, int K, uint8_t *codes, uint8_t *scales, void *stream)
+{
+    if (!gate_codes || !gate_scales || !up_codes || !up_scales || !codes || !scales)
+        return NVFP4_ERR_NULL;
+    if (F < 1 || F > (1 << 30) || K < 1)
+        return NVFP4_ERR_RANGE;
+    if (K % 16 != 0 || K > kMaxK)
+        return NVFP4_ERR_SHAPE;
+    for (const uint8_t *q : {gate_codes, gate_scales, up_codes, up_scales, (const uint8_t *)codes, (const uint8_t *)scales})
+        if (!is_aligned(q, 16))
+            return NVFP4_ERR_ALIGN;
+    const size_t cb = nvfp4_packed_codes_bytes(F, K), sb = nvfp4_packed_scales_bytes(F, K);
+    if (overlap(codes, 2 * cb, gate_codes, cb) || overlap(codes, 2 * cb, up_codes, cb) ||
+        overlap(scales, 2 * sb, gate_scales, sb) || overlap(scales, 2 * sb, up_scales, sb) ||
+        overlap(codes, 2 * cb, scales, 2 * sb) || overlap(codes, 2 * cb, gate_scales, sb) ||
+        overlap(codes, 2 * cb, up_scales, sb) || overlap(scales, 2 * sb, gate_codes, cb) ||
+        overlap(scales, 2 * sb, up_codes, cb))
+        return NVFP4_ERR_OVERLAP;
+    const long long T = k_tiles(K), RG = row_groups(F);
+    const long long cw = 2 * RG * T * 64, sw = 2 * RG * T * 8;
+    if ((cw + 255) / 256 > INT32_MAX)
+        return NVFP4_ERR_SHAPE;
+    int cus = 0;
+    const int st = nvfp4_device_cus(&cus);
+    if (st != NVFP4_OK)
+        return st;
+    hipStream_t s = (hipStream_t)stream;
+    hipLaunchKernelGGL(nvfp4_interleave_kernel, dim3(blocks_of(cw)), dim3(256), 0, s, (const u32x4 *)gate_codes,
+                       (const u32x4 *)up_codes, T * 64, cw, (u32x4 *)codes);
+    hipLaunchKernelGGL(nvfp4_interleave_kernel, dim3(blocks_of(sw)), dim3(256), 0, s, (const u32x4 *)gate_scales,
+                       (const u32x4 *)up_scales, T * 8, sw, (u32x4 *)scales);
+    return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
+}
+
+size_t nvfp4_transposed_codes_bytes(int N, int K)
+{
+    return N > 0 && K > 0 && K % 16 == 0 ? (size_t)(K / 16) * k_tiles(N) * 1024 : 0;
+}
+
+size_t nvfp4_transposed_scales_bytes(int N, int K)
+{
+    return N > 0 && K > 0 && K % 16 == 0 ? (size_t)(K / 16) * k_tiles(N) * 128 : 0;
+}
+
+int nvfp4_pack_transposed(const uint8_t *codes_packed, const uint8_t *scales_packed, int N, int K, uint8_t *codes_t,
+                          uint8_t *scales_t, void *stream)
+{
+    if (!codes_packed || !scales_packed || !codes_t || !scales_t)
+        return NVFP4_ERR_NULL;
+    if (N < 1 || N > (1 << 30) || K < 1)
+        return NVFP4_ERR_RANGE;
+    if (K % 16 != 0 || K > kMaxK)
+        return NVFP4_ERR_SHAPE;
+    for (const uint8_t *q : {codes_packed, scales_packed, (const uint8_t *)codes_t, (const uint8_t *)scales_t})
+        if (!is_aligned(q, 16))
+            return NVFP4_ERR_ALIGN;
+    const size_t cb = nvfp4_packed_codes_bytes(N, K), sb = nvfp4_packed_scales_bytes(N, K);
+    const size_t ct = nvfp4_transposed_codes_bytes(N, K), stb = nvfp4_transposed_scales_bytes(N, K);
+    if (overlap(codes_t, ct, codes_packed, cb) || overlap(codes_t, ct, scales_packed, sb) ||
+        overlap(scales_t, stb, codes_packed, cb) || overlap(scales_t, stb, scales_packed, sb) ||
+        overlap(codes_t, ct, scales_t, stb))
+        return NVFP4_ERR_OVERLAP;
+    const int T = (int)k_tiles(K), RG = (int)row_groups(N), TT = (int)k_tiles(N);
+    const long long chunks = (long long)(K / 16) * TT * 64, words = (long long)(K / 16) * TT * 32;
+    if ((chunks + 255) / 256 > INT32_MAX)
+        return NVFP4_ERR_SHAPE;
+    int cus = 0;
+    const int st = nvfp4_device_cus(&cus);
+    if (st != NVFP4_OK)
+        return st;
+    hipStream_t s = (hipStream_t)stream;
+    hipLaunchKernelGGL(nvfp4_transpose_codes_kernel, dim3(blocks_of(chunks)), dim3(256), 0, s, codes_packed, T, RG, TT,
+                       chunks, (u32x4 *)codes_t);
+    hipLaunchKernelGGL(nvfp4_transpose_scales_kernel, dim3(blocks_of(words)), dim3(256), 0, s, scales_packed, T, RG, TT,
+                       words, (u32 *)scales_t);
+    return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
+}
+
+// ---- forward ----
+
+size_t nvfp4_linear_workspace_bytes(int n, int N, int K)
+{
+    if (n < 0 || n > NVFP4_MAX_GEMM_TOKENS || N < 1 || K < 1 || K % 16 != 0 || K > kMaxK)
+        return 0;
+    return parts_bytes(n, N, K);
+}
+
+int nvfp4_linear(const uint8_t *Wq, const uint8_t *Wscale, float gscale, const uint16_t *X, int64_t ldx, void *Y,
+                 int64_t ldy, int n, int N, int K, const nvfp4_epilogue *epilogue, void *workspace,
+                 size_t workspace_bytes, void *stream)
+{
+    const int st = validate_forward(Wq, Wscale, X, ldx, Y, ldy, n, N, N, K, epilogue, false);
+    if (st != NVFP4_OK || n == 0)
+        return st;
+    return forward(Wq, Wscale, X, ldx, n, N, K, epi_params(epilogue, gscale, 0.f, Y, ldy, N, N), false, workspace,
+                   workspace_bytes, (hipStream_t)stream);
+}
+
+size_t nvfp4_gated_workspace_bytes(int n, int F, int K)
+{
+    if (n < 0 || n > NVFP4_MAX_GEMM_TOKENS || F < 1 || F > (1 << 29) || K < 1 || K % 16 != 0 || K > kMaxK)
+        return 0;
+    return parts_bytes(n, (int)gated_rows(F), K);
+}
+
+int nvfp4_gated(const uint8_t *Wq, const uint8_t *Wscale, float gate_gscale, float up_gscale, const uint16_t *X,
+                int64_t ldx, void *H, int64_t ldh, int n, int F, int K, const nvfp4_epilogue *epilogue, void *workspace,
+                size_t workspace_bytes, void *stream)
+{
+    if (F < 1 || F > (1 << 29))
+        return NVFP4_ERR_RANGE;
+    const int rows = (int)gated_rows(F);
+    const int st = validate_forward(Wq, Wscale, X, ldx, H, ldh, n, F, rows, K, epilogue, true);
+    if (st != NVFP4_OK || n == 0)
+        return st;
+    return forward(Wq, Wscale, X, ldx, n, rows, K, epi_params(epilogue, gate_gscale, up_gscale, H, ldh, F, rows), true,
+                   workspace, workspace_bytes, (hipStream_t)stream);
+}
+
+// ---- backward ----
+
+size_t nvfp4_grad_workspace_bytes(int n, int N, int gated)
+{
+    if (n < 0 || n > NVFP4_MAX_GEMM_TOKENS || N < 1 || N > (1 << 29))
+        return 0;
+    return gated ? grad_bytes(n, (int)(gated_rows(N) / 2), 2) : grad_bytes(n, (N + 7) / 8 * 8, 1);
+}
+
+int nvfp4_linear_grad(const void *dY, int dy_dtype, int64_t ldy, const uint16_t *preact, int64_t ldp, int activation,
+                      uint16_t *dZ, int64_t ldz, void *dbias, int bias_dtype, int n, int N, void *workspace,
+                      size_t workspace_bytes, void *stream)
+{
+    const int cols = N > 0 && N <= (1 << 29) ? (N + 7) / 8 * 8 : 0;
+    if (!cols)
+        return NVFP4_ERR_RANGE;
+    const int st = validate_grad(dY, dy_dtype, ldy, preact, ldp, activation, dZ, ldz, dbias, nullptr, bias_dtype, n, N,
+                                 N, cols);
+    if (st != NVFP4_OK)
+        return st;
+    GradParams p = {};
+    p.dy = dY;
+    p.z = activation == NVFP4_ACT_NONE ? nullptr : preact;
+    p.dz = dZ;
+    p.db[0] = dbias;
+    p.ldy = ldy;
+    p.ldz = ldp;
+    p.lddz = ldz;
+    p.n = n;
+    p.N = N;
+    p.cols = cols;
+    p.act = activation;
+    p.dy_f32 = dy_dtype == NVFP4_DTYPE_F32;
+    p.db_f32 = bias_dtype == NVFP4_DTYPE_F32;
+    p.vec = ldy % 4 == 0 && is_aligned(dY, 4 * dtype_size(dy_dtype));
+    return launch_grad(p, false, workspace, workspace_bytes, (hipStream_t)stream);
+}
+
+int nvfp4_gated_grad(const void *dH, int dh_dtype, int64_t ldh, const uint16_t *preact, int64_t ldp, int activation,
+                     float gate_gscale, float up_gscale, uint16_t *dZ, int64_t ldz, void *dgate_bias, void *dup_bias,
+                     int bias_dtype, int n, int F, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (F < 1 || F > (1 << 29))
+        return NVFP4_ERR_RANGE;
+    if (n > 0 && !preact)
+        return NVFP4_ERR_NULL;
+    const int64_t rows = gated_rows(F);
+    const int st = validate_grad(dH, dh_dtype, ldh, preact, ldp, activation, dZ, ldz, dgate_bias, dup_bias, bias_dtype,
+                                 n, F, rows, rows);
+    if (st != NVFP4_OK)
+        return st;
+    GradParams p = {};
+    p.dy = dH;
+    p.z = preact;
+    p.dz = dZ;
+    p.db[0] = dgate_bias;
+    p.db[1] = dup_bias;
+    p.ldy = ldh;
+    p.ldz = ldp;
+    p.lddz = ldz;
+    p.n = n;
+    p.N = F;
+    p.cols = (int)(rows / 2);
+    p.act = activation;
+    p.dy_f32 = dh_dtype == NVFP4_DTYPE_F32;
+    p.db_f32 = bias_dtype == NVFP4_DTYPE_F32;
+    p.vec = ldh % 4 == 0 && is_aligned(dH, 4 * dtype_size(dh_dtype));
+    p.gscale[0] = gate_gscale;
+    p.gscale[1] = up_gscale;
+    return launch_grad(p, true, workspace, workspace_bytes, (hipStream_t)stream);
+}
+
+int nvfp4_gemm_t(const uint8_t *codes_t, const uint8_t *scales_t, float gscale, const uint16_t *dY, int64_t ldy,
+                 uint16_t *dX, int64_t ldx, int n, int N, int K, void *stream)
+{
+    if (!codes_t || !scales_t || (n > 0 && (!dY || !dX)))
+        return NVFP4_ERR_NULL;
+    if (n < 0 || n > NVFP4_MAX_GEMM_TOKENS || N < 1 || N > (1 << 30) || K < 1)
+        return NVFP4_ERR_RANGE;
+    if (K % 16 != 0 || K > kMaxK)
+        return NVFP4_ERR_SHAPE;
+    const int cols = (N + 7) / 8 * 8;
+    if (ldy < (n > 1 ? cols : N) || ldx < K)
+        return NVFP4_ERR_RANGE;
+    if (ldy > kMaxStride || ldx > INT32_MAX)
+        return NVFP4_ERR_SHAPE;
+    if (!is_aligned(codes_t, 16) || !is_aligned(scales_t, 16) || !is_aligned(dY, 16) || (n > 1 && ldy % 8 != 0) ||
+        !is_aligned(dX, 2))
+        return NVFP4_ERR_ALIGN;
+    const size_t yn = span(n, ldy, cols, 2), xn = span(n, ldx, K, 2);
+    if (overlap(dX, xn, dY, yn) || overlap(dX, xn, codes_t, nvfp4_transposed_codes_bytes(N, K)) ||
+        overlap(dX, xn, scales_t, nvfp4_transposed_scales_bytes(N, K)))
+        return NVFP4_ERR_OVERLAP;
+    if (n == 0)
+        return NVFP4_OK;
+    nvfp4_epilogue ep = {};
+    ep.out_dtype = ep.bias_dtype = ep.residual_dtype = NVFP4_DTYPE_BF16;
+    nvfp4_fused_gemm_args a = {};
+    a.mode = 2;
+    a.codes = codes_t;
+    a.scales = scales_t;
+    a.X = dY;
+    a.ldx = ldy;
+    a.n = n;
+    a.K = cols;
+    a.row_groups = K / 16;
+    a.epi = epi_params(&ep, gscale, 0.f, dX, ldx, K, K);
+    return nvfp4_launch_fused_gemm(a, (hipStream_t)stream);
+}
+
+}  // extern "C"

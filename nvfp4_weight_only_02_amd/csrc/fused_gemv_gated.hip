@@ -1,0 +1,7 @@
+// The gated form of the decode product with a fused epilogue (fused_gemv.inc).
+#include "fused_gemv.inc"
+
+int nvfp4_launch_fused_gemv_gated(const nvfp4_fused_gemv_args &a, hipStream_t stream)
+{
+    return launch_fused_gemv<1>(a, stream);
+}

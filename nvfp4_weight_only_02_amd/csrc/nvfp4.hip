@@ -49,133 +49,12 @@
 #include <string.h>
 
 #include <mutex>
-#include <type_traits>
-#include <utility>
 
 #include "../../include/nvfp4.h"
+#include "device.h"
+#include "internal.h"
 
 namespace {
-
-typedef unsigned int u32;
-typedef u32 u32x4 __attribute__((ext_vector_type(4)));
-typedef u32 u32x2 __attribute__((ext_vector_type(2)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
-constexpr int kRowsPerGroup = 16;      // MFMA N dimension: weight rows per tile
-constexpr int kTileK = 128;            // K columns per tile (8 NVFP4 blocks)
-constexpr int kBlocksPerTile = kTileK / 16;
-constexpr int kMaxTilesPerWave = 8;    // X slice of a wave: 16 VGPRs per tile
-constexpr int kMaxTilesChunked = 7;    // per wave and K chunk when K needs several chunks
-constexpr int kWaves = 8;            // waves per workgroup, one K-slice each
-constexpr int kBufferWord3 = 0x00020000;   // gfx9 raw buffer resource: 32-bit data, no swizzle
-constexpr unsigned kOutOfRange = 0x7FFFFFF0u;   // buffer offset past any resource: reads zeros
-constexpr int kSlots = 8;                        // row-group partials parked in LDS
-constexpr int kMaxK = 1 << 18;                   // keeps every buffer offset within 32 bits
-constexpr int kMaxKParts = 64;                   // K parts of a split launch
-
-// 16-row groups of N rows and 128-column tiles of K columns, rounded up in
-// 64-bit arithmetic (no int near INT_MAX overflows).
-constexpr long long row_groups(long long N)
-{
-    return (N + kRowsPerGroup - 1) / kRowsPerGroup;
-}
-constexpr long long k_tiles(long long K)
-{
-    return (K + kTileK - 1) / kTileK;
-}
-
-struct GemvParams {
-    const u32x4 *codes;    // packed codes, [RG][T][64 lanes] x 16 B
-    const u32x2 *scales;   // packed scales, [RG][T][16 rows] x 8 B
-    const uint16_t *X;     // bf16 [n][K]
-    uint16_t *Y;           // bf16 output, token stride ldy
-    float gscale;
-    int n, N, K, T, RG;
-    int kc;                // K chunks (passes) of a K part: chunk c covers its tiles [c*8*MT, (c+1)*8*MT)
-    int rg_base, rg_rem;   // row groups per workgroup: rg_base, +1 for the first rg_rem
-    int start1, start2;    // first row of the 2nd and 3rd projection (N if absent)
-    long long off0, off1, off2, ldy;
-    // K split: workgroups [q*wpp, (q+1)*wpp) own the tiles [q*tp, min((q+1)*tp, T))
-    // of K part q.  With P set they store fp32 partials P[q][t][r] (unscaled)
-    // instead of Y; nvfp4_ksplit_reduce_kernel then sums the parts.
-    int tp, wpp;
-    float *P;
-};
-
-// Two E2M1 codes (byte `sel` of w) -> two bf16 values, unscaled (scale 1.0).
-__device__ __forceinline__ u32 fp4x2_to_bf16x2(u32 w, int sel)
-{
-    bf16x2 v;
-    switch (sel) {
-    case 0: v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 0); break;
-    case 1: v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 1); break;
-    case 2: v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 2); break;
-    default: v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 3); break;
-    }
-    return __builtin_bit_cast(u32, v);
-}
-
-// Calls f(std::integral_constant<int, j>) for j = 0 .. N-1.
-template <typename F, int... J>
-__device__ __forceinline__ void static_for_impl(F &&f, std::integer_sequence<int, J...>)
-{
-    (f(std::integral_constant<int, J>{}), ...);
-}
-
-template <int N, typename F>
-__device__ __forceinline__ void static_for(F &&f)
-{
-    static_for_impl(f, std::make_integer_sequence<int, N>{});
-}
-
-// A raw buffer resource over [base, base + bytes) (gfx9 layout: 48-bit base,
-// stride 0, byte-granular range check).
-__device__ __forceinline__ u32x4 buffer_rsrc(const void *base, unsigned bytes)
-{
-    const unsigned long long a = (unsigned long long)base;
-    return u32x4{(u32)a, (u32)(a >> 32) & 0xFFFFu, bytes, (u32)kBufferWord3};
-}
-
-// Loads whose completion is tracked by hand (see the vmcnt bookkeeping in
-// the kernel).  Offsets past the resource's range return zeros.
-__device__ __forceinline__ u32x4 buffer_load_b128(u32x4 rsrc, unsigned off)
-{
-    u32x4 v;
-    asm volatile("buffer_load_dwordx4 %0, %1, %2, 0 offen" : "=v"(v) : "v"(off), "s"(rsrc));
-    return v;
-}
-
-__device__ __forceinline__ u32x4 buffer_load_b128_nt(u32x4 rsrc, unsigned off)
-{
-    u32x4 v;
-    asm volatile("buffer_load_dwordx4 %0, %1, %2, 0 offen nt" : "=v"(v) : "v"(off), "s"(rsrc));
-    return v;
-}
-
-// Wait until at most N vector-memory operations are outstanding; the
-// registers passed are the ones the wait makes valid (tied in and out, so no
-// read of them can be scheduled before it).
-template <int N>
-__device__ __forceinline__ void vm_wait4(u32x4 &a, u32x4 &b, u32x4 &c, u32x4 &d, std::integral_constant<int, N>)
-{
-    static_assert(N >= 0 && N <= 63, "vmcnt is a 6-bit field");
-    asm volatile("s_waitcnt vmcnt(%4)" : "+v"(a), "+v"(b), "+v"(c), "+v"(d) : "n"(N));
-}
-
-__device__ __forceinline__ uint16_t f32_to_bf16_bits(float f)
-{
-    return __builtin_bit_cast(uint16_t, (__bf16)f);   // v_cvt_pk_bf16_f32: RNE
-}
-
-template <int N>
-__device__ __forceinline__ void vm_wait1(u32x4 &a, std::integral_constant<int, N>)
-{
-    static_assert(N >= 0 && N <= 63, "vmcnt is a 6-bit field");
-    asm volatile("s_waitcnt vmcnt(%1)" : "+v"(a) : "n"(N));
-}
 
 // One launch covers every token (n <= 16) of one weight matrix.
 //   MT    tiles of the K-slice each of the kWaves waves owns in one K chunk
@@ -195,196 +74,8 @@ __device__ __forceinline__ void vm_wait1(u32x4 &a, std::integral_constant<int, N
 template <int MT, int NV, bool EXACT, bool CHUNKED, bool SPLIT>
 __global__ __launch_bounds__(kWaves * 64) void nvfp4_gemv_kernel(GemvParams p)
 {
-    static_assert(!(SPLIT && CHUNKED), "a K part is one pass");
-    constexpr int W = kWaves;
-    const int lane = threadIdx.x & 63;
-    const int wave = threadIdx.x >> 6;
-    const int i = lane & 15;   // MFMA row of A (token 4*(i%4) + i/4), weight row of B and C
-    const int g = lane >> 4;   // K quarter of A and B, accumulator token offset of C
-
-    const int kpart = SPLIT ? (int)blockIdx.x / p.wpp : 0;   // K part: tiles [pt0, pt1)
-    const int wg = SPLIT ? (int)blockIdx.x - kpart * p.wpp : (int)blockIdx.x;
-    const int pt0 = SPLIT ? kpart * p.tp : 0;
-    const int pt1 = SPLIT ? min(p.T, pt0 + p.tp) : p.T;
-    const int rg0 = wg * p.rg_base + min(wg, p.rg_rem);
-    const int rg1 = rg0 + p.rg_base + (wg < p.rg_rem ? 1 : 0);
-    // Wave w's slice of the K chunk that starts at tile cb: tiles w0 + W * t
-    // (w0 = cb + w, t < MT), of which those before the part's end pt1 exist
-    // (a prefix, since the tiles ascend with t).
-    auto first_tile = [&](int cb) { return cb + wave; };
-    auto tiles_in = [&](int w0) { return max(0, min(MT, (pt1 - w0 + W - 1) / W)); };
-    int tw0 = first_tile(pt0);   // first tile of this wave's slice in the current K chunk
-    int tw = MT;                 // tiles of it that exist
-
-    // All vector-memory loads of the main path are inline buffer loads waited
-    // for with explicit, compile-time vmcnt values: loads retire in issue
-    // order, so "at most N newer loads outstanding" is exact bookkeeping, and
-    // every read of a loaded register goes through the wait statement (its
-    // operands are tied), so nothing reads a register whose load is still in
-    // flight.  Buffer resources: X ends at row n, the weights at this
-    // workgroup's last row group; loads past the end return zeros without a
-    // memory access.
-    const unsigned nrg = (unsigned)(rg1 - rg0);
-    const u32x4 crsrc = buffer_rsrc(p.codes + (size_t)rg0 * p.T * 64, nrg * p.T * 1024u);
-    const u32x4 srsrc = buffer_rsrc(reinterpret_cast<const char *>(p.scales) + (size_t)rg0 * p.T * 128,
-                                    nrg * p.T * 128u);
-    const u32x4 xrsrc = buffer_rsrc(p.X, (unsigned)(p.n * p.K * 2));
-
-    // X first (it is cache-resident after the first workgroups touch it, so
-    // its staging below never waits for an HBM load): lane (chunk, q) loads
-    // the 16-byte chunk `chunk` of token row q*4 + lane/16 of each tile of
-    // the slice (16 lanes cover one row's 256 bytes: whole-line loads).  Only
-    // the NV = ceil(n/4) load instructions per tile whose four token rows hold
-    // a real token are issued.
-    constexpr int kStageRow = kTileK * 2 / 16 + 1;   // 16-byte chunks per row, +1 pad
-    __shared__ u32x4 xstage[W][kRowsPerGroup][kStageRow];
-    const int chunk = lane & 15;
-    const u32x4 z4 = {0u, 0u, 0u, 0u};
-    u32x4 xg[MT][4];
-    auto issue_x = [&]() {
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                xg[t][q] = z4;
-                if (q < NV) {
-                    const int row = q * 4 + (lane >> 4);
-                    const int k = (tw0 + t * W) * kTileK + chunk * 8;
-                    const bool ok = row < p.n && (EXACT || ((!SPLIT || t < tw) && k < p.K));
-                    xg[t][q] = buffer_load_b128(xrsrc, ok ? (unsigned)(row * p.K + k) * 2u : kOutOfRange);
-                }
-            }
-    };
-
-    // Weight ring: one row group of this wave's K-slice, issued as
-    // [scale chunk, code tile 0 .. MT-1].  The scale chunk is the 128 scale
-    // bytes of each tile of the slice (lane l holds bytes 16(l%8) .. +15 of
-    // local tile l/8), so local tile t's scales land at bytes 128t .. 128t+127.
-    u32x4 wsc;
-    u32x4 wc[MT];
-    // Offsets of row group rgl of the K-slice whose first tile is w0 and
-    // which holds wn tiles (w0, w0 + W, ...).
-    auto scale_off_at = [&](int rgl, int w0, int wn) -> unsigned {
-        return lane < 8 * wn ? (unsigned)((rgl * p.T + w0 + (lane >> 3) * W) * 128 + (lane & 7) * 16)
-                             : kOutOfRange;
-    };
-    auto code_off_at = [&](int rgl, int t, int w0, int wn) -> unsigned {
-        return (EXACT || t < wn) ? (unsigned)((rgl * p.T + w0 + t * W) * 1024 + lane * 16) : kOutOfRange;
-    };
-    auto scale_off = [&](int rgl) -> unsigned { return scale_off_at(rgl, tw0, tw); };
-    auto code_off = [&](int rgl, int t) -> unsigned { return code_off_at(rgl, t, tw0, tw); };
-    auto issue_ring = [&](int rgl) {
-        wsc = buffer_load_b128_nt(srsrc, scale_off(rgl));
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-            wc[t] = buffer_load_b128_nt(crsrc, code_off(rgl, t));
-    };
-
-    // Stage X through a per-wave LDS tile into MFMA A-operand layout: lane
-    // (i, g) holds X[4*(i%4) + i/4][k .. k+3] with k = 16*block + 4*g, for
-    // every block of the slice.  Every X load is older than the MT + 1 ring
-    // loads; tile t is staged as soon as its own loads are in, while the
-    // later tiles' X and the ring are still arriving.  The staging is
-    // LDS-bandwidth bound (all waves of a CU stage at once), so only the NV
-    // token quarters in use are written, and only the lanes whose MFMA row
-    // carries one of them read (the other lanes' A rows stay zero; they only
-    // feed outputs that are never stored).
-    u32x2 xr[MT][kBlocksPerTile];
-    const bool xlane = 4 * (i & 3) + (i >> 2) < 4 * NV;
-    // RING_FIRST: this pass's ring was issued before its X loads (by the
-    // previous pass), so only the later tiles' X loads are newer than tile t's.
-    auto stage_x = [&](auto ring_first_tag) {
-    constexpr bool RING_FIRST = decltype(ring_first_tag)::value;
-    static_for<MT>([&](auto tc) {
-        constexpr int t = decltype(tc)::value;
-        // Newer than tile t's X loads: the later tiles' X loads and (unless
-        // it was issued first) the ring.
-        vm_wait4(xg[t][0], xg[t][1], xg[t][2], xg[t][3],
-                 std::integral_constant<int, (MT - 1 - t) * NV + (RING_FIRST ? 0 : MT + 1)>{});
-#pragma unroll
-        for (int q = 0; q < NV; ++q)
-            xstage[wave][q * 4 + (lane >> 4)][chunk] = xg[t][q];
-        const char *base = reinterpret_cast<const char *>(&xstage[wave][4 * (i & 3) + (i >> 2)][0]);
-#pragma unroll
-        for (int b = 0; b < kBlocksPerTile; ++b)
-            xr[t][b] = u32x2{0u, 0u};
-        if (xlane) {
-#pragma unroll
-            for (int b = 0; b < kBlocksPerTile; ++b)
-                xr[t][b] = *reinterpret_cast<const u32x2 *>(base + (16 * b + 4 * g) * 2);
-        }
-    });
-    };
-
-    // Partial sums of a batch of up to kSlots row groups wait in LDS (added
-    // up over the K chunks) and are reduced together, so waves only meet at a
-    // barrier once per batch (once per launch at the decode shapes) instead
-    // of after every row group.
-    __shared__ f32x4 part[kSlots][W][64];
-    __shared__ u32x4 sstage[W][64];
-    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-
-    // One row group of this wave's K-slice.  REFILL: each ring slot is
-    // refilled with the same slot of the next row group as soon as it is
-    // consumed, so every wait has exactly MT newer loads (the ring); on the
-    // last row group nothing is refilled and the counts fall as it drains.
-    // Blocks run as a software pipeline (the scale FMA of a block trails its
-    // MFMA by two blocks).
-    auto rowgroup = [&](auto refill_tag, int rg, int nrgl, int nw0, int nwn) -> f32x4 {
-        constexpr bool REFILL = decltype(refill_tag)::value;
-        vm_wait1(wsc, std::integral_constant<int, MT>{});
-        sstage[wave][lane] = wsc;
-        asm volatile("" ::: "memory");
-        if constexpr (REFILL)
-            wsc = buffer_load_b128_nt(srsrc, scale_off_at(nrgl, nw0, nwn));
-        const char *sbase = reinterpret_cast<const char *>(&sstage[wave][0]) + i * 8;
-        f32x4 acc = zero, p1 = zero, p2 = zero;
-        float s1 = 0.f, s2 = 0.f;
-        static_for<MT>([&](auto tc) {
-            constexpr int t = decltype(tc)::value;
-            // E4M3 scales of blocks 0..7 of tile t for weight row i.
-            const u32x2 sb = *reinterpret_cast<const u32x2 *>(sbase + t * 128);
-            float sc[kBlocksPerTile];
-            static_for<4>([&](auto hc) {
-                constexpr int h = decltype(hc)::value;
-                const auto f2 = __builtin_amdgcn_cvt_pk_f32_fp8((int)sb[h >> 1], (h & 1) != 0);
-                sc[2 * h] = f2[0];
-                sc[2 * h + 1] = f2[1];
-            });
-            vm_wait1(wc[t], std::integral_constant<int, REFILL ? MT : MT - 1 - t>{});
-            const u32x4 c = wc[t];
-#pragma unroll
-            for (int b = 0; b < kBlocksPerTile; ++b) {
-                // B operand: W[row i][16*block + 4*g + e], e = 0..3, from
-                // bytes 2*(b&1) and 2*(b&1)+1 of dword b/2.
-                const u32 cw = c[b >> 1];
-                const u32 lo = fp4x2_to_bf16x2(cw, (b & 1) * 2);
-                const u32 hi = fp4x2_to_bf16x2(cw, (b & 1) * 2 + 1);
-                const s16x4 bop = __builtin_bit_cast(s16x4, u32x2{lo, hi});
-                const s16x4 aop = __builtin_bit_cast(s16x4, xr[t][b]);
-                const f32x4 pr = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(aop, bop, zero, 0, 0, 0);
-#pragma unroll
-                for (int v = 0; v < NV; ++v)
-                    acc[v] = __builtin_fmaf(s2, p2[v], acc[v]);
-                p2 = p1;
-                s2 = s1;
-                p1 = pr;
-                s1 = sc[b];
-                // Pin the FMAs of this step here (instruction selection
-                // would otherwise sink the whole FMA chain below every
-                // MFMA and keep all partials live).
-                asm volatile("" : "+v"(acc[0]), "+v"(acc[1]), "+v"(acc[2]), "+v"(acc[3]));
-            }
-            // Refill the slot once its codes are consumed, so the next
-            // row group's tile lands in the same registers.
-            if constexpr (REFILL)
-                wc[t] = buffer_load_b128_nt(crsrc, code_off_at(nrgl, t, nw0, nwn));
-        });
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-            acc[v] = __builtin_fmaf(s1, p1[v], __builtin_fmaf(s2, p2[v], acc[v]));
-        return acc;
-    };
+    constexpr int kGroups = 1;
+#include "gemv_product.inc"
 
     // Sum the K-slices of row group rg in wave order 0..W-1, scale by gscale,
     // round to bf16 and store the row group's outputs.  Component v of lane
@@ -426,91 +117,7 @@ __global__ __launch_bounds__(kWaves * 64) void nvfp4_gemv_kernel(GemvParams p)
         }
     };
 
-    // Add chunk c's partial of the row group in `slot` to this wave's LDS slot.
-    auto park = [&](int slot, int c, const f32x4 acc) {
-        if (c == 0) {
-            part[slot][wave][lane] = acc;
-        } else {
-            f32x4 q = part[slot][wave][lane];
-#pragma unroll
-            for (int v = 0; v < NV; ++v)
-                q[v] = q[v] + acc[v];
-            part[slot][wave][lane] = q;
-        }
-    };
-
-    // Row groups in batches of up to kSlots (one batch at the decode shapes).
-    auto batch_end = [&](int b0, int b1) {
-        __syncthreads();
-        for (int sl = wave; sl < b1 - b0; sl += W)
-            reduce_store(b0 + sl, sl);
-        if (b1 < rg1)
-            __syncthreads();
-    };
-    if constexpr (CHUNKED) {
-        // Work items (batch of up to kSlots row groups, K chunk c, row group)
-        // in order, one row-group call site: every row group refills the ring
-        // with the next item's tiles -- the next row group of this pass, else
-        // the first row group of the next pass (next chunk, else the next
-        // batch's first chunk) -- so only the first pass starts on an empty
-        // ring; after the last item the refill offsets lie past the buffer
-        // resources (loads that read nothing) and are drained at the end.
-        int b0 = rg0, b1 = min(rg0 + kSlots, rg1), c = 0, rg = rg0;
-        tw = EXACT ? MT : tiles_in(tw0);
-        issue_x();
-        issue_ring(0);
-        stage_x(std::false_type{});
-        while (true) {
-            int nb0 = b0, nb1 = b1, nc = c, nrg = rg + 1;
-            if (nrg == b1) {
-                nrg = b0;
-                nc = c + 1;
-                if (nc == p.kc) {
-                    nc = 0;
-                    nb0 = b1;
-                    nb1 = min(b1 + kSlots, rg1);
-                    nrg = nb0;
-                }
-            }
-            const bool more = nb0 < rg1;
-            const int nw0 = first_tile(pt0 + nc * W * MT);
-            const int nwn = more ? (EXACT ? MT : tiles_in(nw0)) : 0;
-            park(rg - b0, c, rowgroup(std::true_type{}, rg, more ? nrg - rg0 : rg1 - rg0, nw0, nwn));
-            if (rg == b1 - 1 && c == p.kc - 1)
-                batch_end(b0, b1);
-            if (!more)
-                break;
-            const bool new_pass = nc != c || nb0 != b0;
-            b0 = nb0;
-            b1 = nb1;
-            c = nc;
-            rg = nrg;
-            if (new_pass) {
-                tw0 = nw0;
-                tw = nwn;
-                issue_x();
-                stage_x(std::true_type{});
-            }
-        }
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    } else {
-        // One K chunk: X is loaded and staged once for the whole launch, and
-        // the ring runs on across batches (each slot refilled with the next
-        // row group whatever batch it belongs to).
-        tw = EXACT ? MT : tiles_in(tw0);
-        issue_x();
-        issue_ring(0);
-        stage_x(std::false_type{});
-        auto finish = [&](int rg, const f32x4 acc) {
-            const int slot = (rg - rg0) % kSlots;
-            park(slot, 0, acc);
-            if (slot == kSlots - 1 || rg == rg1 - 1)
-                batch_end(rg - slot, rg + 1);
-        };
-        for (int rg = rg0; rg < rg1 - 1; ++rg)
-            finish(rg, rowgroup(std::true_type{}, rg, rg - rg0 + 1, tw0, tw));
-        finish(rg1 - 1, rowgroup(std::false_type{}, rg1 - 1, 0, 0, 0));
-    }
+#include "gemv_passes.inc"
 }
 
 // K-split epilogue: Y[t][r] = bf16_RNE(gscale * (((P[0] + P[1]) + P[2]) + ...)),
@@ -575,40 +182,6 @@ struct GemmParams {
 
 constexpr int kXRow = kTileK * 2 + 32;        // LDS bytes of one token's 128-column X slice, padded
                                               // (measured: half the bank conflicts of +16)
-
-// A wave-uniform value the compiler cannot prove uniform, moved to SGPRs.
-__device__ __forceinline__ u32x4 uniform(u32x4 v)
-{
-    return u32x4{(u32)__builtin_amdgcn_readfirstlane((int)v[0]), (u32)__builtin_amdgcn_readfirstlane((int)v[1]),
-                 (u32)__builtin_amdgcn_readfirstlane((int)v[2]), (u32)__builtin_amdgcn_readfirstlane((int)v[3])};
-}
-
-__device__ __forceinline__ u32x2 buffer_load_b64_nt(u32x4 rsrc, unsigned off)
-{
-    u32x2 v;
-    asm volatile("buffer_load_dwordx2 %0, %1, %2, 0 offen nt" : "=v"(v) : "v"(off), "s"(rsrc));
-    return v;
-}
-
-// Exact bf16 of the 8 weights of one lane for blocks 2j and 2j+1: codes in
-// dword `w` (bytes 0, 1: block 2j; bytes 2, 3: block 2j+1; low nibble first),
-// E4M3 scales of the two blocks in bytes 2H, 2H+1 of `sw`.
-template <bool H>
-__device__ __forceinline__ u32x4 dequant_pair(u32 w, u32 sw)
-{
-    const auto s2 = __builtin_amdgcn_cvt_pk_f32_fp8((int)sw, H);
-    typedef float f32x2 __attribute__((ext_vector_type(2)));
-    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
-    const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
-    const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
-    const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
-    const bf16x2 o0 = {(__bf16)(a[0] * s2[0]), (__bf16)(a[1] * s2[0])};
-    const bf16x2 o1 = {(__bf16)(b[0] * s2[0]), (__bf16)(b[1] * s2[0])};
-    const bf16x2 o2 = {(__bf16)(c[0] * s2[1]), (__bf16)(c[1] * s2[1])};
-    const bf16x2 o3 = {(__bf16)(d[0] * s2[1]), (__bf16)(d[1] * s2[1])};
-    return u32x4{__builtin_bit_cast(u32, o0), __builtin_bit_cast(u32, o1), __builtin_bit_cast(u32, o2),
-                 __builtin_bit_cast(u32, o3)};
-}
 
 // Steps of K whose loads are in flight ahead of the one computing: X and
 // weights share one distance (loads complete in issue order).  Smaller token
@@ -1103,11 +676,7 @@ GemvKernel pick_kernel(int n, int mt, bool exact, bool chunked, bool split)
     }
 }
 
-struct Geometry {
-    int workgroups, mt, kc;
-    int ks, tp, wpp;   // K parts, tiles per part, workgroups per part
-    bool exact;
-};
+typedef nvfp4_gemv_geometry Geometry;
 
 constexpr int kMaxDevices = 64;
 int g_cus[kMaxDevices];
@@ -1452,6 +1021,16 @@ int validate_kparts(const uint8_t *Wq, const uint8_t *Wscale, const uint16_t *X,
 }
 
 }  // namespace
+
+int nvfp4_device_cus(int *cus)
+{
+    return current_device_info(cus);
+}
+
+bool nvfp4_gemv_geometry_for(int N, int K, int cus, int ks, nvfp4_gemv_geometry *geo)
+{
+    return geometry_for(N, K, cus, ks, geo);
+}
 
 extern "C" {
 
@@ -1828,6 +1407,7 @@ const char *nvfp4_strerror(int status)
     case NVFP4_ERR_DEVICE: return "current device is not gfx950";
     case NVFP4_ERR_WORKSPACE: return "workspace missing or too small";
     case NVFP4_ERR_SCRATCH: return "call needs more than the library's fixed scratch memory";
+    case NVFP4_ERR_OVERLAP: return "an output overlaps another argument";
     default: return "unknown status";
     }
 }

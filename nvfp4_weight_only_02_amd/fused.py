@@ -1,0 +1,482 @@
+"""Fused operators on NVFP4 weights: the projection with bias, activation and
+residual in its epilogue, the gated feed-forward block, the product through
+the transposed weight, and their gradients (the weight is frozen: gradients go
+to the activations, the biases and the residual).
+
+    y = linear(w, X, bias=b, activation="gelu", residual=r)
+    h = gated(GatedWeight.from_float(Wg, Wu), X, activation="silu")
+
+Both are differentiable when given the weight's transposed copy
+(``transposed=w.transpose()``, made once); ``linear_backward`` and
+``gated_backward`` are the same gradients without autograd, for captured
+graphs and programs that run their own backward pass.
+
+Every launch goes to ``stream`` (the current stream by default).  Results and
+temporary memory are allocated on it, and tensors of the call are recorded on
+it, so that memory freed by the caller is not reused while the launch reads it.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from dataclasses import dataclass
+
+import torch
+
+from . import PackedWeight, _check, _dev, _i32, _i64, _stream, _vp, lib, packed_codes_bytes, packed_scales_bytes
+
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+class _Epilogue(ctypes.Structure):
+    _fields_ = [("bias", _vp), ("up_bias", _vp), ("residual", _vp), ("preact", _vp), ("ldr", _i64), ("ldp", _i64),
+                ("activation", ctypes.c_int32), ("bias_dtype", ctypes.c_int32),
+                ("residual_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+_SIZE = ctypes.c_size_t
+_F32 = ctypes.c_float
+_SIGNATURES = {
+    "nvfp4_linear": (_i32, [_vp, _vp, _F32, _vp, _i64, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _SIZE, _vp]),
+    "nvfp4_linear_workspace_bytes": (_SIZE, [_i32, _i32, _i32]),
+    "nvfp4_gated_rows": (_SIZE, [_i32]),
+    "nvfp4_pack_gated": (_i32, [_vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp]),
+    "nvfp4_gated": (_i32, [_vp, _vp, _F32, _F32, _vp, _i64, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _SIZE, _vp]),
+    "nvfp4_gated_workspace_bytes": (_SIZE, [_i32, _i32, _i32]),
+    "nvfp4_transposed_codes_bytes": (_SIZE, [_i32, _i32]),
+    "nvfp4_transposed_scales_bytes": (_SIZE, [_i32, _i32]),
+    "nvfp4_pack_transposed": (_i32, [_vp, _vp, _i32, _i32, _vp, _vp, _vp]),
+    "nvfp4_gemm_t": (_i32, [_vp, _vp, _F32, _vp, _i64, _vp, _i64, _i32, _i32, _i32, _vp]),
+    "nvfp4_linear_grad": (_i32, [_vp, _i32, _i64, _vp, _i64, _i32, _vp, _i64, _vp, _i32, _i32, _i32, _vp, _SIZE, _vp]),
+    "nvfp4_gated_grad": (_i32, [_vp, _i32, _i64, _vp, _i64, _i32, _F32, _F32, _vp, _i64, _vp, _vp, _i32, _i32, _i32,
+                                _vp, _SIZE, _vp]),
+    "nvfp4_grad_workspace_bytes": (_SIZE, [_i32, _i32, _i32]),
+}
+
+
+def _call(name: str):
+    f = getattr(lib(), name)
+    if f.argtypes is None:
+        f.restype, f.argtypes = _SIGNATURES[name]
+    return f
+
+
+# ---- checks, streams and memory ---------------------------------------------------
+
+def _act(activation) -> int:
+    if activation is None:
+        return 0
+    if activation not in ACTIVATIONS:
+        raise ValueError("activation must be one of %s, got %r" % (", ".join(ACTIVATIONS), activation))
+    return ACTIVATIONS[activation]
+
+
+def _mat(t, dtypes, name: str, n, cols) -> torch.Tensor:
+    """A device matrix of n rows (None: any) and cols columns, unit stride
+    along a row."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA (HIP) tensor" % name)
+    if t.dtype not in dtypes:
+        raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
+    if t.dim() != 2 or t.shape[1] != cols or (n is not None and t.shape[0] != n):
+        raise ValueError("%s must be [%s, %d], got %s" % (name, "n" if n is None else n, cols, list(t.shape)))
+    if cols > 1 and t.shape[0] > 0 and t.stride(1) != 1:
+        raise ValueError("%s must have unit stride along a row" % name)
+    return t
+
+
+def _ld(t) -> int:
+    """Row stride in elements; of no meaning with fewer than two rows."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _vec(t, dtypes, name: str, size: int):
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA (HIP) tensor" % name)
+    if t.dtype not in dtypes:
+        raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
+    if t.dim() != 1 or t.shape[0] != size or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous [%d]" % (name, size))
+    return t
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+class _Launch:
+    """The stream of a call and the memory rules of one that is not the
+    current stream."""
+
+    def __init__(self, stream, *tensors):
+        self.tensors = [t for t in tensors if t is not None]
+        self.handle = _stream(stream, *self.tensors)
+        current = torch.cuda.current_stream()
+        self.stream = stream if stream is not None else current
+        self.side = self.stream != current
+        self.current = current
+        for t in self.tensors if self.side else ():
+            t.record_stream(self.stream)
+
+    def alloc(self, *shape, dtype):
+        """Memory of the launch's stream."""
+        with torch.cuda.stream(self.stream) if self.side else contextlib.nullcontext():
+            t = torch.empty(*shape, dtype=dtype, device="cuda")
+        if self.side:
+            t.record_stream(self.current)   # a result is read there
+        return t
+
+    def workspace(self, given, need: int):
+        """(pointer, bytes, tensor) of `need` workspace bytes."""
+        if given is None:
+            if not need:
+                return None, 0, None
+            given = self.alloc(need, dtype=torch.uint8)
+        return given.data_ptr(), given.numel(), given
+
+
+# ---- weights -----------------------------------------------------------------------
+
+@dataclass
+class TransposedWeight:
+    """The transposed copy of a packed weight, which gradients go through:
+    another 9/16 byte a weight, made once where gradients are wanted."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    gscale: float
+    N: int                   # rows of the packed weight
+    K: int
+
+
+def _transpose(codes, scales, gscale, N, K, stream) -> TransposedWeight:
+    run = _Launch(stream, codes, scales)
+    ct = run.alloc(int(_call("nvfp4_transposed_codes_bytes")(N, K)), dtype=torch.uint8)
+    st = run.alloc(int(_call("nvfp4_transposed_scales_bytes")(N, K)), dtype=torch.uint8)
+    _check(_call("nvfp4_pack_transposed")(codes.data_ptr(), scales.data_ptr(), N, K, ct.data_ptr(), st.data_ptr(),
+                                          run.handle), "nvfp4_pack_transposed")
+    return TransposedWeight(ct, st, gscale, N, K)
+
+
+def transpose(w: PackedWeight, stream=None) -> TransposedWeight:
+    """The transposed copy of ``w`` (also ``w.transpose()``)."""
+    return _transpose(w.codes, w.scales, w.gscale, w.N, w.K, stream)
+
+
+def gated_rows(F: int) -> int:
+    """Rows of the packed weight of a gated block with F outputs."""
+    return int(_call("nvfp4_gated_rows")(F))
+
+
+@dataclass
+class GatedWeight:
+    """The gate and up weights of a gated block in one packed weight whose
+    16-row groups alternate gate, up."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    gate_gscale: float
+    up_gscale: float
+    F: int
+    K: int
+
+    @classmethod
+    def from_packed(cls, gate: PackedWeight, up: PackedWeight, stream=None) -> "GatedWeight":
+        if (gate.N, gate.K) != (up.N, up.K):
+            raise ValueError("the gate and up weights must have one shape")
+        run = _Launch(stream, gate.codes, gate.scales, up.codes, up.scales)
+        rows = gated_rows(gate.N)
+        codes = run.alloc(packed_codes_bytes(rows, gate.K), dtype=torch.uint8)
+        scales = run.alloc(packed_scales_bytes(rows, gate.K), dtype=torch.uint8)
+        _check(_call("nvfp4_pack_gated")(gate.codes.data_ptr(), gate.scales.data_ptr(), up.codes.data_ptr(),
+                                         up.scales.data_ptr(), gate.N, gate.K, codes.data_ptr(), scales.data_ptr(),
+                                         run.handle), "nvfp4_pack_gated")
+        return cls(codes, scales, gate.gscale, up.gscale, gate.N, gate.K)
+
+    @classmethod
+    def from_float(cls, Wg: torch.Tensor, Wu: torch.Tensor, stream=None) -> "GatedWeight":
+        """Quantise fp32 or bf16 gate and up weights [F, K], each with its own
+        tensor scale."""
+        return cls.from_packed(PackedWeight.from_float(Wg, stream), PackedWeight.from_float(Wu, stream), stream)
+
+    def transpose(self, stream=None) -> TransposedWeight:
+        """The transposed copy, for gradients (its tensor scales are applied
+        to the gradient rows, so its own is 1)."""
+        return _transpose(self.codes, self.scales, 1.0, gated_rows(self.F), self.K, stream)
+
+
+# ---- forward -------------------------------------------------------------------------
+
+def _out(run, out, out_dtype, n, cols):
+    if out is None:
+        if out_dtype not in _DTYPES:
+            raise TypeError("out_dtype must be torch.bfloat16 or torch.float32, got %s" % out_dtype)
+        return run.alloc(n, cols, dtype=out_dtype)
+    if out.dtype != out_dtype:
+        raise TypeError("out is %s, out_dtype %s" % (out.dtype, out_dtype))
+    return out
+
+
+def _linear_forward(w, X, bias, act, residual, out, out_dtype, preact, workspace, stream):
+    n = X.shape[0]
+    run = _Launch(stream, w.codes, w.scales, X, bias, residual, out, preact, workspace)
+    Y = _out(run, out, out_dtype, n, w.N)
+    ep = _Epilogue(_ptr(bias), None, _ptr(residual), _ptr(preact), _ld(residual) if residual is not None else 0,
+                   _ld(preact) if preact is not None else 0, act, _DTYPES[bias.dtype] if bias is not None else 1,
+                   _DTYPES[residual.dtype] if residual is not None else 1, _DTYPES[Y.dtype])
+    ws, size, keep = run.workspace(workspace, int(_call("nvfp4_linear_workspace_bytes")(n, w.N, w.K)))
+    _check(_call("nvfp4_linear")(w.codes.data_ptr(), w.scales.data_ptr(), w.gscale, X.data_ptr(), _ld(X),
+                                 Y.data_ptr(), _ld(Y), n, w.N, w.K, ctypes.byref(ep), ws, size, run.handle),
+           "nvfp4_linear")
+    return Y
+
+
+def _gated_forward(w, X, act, gate_bias, up_bias, out, out_dtype, preact, workspace, stream):
+    n = X.shape[0]
+    run = _Launch(stream, w.codes, w.scales, X, gate_bias, up_bias, out, preact, workspace)
+    H = _out(run, out, out_dtype, n, w.F)
+    some = gate_bias if gate_bias is not None else up_bias
+    ep = _Epilogue(_ptr(gate_bias), _ptr(up_bias), None, _ptr(preact), 0, _ld(preact) if preact is not None else 0,
+                   act, _DTYPES[some.dtype] if some is not None else 1, 1, _DTYPES[H.dtype])
+    ws, size, keep = run.workspace(workspace, int(_call("nvfp4_gated_workspace_bytes")(n, w.F, w.K)))
+    _check(_call("nvfp4_gated")(w.codes.data_ptr(), w.scales.data_ptr(), w.gate_gscale, w.up_gscale, X.data_ptr(),
+                                _ld(X), H.data_ptr(), _ld(H), n, w.F, w.K, ctypes.byref(ep), ws, size, run.handle),
+           "nvfp4_gated")
+    return H
+
+
+_FLOATS = (torch.bfloat16, torch.float32)
+
+
+def _pad8(cols: int) -> int:
+    return (cols + 7) // 8 * 8
+
+
+def preact_columns(w) -> int:
+    """Columns of the bf16 pre-activation buffer of ``w`` (a PackedWeight or a
+    GatedWeight): the outputs up to a multiple of 8, or the gated weight's rows."""
+    return gated_rows(w.F) if isinstance(w, GatedWeight) else _pad8(w.N)
+
+
+def _preact_arg(preact, w, n):
+    return None if preact is None else _mat(preact, (torch.bfloat16,), "preact", n, preact_columns(w))
+
+
+def _workspace_arg(workspace):
+    return None if workspace is None else _dev(workspace, torch.uint8, "workspace")
+
+
+def _wants_grad(*tensors) -> bool:
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+def _check_grad(X, transposed, N, K, stream, *buffers):
+    if any(b is not None for b in buffers):
+        raise ValueError("out, preact and workspace go with calls that need no gradient")
+    if stream is not None and stream != torch.cuda.current_stream():
+        raise ValueError("with gradients the launch stream is the current one (torch.cuda.stream)")
+    if X.requires_grad:
+        if transposed is None:
+            raise ValueError("a gradient of X needs the weight's transposed copy (transposed=w.transpose())")
+        if (transposed.N, transposed.K) != (N, K):
+            raise ValueError("transposed is not a copy of this weight's shape")
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, X, bias, residual, w, transposed, act, out_dtype):
+        ctx.transposed, ctx.act, ctx.N = transposed, act, w.N
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        ctx.residual_dtype = None if residual is None else residual.dtype
+        preact = None
+        if act and (ctx.needs_input_grad[0] or ctx.needs_input_grad[1]):
+            preact = torch.empty(X.shape[0], _pad8(w.N), dtype=torch.bfloat16, device=X.device)
+        ctx.save_for_backward(preact)
+        return _linear_forward(w, X, bias, act, residual, None, out_dtype, preact, None, None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dY):
+        (preact,) = ctx.saved_tensors
+        need_x, need_b, need_r = ctx.needs_input_grad[:3]
+        dX = db = None
+        if need_x or need_b:
+            dX, db = _linear_backward(ctx.transposed if need_x else None, dY, ctx.act, preact,
+                                      ctx.bias_dtype if need_b else None, None, None)
+        return dX, db, dY.to(ctx.residual_dtype) if need_r else None, None, None, None, None
+
+
+class _Gated(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, X, gate_bias, up_bias, w, transposed, act, out_dtype):
+        ctx.w, ctx.transposed, ctx.act = w, transposed, act
+        ctx.bias_dtype = next((b.dtype for b in (gate_bias, up_bias) if b is not None), None)
+        preact = torch.empty(X.shape[0], gated_rows(w.F), dtype=torch.bfloat16, device=X.device)
+        ctx.save_for_backward(preact)
+        return _gated_forward(w, X, act, gate_bias, up_bias, None, out_dtype, preact, None, None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dH):
+        (preact,) = ctx.saved_tensors
+        need_x, need_g, need_u = ctx.needs_input_grad[:3]
+        grads = _gated_backward(ctx.w, ctx.transposed if need_x else None, dH, ctx.act, preact,
+                                ctx.bias_dtype if need_g else None, ctx.bias_dtype if need_u else None, None, None)
+        return grads + (None, None, None, None)
+
+
+def linear(w: PackedWeight, X: torch.Tensor, bias: torch.Tensor = None, activation: str = None,
+           residual: torch.Tensor = None, *, transposed: TransposedWeight = None, out: torch.Tensor = None,
+           out_dtype=None, preact: torch.Tensor = None, workspace: torch.Tensor = None,
+           stream=None) -> torch.Tensor:
+    """Y = act(X . dequant(W)^T + bias) + residual for any number of tokens.
+
+    X: bf16 [n, K]; bias: bf16 or fp32 [N]; residual: bf16 or fp32 [n, N] (it
+    may be ``out`` itself); Y: bf16, or fp32 with ``out_dtype``.  Rows may be
+    strided; X rows are 16-byte aligned.  ``preact`` (bf16 [n,
+    preact_columns(w)]) receives the pre-activations ``linear_backward`` needs.
+    ``workspace``: uint8, nvfp4_linear_workspace_bytes (allocated otherwise).
+    Differentiable in X (given ``transposed``), bias and residual."""
+    act = _act(activation)
+    _mat(X, (torch.bfloat16,), "X", None, w.K)
+    n = X.shape[0]
+    _vec(bias, _FLOATS, "bias", w.N)
+    if residual is not None:
+        _mat(residual, _FLOATS, "residual", n, w.N)
+    if out is not None:
+        _mat(out, _FLOATS, "out", n, w.N)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else torch.bfloat16
+    if _wants_grad(X, bias, residual):
+        _check_grad(X, transposed, w.N, w.K, stream, out, preact, workspace)
+        return _Linear.apply(X, bias, residual, w, transposed, act, out_dtype)
+    return _linear_forward(w, X, bias, act, residual, out, out_dtype, _preact_arg(preact, w, n),
+                           _workspace_arg(workspace), stream)
+
+
+def gated(w: GatedWeight, X: torch.Tensor, activation: str = "silu", gate_bias: torch.Tensor = None,
+          up_bias: torch.Tensor = None, *, transposed: TransposedWeight = None, out: torch.Tensor = None,
+          out_dtype=None, preact: torch.Tensor = None, workspace: torch.Tensor = None,
+          stream=None) -> torch.Tensor:
+    """H = act(X . dequant(Wg)^T + gate_bias) * (X . dequant(Wu)^T + up_bias),
+    both projections, the activation and the product in one launch.  Arguments
+    as ``linear``; the biases have one dtype.  Differentiable in X (given
+    ``transposed``) and the biases."""
+    act = _act(activation)
+    _mat(X, (torch.bfloat16,), "X", None, w.K)
+    n = X.shape[0]
+    _vec(gate_bias, _FLOATS, "gate_bias", w.F)
+    _vec(up_bias, _FLOATS, "up_bias", w.F)
+    if gate_bias is not None and up_bias is not None and gate_bias.dtype != up_bias.dtype:
+        raise TypeError("gate_bias and up_bias must have one dtype")
+    if out is not None:
+        _mat(out, _FLOATS, "out", n, w.F)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else torch.bfloat16
+    if _wants_grad(X, gate_bias, up_bias):
+        _check_grad(X, transposed, gated_rows(w.F), w.K, stream, out, preact, workspace)
+        return _Gated.apply(X, gate_bias, up_bias, w, transposed, act, out_dtype)
+    return _gated_forward(w, X, act, gate_bias, up_bias, out, out_dtype, _preact_arg(preact, w, n),
+                          _workspace_arg(workspace), stream)
+
+
+# ---- backward ------------------------------------------------------------------------
+
+def _rows_ok(t) -> bool:
+    """Rows gemm_t can load as they are."""
+    return (t.dtype == torch.bfloat16 and t.shape[1] % 8 == 0 and t.data_ptr() % 16 == 0 and
+            (t.shape[0] < 2 or t.stride(0) % 8 == 0))
+
+
+def _incoming(dY, n, N, name):
+    """A gradient as autograd hands it over: any strides."""
+    if not isinstance(dY, torch.Tensor) or not dY.is_cuda:
+        raise TypeError("%s must be a CUDA (HIP) tensor" % name)
+    if dY.dim() == 2 and (dY.stride(1) != 1 or dY.stride(0) < dY.shape[1]):
+        dY = dY.contiguous()
+    return _mat(dY, _FLOATS, name, n, N)
+
+
+def _gemm_t_launch(wt, dZ, out, run):
+    n = dZ.shape[0]
+    dX = out if out is not None else run.alloc(n, wt.K, dtype=torch.bfloat16)
+    _check(_call("nvfp4_gemm_t")(wt.codes.data_ptr(), wt.scales.data_ptr(), wt.gscale, dZ.data_ptr(), _ld(dZ),
+                                 dX.data_ptr(), _ld(dX), n, wt.N, wt.K, run.handle), "nvfp4_gemm_t")
+    return dX
+
+
+def _linear_backward(wt, dY, act, preact, bias_dtype, out, stream):
+    dY = _incoming(dY, None, wt.N if wt is not None else dY.shape[-1], "dY")
+    n, N = dY.shape
+    run = _Launch(stream, dY, preact, out, *((wt.codes, wt.scales) if wt is not None else ()))
+    db = run.alloc(N, dtype=bias_dtype) if bias_dtype is not None else None
+    dZ = None
+    if wt is not None and (act or not _rows_ok(dY)):
+        dZ = run.alloc(n, _pad8(N), dtype=torch.bfloat16)
+    if db is not None or dZ is not None:
+        need = int(_call("nvfp4_grad_workspace_bytes")(n, N, 0)) if db is not None else 0
+        ws, size, keep = run.workspace(None, need)
+        _check(_call("nvfp4_linear_grad")(dY.data_ptr(), _DTYPES[dY.dtype], _ld(dY), _ptr(preact),
+                                          _ld(preact) if preact is not None else 0, act, _ptr(dZ), _pad8(N), _ptr(db),
+                                          _DTYPES[bias_dtype] if db is not None else 1, n, N, ws, size, run.handle),
+               "nvfp4_linear_grad")
+    dX = _gemm_t_launch(wt, dY if dZ is None else dZ, out, run) if wt is not None else None
+    return dX, db
+
+
+def _gated_backward(w, wt, dH, act, preact, gate_dtype, up_dtype, out, stream):
+    dH = _incoming(dH, None, w.F, "dH")
+    n, rows = dH.shape[0], gated_rows(w.F)
+    run = _Launch(stream, dH, preact, out, *((wt.codes, wt.scales) if wt is not None else ()))
+    dg = run.alloc(w.F, dtype=gate_dtype) if gate_dtype is not None else None
+    du = run.alloc(w.F, dtype=up_dtype) if up_dtype is not None else None
+    dZ = run.alloc(n, rows, dtype=torch.bfloat16) if wt is not None else None
+    some = gate_dtype if gate_dtype is not None else up_dtype
+    need = int(_call("nvfp4_grad_workspace_bytes")(n, w.F, 1)) if some is not None else 0
+    ws, size, keep = run.workspace(None, need)
+    _check(_call("nvfp4_gated_grad")(dH.data_ptr(), _DTYPES[dH.dtype], _ld(dH), preact.data_ptr(), _ld(preact), act,
+                                     w.gate_gscale, w.up_gscale, _ptr(dZ), rows, _ptr(dg), _ptr(du),
+                                     _DTYPES[some] if some is not None else 1, n, w.F, ws, size, run.handle),
+           "nvfp4_gated_grad")
+    dX = _gemm_t_launch(wt, dZ, out, run) if wt is not None else None
+    return dX, dg, du
+
+
+def gemm_t(wt: TransposedWeight, dY: torch.Tensor, out: torch.Tensor = None, stream=None) -> torch.Tensor:
+    """dX[n, K] = dY[n, N] . dequant(W) (bf16 in and out, fp32 accumulation):
+    the gradient of ``gemv``, ``gemm`` or a plain ``linear`` with respect to
+    its input.  dY rows that are not 16-byte aligned, or an N that is no
+    multiple of 8, cost a padded copy of dY."""
+    _mat(dY, (torch.bfloat16,), "dY", None, wt.N)
+    if out is not None:
+        _mat(out, (torch.bfloat16,), "out", dY.shape[0], wt.K)
+    return _linear_backward(wt, dY, 0, None, None, out, stream)[0]
+
+
+def linear_backward(wt: TransposedWeight, dY: torch.Tensor, activation: str = None, preact: torch.Tensor = None,
+                    bias_dtype=None, out: torch.Tensor = None, stream=None):
+    """(dX, dbias) of ``linear``: dX bf16 [n, K] (None without ``wt``), dbias in
+    ``bias_dtype`` (None without).  ``preact`` as ``linear`` filled it (not
+    needed without an activation).  The residual's gradient is dY."""
+    act = _act(activation)
+    if act:
+        if preact is None:
+            raise ValueError("the gradient of an activation needs preact")
+        _mat(preact, (torch.bfloat16,), "preact", dY.shape[0], _pad8(dY.shape[-1]))
+    if out is not None:
+        _mat(out, (torch.bfloat16,), "out", dY.shape[0], wt.K)
+    return _linear_backward(wt, dY, act, preact if act else None, bias_dtype, out, stream)
+
+
+def gated_backward(w: GatedWeight, wt: TransposedWeight, dH: torch.Tensor, preact: torch.Tensor,
+                   activation: str = "silu", bias_dtype=None, out: torch.Tensor = None, stream=None):
+    """(dX, dgate_bias, dup_bias) of ``gated``; the bias gradients in
+    ``bias_dtype`` (None without)."""
+    act = _act(activation)
+    _mat(preact, (torch.bfloat16,), "preact", dH.shape[0], gated_rows(w.F))
+    if wt is not None and (wt.N, wt.K) != (gated_rows(w.F), w.K):
+        raise ValueError("wt is not the transposed copy of this gated weight")
+    if out is not None:
+        _mat(out, (torch.bfloat16,), "out", dH.shape[0], w.K)
+    return _gated_backward(w, wt, dH, act, preact, bias_dtype, bias_dtype, out, stream)

@@ -1,0 +1,145 @@
+"""Argument checks and host functions of the fused operators, no GPU: every
+refusal comes before any HIP call."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import fused_reference as R
+import nvfp4_weight_only_02_amd as nv
+from nvfp4_weight_only_02_amd import fused
+
+OK, NULL, RANGE, ALIGN, SHAPE, DEVICE, WORKSPACE, OVERLAP = 0, 1, 2, 3, 4, 7, 8, 10
+
+
+def at(i):
+    """Fake device addresses, far apart."""
+    return (i + 1) * (1 << 40)
+
+
+def epilogue(**kw):
+    base = dict(bias=None, up_bias=None, residual=None, preact=None, ldr=0, ldp=0, activation=0, bias_dtype=1,
+                residual_dtype=1, out_dtype=1)
+    base.update(kw)
+    return fused._Epilogue(*[base[f] for f, _ in fused._Epilogue._fields_])
+
+
+def linear(wq=at(0), ws=at(1), x=at(2), ldx=None, y=at(3), ldy=None, n=4, N=64, K=256, ep=None, work=None, size=0):
+    ep = ep if ep is not None else epilogue()
+    return fused._call("nvfp4_linear")(wq, ws, 1.0, x, K if ldx is None else ldx, y, N if ldy is None else ldy, n, N,
+                                       K, ctypes.byref(ep) if ep != 0 else None, work, size, None)
+
+
+def gated(x=at(2), ldx=None, h=at(3), ldh=None, n=4, F=64, K=256, ep=None, work=None, size=0):
+    ep = ep if ep is not None else epilogue()
+    return fused._call("nvfp4_gated")(at(0), at(1), 1.0, 1.0, x, K if ldx is None else ldx, h,
+                                      F if ldh is None else ldh, n, F, K, ctypes.byref(ep), work, size, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(wq=None), NULL), (dict(x=None), NULL), (dict(y=None), NULL), (dict(ep=0), NULL),
+    (dict(n=-1), RANGE), (dict(n=(1 << 20) + 1), RANGE), (dict(N=0), RANGE), (dict(K=0), RANGE),
+    (dict(K=250), SHAPE), (dict(K=(1 << 18) + 16), SHAPE), (dict(ldx=240), RANGE), (dict(ldy=63), RANGE),
+    (dict(ldx=260), ALIGN), (dict(x=at(2) + 8), ALIGN), (dict(wq=at(0) + 4), ALIGN), (dict(y=at(3) + 1), ALIGN),
+    (dict(ldx=(1 << 22) + 8), SHAPE),
+    (dict(ep=epilogue(activation=5)), RANGE), (dict(ep=epilogue(activation=-1)), RANGE),
+    (dict(ep=epilogue(out_dtype=2)), RANGE), (dict(ep=epilogue(up_bias=at(5))), RANGE),
+    (dict(ep=epilogue(bias=at(5), bias_dtype=7)), RANGE), (dict(ep=epilogue(bias=at(5) + 1)), ALIGN),
+    (dict(ep=epilogue(residual=at(5), ldr=63)), RANGE), (dict(ep=epilogue(residual=at(5) + 2, ldr=64, residual_dtype=0)), ALIGN),
+    (dict(ep=epilogue(preact=at(5), ldp=60)), RANGE), (dict(ep=epilogue(preact=at(5), ldp=68)), ALIGN),
+    (dict(ep=epilogue(preact=at(5) + 8, ldp=64)), ALIGN),
+    (dict(y=at(2)), OVERLAP), (dict(y=at(2) + 3 * 512 + 510), OVERLAP), (dict(y=at(0)), OVERLAP),
+    (dict(ep=epilogue(residual=at(3) + 2, ldr=64)), OVERLAP), (dict(ep=epilogue(residual=at(3), ldr=72)), OVERLAP),
+    (dict(ep=epilogue(residual=at(3), ldr=64, residual_dtype=0)), OVERLAP),
+    (dict(ep=epilogue(preact=at(3), ldp=64)), OVERLAP), (dict(ep=epilogue(bias=at(3))), OVERLAP),
+    (dict(ep=epilogue(preact=at(2), ldp=64)), OVERLAP),
+])
+def test_linear_refuses(kw, status):
+    assert linear(**kw) == status
+
+
+def test_valid_calls_reach_the_device_check():
+    # valid arguments: the first thing that can fail is the missing GPU (with
+    # one, these addresses would be launched on)
+    if nv.torch.cuda.is_available():
+        pytest.skip("needs a machine without a GPU")
+    for kw in (dict(), dict(n=40), dict(ep=epilogue(residual=at(3), ldr=64)), dict(n=1, ldx=257)):
+        assert linear(**kw) == DEVICE
+    assert linear(n=0) == OK and linear(n=0, x=None, y=None) == OK and gated(n=0) == OK
+
+
+def test_long_rows_need_a_workspace():
+    need = fused._call("nvfp4_linear_workspace_bytes")(4, 64, 8208)
+    assert need == nv.gemv_kparts(64, 8208) * 4 * 64 * 4
+    assert linear(K=8208) == WORKSPACE
+    assert linear(K=8208, work=at(7), size=need - 1) == WORKSPACE
+    assert linear(K=8208, work=at(7) + 4, size=need) == ALIGN
+    assert fused._call("nvfp4_linear_workspace_bytes")(17, 64, 8208) == 0
+    assert fused._call("nvfp4_linear_workspace_bytes")(4, 64, 8192) == 0
+    rows = nv.gated_rows(50)
+    assert rows == 128
+    assert fused._call("nvfp4_gated_workspace_bytes")(4, 50, 8208) == nv.gemv_kparts(rows, 8208) * 4 * rows * 4
+    assert gated(F=50, K=8208) == WORKSPACE
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(F=0), RANGE), (dict(ep=epilogue(residual=at(5), ldr=64)), RANGE),
+    (dict(ep=epilogue(preact=at(5), ldp=64)), RANGE), (dict(ep=epilogue(up_bias=at(3))), OVERLAP),
+    (dict(K=264), SHAPE), (dict(ldh=60), RANGE), (dict(x=None), NULL)])
+def test_gated_refuses(kw, status):
+    assert gated(**kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(c=None), NULL), (dict(dy=None), NULL), (dict(n=-1), RANGE), (dict(N=0), RANGE), (dict(K=40), SHAPE),
+    (dict(ldy=93), RANGE), (dict(ldy=100), ALIGN), (dict(dy=at(2) + 2), ALIGN), (dict(ldx=40), RANGE),
+    (dict(dx=at(2)), OVERLAP), (dict(dx=at(0)), OVERLAP), (dict(n=0), OK)])
+def test_gemm_t_refuses(kw, status):
+    a = dict(c=at(0), s=at(1), dy=at(2), ldy=96, dx=at(3), ldx=None, n=4, N=93, K=48)
+    a.update(kw)
+    if a["ldx"] is None:
+        a["ldx"] = a["K"]
+    assert fused._call("nvfp4_gemm_t")(a["c"], a["s"], 1.0, a["dy"], a["ldy"], a["dx"], a["ldx"], a["n"], a["N"],
+                                       a["K"], None) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dy=None), NULL), (dict(z=None), NULL), (dict(n=-1), RANGE), (dict(act=9), RANGE), (dict(dt=3), RANGE),
+    (dict(ldy=90), RANGE), (dict(ldz=88), RANGE), (dict(ldz=100), ALIGN), (dict(dz=at(4) + 2), ALIGN),
+    (dict(ldp=95), ALIGN), (dict(dz=at(2)), OVERLAP), (dict(db=at(4)), OVERLAP), (dict(db=at(3)), OVERLAP),
+    (dict(n=4000, N=2000, ldy=2000, ldp=2000, ldz=2000), WORKSPACE)])
+def test_linear_grad_refuses(kw, status):
+    a = dict(dy=at(2), dt=1, ldy=93, z=at(3), ldp=96, act=2, dz=at(4), ldz=96, db=at(5), bt=0, n=4, N=93)
+    a.update(kw)
+    assert fused._call("nvfp4_linear_grad")(a["dy"], a["dt"], a["ldy"], a["z"], a["ldp"], a["act"], a["dz"], a["ldz"],
+                                            a["db"], a["bt"], a["n"], a["N"], None, 0, None) == status
+
+
+def test_pack_refuses():
+    f = fused._call("nvfp4_pack_gated")
+    assert f(at(0), at(1), at(2), at(3), 0, 256, at(4), at(5), None) == RANGE
+    assert f(at(0), at(1), at(2), at(3), 16, 250, at(4), at(5), None) == SHAPE
+    assert f(at(0), at(1), at(2), None, 16, 256, at(4), at(5), None) == NULL
+    assert f(at(0), at(1), at(2), at(3), 16, 256, at(0), at(5), None) == OVERLAP
+    assert f(at(0) + 8, at(1), at(2), at(3), 16, 256, at(4), at(5), None) == ALIGN
+    t = fused._call("nvfp4_pack_transposed")
+    assert t(at(0), at(1), 0, 256, at(4), at(5), None) == RANGE
+    assert t(at(0), at(1), 16, 256, at(1), at(5), None) == OVERLAP
+    assert t(at(0), at(1), 16, 256, at(4), at(5) + 1, None) == ALIGN
+
+
+def test_transposed_sizes():
+    c, s = fused._call("nvfp4_transposed_codes_bytes"), fused._call("nvfp4_transposed_scales_bytes")
+    assert c(256, 64) == 256 * 64 // 2 and s(256, 64) == 256 * 64 // 16
+    assert c(129, 16) == 256 * 16 // 2 and s(129, 16) == 256
+    assert c(0, 16) == 0 and s(16, 24) == 0
+    assert c(1 << 20, 1 << 18) == (1 << 37)
+
+
+@pytest.mark.parametrize("kind", R.ACTS)
+def test_reference_gradients_are_differences(kind):
+    z = np.linspace(-9, 9, 4001) + 1e-3
+    t = 1e-5
+    diff = (R.act(z + t, kind) - R.act(z - t, kind)) / (2 * t)
+    assert np.abs(diff - R.act_grad(z, kind)).max() < 1e-8
+    assert np.abs(R.act_grad(z, kind)).max() <= R.LIP

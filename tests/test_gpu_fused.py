@@ -1,0 +1,394 @@
+"""GPU parity of the fused operators (projection with epilogue, gated block,
+product through the transposed weight, gradients) against 64-bit arithmetic,
+through the Python entry points, within the bounds of fused_reference."""
+import numpy as np
+import pytest
+import torch
+
+import fused_reference as R
+import nvfp4_weight_only_02_amd as nv
+import oracle as O
+from nvfp4_weight_only_02_amd import inputs
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    assert torch.cuda.is_available(), "GPU tests need a HIP device"
+    nv.lib()
+    yield
+    torch.cuda.synchronize()
+
+
+def say(*a):
+    print(*a, flush=True)
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def weight(N, K, seed, std=0.05):
+    """(PackedWeight, its 64-bit values)"""
+    codes, scales, g = O.quantize(inputs.weights_f32(N, K, seed, std))
+    pw = nv.PackedWeight.from_canonical(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), g, N, K)
+    return pw, np.asarray(O.dequant(codes, scales, g), dtype=np.float64)
+
+
+def randn(shape, seed, dtype=BF16, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * std).to(dtype).cuda()
+
+
+def check(got, want, what):
+    ref, bound = want
+    err = np.abs(f64(got) - ref)
+    assert np.isfinite(f64(got)).all(), what
+    assert (err <= bound).all(), "%s: worst err/bound %.3g" % (what, float((err / bound).max()))
+
+
+SHAPES = [(1, 16), (37, 144), (200, 656), (64, 8208), (330, 2064)]
+LINEAR = [  # activation, bias, residual, out
+    ("none", None, None, BF16), ("silu", BF16, BF16, BF16), ("gelu", F32, F32, F32),
+    ("gelu_tanh", BF16, F32, BF16), ("relu", F32, BF16, F32)]
+
+
+@pytest.mark.parametrize("N,K", SHAPES)
+@pytest.mark.parametrize("n", [1, 4, 13, 16, 17, 40, 70, 150])
+@pytest.mark.parametrize("act,bias,residual,out", LINEAR)
+def test_linear(n, N, K, act, bias, residual, out):
+    say("linear", n, N, K, act, bias, residual, out)
+    w, W = weight(N, K, 1 + N)
+    X = randn((n, K), 2)
+    b = None if bias is None else randn((N,), 3, bias)
+    r = None if residual is None else randn((n, N), 4, residual, 3.0)
+    Y = nv.linear(w, X, bias=b, activation=act, residual=r, out_dtype=out)
+    assert Y.dtype == out
+    check(Y, R.linear(f64(X), W, None if b is None else f64(b), act, None if r is None else f64(r), out == F32), "Y")
+
+
+@pytest.mark.parametrize("F,K", [(1, 16), (17, 144), (40, 656), (64, 8208), (129, 2064)])
+@pytest.mark.parametrize("n", [1, 4, 13, 16, 17, 40, 150])
+@pytest.mark.parametrize("act,bias,out", [("silu", None, BF16), ("gelu", F32, F32), ("gelu_tanh", BF16, BF16),
+                                          ("relu", None, F32), ("none", BF16, BF16)])
+def test_gated(n, F, K, act, bias, out):
+    say("gated", n, F, K, act, bias, out)
+    (g, Wg), (u, Wu) = weight(F, K, 5, 0.05), weight(F, K, 6, 0.02)
+    X = randn((n, K), 7)
+    bg = None if bias is None else randn((F,), 8, bias)
+    bu = None if bias is None else randn((F,), 9, bias)
+    H = nv.gated(nv.GatedWeight.from_packed(g, u), X, activation=act, gate_bias=bg, up_bias=bu, out_dtype=out)
+    check(H, R.gated(f64(X), Wg, Wu, None if bg is None else f64(bg), None if bu is None else f64(bu), act,
+                     out == F32), "H")
+
+
+@pytest.mark.parametrize("N,K", SHAPES + [(129, 48)])
+@pytest.mark.parametrize("n", [1, 15, 33, 70, 150])
+def test_gemm_t(n, N, K):
+    say("gemm_t", n, N, K)
+    w, W = weight(N, K, 10 + K)
+    dY = randn((n, N), 11)
+    dX = nv.gemm_t(w.transpose(), dY)
+    D = f64(dY)
+    ref = D @ W
+    b = (N + 32) * R.HALF_F32 * (np.abs(D) @ np.abs(W))
+    check(dX, (ref, b + R.HALF_BF16 * (np.abs(ref) + b) + 2.0 ** -133), "dX")
+
+
+def test_gemm_t_one_hot_is_exact_dequant():
+    say("gemm_t one-hot")
+    rng = np.random.default_rng(22)
+    N, K = 80, 272
+    codes = rng.integers(0, 256, size=(N, K // 2), dtype=np.uint8)
+    scales = rng.integers(0, 0x7F, size=(N, K // 16), dtype=np.uint8)
+    w = nv.PackedWeight.from_canonical(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), 1.0, N, K)
+    dX = nv.gemm_t(w.transpose(), torch.eye(N, device="cuda", dtype=BF16))
+    assert np.array_equal(f64(dX), O.dequant(codes, scales, 1.0))
+
+
+@pytest.mark.parametrize("n,N,K", [(3, 200, 656), (16, 37, 144), (21, 330, 272), (150, 129, 656)])
+@pytest.mark.parametrize("act,bias", [("none", F32), ("silu", BF16), ("gelu", BF16), ("gelu_tanh", F32),
+                                      ("relu", None)])
+def test_linear_gradients(n, N, K, act, bias):
+    say("linear grad", n, N, K, act, bias)
+    w, W = weight(N, K, 12)
+    X = randn((n, K), 13).requires_grad_()
+    b = None if bias is None else randn((N,), 14, bias).requires_grad_()
+    r = randn((n, N), 15).requires_grad_()
+    dY = randn((n, N), 16, std=0.1)
+    Y = nv.linear(w, X, bias=b, activation=act, residual=r, transposed=w.transpose())
+    check(Y, R.linear(f64(X), W, None if b is None else f64(b), act, f64(r)), "Y")
+    grads = torch.autograd.grad(Y, [X, r] + ([b] if b is not None else []), dY)
+    dX, db = R.linear_grads(f64(X), W, f64(dY), None if b is None else f64(b), act, bias == F32)
+    check(grads[0], dX, "dX")
+    assert torch.equal(grads[1], dY)
+    if b is not None:
+        assert grads[2].dtype == bias
+        check(grads[2], db, "db")
+
+
+@pytest.mark.parametrize("n,F,K", [(3, 200, 656), (16, 17, 144), (21, 330, 272), (150, 129, 656)])
+@pytest.mark.parametrize("act,bias", [("silu", None), ("gelu", BF16), ("gelu_tanh", F32), ("none", F32)])
+def test_gated_gradients(n, F, K, act, bias):
+    say("gated grad", n, F, K, act, bias)
+    (g, Wg), (u, Wu) = weight(F, K, 17), weight(F, K, 18, 0.02)
+    w = nv.GatedWeight.from_packed(g, u)
+    X = randn((n, K), 19).requires_grad_()
+    bg = None if bias is None else randn((F,), 20, bias).requires_grad_()
+    bu = None if bias is None else randn((F,), 21, bias).requires_grad_()
+    dH = randn((n, F), 22, std=0.1)
+    H = nv.gated(w, X, activation=act, gate_bias=bg, up_bias=bu, transposed=w.transpose())
+    grads = torch.autograd.grad(H, [X] + ([bg, bu] if bias is not None else []), dH)
+    none = bias is None
+    dX, dbg, dbu = R.gated_grads(f64(X), Wg, Wu, f64(dH), None if none else f64(bg), None if none else f64(bu), act,
+                                 bias == F32)
+    check(grads[0], dX, "dX")
+    if not none:
+        check(grads[1], dbg, "dbg")
+        check(grads[2], dbu, "dbu")
+
+
+@pytest.mark.parametrize("act", R.ACTS)
+def test_elementwise_gradient_tight(act):
+    """dZ from given bf16 pre-activations: one rounding, over a wide range of z."""
+    say("dZ", act)
+    n, N, K = 40, 333, 16
+    w, _ = weight(N, K, 23)
+    z = torch.zeros(n, 336, dtype=BF16, device="cuda")
+    z[:, :N] = randn((n, N), 24, std=4.0)
+    z[:, N:] = float("nan")              # columns that do not exist
+    dY = torch.ones(n, N, device="cuda", dtype=BF16)
+    _, db = nv.linear_backward(None, dY, activation=act, preact=z, bias_dtype=F32)
+    d = R.act_grad(f64(z)[:, :N], act)
+    s, b = R.column_sum(d, 4 * R.ACT_EPS * (1 + np.abs(f64(z)[:, :N])), True)
+    check(db, (s, b), "column sums")
+
+
+def test_strides_guards_and_in_place_residual():
+    """Strided X with NaN between its rows, an unaligned strided output whose
+    surroundings stay as they were, the residual in place."""
+    for n in (5, 16, 40):
+        say("strides", n)
+        N, K = 93, 208
+        w, W = weight(N, K, 25)
+        big = torch.full((n, K + 24), float("nan"), device="cuda", dtype=BF16)
+        big[:, :K] = randn((n, K), 26)
+        X = big[:, :K]
+        for dtype in (BF16, F32):
+            buf = torch.full((n + 2, 131), 7.0, device="cuda", dtype=dtype)
+            out = buf[1:n + 1, 3:3 + N]
+            r = randn((n, N), 27, dtype)
+            out.copy_(r)
+            Y = nv.linear(w, X, residual=out, out=out)
+            assert Y.data_ptr() == out.data_ptr()
+            check(out, R.linear(f64(X), W, None, "none", f64(r), dtype == F32), "in place")
+            buf[1:n + 1, 3:3 + N] = 7.0
+            assert (buf == 7.0).all()
+        g, _ = weight(N, K, 28)
+        gw = nv.GatedWeight.from_packed(w, g)
+        buf = torch.full((n + 2, 140), 7.0, device="cuda", dtype=BF16)
+        H = nv.gated(gw, X, out=buf[1:n + 1, 5:5 + N])
+        assert torch.equal(H, nv.gated(gw, X.contiguous()))
+        buf[1:n + 1, 5:5 + N] = 7.0
+        assert (buf == 7.0).all()
+
+
+def test_results_do_not_depend_on_the_batch():
+    say("batch identity")
+    N, K = 200, 656
+    w, _ = weight(N, K, 29)
+    gw = nv.GatedWeight.from_packed(w, w)
+    wt = w.transpose()
+    X, dY = randn((300, K), 30), randn((300, N), 31)
+    full = nv.linear(w, X, activation="silu"), nv.gated(gw, X), nv.gemm_t(wt, dY)
+    for a, b in ((0, 17), (100, 164), (37, 300), (283, 300)):
+        part = nv.linear(w, X[a:b], activation="silu"), nv.gated(gw, X[a:b]), nv.gemm_t(wt, dY[a:b])
+        for p, q in zip(part, full):
+            assert torch.equal(p, q[a:b]), (a, b)
+    one = nv.linear(w, X[:16]), nv.gated(gw, X[:16])
+    for a, b in ((0, 1), (3, 9), (15, 16)):
+        assert torch.equal(nv.linear(w, X[a:b]), one[0][a:b])
+        assert torch.equal(nv.gated(gw, X[a:b]), one[1][a:b])
+
+
+def test_linear_without_epilogue_is_gemv():
+    say("linear == gemv")
+    w, _ = weight(200, 656, 32)
+    X = randn((9, 656), 33)
+    assert torch.equal(nv.linear(w, X), nv.gemv(w, X))
+
+
+def test_nonfinite_stays_in_its_token():
+    for n in (9, 50):
+        say("nonfinite", n)
+        w, _ = weight(70, 272, 34)
+        gw = nv.GatedWeight.from_packed(w, w)
+        wt = w.transpose()
+        X, dY = randn((n, 272), 35), randn((n, 70), 36)
+        clean = nv.linear(w, X, activation="gelu"), nv.gated(gw, X), nv.gemm_t(wt, dY)
+        X[4, 100], dY[4, 69] = float("nan"), float("inf")
+        dirty = nv.linear(w, X, activation="gelu"), nv.gated(gw, X), nv.gemm_t(wt, dY)
+        keep = [t for t in range(n) if t != 4]
+        for c, d in zip(clean, dirty):
+            assert torch.equal(c[keep], d[keep])
+            assert not torch.isfinite(d[4]).any()
+
+
+def test_no_tokens():
+    say("no tokens")
+    w, _ = weight(70, 272, 37)
+    gw = nv.GatedWeight.from_packed(w, w)
+    X = torch.empty(0, 272, device="cuda", dtype=BF16, requires_grad=True)
+    b = randn((70,), 38).requires_grad_()
+    Y = nv.linear(w, X, bias=b, activation="silu", transposed=w.transpose())
+    dX, db = torch.autograd.grad(Y, [X, b], torch.empty(0, 70, device="cuda", dtype=BF16))
+    assert Y.shape == (0, 70) and dX.shape == (0, 272) and (db == 0).all()
+    H = nv.gated(gw, X, gate_bias=b, transposed=gw.transpose())
+    dX, db = torch.autograd.grad(H, [X, b], torch.empty(0, 70, device="cuda", dtype=BF16))
+    assert H.shape == (0, 70) and dX.shape == (0, 272) and (db == 0).all()
+    assert nv.gemm_t(w.transpose(), torch.empty(0, 70, device="cuda", dtype=BF16)).shape == (0, 272)
+
+
+def block(g, u, d, gt, dt, X, bg, bd):
+    """A feed-forward block: gated, then the down projection onto the residual stream."""
+    h = nv.gated(g, X, gate_bias=bg, transposed=gt)
+    return nv.linear(d, h, bias=bd, residual=X, transposed=dt)
+
+
+@pytest.mark.parametrize("n", [1, 16, 64])
+def test_block_forward_and_backward(n):
+    """The operators as a program runs them together, with an expanded
+    incoming gradient, against central differences of the 64-bit block."""
+    say("block", n)
+    K, F = 160, 96
+    (g, Wg), (u, Wu), (d, Wd) = weight(F, K, 40), weight(F, K, 41), weight(K, F, 42)
+    gw = nv.GatedWeight.from_packed(g, u)
+    X = randn((n, K), 43).requires_grad_()
+    bg = randn((F,), 44, F32).requires_grad_()
+    bd = randn((K,), 45, F32).requires_grad_()
+    Y = block(gw, u, d, gw.transpose(), d.transpose(), X, bg, bd)
+
+    def f(x, b):
+        return x + f64(bd) + R.gated(x, Wg, Wu, b, None, "silu")[0] @ Wd.T
+    x, b = f64(X), f64(bg)
+    ref = f(x, b)
+    scale = np.abs(ref).max()
+    # h and Y are rounded to bf16: 2^-8 of each term of the down projection, and of Y
+    assert np.abs(f64(Y) - ref).max() <= R.HALF_BF16 * (scale + (np.abs(R.gated(x, Wg, Wu, b)[0]) @ np.abs(Wd).T).max())
+    dX, dbg, dbd = torch.autograd.grad(Y.sum(), [X, bg, bd])
+    assert np.array_equal(f64(dbd), np.full(K, float(n)))
+    rng = np.random.default_rng(46)
+    for leaf, grad, which in ((x, dX, 0), (b, dbg, 1)):
+        for _ in range(8):
+            v = rng.standard_normal(leaf.shape)
+            t = 1e-4
+            args = lambda s: (x + s * v, b) if which == 0 else (x, b + s * v)   # noqa: E731
+            diff = (f(*args(t)).sum() - f(*args(-t)).sum()) / (2 * t)
+            got = float((f64(grad) * v).sum())
+            # at most three roundings to bf16 (h's gradient, dZ, dX) and the
+            # rounded pre-activations on every term
+            assert abs(got - diff) <= 8 * R.HALF_BF16 * float((np.abs(f64(grad)) * np.abs(v)).sum()) + 1e-3, which
+
+
+def test_graph_replays_match_eager():
+    """Forward and backward captured, two graphs with their own memory, replayed
+    with changing inputs between eager calls."""
+    say("graphs")
+    K, F = 272, 144
+    (g, _), (u, _), (d, _) = weight(F, K, 50), weight(F, K, 51), weight(K, F, 52)
+    gw = nv.GatedWeight.from_packed(g, u)
+    gt, dt = gw.transpose(), d.transpose()
+
+    def step(X, dY, b):
+        n = X.shape[0]
+        pre = torch.empty(n, nv.preact_columns(gw), dtype=BF16, device="cuda")
+        H = nv.gated(gw, X, gate_bias=b, preact=pre)
+        Y = nv.linear(d, H, residual=X)
+        dH, _ = nv.linear_backward(dt, dY)
+        dX, db, _ = nv.gated_backward(gw, gt, dH, pre, bias_dtype=F32)
+        return Y, dX, db
+
+    graphs = []
+    for n in (6, 200):
+        X, dY, b = randn((n, K), 53), randn((n, K), 54), randn((F,), 55, F32)
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            step(X, dY, b)
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step(X, dY, b)
+        graphs.append((n, X, dY, b, graph, out))
+    for trip in range(4):
+        for n, X, dY, b, graph, out in graphs:
+            X.copy_(randn((n, K), 60 + trip))
+            dY.copy_(randn((n, K), 70 + trip))
+            graph.replay()
+            torch.cuda.synchronize()
+            for o, e in zip(out, step(X, dY, b)):
+                assert torch.equal(o, e), (trip, n)
+
+
+def test_side_stream_and_given_buffers():
+    say("streams")
+    w, _ = weight(64, 8208, 56)
+    gw = nv.GatedWeight.from_packed(w, w)
+    X = randn((7, 8208), 57)
+    want = nv.linear(w, X, activation="silu"), nv.gated(gw, X), nv.gemm_t(w.transpose(), randn((7, 64), 58))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    ws = torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")
+    s.wait_stream(torch.cuda.current_stream())
+    a = nv.linear(w, X, activation="silu", stream=s)
+    b = nv.gated(gw, X, workspace=ws, stream=s)
+    c = nv.gemm_t(w.transpose(stream=s), randn((7, 64), 58), stream=s)
+    s.synchronize()
+    for p, q in zip((a, b, c), want):
+        assert torch.equal(p, q)
+
+
+def test_unaligned_and_expanded_gradients():
+    say("unaligned dY")
+    w, W = weight(40, 272, 59)
+    wt = w.transpose()
+    buf = randn((30, 101), 61)
+    dY = buf[:, 1:41]                       # rows not 16-byte aligned
+    assert torch.equal(nv.gemm_t(wt, dY), nv.gemm_t(wt, dY.contiguous()))
+    X = randn((30, 272), 62).requires_grad_()
+    Y = nv.linear(w, X, transposed=wt)
+    (a,) = torch.autograd.grad(Y.sum(), X)
+    assert torch.equal(a, nv.gemm_t(wt, torch.ones(30, 40, device="cuda", dtype=BF16)))
+
+
+def test_refusals():
+    say("refusals")
+    w, _ = weight(40, 272, 63)
+    gw = nv.GatedWeight.from_packed(w, w)
+    X = randn((5, 272), 64)
+    with pytest.raises(ValueError):
+        nv.linear(w, X, activation="tanh")
+    with pytest.raises(ValueError):
+        nv.linear(w, X.t().contiguous().t())
+    with pytest.raises(ValueError):
+        nv.linear(w, X[:, :256])
+    with pytest.raises(TypeError):
+        nv.linear(w, X.float())
+    with pytest.raises(ValueError):
+        nv.linear(w, X, bias=randn((41,), 65))
+    with pytest.raises(ValueError):
+        nv.linear(w, X.clone().requires_grad_())                     # no transposed copy
+    with pytest.raises(ValueError):
+        nv.linear(w, X.clone().requires_grad_(), transposed=gw.transpose())
+    with pytest.raises(TypeError):
+        nv.gated(gw, X, gate_bias=randn((40,), 66), up_bias=randn((40,), 67, F32))
+    with pytest.raises(ValueError):
+        nv.GatedWeight.from_packed(w, weight(41, 272, 68)[0])
+    odd = torch.empty(5 * 273 + 8, device="cuda", dtype=BF16)
+    with pytest.raises(nv.Nvfp4Error) as e:
+        nv.linear(w, odd[:5 * 273].view(5, 273)[:, :272])
+    assert e.value.status == 3
+    with pytest.raises(nv.Nvfp4Error) as e:
+        nv.linear(w, X, out=X.view(-1)[:200].view(5, 40))
+    assert e.value.status == 10
