@@ -13,6 +13,7 @@ struct FusedGemmParams {
     const uint16_t *X;     // bf16 [n][ldx]
     long long ldx;
     int n, K, T, RG;       // K: columns contracted (a multiple of 8), T its tiles
+    int tiles_x, tiles_y;  // row and token tiles
     nvfp4_epi_params e;
 };
 
@@ -40,28 +41,106 @@ __device__ __forceinline__ u32x4 dequant_rows(u32 w, u32 s0, u32 s1)
                  __builtin_bit_cast(u32, o3)};
 }
 
+// LDS-direct load: lane l's 16 bytes go to `lds` + 16 l (a wave-uniform LDS
+// address); offsets past the resource write zeros.  No register is written, so
+// only the vmcnt wait before the barrier orders it.
+__device__ __forceinline__ void load_lds_b128(u32x4 rsrc, unsigned voff, unsigned soff, unsigned lds)
+{
+    asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                 :: "v"(voff), "s"(rsrc), "s"(soff), "s"(lds) : "memory");   // M0 is reserved: the compiler keeps nothing in it
+}
+
+__device__ __forceinline__ u32x4 buffer_load_b128_s(u32x4 rsrc, unsigned voff, unsigned soff)
+{
+    u32x4 v;
+    asm volatile("buffer_load_dwordx4 %0, %1, %2, %3 offen" : "=v"(v) : "v"(voff), "s"(rsrc), "s"(soff));
+    return v;
+}
+
+// Byte address of LDS memory, as the M0 of an LDS-direct load takes it.
+__device__ __forceinline__ unsigned lds_address(const void *p)
+{
+    return (unsigned)(uintptr_t)(__attribute__((address_space(3))) const char *)p;
+}
+
 // One workgroup: 4 waves x RG row groups (64 * RG weight rows) times 16 * TB
-// tokens.  A step covers 128 contracted columns: the tokens' slice goes
-// through LDS, each wave turns its own code tiles into MFMA operands in
-// registers.  MODE: 0 linear, 1 gated (row groups alternate gate, up), 2
-// transposed weight, plain output.
+// tokens.  A step covers 128 contracted columns: the tokens' slice and the
+// scales go straight to LDS, each wave turns its own code tiles into MFMA
+// operands in registers.  The loads of step s + 1 are issued before step s is
+// computed and waited for after it (two LDS buffers).  MODE: 0 linear, 1 gated
+// (row groups alternate gate, up), 2 transposed weight, plain output.
 //
 // LDS layout of the slice: token t's 16-byte chunk c (8 columns) at
 //     (t / 4) * kQuad + (t % 4) * 256 + (c ^ (t % 4)) * 16.
 // An operand is two 8-byte pieces, columns 32j + 4g and 32j + 16 + 4g, of 16
 // tokens a read; the XOR and the 64 bytes between quads put the 16 tokens in
 // 16 different 16-byte slots of the 256-byte bank row, and leave the step j
-// and the token block as constant offsets.
+// and the token block as constant offsets.  A quad is 1 KiB of consecutive
+// LDS, one LDS-direct load of a wave.
 template <int RG, int TB, int MODE>
-__global__ __launch_bounds__(256) void nvfp4_fused_gemm_kernel(FusedGemmParams p)
+__global__ __launch_bounds__(256, (RG * TB <= 32 ? 2 : 1)) void nvfp4_fused_gemm_kernel(FusedGemmParams p)
 {
     constexpr int BM = TB * 16;
+    constexpr int kSlice = BM / 4 * kQuad;         // LDS bytes of a step's token slice
+    constexpr int kBuf = kSlice + 4 * 1024;        // and of the waves' scales, 1 KiB each
+    constexpr int XL = TB;                         // quads a wave stages: BM / 4 / 4 waves
     const int tid = threadIdx.x;
-    const int lane = tid & 63, wave = tid >> 6;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int i = lane & 15, g = lane >> 4;
-    const int rg0 = (blockIdx.x * 4 + wave) * RG;
-    const int tok0 = blockIdx.y * BM;
-    __shared__ __align__(16) char xs[BM / 4 * kQuad < 16 * (64 * RG + 4) * 4 ? 16 * (64 * RG + 4) * 4 : BM / 4 * kQuad];
+
+    // Tile of this workgroup.  Consecutive workgroups go to the 8 XCDs in
+    // turn; each XCD takes a contiguous share of the tiles, in blocks of 8 row
+    // tiles x every token tile, so that the workgroups that run on it together
+    // share both operands through its L2.
+    int tx, ty;
+    {
+        const int total = p.tiles_x * p.tiles_y;
+        const int b = blockIdx.x, x = b & 7;
+        const int per = total >> 3, rem = total & 7;
+        const int idx = x * per + min(x, rem) + (b >> 3);
+        const int block = 8 * p.tiles_y;
+        const int x0 = idx / block * 8, w = min(8, p.tiles_x - x0), at = idx % block;
+        tx = x0 + at % w;
+        ty = at / w;
+    }
+    const int rg0 = (tx * 4 + wave) * RG;
+    const int tok0 = ty * BM;
+    const int ntok = min(BM, p.n - tok0);
+    const int nrg = max(0, min(RG, p.RG - rg0)), rgb = min(rg0, p.RG);
+    __shared__ __align__(1024) char lds[2][kBuf];
+
+    // Loads past these ranges (tokens beyond n, row groups beyond RG) read
+    // zeros without touching memory.
+    const u32x4 xrsrc = uniform(buffer_rsrc(p.X + tok0 * p.ldx, (unsigned)(((ntok - 1) * p.ldx + p.K) * 2)));
+    const u32x4 crsrc = uniform(buffer_rsrc(p.codes + (size_t)rgb * p.T * 64, (unsigned)(nrg * p.T) * 1024u));
+    const u32x4 srsrc = uniform(buffer_rsrc(p.scales + (size_t)rgb * p.T * 128, (unsigned)(nrg * p.T) * 128u));
+    const int ldx2 = (int)p.ldx * 2;
+    const int xcol = 8 * (i ^ g);   // lane (i, g) stages chunk i ^ g of token 4 q + g
+    const unsigned xoff = (unsigned)((wave * XL * 4 + g) * ldx2 + xcol * 2);
+    const unsigned soff = lane < 8 * RG ? (unsigned)((lane >> 3) * p.T * 128 + (lane & 7) * 16) : kOutOfRange;
+    const unsigned ldsb = lds_address(lds) + wave * XL * kQuad;
+    const unsigned ldss = lds_address(lds) + kSlice + wave * 1024;
+
+    u32x4 cw[RG];
+    auto issue = [&](int s) {
+        const unsigned buf = (s & 1) * kBuf;
+        const unsigned xv = s * kTileK + xcol < p.K ? xoff : kOutOfRange;
+#pragma unroll
+        for (int u = 0; u < XL; ++u)
+            load_lds_b128(xrsrc, xv, (unsigned)(u * 4 * ldx2 + s * 256), ldsb + buf + u * kQuad);
+        load_lds_b128(srsrc, soff, (unsigned)(s * 128), ldss + buf);
+#pragma unroll
+        for (int r = 0; r < RG; ++r)
+            cw[r] = buffer_load_b128_s(crsrc, (unsigned)(lane * 16), (unsigned)((r * p.T + s) * 1024));
+    };
+    auto land = [&]() {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+        for (int r = 0; r < RG; ++r)
+            asm volatile("" : "+v"(cw[r]));
+        __syncthreads();
+    };
 
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
     f32x4 acc[RG][TB];
@@ -71,61 +150,60 @@ __global__ __launch_bounds__(256) void nvfp4_fused_gemm_kernel(FusedGemmParams p
         for (int tb = 0; tb < TB; ++tb)
             acc[r][tb] = zero;
 
-    const char *xa = xs + (i >> 2) * kQuad + (i & 3) * 256 + 8 * (g & 1);
-    const char *x0 = xa + (((g >> 1)) ^ (i & 3)) * 16;
-    const char *x1 = xa + (((g >> 1) | 2) ^ (i & 3)) * 16;
+    const int xa = (i >> 2) * kQuad + (i & 3) * 256 + 8 * (g & 1);
+    const int x0 = xa + ((g >> 1) ^ (i & 3)) * 16, x1 = xa + (((g >> 1) | 2) ^ (i & 3)) * 16;
+    const int sa = kSlice + wave * 1024 + (MODE == 2 ? g * 32 : i * 8);
 
-    for (int s = 0; s < p.T; ++s) {
-        __syncthreads();
+    auto compute = [&](int s, const u32x4 *c) {
+        const char *buf = lds[s & 1];
+        u32x2 sw[RG];
+        if constexpr (MODE != 2) {
 #pragma unroll
-        for (int u = 0; u < TB; ++u) {
-            const int t = (tid >> 4) + 16 * u, c = tid & 15;
-            const int k = s * kTileK + 8 * c;
-            u32x4 v = {0u, 0u, 0u, 0u};
-            if (tok0 + t < p.n && k < p.K)
-                v = *reinterpret_cast<const u32x4 *>(p.X + (tok0 + t) * p.ldx + k);
-            *reinterpret_cast<u32x4 *>(xs + (t >> 2) * kQuad + (t & 3) * 256 + (c ^ (t & 3)) * 16) = v;
+            for (int r = 0; r < RG; ++r)
+                sw[r] = *reinterpret_cast<const u32x2 *>(buf + sa + r * 128);
         }
-        u32x4 cw[RG];
-        u32x4 sa[RG], sb[RG];
-#pragma unroll
-        for (int r = 0; r < RG; ++r) {
-            const long long tile = (long long)min(rg0 + r, p.RG - 1) * p.T + s;   // rows past the end: any tile, not stored
-            cw[r] = p.codes[tile * 64 + lane];
-            if constexpr (MODE == 2) {
-                const u32x4 *src = reinterpret_cast<const u32x4 *>(p.scales + tile * 128 + g * 32);
-                sa[r] = src[0];
-                sb[r] = src[1];
-            } else {
-                const u32x2 v = *reinterpret_cast<const u32x2 *>(p.scales + tile * 128 + i * 8);
-                sa[r][0] = v[0];
-                sa[r][1] = v[1];
-            }
-        }
-        __syncthreads();
-        static_for<4>([&](auto jc) {
+        bf16x8 w[2][RG];
+        auto dequant = [&](auto jc, int q) {
             constexpr int j = decltype(jc)::value;
-            bf16x8 w[RG];
 #pragma unroll
             for (int r = 0; r < RG; ++r) {
                 if constexpr (MODE == 2) {
-                    const u32x4 sv = j < 2 ? sa[r] : sb[r];
-                    w[r] = __builtin_bit_cast(bf16x8, dequant_rows(cw[r][j], sv[2 * (j & 1)], sv[2 * (j & 1) + 1]));
+                    const u32x2 sv = *reinterpret_cast<const u32x2 *>(buf + sa + r * 128 + 8 * j);
+                    w[q][r] = __builtin_bit_cast(bf16x8, dequant_rows(c[r][j], sv[0], sv[1]));
                 } else {
-                    w[r] = __builtin_bit_cast(bf16x8, dequant_pair<(j & 1) != 0>(cw[r][j], sa[r][j >> 1]));
+                    w[q][r] = __builtin_bit_cast(bf16x8, dequant_pair<(j & 1) != 0>(c[r][j], sw[r][j >> 1]));
                 }
             }
+        };
+        dequant(std::integral_constant<int, 0>{}, 0);
+        static_for<4>([&](auto jc) {
+            constexpr int j = decltype(jc)::value;
+            if constexpr (j < 3)
+                dequant(std::integral_constant<int, j + 1>{}, (j + 1) & 1);
 #pragma unroll
             for (int tb = 0; tb < TB; ++tb) {
-                const u32x2 lo = *reinterpret_cast<const u32x2 *>(x0 + tb * 4 * kQuad + 64 * j);
-                const u32x2 hi = *reinterpret_cast<const u32x2 *>(x1 + tb * 4 * kQuad + 64 * j);
+                const u32x2 lo = *reinterpret_cast<const u32x2 *>(buf + x0 + tb * 4 * kQuad + 64 * j);
+                const u32x2 hi = *reinterpret_cast<const u32x2 *>(buf + x1 + tb * 4 * kQuad + 64 * j);
                 const bf16x8 x = __builtin_bit_cast(bf16x8, u32x4{lo[0], lo[1], hi[0], hi[1]});
 #pragma unroll
                 for (int r = 0; r < RG; ++r)
-                    acc[r][tb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[r], x, acc[r][tb], 0, 0, 0);
+                    acc[r][tb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j & 1][r], x, acc[r][tb], 0, 0, 0);
             }
             __builtin_amdgcn_sched_barrier(0);   // one substep's operands live at a time
         });
+    };
+
+    issue(0);
+    land();
+    for (int s = 0; s < p.T; ++s) {
+        u32x4 c[RG];
+#pragma unroll
+        for (int r = 0; r < RG; ++r)
+            c[r] = cw[r];
+        if (s + 1 < p.T)
+            issue(s + 1);
+        compute(s, c);
+        land();
     }
 
     // Epilogue, one token block at a time through LDS, so that a wave writes
@@ -134,9 +212,9 @@ __global__ __launch_bounds__(256) void nvfp4_fused_gemm_kernel(FusedGemmParams p
     // of token tok0 + 16*tb + i.
     constexpr int kRows = 64 * RG, kPitch = kRows + 4;
     constexpr int kOuts = MODE == 1 ? kRows / 2 : kRows;   // outputs a token
-    static_assert(16 * kPitch * 4 <= sizeof(xs), "the staged block fits the slice's LDS");
-    float *stage = reinterpret_cast<float *>(xs);
-    const int out0 = blockIdx.x * kOuts;
+    static_assert(16 * kPitch * 4 <= sizeof(lds), "the staged block fits the slice's LDS");
+    float *stage = reinterpret_cast<float *>(lds);
+    const int out0 = tx * kOuts;
 #pragma unroll 1
     for (int b = 0; b < TB && tok0 + 16 * b < p.n; ++b) {
         __syncthreads();
@@ -167,10 +245,14 @@ __global__ __launch_bounds__(256) void nvfp4_fused_gemm_kernel(FusedGemmParams p
 }
 
 template <int RG, int TB, int MODE>
-int launch_one(const FusedGemmParams &p, hipStream_t stream)
+int launch_one(FusedGemmParams p, hipStream_t stream)
 {
-    const dim3 grid((unsigned)((p.RG + 4 * RG - 1) / (4 * RG)), (unsigned)((p.n + TB * 16 - 1) / (TB * 16)));
-    hipLaunchKernelGGL((nvfp4_fused_gemm_kernel<RG, TB, MODE>), grid, dim3(256), 0, stream, p);
+    p.tiles_x = (p.RG + 4 * RG - 1) / (4 * RG);
+    p.tiles_y = (p.n + TB * 16 - 1) / (TB * 16);
+    const long long total = (long long)p.tiles_x * p.tiles_y;
+    if (total > INT32_MAX || (long long)p.T * RG * 1024 > INT32_MAX)
+        return NVFP4_ERR_SHAPE;   // a wave's codes must stay within a 32-bit buffer offset
+    hipLaunchKernelGGL((nvfp4_fused_gemm_kernel<RG, TB, MODE>), dim3((unsigned)total), dim3(256), 0, stream, p);
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
 }
 
@@ -179,7 +261,9 @@ int launch_mode(const FusedGemmParams &p, hipStream_t stream)
 {
     if (p.n <= 32)
         return launch_one<2, 2, MODE>(p, stream);
-    return launch_one<2, 4, MODE>(p, stream);
+    if (p.n <= 64)
+        return launch_one<2, 4, MODE>(p, stream);
+    return launch_one<4, 8, MODE>(p, stream);
 }
 
 }  // namespace
