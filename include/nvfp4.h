@@ -300,8 +300,13 @@ int nvfp4_gemm_geometry(int n, int N, int K, int *rows_per_workgroup,
  *     stored;
  *   - outputs may not overlap other arguments (OVERLAP), except that the
  *     residual may be the output itself (same address, stride and type);
- *   - for n <= 16 each token's result depends only on (N, K), for n > 16 on
- *     the same order of sums whatever n: results do not vary from run to run. */
+ *   - a call may run in K parts: fp32 partial sums in a workspace the caller
+ *     owns (16-byte aligned, at least the bytes its _workspace_bytes function
+ *     names, 0 for most sizes), added in part order by a second launch.  Calls
+ *     that share a workspace must be ordered (one stream); graphs captured with
+ *     one must not run at the same time;
+ *   - the order of every sum depends on the sizes (n, N, K) alone, and for n <=
+ *     16 on (N, K) alone: results do not vary from run to run. */
 
 /* Activations: z; max(z, 0); z / (1 + exp(-z)); z Phi(z) (erf form);
  * 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))). */
@@ -328,9 +333,8 @@ typedef struct nvfp4_epilogue {
 
 /* Y = act(gscale X dequant(W)^T + bias) + residual for any n up to
  * NVFP4_MAX_GEMM_TOKENS, Wq / Wscale packed (nvfp4_pack).  Up to 16 tokens run
- * the decode product (K parts beyond K = 8192, which need a workspace of
- * nvfp4_linear_workspace_bytes(n, N, K) bytes, 16-byte aligned; calls that
- * share one on different streams race), more run a token-tiled product.
+ * the decode product (K parts beyond K = 8192), more a token-tiled product (K
+ * parts where its tiles alone would leave compute units idle).
  * Errors: NULL, RANGE (n, N, K, strides, activation, types; up_bias set),
  * SHAPE (K % 16, K > 262144, strides), ALIGN, OVERLAP, WORKSPACE, DEVICE,
  * LAUNCH. */
@@ -370,10 +374,13 @@ int nvfp4_pack_transposed(const uint8_t *codes_packed, const uint8_t *scales_pac
 
 /* dX[n][K] = gscale dY[n][N] . dequant(W), bf16: the gradient of a projection
  * with respect to its input.  Where N is not a multiple of 8, the elements up
- * to the next multiple are read from each dY row and must be zero.
- * Errors: NULL, RANGE, SHAPE, ALIGN, OVERLAP, DEVICE, LAUNCH. */
+ * to the next multiple are read from each dY row and must be zero.  Workspace
+ * as nvfp4_linear: nvfp4_gemm_t_workspace_bytes(n, N, K).  Errors: NULL, RANGE,
+ * SHAPE, ALIGN, OVERLAP, WORKSPACE, DEVICE, LAUNCH. */
 int nvfp4_gemm_t(const uint8_t *codes_t, const uint8_t *scales_t, float gscale, const uint16_t *dY, int64_t ldy,
-                 uint16_t *dX, int64_t ldx, int n, int N, int K, void *stream);
+                 uint16_t *dX, int64_t ldx, int n, int N, int K, void *workspace, size_t workspace_bytes,
+                 void *stream);
+size_t nvfp4_gemm_t_workspace_bytes(int n, int N, int K);
 
 /* The elementwise half of nvfp4_linear's gradient: dZ = dY * act'(Z) in bf16
  * with columns N .. next multiple of 8 zero (ready for nvfp4_gemm_t; ldz a

@@ -75,25 +75,28 @@ __global__ void nvfp4_transpose_scales_kernel(const uint8_t *scales, int T, int 
 
 // ---- K parts ------------------------------------------------------------------------
 
-// The parts of each output added in part order, then the epilogue.  Grid
-// (ceil(outputs / 256), n).
+// The parts of each output added in part order, then the epilogue: one thread
+// for four consecutive outputs of a token, the parts of a batch in flight
+// together.  P: [ks][n][pitch].
 template <bool GATED>
-__global__ __launch_bounds__(256) void nvfp4_fused_reduce_kernel(nvfp4_epi_params e, const float *P, int n, int rows, int ks)
+__global__ __launch_bounds__(256) void nvfp4_fused_reduce_kernel(nvfp4_epi_params e, const float *P, int n, int pitch, int ks)
 {
-    const int r = blockIdx.x * 256 + threadIdx.x;
-    const int tok = blockIdx.y;
-    if (r >= e.N)
+    const int quads = (e.N + 3) / 4;
+    const long long idx = (long long)blockIdx.x * 256 + threadIdx.x;
+    const long long tok = idx / quads;
+    if (tok >= n)
         return;
-    const long long count = (long long)n * rows;
+    const int r = (int)(idx % quads) * 4;
+    const long long count = (long long)n * pitch;
     auto total = [&](long long row) {
-        const float *src = P + (long long)tok * rows + row;
-        constexpr int kBatch = 8;   // loads in flight together
-        float s = 0.f;
+        const f32x4 *src = reinterpret_cast<const f32x4 *>(P + tok * pitch + row);
+        constexpr int kBatch = 4;
+        f32x4 s = {0.f, 0.f, 0.f, 0.f};
         for (int q0 = 0; q0 < ks; q0 += kBatch) {
-            float v[kBatch];
+            f32x4 v[kBatch];
 #pragma unroll
             for (int j = 0; j < kBatch; ++j)
-                v[j] = q0 + j < ks ? __builtin_nontemporal_load(src + (q0 + j) * count) : 0.f;
+                v[j] = q0 + j < ks ? __builtin_nontemporal_load(src + (q0 + j) * count / 4) : f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < kBatch; ++j)
                 if (q0 + j < ks)
@@ -102,9 +105,9 @@ __global__ __launch_bounds__(256) void nvfp4_fused_reduce_kernel(nvfp4_epi_param
         return s;
     };
     if constexpr (GATED)
-        gated_out(e, tok, r, total(gated_row(r, 0)), total(gated_row(r, 1)));
+        gated_out4(e, (int)tok, r, total(gated_row(r, 0)), total(gated_row(r, 1)));
     else
-        linear_out(e, tok, r, total(r));
+        linear_out4(e, (int)tok, r, total(r));
 }
 
 // ---- the elementwise half of the gradients ---------------------------------------------
@@ -341,16 +344,53 @@ nvfp4_epi_params epi_params(const nvfp4_epilogue *ep, float gscale, float up_gsc
     return e;
 }
 
-// K parts of a fused call: one launch up to 8192 columns and beyond 16 tokens.
-int fused_kparts(int n, int rows, int K)
+int padded_rows(int rows)
 {
-    return n <= NVFP4_MAX_TOKENS ? nvfp4_gemv_kparts(rows, K) : 1;
+    return (int)(kRowsPerGroup * row_groups(rows));
 }
 
+// Workspace of a call that runs in K parts: fp32 sums [ks][n][rows to 16].
 size_t parts_bytes(int n, int rows, int K)
 {
-    const int ks = n > 0 ? fused_kparts(n, rows, K) : 1;
-    return ks > 1 ? (size_t)ks * n * rows * sizeof(float) : 0;
+    if (n < 1)
+        return 0;
+    const int ks = n <= NVFP4_MAX_TOKENS ? nvfp4_gemv_kparts(rows, K)
+                                         : nvfp4_plan_fused_gemm(n, (int)row_groups(rows), K).ks;
+    return ks > 1 ? (size_t)ks * n * padded_rows(rows) * sizeof(float) : 0;
+}
+
+int check_workspace(const void *workspace, size_t bytes, size_t need)
+{
+    if (need && (!workspace || bytes < need))
+        return NVFP4_ERR_WORKSPACE;
+    return need && !is_aligned(workspace, 16) ? NVFP4_ERR_ALIGN : NVFP4_OK;
+}
+
+// The second launch of a call in K parts.
+int launch_reduce(const nvfp4_epi_params &e, const float *partial, int n, int pitch, int ks, bool gated, hipStream_t stream)
+{
+    const long long quads = ((long long)e.N + 3) / 4 * n;
+    const dim3 grid((unsigned)((quads + 255) / 256));
+    if (gated)
+        hipLaunchKernelGGL(nvfp4_fused_reduce_kernel<true>, grid, dim3(256), 0, stream, e, partial, n, pitch, ks);
+    else
+        hipLaunchKernelGGL(nvfp4_fused_reduce_kernel<false>, grid, dim3(256), 0, stream, e, partial, n, pitch, ks);
+    return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
+}
+
+// The many-token product; rows: of the packed weight (its K tiles when transposed).
+int launch_product(nvfp4_fused_gemm_args a, void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    const nvfp4_fused_gemm_plan plan = nvfp4_plan_fused_gemm(a.n, a.row_groups, a.K);
+    const int pitch = a.row_groups * kRowsPerGroup;
+    int st = check_workspace(workspace, workspace_bytes, plan.ks > 1 ? (size_t)plan.ks * a.n * pitch * sizeof(float) : 0);
+    if (st != NVFP4_OK)
+        return st;
+    a.partial = static_cast<float *>(workspace);
+    st = nvfp4_launch_fused_gemm(a, plan, stream);
+    if (st != NVFP4_OK || plan.ks == 1)
+        return st;
+    return launch_reduce(a.epi, a.partial, a.n, pitch, plan.ks, a.mode == 1, stream);
 }
 
 // rows: rows of the packed weight; gated: its row groups alternate gate, up.
@@ -358,7 +398,7 @@ int forward(const uint8_t *Wq, const uint8_t *Wscale, const uint16_t *X, int64_t
             const nvfp4_epi_params &e, bool gated, void *workspace, size_t workspace_bytes, hipStream_t stream)
 {
     if (n <= NVFP4_MAX_TOKENS) {
-        const int ks = fused_kparts(n, rows, K);
+        const int ks = nvfp4_gemv_kparts(rows, K);
         if (ks < 1)
             return -ks;
         nvfp4_fused_gemv_args a = {};
@@ -368,26 +408,18 @@ int forward(const uint8_t *Wq, const uint8_t *Wscale, const uint16_t *X, int64_t
         a.ldx = (int)ldx;
         a.n = n;
         a.K = K;
-        a.rows = rows;
+        a.rows = padded_rows(rows);
         a.units = (int)(row_groups(rows) / (gated && ks == 1 ? 2 : 1));
         a.ks = ks;
         a.epi = e;
         if (ks == 1)
             return gated ? nvfp4_launch_fused_gemv_gated(a, stream) : nvfp4_launch_fused_gemv_linear(a, stream);
-        if (!workspace || workspace_bytes < parts_bytes(n, rows, K))
-            return NVFP4_ERR_WORKSPACE;
-        if (!is_aligned(workspace, 16))
-            return NVFP4_ERR_ALIGN;
-        a.partials = static_cast<float *>(workspace);
-        const int st = nvfp4_launch_fused_gemv_partial(a, stream);
+        int st = check_workspace(workspace, workspace_bytes, parts_bytes(n, rows, K));
         if (st != NVFP4_OK)
             return st;
-        const dim3 grid((unsigned)((e.N + 255) / 256), (unsigned)n);
-        if (gated)
-            hipLaunchKernelGGL(nvfp4_fused_reduce_kernel<true>, grid, dim3(256), 0, stream, e, a.partials, n, rows, ks);
-        else
-            hipLaunchKernelGGL(nvfp4_fused_reduce_kernel<false>, grid, dim3(256), 0, stream, e, a.partials, n, rows, ks);
-        return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
+        a.partials = static_cast<float *>(workspace);
+        st = nvfp4_launch_fused_gemv_partial(a, stream);
+        return st != NVFP4_OK ? st : launch_reduce(e, a.partials, n, a.rows, ks, gated, stream);
     }
     nvfp4_fused_gemm_args a = {};
     a.mode = gated ? 1 : 0;
@@ -399,7 +431,7 @@ int forward(const uint8_t *Wq, const uint8_t *Wscale, const uint16_t *X, int64_t
     a.K = K;
     a.row_groups = (int)row_groups(rows);
     a.epi = e;
-    return nvfp4_launch_fused_gemm(a, stream);
+    return launch_product(a, workspace, workspace_bytes, stream);
 }
 
 // Rows of the packed weight of a gated block of F outputs.
@@ -700,8 +732,16 @@ int nvfp4_gated_grad(const void *dH, int dh_dtype, int64_t ldh, const uint16_t *
     return launch_grad(p, true, workspace, workspace_bytes, (hipStream_t)stream);
 }
 
+size_t nvfp4_gemm_t_workspace_bytes(int n, int N, int K)
+{
+    if (n < 1 || n > NVFP4_MAX_GEMM_TOKENS || N < 1 || N > (1 << 30) || K < 1 || K % 16 != 0 || K > kMaxK)
+        return 0;
+    const int ks = nvfp4_plan_fused_gemm(n, K / 16, (N + 7) / 8 * 8).ks;
+    return ks > 1 ? (size_t)ks * n * K * sizeof(float) : 0;
+}
+
 int nvfp4_gemm_t(const uint8_t *codes_t, const uint8_t *scales_t, float gscale, const uint16_t *dY, int64_t ldy,
-                 uint16_t *dX, int64_t ldx, int n, int N, int K, void *stream)
+                 uint16_t *dX, int64_t ldx, int n, int N, int K, void *workspace, size_t workspace_bytes, void *stream)
 {
     if (!codes_t || !scales_t || (n > 0 && (!dY || !dX)))
         return NVFP4_ERR_NULL;
@@ -735,7 +775,7 @@ int nvfp4_gemm_t(const uint8_t *codes_t, const uint8_t *scales_t, float gscale, 
     a.K = cols;
     a.row_groups = K / 16;
     a.epi = epi_params(&ep, gscale, 0.f, dX, ldx, K, K);
-    return nvfp4_launch_fused_gemm(a, (hipStream_t)stream);
+    return launch_product(a, workspace, workspace_bytes, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -14,6 +14,8 @@ struct FusedGemmParams {
     long long ldx;
     int n, K, T, RG;       // K: columns contracted (a multiple of 8), T its tiles
     int tiles_x, tiles_y;  // row and token tiles
+    int ks, tp;            // K parts of tp tiles (the last may be shorter)
+    float *partial;        // ks > 1: unscaled sums [ks][n][16 RG]
     nvfp4_epi_params e;
 };
 
@@ -64,11 +66,13 @@ __device__ __forceinline__ unsigned lds_address(const void *p)
 }
 
 // One workgroup: 4 waves x RG row groups (64 * RG weight rows) times 16 * TB
-// tokens.  A step covers 128 contracted columns: the tokens' slice and the
-// scales go straight to LDS, each wave turns its own code tiles into MFMA
-// operands in registers.  The loads of step s + 1 are issued before step s is
-// computed and waited for after it (two LDS buffers).  MODE: 0 linear, 1 gated
-// (row groups alternate gate, up), 2 transposed weight, plain output.
+// tokens, over the steps of one K part.  A step covers 128 contracted columns:
+// the tokens' slice and the scales go straight to LDS, each wave turns its own
+// code tiles into MFMA operands in registers.  NB LDS buffers: the loads of
+// step s + NB - 1 are issued before step s is computed.  With two buffers the
+// codes are loaded into registers (LDS would leave room for one workgroup a
+// compute unit only), with more they go through LDS too.  MODE: 0 linear, 1
+// gated (row groups alternate gate, up), 2 transposed weight, plain output.
 //
 // LDS layout of the slice: token t's 16-byte chunk c (8 columns) at
 //     (t / 4) * kQuad + (t % 4) * 256 + (c ^ (t % 4)) * 16.
@@ -77,13 +81,17 @@ __device__ __forceinline__ unsigned lds_address(const void *p)
 // 16 different 16-byte slots of the 256-byte bank row, and leave the step j
 // and the token block as constant offsets.  A quad is 1 KiB of consecutive
 // LDS, one LDS-direct load of a wave.
-template <int RG, int TB, int MODE>
-__global__ __launch_bounds__(256, (RG * TB <= 32 ? 2 : 1)) void nvfp4_fused_gemm_kernel(FusedGemmParams p)
+template <int RG, int TB, int NB, int MODE>
+__global__ __launch_bounds__(256, 2) void nvfp4_fused_gemm_kernel(FusedGemmParams p)
 {
     constexpr int BM = TB * 16;
+    constexpr bool kLdsCodes = NB > 2;
     constexpr int kSlice = BM / 4 * kQuad;         // LDS bytes of a step's token slice
-    constexpr int kBuf = kSlice + 4 * 1024;        // and of the waves' scales, 1 KiB each
+    constexpr int kCodes = kSlice + 4 * RG * 128;  // after the waves' scales
+    constexpr int kBuf = kCodes + (kLdsCodes ? 4 * RG * 1024 : 0);
     constexpr int XL = TB;                         // quads a wave stages: BM / 4 / 4 waves
+    constexpr int kLoads = XL + 1 + RG;            // loads of a step and wave
+    static_assert((NB - 2) * kLoads <= 63, "vmcnt is a 6-bit field");
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -93,12 +101,14 @@ __global__ __launch_bounds__(256, (RG * TB <= 32 ? 2 : 1)) void nvfp4_fused_gemm
     // turn; each XCD takes a contiguous share of the tiles, in blocks of 8 row
     // tiles x every token tile, so that the workgroups that run on it together
     // share both operands through its L2.
-    int tx, ty;
+    int tx, ty, part;
     {
         const int total = p.tiles_x * p.tiles_y;
         const int b = blockIdx.x, x = b & 7;
-        const int per = total >> 3, rem = total & 7;
-        const int idx = x * per + min(x, rem) + (b >> 3);
+        const int per = (int)gridDim.x >> 3, rem = gridDim.x & 7;
+        const int all = x * per + min(x, rem) + (b >> 3);
+        part = all / total;
+        const int idx = all % total;
         const int block = 8 * p.tiles_y;
         const int x0 = idx / block * 8, w = min(8, p.tiles_x - x0), at = idx % block;
         tx = x0 + at % w;
@@ -108,7 +118,8 @@ __global__ __launch_bounds__(256, (RG * TB <= 32 ? 2 : 1)) void nvfp4_fused_gemm
     const int tok0 = ty * BM;
     const int ntok = min(BM, p.n - tok0);
     const int nrg = max(0, min(RG, p.RG - rg0)), rgb = min(rg0, p.RG);
-    __shared__ __align__(1024) char lds[2][kBuf];
+    const int s0 = part * p.tp, s1 = min(p.T, s0 + p.tp);
+    __shared__ __align__(1024) char lds[NB][kBuf];
 
     // Loads past these ranges (tokens beyond n, row groups beyond RG) read
     // zeros without touching memory.
@@ -118,27 +129,40 @@ __global__ __launch_bounds__(256, (RG * TB <= 32 ? 2 : 1)) void nvfp4_fused_gemm
     const int ldx2 = (int)p.ldx * 2;
     const int xcol = 8 * (i ^ g);   // lane (i, g) stages chunk i ^ g of token 4 q + g
     const unsigned xoff = (unsigned)((wave * XL * 4 + g) * ldx2 + xcol * 2);
-    const unsigned soff = lane < 8 * RG ? (unsigned)((lane >> 3) * p.T * 128 + (lane & 7) * 16) : kOutOfRange;
+    const unsigned soff = (unsigned)((lane >> 3) * p.T * 128 + (lane & 7) * 16);
     const unsigned ldsb = lds_address(lds) + wave * XL * kQuad;
-    const unsigned ldss = lds_address(lds) + kSlice + wave * 1024;
+    const unsigned ldss = lds_address(lds) + kSlice + wave * RG * 128;
+    const unsigned ldsc = lds_address(lds) + kCodes + wave * RG * 1024;
 
     u32x4 cw[RG];
-    auto issue = [&](int s) {
-        const unsigned buf = (s & 1) * kBuf;
-        const unsigned xv = s * kTileK + xcol < p.K ? xoff : kOutOfRange;
+    // Loads of step s into LDS buffer `b`.  Steps past the part read zeros
+    // (every step issues the same loads, so that the waits can count them).
+    auto issue = [&](int s, int b) {
+        const unsigned buf = b * kBuf;
+        const bool live = s < s1;
+        const unsigned xv = live && s * kTileK + xcol < p.K ? xoff : kOutOfRange;
 #pragma unroll
         for (int u = 0; u < XL; ++u)
             load_lds_b128(xrsrc, xv, (unsigned)(u * 4 * ldx2 + s * 256), ldsb + buf + u * kQuad);
-        load_lds_b128(srsrc, soff, (unsigned)(s * 128), ldss + buf);
+        if (lane < 8 * RG)   // the wave's 128 RG bytes of scales
+            load_lds_b128(srsrc, live ? soff : kOutOfRange, (unsigned)(s * 128), ldss + buf);
 #pragma unroll
-        for (int r = 0; r < RG; ++r)
-            cw[r] = buffer_load_b128_s(crsrc, (unsigned)(lane * 16), (unsigned)((r * p.T + s) * 1024));
+        for (int r = 0; r < RG; ++r) {
+            const unsigned at = (unsigned)((r * p.T + s) * 1024);
+            if constexpr (kLdsCodes)
+                load_lds_b128(crsrc, live ? (unsigned)(lane * 16) : kOutOfRange, at, ldsc + buf + r * 1024);
+            else
+                cw[r] = buffer_load_b128_s(crsrc, (unsigned)(lane * 16), at);
+        }
     };
+    // Wait for the oldest step in flight, of NB - 1.
     auto land = [&]() {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NB - 2) * kLoads) : "memory");
+        if constexpr (!kLdsCodes) {
 #pragma unroll
-        for (int r = 0; r < RG; ++r)
-            asm volatile("" : "+v"(cw[r]));
+            for (int r = 0; r < RG; ++r)
+                asm volatile("" : "+v"(cw[r]));
+        }
         __syncthreads();
     };
 
@@ -152,10 +176,10 @@ __global__ __launch_bounds__(256, (RG * TB <= 32 ? 2 : 1)) void nvfp4_fused_gemm
 
     const int xa = (i >> 2) * kQuad + (i & 3) * 256 + 8 * (g & 1);
     const int x0 = xa + ((g >> 1) ^ (i & 3)) * 16, x1 = xa + (((g >> 1) | 2) ^ (i & 3)) * 16;
-    const int sa = kSlice + wave * 1024 + (MODE == 2 ? g * 32 : i * 8);
+    const int sa = kSlice + wave * RG * 128 + (MODE == 2 ? g * 32 : i * 8);
 
-    auto compute = [&](int s, const u32x4 *c) {
-        const char *buf = lds[s & 1];
+    auto compute = [&](int b, const u32x4 *c) {
+        const char *buf = lds[b];
         u32x2 sw[RG];
         if constexpr (MODE != 2) {
 #pragma unroll
@@ -193,17 +217,54 @@ __global__ __launch_bounds__(256, (RG * TB <= 32 ? 2 : 1)) void nvfp4_fused_gemm
         });
     };
 
-    issue(0);
-    land();
-    for (int s = 0; s < p.T; ++s) {
-        u32x4 c[RG];
-#pragma unroll
-        for (int r = 0; r < RG; ++r)
-            c[r] = cw[r];
-        if (s + 1 < p.T)
-            issue(s + 1);
-        compute(s, c);
+    if constexpr (kLdsCodes) {
+        static_for<NB - 1>([&](auto q) { issue(s0 + decltype(q)::value, decltype(q)::value); });
         land();
+        int b = 0;
+        for (int s = s0; s < s1; ++s) {
+            const int free = b == 0 ? NB - 1 : b - 1;   // the buffer computed from in the last step
+            issue(s + NB - 1, free);
+            u32x4 c[RG];
+#pragma unroll
+            for (int r = 0; r < RG; ++r)
+                c[r] = *reinterpret_cast<const u32x4 *>(lds[b] + kCodes + (wave * RG + r) * 1024 + lane * 16);
+            compute(b, c);
+            land();
+            b = b == NB - 1 ? 0 : b + 1;
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing still writes LDS
+    } else {
+        issue(s0, 0);
+        land();
+        for (int s = s0; s < s1; ++s) {
+            const int b = (s - s0) & 1;
+            u32x4 c[RG];
+#pragma unroll
+            for (int r = 0; r < RG; ++r)
+                c[r] = cw[r];
+            if (s + 1 < s1)
+                issue(s + 1, b ^ 1);
+            compute(b, c);
+            land();
+        }
+    }
+
+    // A K part stores its sums as they are: nvfp4_fused_reduce_kernel adds the
+    // parts in order and runs the epilogue.
+    if (p.ks > 1) {
+        const int pitch = p.RG * kRowsPerGroup;
+#pragma unroll
+        for (int tb = 0; tb < TB; ++tb) {
+            const int tok = tok0 + 16 * tb + i;
+            if (tok >= p.n)
+                continue;
+            float *dst = p.partial + ((long long)part * p.n + tok) * pitch + rg0 * kRowsPerGroup + 4 * g;
+#pragma unroll
+            for (int r = 0; r < RG; ++r)
+                if (rg0 + r < p.RG)
+                    *reinterpret_cast<f32x4 *>(dst + r * kRowsPerGroup) = acc[r][tb];
+        }
+        return;
     }
 
     // Epilogue, one token block at a time through LDS, so that a wave writes
@@ -244,31 +305,72 @@ __global__ __launch_bounds__(256, (RG * TB <= 32 ? 2 : 1)) void nvfp4_fused_gemm
     }
 }
 
-template <int RG, int TB, int MODE>
-int launch_one(FusedGemmParams p, hipStream_t stream)
+template <int RG, int TB, int NB>
+int launch_one(FusedGemmParams p, int mode, hipStream_t stream)
 {
     p.tiles_x = (p.RG + 4 * RG - 1) / (4 * RG);
     p.tiles_y = (p.n + TB * 16 - 1) / (TB * 16);
-    const long long total = (long long)p.tiles_x * p.tiles_y;
+    const long long total = (long long)p.tiles_x * p.tiles_y * p.ks;
     if (total > INT32_MAX || (long long)p.T * RG * 1024 > INT32_MAX)
         return NVFP4_ERR_SHAPE;   // a wave's codes must stay within a 32-bit buffer offset
-    hipLaunchKernelGGL((nvfp4_fused_gemm_kernel<RG, TB, MODE>), dim3((unsigned)total), dim3(256), 0, stream, p);
+    auto k = mode == 0 ? nvfp4_fused_gemm_kernel<RG, TB, NB, 0>
+                       : (mode == 1 ? nvfp4_fused_gemm_kernel<RG, TB, NB, 1> : nvfp4_fused_gemm_kernel<RG, TB, NB, 2>);
+    hipLaunchKernelGGL(k, dim3((unsigned)total), dim3(256), 0, stream, p);
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
 }
 
-template <int MODE>
-int launch_mode(const FusedGemmParams &p, hipStream_t stream)
-{
-    if (p.n <= 32)
-        return launch_one<2, 2, MODE>(p, stream);
-    if (p.n <= 64)
-        return launch_one<2, 4, MODE>(p, stream);
-    return launch_one<4, 8, MODE>(p, stream);
-}
+// Tile shapes: row groups a wave, token blocks, and what a step of one
+// workgroup costs (ns) with one workgroup on its compute unit and with `full`
+// of them there (per workgroup).
+struct Tile {
+    int rg, tb, full;
+    int alone, shared;
+};
+constexpr Tile kTiles[] = {
+    {2, 2, 2, 900, 500},
+    {2, 4, 2, 1000, 600},
+    {4, 8, 2, 2440, 1750},
+};
 
 }  // namespace
 
-int nvfp4_launch_fused_gemm(const nvfp4_fused_gemm_args &a, hipStream_t stream)
+nvfp4_fused_gemm_plan nvfp4_plan_fused_gemm(int n, int row_groups, int K)
+{
+    const int T = (int)k_tiles(K);
+    nvfp4_fused_gemm_plan best = {};
+    double best_cost = -1;
+    for (int c = 0; c < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++c) {
+        const Tile &t = kTiles[c];
+        if (t.tb > 2 && n <= 8 * t.tb)
+            continue;   // a smaller token tile holds them
+        const long long tiles = (long long)((row_groups + 4 * t.rg - 1) / (4 * t.rg)) * ((n + 16 * t.tb - 1) / (16 * t.tb));
+        for (int ks = 1; ks <= 16; ++ks) {
+            const int tp = (T + ks - 1) / ks;
+            if (ks > 1 && (tp < 4 || (long long)(ks - 1) * tp >= T))
+                continue;
+            const long long units = tiles * ks, slots = 256LL * t.full;
+            const long long rest = units % slots;
+            const int r = (int)((rest + 255) / 256);
+            double cost = (double)(units / slots) * t.full * t.shared;
+            if (r == 1)
+                cost += t.alone;
+            else
+                cost += (double)r * t.shared;
+            cost = cost * tp + 3000;
+            if (ks > 1)
+                cost += 3000 + (double)ks * n * row_groups * 16 * 8 / 5500;
+            if (best_cost < 0 || cost < best_cost) {
+                best_cost = cost;
+                best.tile = c;
+                best.ks = ks;
+                best.tp = tp;
+            }
+        }
+    }
+    return best;
+}
+
+int nvfp4_launch_fused_gemm(const nvfp4_fused_gemm_args &a, const nvfp4_fused_gemm_plan &plan, hipStream_t stream)
 {
     int cus = 0;
     const int st = nvfp4_device_cus(&cus);
@@ -284,9 +386,12 @@ int nvfp4_launch_fused_gemm(const nvfp4_fused_gemm_args &a, hipStream_t stream)
     p.T = (int)k_tiles(a.K);
     p.RG = a.row_groups;
     p.e = a.epi;
-    switch (a.mode) {
-    case 0: return launch_mode<0>(p, stream);
-    case 1: return launch_mode<1>(p, stream);
-    default: return launch_mode<2>(p, stream);
+    p.ks = plan.ks;
+    p.tp = plan.tp;
+    p.partial = a.partial;
+    switch (plan.tile) {
+    case 0: return launch_one<2, 2, 3>(p, a.mode, stream);
+    case 1: return launch_one<2, 4, 3>(p, a.mode, stream);
+    default: return launch_one<4, 8, 2>(p, a.mode, stream);
     }
 }

@@ -47,7 +47,8 @@ _SIGNATURES = {
     "nvfp4_transposed_codes_bytes": (_SIZE, [_i32, _i32]),
     "nvfp4_transposed_scales_bytes": (_SIZE, [_i32, _i32]),
     "nvfp4_pack_transposed": (_i32, [_vp, _vp, _i32, _i32, _vp, _vp, _vp]),
-    "nvfp4_gemm_t": (_i32, [_vp, _vp, _F32, _vp, _i64, _vp, _i64, _i32, _i32, _i32, _vp]),
+    "nvfp4_gemm_t": (_i32, [_vp, _vp, _F32, _vp, _i64, _vp, _i64, _i32, _i32, _i32, _vp, _SIZE, _vp]),
+    "nvfp4_gemm_t_workspace_bytes": (_SIZE, [_i32, _i32, _i32]),
     "nvfp4_linear_grad": (_i32, [_vp, _i32, _i64, _vp, _i64, _i32, _vp, _i64, _vp, _i32, _i32, _i32, _vp, _SIZE, _vp]),
     "nvfp4_gated_grad": (_i32, [_vp, _i32, _i64, _vp, _i64, _i32, _F32, _F32, _vp, _i64, _vp, _vp, _i32, _i32, _i32,
                                 _vp, _SIZE, _vp]),
@@ -401,8 +402,9 @@ def _incoming(dY, n, N, name):
 def _gemm_t_launch(wt, dZ, out, run):
     n = dZ.shape[0]
     dX = out if out is not None else run.alloc(n, wt.K, dtype=torch.bfloat16)
+    ws, size, keep = run.workspace(None, int(_call("nvfp4_gemm_t_workspace_bytes")(n, wt.N, wt.K)))
     _check(_call("nvfp4_gemm_t")(wt.codes.data_ptr(), wt.scales.data_ptr(), wt.gscale, dZ.data_ptr(), _ld(dZ),
-                                 dX.data_ptr(), _ld(dX), n, wt.N, wt.K, run.handle), "nvfp4_gemm_t")
+                                 dX.data_ptr(), _ld(dX), n, wt.N, wt.K, ws, size, run.handle), "nvfp4_gemm_t")
     return dX
 
 

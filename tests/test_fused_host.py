@@ -74,7 +74,7 @@ def test_long_rows_need_a_workspace():
     assert linear(K=8208) == WORKSPACE
     assert linear(K=8208, work=at(7), size=need - 1) == WORKSPACE
     assert linear(K=8208, work=at(7) + 4, size=need) == ALIGN
-    assert fused._call("nvfp4_linear_workspace_bytes")(17, 64, 8208) == 0
+    assert linear(n=17, K=8208) == WORKSPACE        # many columns for one row tile: K parts here too
     assert fused._call("nvfp4_linear_workspace_bytes")(4, 64, 8192) == 0
     rows = nv.gated_rows(50)
     assert rows == 128
@@ -100,7 +100,7 @@ def test_gemm_t_refuses(kw, status):
     if a["ldx"] is None:
         a["ldx"] = a["K"]
     assert fused._call("nvfp4_gemm_t")(a["c"], a["s"], 1.0, a["dy"], a["ldy"], a["dx"], a["ldx"], a["n"], a["N"],
-                                       a["K"], None) == status
+                                       a["K"], None, 0, None) == status
 
 
 @pytest.mark.parametrize("kw,status", [
