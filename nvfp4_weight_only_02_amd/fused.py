@@ -17,23 +17,23 @@ it, so that memory freed by the caller is not reused while the launch reads it.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
+import struct
 from dataclasses import dataclass
 
 import torch
 
-from . import PackedWeight, _check, _dev, _i32, _i64, _stream, _vp, lib, packed_codes_bytes, packed_scales_bytes
+from . import (Nvfp4Error, PackedWeight, _dev, _i32, _i64, _vp, check_devices, lib, packed_codes_bytes,
+               packed_scales_bytes)
 
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
-class _Epilogue(ctypes.Structure):
-    _fields_ = [("bias", _vp), ("up_bias", _vp), ("residual", _vp), ("preact", _vp), ("ldr", _i64), ("ldp", _i64),
-                ("activation", ctypes.c_int32), ("bias_dtype", ctypes.c_int32),
-                ("residual_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
-
+# nvfp4_epilogue: bias, up_bias, residual, preact, ldr, ldp, activation,
+# bias_dtype, residual_dtype, out_dtype
+_EPILOGUE = struct.Struct("@4P2q4i")
 
 _SIZE = ctypes.c_size_t
 _F32 = ctypes.c_float
@@ -56,11 +56,17 @@ _SIGNATURES = {
 }
 
 
+@functools.lru_cache(maxsize=None)
 def _call(name: str):
     f = getattr(lib(), name)
-    if f.argtypes is None:
-        f.restype, f.argtypes = _SIGNATURES[name]
+    f.restype, f.argtypes = _SIGNATURES[name]
     return f
+
+
+def _run(name: str, *args) -> None:
+    status = _call(name)(*args)
+    if status:
+        raise Nvfp4Error(status, name)
 
 
 # ---- checks, streams and memory ---------------------------------------------------
@@ -73,16 +79,21 @@ def _act(activation) -> int:
     return ACTIVATIONS[activation]
 
 
-def _mat(t, dtypes, name: str, n, cols) -> torch.Tensor:
-    """A device matrix of n rows (None: any) and cols columns, unit stride
-    along a row."""
+def _typed(t, dtypes, name: str) -> None:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA (HIP) tensor" % name)
     if t.dtype not in dtypes:
         raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
-    if t.dim() != 2 or t.shape[1] != cols or (n is not None and t.shape[0] != n):
-        raise ValueError("%s must be [%s, %d], got %s" % (name, "n" if n is None else n, cols, list(t.shape)))
-    if cols > 1 and t.shape[0] > 0 and t.stride(1) != 1:
+
+
+def _mat(t, dtypes, name: str, n, cols) -> torch.Tensor:
+    """A device matrix of n rows (None: any) and cols columns, unit stride
+    along a row."""
+    _typed(t, dtypes, name)
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols or (n is not None and shape[0] != n):
+        raise ValueError("%s must be [%s, %d], got %s" % (name, "n" if n is None else n, cols, list(shape)))
+    if cols > 1 and shape[0] > 0 and t.stride(1) != 1:
         raise ValueError("%s must have unit stride along a row" % name)
     return t
 
@@ -93,48 +104,54 @@ def _ld(t) -> int:
 
 
 def _vec(t, dtypes, name: str, size: int):
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError("%s must be a CUDA (HIP) tensor" % name)
-    if t.dtype not in dtypes:
-        raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
+    _typed(t, dtypes, name)
     if t.dim() != 1 or t.shape[0] != size or not t.is_contiguous():
         raise ValueError("%s must be a contiguous [%d]" % (name, size))
-    return t
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _ptr(t) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 class _Launch:
-    """The stream of a call and the memory rules of one that is not the
-    current stream."""
+    """The stream of a call, after checking that it and every tensor are on
+    the current device, and the memory rules of a stream that is not the
+    current one.  (With stream None the raw current stream is looked up: a
+    torch Stream object costs several times the rest of this.)"""
+    __slots__ = ("device", "handle", "stream", "current")
 
     def __init__(self, stream, *tensors):
-        self.tensors = [t for t in tensors if t is not None]
-        self.handle = _stream(stream, *self.tensors)
-        current = torch.cuda.current_stream()
-        self.stream = stream if stream is not None else current
-        self.side = self.stream != current
-        self.current = current
-        for t in self.tensors if self.side else ():
-            t.record_stream(self.stream)
+        device = self.device = torch.cuda.current_device()
+        for t in tensors:
+            if t is not None and t.get_device() != device:
+                check_devices([t.device], device, torch.device("cuda", device))
+        self.stream = None
+        if stream is None:
+            self.handle = torch._C._cuda_getCurrentRawStream(device)
+            return
+        check_devices((), device, stream.device)
+        self.handle = stream.cuda_stream
+        self.current = torch.cuda.current_stream()
+        if stream != self.current:
+            self.stream = stream
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
 
     def alloc(self, *shape, dtype):
         """Memory of the launch's stream."""
-        with torch.cuda.stream(self.stream) if self.side else contextlib.nullcontext():
-            t = torch.empty(*shape, dtype=dtype, device="cuda")
-        if self.side:
-            t.record_stream(self.current)   # a result is read there
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device="cuda")
+        with torch.cuda.stream(self.stream):
+            t = torch.empty(shape, dtype=dtype, device="cuda")
+        t.record_stream(self.current)   # a result is read there
         return t
 
     def workspace(self, given, need: int):
         """(pointer, bytes, tensor) of `need` workspace bytes."""
         if given is None:
             if not need:
-                return None, 0, None
+                return 0, 0, None
             given = self.alloc(need, dtype=torch.uint8)
         return given.data_ptr(), given.numel(), given
 
@@ -153,11 +170,11 @@ class TransposedWeight:
 
 
 def _transpose(codes, scales, gscale, N, K, stream) -> TransposedWeight:
-    run = _Launch(stream, codes, scales)
-    ct = run.alloc(int(_call("nvfp4_transposed_codes_bytes")(N, K)), dtype=torch.uint8)
-    st = run.alloc(int(_call("nvfp4_transposed_scales_bytes")(N, K)), dtype=torch.uint8)
-    _check(_call("nvfp4_pack_transposed")(codes.data_ptr(), scales.data_ptr(), N, K, ct.data_ptr(), st.data_ptr(),
-                                          run.handle), "nvfp4_pack_transposed")
+    at = _Launch(stream, codes, scales)
+    ct = at.alloc(int(_call("nvfp4_transposed_codes_bytes")(N, K)), dtype=torch.uint8)
+    st = at.alloc(int(_call("nvfp4_transposed_scales_bytes")(N, K)), dtype=torch.uint8)
+    _run("nvfp4_pack_transposed", codes.data_ptr(), scales.data_ptr(), N, K, ct.data_ptr(), st.data_ptr(),
+         at.handle)
     return TransposedWeight(ct, st, gscale, N, K)
 
 
@@ -186,13 +203,13 @@ class GatedWeight:
     def from_packed(cls, gate: PackedWeight, up: PackedWeight, stream=None) -> "GatedWeight":
         if (gate.N, gate.K) != (up.N, up.K):
             raise ValueError("the gate and up weights must have one shape")
-        run = _Launch(stream, gate.codes, gate.scales, up.codes, up.scales)
+        at = _Launch(stream, gate.codes, gate.scales, up.codes, up.scales)
         rows = gated_rows(gate.N)
-        codes = run.alloc(packed_codes_bytes(rows, gate.K), dtype=torch.uint8)
-        scales = run.alloc(packed_scales_bytes(rows, gate.K), dtype=torch.uint8)
-        _check(_call("nvfp4_pack_gated")(gate.codes.data_ptr(), gate.scales.data_ptr(), up.codes.data_ptr(),
-                                         up.scales.data_ptr(), gate.N, gate.K, codes.data_ptr(), scales.data_ptr(),
-                                         run.handle), "nvfp4_pack_gated")
+        codes = at.alloc(packed_codes_bytes(rows, gate.K), dtype=torch.uint8)
+        scales = at.alloc(packed_scales_bytes(rows, gate.K), dtype=torch.uint8)
+        _run("nvfp4_pack_gated", gate.codes.data_ptr(), gate.scales.data_ptr(), up.codes.data_ptr(),
+             up.scales.data_ptr(), gate.N, gate.K, codes.data_ptr(), scales.data_ptr(),
+             at.handle)
         return cls(codes, scales, gate.gscale, up.gscale, gate.N, gate.K)
 
     @classmethod
@@ -209,11 +226,11 @@ class GatedWeight:
 
 # ---- forward -------------------------------------------------------------------------
 
-def _out(run, out, out_dtype, n, cols):
+def _out(at, out, out_dtype, n, cols):
     if out is None:
         if out_dtype not in _DTYPES:
             raise TypeError("out_dtype must be torch.bfloat16 or torch.float32, got %s" % out_dtype)
-        return run.alloc(n, cols, dtype=out_dtype)
+        return at.alloc(n, cols, dtype=out_dtype)
     if out.dtype != out_dtype:
         raise TypeError("out is %s, out_dtype %s" % (out.dtype, out_dtype))
     return out
@@ -221,29 +238,27 @@ def _out(run, out, out_dtype, n, cols):
 
 def _linear_forward(w, X, bias, act, residual, out, out_dtype, preact, workspace, stream):
     n = X.shape[0]
-    run = _Launch(stream, w.codes, w.scales, X, bias, residual, out, preact, workspace)
-    Y = _out(run, out, out_dtype, n, w.N)
-    ep = _Epilogue(_ptr(bias), None, _ptr(residual), _ptr(preact), _ld(residual) if residual is not None else 0,
-                   _ld(preact) if preact is not None else 0, act, _DTYPES[bias.dtype] if bias is not None else 1,
-                   _DTYPES[residual.dtype] if residual is not None else 1, _DTYPES[Y.dtype])
-    ws, size, keep = run.workspace(workspace, int(_call("nvfp4_linear_workspace_bytes")(n, w.N, w.K)))
-    _check(_call("nvfp4_linear")(w.codes.data_ptr(), w.scales.data_ptr(), w.gscale, X.data_ptr(), _ld(X),
-                                 Y.data_ptr(), _ld(Y), n, w.N, w.K, ctypes.byref(ep), ws, size, run.handle),
-           "nvfp4_linear")
+    at = _Launch(stream, w.codes, w.scales, X, bias, residual, out, preact, workspace)
+    Y = _out(at, out, out_dtype, n, w.N)
+    ep = _EPILOGUE.pack(_ptr(bias), 0, _ptr(residual), _ptr(preact), 0 if residual is None else _ld(residual),
+                        0 if preact is None else _ld(preact), act, 1 if bias is None else _DTYPES[bias.dtype],
+                        1 if residual is None else _DTYPES[residual.dtype], _DTYPES[Y.dtype])
+    ws, size, keep = at.workspace(workspace, int(_call("nvfp4_linear_workspace_bytes")(n, w.N, w.K)))
+    _run("nvfp4_linear", w.codes.data_ptr(), w.scales.data_ptr(), w.gscale, X.data_ptr(), _ld(X),
+         Y.data_ptr(), _ld(Y), n, w.N, w.K, ep, ws, size, at.handle)
     return Y
 
 
 def _gated_forward(w, X, act, gate_bias, up_bias, out, out_dtype, preact, workspace, stream):
     n = X.shape[0]
-    run = _Launch(stream, w.codes, w.scales, X, gate_bias, up_bias, out, preact, workspace)
-    H = _out(run, out, out_dtype, n, w.F)
+    at = _Launch(stream, w.codes, w.scales, X, gate_bias, up_bias, out, preact, workspace)
+    H = _out(at, out, out_dtype, n, w.F)
     some = gate_bias if gate_bias is not None else up_bias
-    ep = _Epilogue(_ptr(gate_bias), _ptr(up_bias), None, _ptr(preact), 0, _ld(preact) if preact is not None else 0,
-                   act, _DTYPES[some.dtype] if some is not None else 1, 1, _DTYPES[H.dtype])
-    ws, size, keep = run.workspace(workspace, int(_call("nvfp4_gated_workspace_bytes")(n, w.F, w.K)))
-    _check(_call("nvfp4_gated")(w.codes.data_ptr(), w.scales.data_ptr(), w.gate_gscale, w.up_gscale, X.data_ptr(),
-                                _ld(X), H.data_ptr(), _ld(H), n, w.F, w.K, ctypes.byref(ep), ws, size, run.handle),
-           "nvfp4_gated")
+    ep = _EPILOGUE.pack(_ptr(gate_bias), _ptr(up_bias), 0, _ptr(preact), 0, 0 if preact is None else _ld(preact), act,
+                        1 if some is None else _DTYPES[some.dtype], 1, _DTYPES[H.dtype])
+    ws, size, keep = at.workspace(workspace, int(_call("nvfp4_gated_workspace_bytes")(n, w.F, w.K)))
+    _run("nvfp4_gated", w.codes.data_ptr(), w.scales.data_ptr(), w.gate_gscale, w.up_gscale, X.data_ptr(),
+         _ld(X), H.data_ptr(), _ld(H), n, w.F, w.K, ep, ws, size, at.handle)
     return H
 
 
@@ -269,7 +284,11 @@ def _workspace_arg(workspace):
 
 
 def _wants_grad(*tensors) -> bool:
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return True
+    return False
 
 
 def _check_grad(X, transposed, N, K, stream, *buffers):
@@ -342,7 +361,8 @@ def linear(w: PackedWeight, X: torch.Tensor, bias: torch.Tensor = None, activati
     act = _act(activation)
     _mat(X, (torch.bfloat16,), "X", None, w.K)
     n = X.shape[0]
-    _vec(bias, _FLOATS, "bias", w.N)
+    if bias is not None:
+        _vec(bias, _FLOATS, "bias", w.N)
     if residual is not None:
         _mat(residual, _FLOATS, "residual", n, w.N)
     if out is not None:
@@ -367,8 +387,9 @@ def gated(w: GatedWeight, X: torch.Tensor, activation: str = "silu", gate_bias: 
     act = _act(activation)
     _mat(X, (torch.bfloat16,), "X", None, w.K)
     n = X.shape[0]
-    _vec(gate_bias, _FLOATS, "gate_bias", w.F)
-    _vec(up_bias, _FLOATS, "up_bias", w.F)
+    for b, name in ((gate_bias, "gate_bias"), (up_bias, "up_bias")):
+        if b is not None:
+            _vec(b, _FLOATS, name, w.F)
     if gate_bias is not None and up_bias is not None and gate_bias.dtype != up_bias.dtype:
         raise TypeError("gate_bias and up_bias must have one dtype")
     if out is not None:
@@ -399,49 +420,47 @@ def _incoming(dY, n, N, name):
     return _mat(dY, _FLOATS, name, n, N)
 
 
-def _gemm_t_launch(wt, dZ, out, run):
+def _gemm_t_launch(wt, dZ, out, at):
     n = dZ.shape[0]
-    dX = out if out is not None else run.alloc(n, wt.K, dtype=torch.bfloat16)
-    ws, size, keep = run.workspace(None, int(_call("nvfp4_gemm_t_workspace_bytes")(n, wt.N, wt.K)))
-    _check(_call("nvfp4_gemm_t")(wt.codes.data_ptr(), wt.scales.data_ptr(), wt.gscale, dZ.data_ptr(), _ld(dZ),
-                                 dX.data_ptr(), _ld(dX), n, wt.N, wt.K, ws, size, run.handle), "nvfp4_gemm_t")
+    dX = out if out is not None else at.alloc(n, wt.K, dtype=torch.bfloat16)
+    ws, size, keep = at.workspace(None, int(_call("nvfp4_gemm_t_workspace_bytes")(n, wt.N, wt.K)))
+    _run("nvfp4_gemm_t", wt.codes.data_ptr(), wt.scales.data_ptr(), wt.gscale, dZ.data_ptr(), _ld(dZ),
+         dX.data_ptr(), _ld(dX), n, wt.N, wt.K, ws, size, at.handle)
     return dX
 
 
 def _linear_backward(wt, dY, act, preact, bias_dtype, out, stream):
     dY = _incoming(dY, None, wt.N if wt is not None else dY.shape[-1], "dY")
     n, N = dY.shape
-    run = _Launch(stream, dY, preact, out, *((wt.codes, wt.scales) if wt is not None else ()))
-    db = run.alloc(N, dtype=bias_dtype) if bias_dtype is not None else None
+    at = _Launch(stream, dY, preact, out, *((wt.codes, wt.scales) if wt is not None else ()))
+    db = at.alloc(N, dtype=bias_dtype) if bias_dtype is not None else None
     dZ = None
     if wt is not None and (act or not _rows_ok(dY)):
-        dZ = run.alloc(n, _pad8(N), dtype=torch.bfloat16)
+        dZ = at.alloc(n, _pad8(N), dtype=torch.bfloat16)
     if db is not None or dZ is not None:
         need = int(_call("nvfp4_grad_workspace_bytes")(n, N, 0)) if db is not None else 0
-        ws, size, keep = run.workspace(None, need)
-        _check(_call("nvfp4_linear_grad")(dY.data_ptr(), _DTYPES[dY.dtype], _ld(dY), _ptr(preact),
-                                          _ld(preact) if preact is not None else 0, act, _ptr(dZ), _pad8(N), _ptr(db),
-                                          _DTYPES[bias_dtype] if db is not None else 1, n, N, ws, size, run.handle),
-               "nvfp4_linear_grad")
-    dX = _gemm_t_launch(wt, dY if dZ is None else dZ, out, run) if wt is not None else None
+        ws, size, keep = at.workspace(None, need)
+        _run("nvfp4_linear_grad", dY.data_ptr(), _DTYPES[dY.dtype], _ld(dY), _ptr(preact),
+             _ld(preact) if preact is not None else 0, act, _ptr(dZ), _pad8(N), _ptr(db),
+             _DTYPES[bias_dtype] if db is not None else 1, n, N, ws, size, at.handle)
+    dX = _gemm_t_launch(wt, dY if dZ is None else dZ, out, at) if wt is not None else None
     return dX, db
 
 
 def _gated_backward(w, wt, dH, act, preact, gate_dtype, up_dtype, out, stream):
     dH = _incoming(dH, None, w.F, "dH")
     n, rows = dH.shape[0], gated_rows(w.F)
-    run = _Launch(stream, dH, preact, out, *((wt.codes, wt.scales) if wt is not None else ()))
-    dg = run.alloc(w.F, dtype=gate_dtype) if gate_dtype is not None else None
-    du = run.alloc(w.F, dtype=up_dtype) if up_dtype is not None else None
-    dZ = run.alloc(n, rows, dtype=torch.bfloat16) if wt is not None else None
+    at = _Launch(stream, dH, preact, out, *((wt.codes, wt.scales) if wt is not None else ()))
+    dg = at.alloc(w.F, dtype=gate_dtype) if gate_dtype is not None else None
+    du = at.alloc(w.F, dtype=up_dtype) if up_dtype is not None else None
+    dZ = at.alloc(n, rows, dtype=torch.bfloat16) if wt is not None else None
     some = gate_dtype if gate_dtype is not None else up_dtype
     need = int(_call("nvfp4_grad_workspace_bytes")(n, w.F, 1)) if some is not None else 0
-    ws, size, keep = run.workspace(None, need)
-    _check(_call("nvfp4_gated_grad")(dH.data_ptr(), _DTYPES[dH.dtype], _ld(dH), preact.data_ptr(), _ld(preact), act,
-                                     w.gate_gscale, w.up_gscale, _ptr(dZ), rows, _ptr(dg), _ptr(du),
-                                     _DTYPES[some] if some is not None else 1, n, w.F, ws, size, run.handle),
-           "nvfp4_gated_grad")
-    dX = _gemm_t_launch(wt, dZ, out, run) if wt is not None else None
+    ws, size, keep = at.workspace(None, need)
+    _run("nvfp4_gated_grad", dH.data_ptr(), _DTYPES[dH.dtype], _ld(dH), preact.data_ptr(), _ld(preact), act,
+         w.gate_gscale, w.up_gscale, _ptr(dZ), rows, _ptr(dg), _ptr(du),
+         _DTYPES[some] if some is not None else 1, n, w.F, ws, size, at.handle)
+    dX = _gemm_t_launch(wt, dZ, out, at) if wt is not None else None
     return dX, dg, du
 
 

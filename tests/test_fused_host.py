@@ -1,7 +1,5 @@
 """Argument checks and host functions of the fused operators, no GPU: every
 refusal comes before any HIP call."""
-import ctypes
-
 import numpy as np
 import pytest
 
@@ -18,22 +16,22 @@ def at(i):
 
 
 def epilogue(**kw):
-    base = dict(bias=None, up_bias=None, residual=None, preact=None, ldr=0, ldp=0, activation=0, bias_dtype=1,
-                residual_dtype=1, out_dtype=1)
+    base = dict(bias=0, up_bias=0, residual=0, preact=0, ldr=0, ldp=0, activation=0, bias_dtype=1, residual_dtype=1,
+                out_dtype=1)
     base.update(kw)
-    return fused._Epilogue(*[base[f] for f, _ in fused._Epilogue._fields_])
+    return fused._EPILOGUE.pack(*base.values())
 
 
 def linear(wq=at(0), ws=at(1), x=at(2), ldx=None, y=at(3), ldy=None, n=4, N=64, K=256, ep=None, work=None, size=0):
     ep = ep if ep is not None else epilogue()
     return fused._call("nvfp4_linear")(wq, ws, 1.0, x, K if ldx is None else ldx, y, N if ldy is None else ldy, n, N,
-                                       K, ctypes.byref(ep) if ep != 0 else None, work, size, None)
+                                       K, ep if ep != 0 else None, work, size, None)
 
 
 def gated(x=at(2), ldx=None, h=at(3), ldh=None, n=4, F=64, K=256, ep=None, work=None, size=0):
     ep = ep if ep is not None else epilogue()
     return fused._call("nvfp4_gated")(at(0), at(1), 1.0, 1.0, x, K if ldx is None else ldx, h,
-                                      F if ldh is None else ldh, n, F, K, ctypes.byref(ep), work, size, None)
+                                      F if ldh is None else ldh, n, F, K, ep, work, size, None)
 
 
 @pytest.mark.parametrize("kw,status", [
