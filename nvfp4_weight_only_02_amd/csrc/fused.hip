@@ -230,8 +230,16 @@ __global__ __launch_bounds__(256) void nvfp4_grad_sum_kernel(GradParams p, int b
     if (col >= p.N)
         return;
     float s = 0.f;
-    for (int y = 0; y < blocks; ++y)
-        s += p.partial[((long long)y * halves + h) * p.cols + col];
+    constexpr int kBatch = 8;   // loads in flight together
+    for (int y0 = 0; y0 < blocks; y0 += kBatch) {
+        float v[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+            v[j] = y0 + j < blocks ? p.partial[((long long)(y0 + j) * halves + h) * p.cols + col] : 0.f;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+            s += v[j];
+    }
     store_db(p, h, col, s);
 }
 

@@ -21,26 +21,26 @@ struct FusedGemmParams {
 
 constexpr int kQuad = 4 * kTileK * 2 + 64;   // LDS bytes of four tokens' 128 columns, padded (see below)
 
-// Exact bf16 of the 8 weights of one lane of a transposed tile, dword `w` of
-// its codes: two blocks of 4 contracted rows, each row with its own E4M3 scale
-// (bytes of s0 and s1).
-__device__ __forceinline__ u32x4 dequant_rows(u32 w, u32 s0, u32 s1)
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// Exact bf16 (an E2M1 code times an E4M3 scale has at most 6 significant bits)
+// of the codes in half H of w: 2 bytes, low nibble first, scales s.
+template <int H>
+__device__ __forceinline__ u32x2 dequant4(u32 w, f32x2 sa, f32x2 sb)
 {
-    typedef float f32x2 __attribute__((ext_vector_type(2)));
-    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
-    const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
-    const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
-    const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
-    const auto sa = __builtin_amdgcn_cvt_pk_f32_fp8((int)s0, false);
-    const auto sb = __builtin_amdgcn_cvt_pk_f32_fp8((int)s0, true);
-    const auto sc = __builtin_amdgcn_cvt_pk_f32_fp8((int)s1, false);
-    const auto sd = __builtin_amdgcn_cvt_pk_f32_fp8((int)s1, true);
-    const bf16x2 o0 = {(__bf16)(a[0] * sa[0]), (__bf16)(a[1] * sa[1])};
-    const bf16x2 o1 = {(__bf16)(b[0] * sb[0]), (__bf16)(b[1] * sb[1])};
-    const bf16x2 o2 = {(__bf16)(c[0] * sc[0]), (__bf16)(c[1] * sc[1])};
-    const bf16x2 o3 = {(__bf16)(d[0] * sd[0]), (__bf16)(d[1] * sd[1])};
-    return u32x4{__builtin_bit_cast(u32, o0), __builtin_bit_cast(u32, o1), __builtin_bit_cast(u32, o2),
-                 __builtin_bit_cast(u32, o3)};
+    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2 * H);
+    const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2 * H + 1);
+    const bf16x2 x = {(__bf16)(a[0] * sa[0]), (__bf16)(a[1] * sa[1])};
+    const bf16x2 y = {(__bf16)(b[0] * sb[0]), (__bf16)(b[1] * sb[1])};
+    return u32x2{__builtin_bit_cast(u32, x), __builtin_bit_cast(u32, y)};
+}
+
+template <bool H>
+__device__ __forceinline__ f32x2 scales2(u32 w)
+{
+    const auto s = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, H);
+    return f32x2{s[0], s[1]};
 }
 
 // LDS-direct load: lane l's 16 bytes go to `lds` + 16 l (a wave-uniform LDS
@@ -76,11 +76,19 @@ __device__ __forceinline__ unsigned lds_address(const void *p)
 //
 // LDS layout of the slice: token t's 16-byte chunk c (8 columns) at
 //     (t / 4) * kQuad + (t % 4) * 256 + (c ^ (t % 4)) * 16.
-// An operand is two 8-byte pieces, columns 32j + 4g and 32j + 16 + 4g, of 16
-// tokens a read; the XOR and the 64 bytes between quads put the 16 tokens in
-// 16 different 16-byte slots of the 256-byte bank row, and leave the step j
-// and the token block as constant offsets.  A quad is 1 KiB of consecutive
-// LDS, one LDS-direct load of a wave.
+// An operand is a chunk of 32 tokens; the XOR and the 64 bytes between quads
+// put 16 of them in 16 different 16-byte slots of the 256-byte bank row, and
+// leave the substep and the token block as constant offsets.  A quad is 1 KiB
+// of consecutive LDS, one LDS-direct load of a wave.
+//
+// The MFMA is v_mfma_f32_32x32x16_bf16 (rows x tokens): two row groups fill
+// its 32 rows.  A code tile's lane (i, g) holds row i's columns 16b + 4g + e;
+// one v_permlane16_swap a code dword of two row groups gives every lane (row
+// 16 (g % 2) + i, half h = g / 2) the columns 16b + 8h + 0 .. 3 in one dword
+// and + 4 .. 7 in the other: the 8 consecutive columns of a chunk, so that the
+// tokens' operand is one 16-byte read.  Against the 16-row form (whose operand
+// is two 8-byte reads) it halves the MFMA and LDS instructions that the
+// dequantisation has to share the issue slots with.
 template <int RG, int TB, int NB, int MODE>
 __global__ __launch_bounds__(256, 2) void nvfp4_fused_gemm_kernel(FusedGemmParams p)
 {
@@ -166,37 +174,62 @@ __global__ __launch_bounds__(256, 2) void nvfp4_fused_gemm_kernel(FusedGemmParam
         __syncthreads();
     };
 
-    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-    f32x4 acc[RG][TB];
+    constexpr int RP = RG / 2, TP = TB / 2;   // 32-row and 32-token blocks
+    f32x16 acc[RP][TP];
 #pragma unroll
-    for (int r = 0; r < RG; ++r)
+    for (int r = 0; r < RP; ++r)
 #pragma unroll
-        for (int tb = 0; tb < TB; ++tb)
-            acc[r][tb] = zero;
+        for (int t = 0; t < TP; ++t)
+#pragma unroll
+            for (int v = 0; v < 16; ++v)
+                acc[r][t][v] = 0.f;
 
-    const int xa = (i >> 2) * kQuad + (i & 3) * 256 + 8 * (g & 1);
-    const int x0 = xa + ((g >> 1) ^ (i & 3)) * 16, x1 = xa + (((g >> 1) | 2) ^ (i & 3)) * 16;
-    const int sa = kSlice + wave * RG * 128 + (MODE == 2 ? g * 32 : i * 8);
+    const int h = lane >> 5, tl = lane & 31;   // column half, token of the operand
+    const int xa = (tl >> 2) * kQuad + (tl & 3) * 256;
+    const int x0 = xa + (h ^ (tl & 3)) * 16, x1 = xa + ((h | 2) ^ (tl & 3)) * 16;
+    const int sa = kSlice + wave * RG * 128 + (g & 1) * 128 + (MODE == 2 ? h * 64 : i * 8);
 
     auto compute = [&](int b, const u32x4 *c) {
         const char *buf = lds[b];
-        u32x2 sw[RG];
+        u32 lo[RP][4], hi[RP][4];   // columns 8h + 0..3 and 4..7 of each block
+#pragma unroll
+        for (int r = 0; r < RP; ++r)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const auto q = __builtin_amdgcn_permlane16_swap(c[2 * r][j], c[2 * r + 1][j], false, false);
+                lo[r][j] = q[0];
+                hi[r][j] = q[1];
+            }
+        u32x2 sw[RP];
         if constexpr (MODE != 2) {
 #pragma unroll
-            for (int r = 0; r < RG; ++r)
-                sw[r] = *reinterpret_cast<const u32x2 *>(buf + sa + r * 128);
+            for (int r = 0; r < RP; ++r)
+                sw[r] = *reinterpret_cast<const u32x2 *>(buf + sa + r * 256);
         }
-        bf16x8 w[2][RG];
+        bf16x8 w[2][RP][2];   // of substep j: blocks 2j and 2j + 1
         auto dequant = [&](auto jc, int q) {
             constexpr int j = decltype(jc)::value;
 #pragma unroll
-            for (int r = 0; r < RG; ++r) {
+            for (int r = 0; r < RP; ++r) {
+                u32x2 l0, l1, h0, h1;
                 if constexpr (MODE == 2) {
-                    const u32x2 sv = *reinterpret_cast<const u32x2 *>(buf + sa + r * 128 + 8 * j);
-                    w[q][r] = __builtin_bit_cast(bf16x8, dequant_rows(c[r][j], sv[0], sv[1]));
+                    // a scale for each contracted row: of columns 8h + 0..3, and 4..7
+                    const u32x2 s = *reinterpret_cast<const u32x2 *>(buf + sa + r * 256 + 8 * j);
+                    const u32x2 t = *reinterpret_cast<const u32x2 *>(buf + sa + r * 256 + 8 * j + 32);
+                    l0 = dequant4<0>(lo[r][j], scales2<false>(s[0]), scales2<true>(s[0]));
+                    h0 = dequant4<0>(hi[r][j], scales2<false>(t[0]), scales2<true>(t[0]));
+                    l1 = dequant4<1>(lo[r][j], scales2<false>(s[1]), scales2<true>(s[1]));
+                    h1 = dequant4<1>(hi[r][j], scales2<false>(t[1]), scales2<true>(t[1]));
                 } else {
-                    w[q][r] = __builtin_bit_cast(bf16x8, dequant_pair<(j & 1) != 0>(c[r][j], sw[r][j >> 1]));
+                    const f32x2 s = scales2<(j & 1) != 0>(sw[r][j >> 1]);   // of blocks 2j and 2j + 1
+                    const f32x2 s0 = {s[0], s[0]}, s1 = {s[1], s[1]};
+                    l0 = dequant4<0>(lo[r][j], s0, s0);
+                    h0 = dequant4<0>(hi[r][j], s0, s0);
+                    l1 = dequant4<1>(lo[r][j], s1, s1);
+                    h1 = dequant4<1>(hi[r][j], s1, s1);
                 }
+                w[q][r][0] = __builtin_bit_cast(bf16x8, u32x4{l0[0], l0[1], h0[0], h0[1]});
+                w[q][r][1] = __builtin_bit_cast(bf16x8, u32x4{l1[0], l1[1], h1[0], h1[1]});
             }
         };
         dequant(std::integral_constant<int, 0>{}, 0);
@@ -205,13 +238,15 @@ __global__ __launch_bounds__(256, 2) void nvfp4_fused_gemm_kernel(FusedGemmParam
             if constexpr (j < 3)
                 dequant(std::integral_constant<int, j + 1>{}, (j + 1) & 1);
 #pragma unroll
-            for (int tb = 0; tb < TB; ++tb) {
-                const u32x2 lo = *reinterpret_cast<const u32x2 *>(buf + x0 + tb * 4 * kQuad + 64 * j);
-                const u32x2 hi = *reinterpret_cast<const u32x2 *>(buf + x1 + tb * 4 * kQuad + 64 * j);
-                const bf16x8 x = __builtin_bit_cast(bf16x8, u32x4{lo[0], lo[1], hi[0], hi[1]});
+            for (int t = 0; t < TP; ++t) {
+                const bf16x8 a = *reinterpret_cast<const bf16x8 *>(buf + x0 + t * 8 * kQuad + 64 * j);
+                const bf16x8 d = *reinterpret_cast<const bf16x8 *>(buf + x1 + t * 8 * kQuad + 64 * j);
 #pragma unroll
-                for (int r = 0; r < RG; ++r)
-                    acc[r][tb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j & 1][r], x, acc[r][tb], 0, 0, 0);
+                for (int r = 0; r < RP; ++r)
+                    acc[r][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j & 1][r][0], a, acc[r][t], 0, 0, 0);
+#pragma unroll
+                for (int r = 0; r < RP; ++r)
+                    acc[r][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j & 1][r][1], d, acc[r][t], 0, 0, 0);
             }
             __builtin_amdgcn_sched_barrier(0);   // one substep's operands live at a time
         });
@@ -249,49 +284,60 @@ __global__ __launch_bounds__(256, 2) void nvfp4_fused_gemm_kernel(FusedGemmParam
         }
     }
 
+    // Components 4q .. 4q + 3 of acc[r][t]: weight rows 8q + 4h .. + 3 of the
+    // 32 of row pair r, token 32 t + lane % 32.
+    auto sums = [&](const f32x16 &c, auto qc) {
+        constexpr int q = 4 * decltype(qc)::value;
+        return f32x4{c[q], c[q + 1], c[q + 2], c[q + 3]};
+    };
+
     // A K part stores its sums as they are: nvfp4_fused_reduce_kernel adds the
     // parts in order and runs the epilogue.
     if (p.ks > 1) {
         const int pitch = p.RG * kRowsPerGroup;
 #pragma unroll
-        for (int tb = 0; tb < TB; ++tb) {
-            const int tok = tok0 + 16 * tb + i;
+        for (int t = 0; t < TP; ++t) {
+            const int tok = tok0 + 32 * t + tl;
             if (tok >= p.n)
                 continue;
-            float *dst = p.partial + ((long long)part * p.n + tok) * pitch + rg0 * kRowsPerGroup + 4 * g;
+            float *dst = p.partial + ((long long)part * p.n + tok) * pitch + rg0 * kRowsPerGroup + 4 * h;
 #pragma unroll
-            for (int r = 0; r < RG; ++r)
-                if (rg0 + r < p.RG)
-                    *reinterpret_cast<f32x4 *>(dst + r * kRowsPerGroup) = acc[r][tb];
+            for (int r = 0; r < RP; ++r)
+                static_for<4>([&](auto qc) {
+                    constexpr int q = decltype(qc)::value;
+                    if (rg0 + 2 * r + q / 2 < p.RG)
+                        *reinterpret_cast<f32x4 *>(dst + r * 32 + 8 * q) = sums(acc[r][t], qc);
+                });
         }
         return;
     }
 
     // Epilogue, one token block at a time through LDS, so that a wave writes
     // whole lines of consecutive outputs and the epilogue's code exists once.
-    // Component v of lane (g, i) of acc[r][tb]: weight row 16*(rg0 + r) + 4g + v
-    // of token tok0 + 16*tb + i.
     constexpr int kRows = 64 * RG, kPitch = kRows + 4;
     constexpr int kOuts = MODE == 1 ? kRows / 2 : kRows;   // outputs a token
-    static_assert(16 * kPitch * 4 <= sizeof(lds), "the staged block fits the slice's LDS");
+    static_assert(32 * kPitch * 4 <= sizeof(lds), "the staged block fits the slice's LDS");
     float *stage = reinterpret_cast<float *>(lds);
     const int out0 = tx * kOuts;
 #pragma unroll 1
-    for (int b = 0; b < TB && tok0 + 16 * b < p.n; ++b) {
+    for (int b = 0; b < TP && tok0 + 32 * b < p.n; ++b) {
         __syncthreads();
-        static_for<TB>([&](auto tc) {
-            constexpr int tb = decltype(tc)::value;
-            if (tb == b) {
+        static_for<TP>([&](auto tc) {
+            constexpr int t = decltype(tc)::value;
+            if (t == b) {
 #pragma unroll
-                for (int r = 0; r < RG; ++r)
-                    *reinterpret_cast<f32x4 *>(stage + i * kPitch + (wave * RG + r) * 16 + 4 * g) = acc[r][tb];
+                for (int r = 0; r < RP; ++r)
+                    static_for<4>([&](auto qc) {
+                        *reinterpret_cast<f32x4 *>(stage + tl * kPitch + (wave * RG + 2 * r) * 16 + 8 * decltype(qc)::value +
+                                                   4 * h) = sums(acc[r][t], qc);
+                    });
             }
         });
         __syncthreads();
 #pragma unroll 1
-        for (int q = tid * 4; q < 16 * kOuts; q += 1024) {
+        for (int q = tid * 4; q < 32 * kOuts; q += 1024) {
             const int t = q / kOuts, o = q % kOuts;
-            const int tok = tok0 + 16 * b + t;
+            const int tok = tok0 + 32 * b + t;
             if (tok >= p.n)
                 break;
             if constexpr (MODE == 1) {
