@@ -68,10 +68,11 @@ __device__ __forceinline__ unsigned lds_address(const void *p)
 // One workgroup: 4 waves x RG row groups (64 * RG weight rows) times 16 * TB
 // tokens, over the steps of one K part.  A step covers 128 contracted columns:
 // the tokens' slice and the scales go straight to LDS, each wave turns its own
-// code tiles into MFMA operands in registers.  NB LDS buffers: the loads of
-// step s + NB - 1 are issued before step s is computed.  With two buffers the
-// codes are loaded into registers (LDS would leave room for one workgroup a
-// compute unit only), with more they go through LDS too.  MODE: 0 linear, 1
+// code tiles into MFMA operands in registers.  The loads of step s + 1 are
+// issued before step s is computed and waited for after it: two LDS buffers,
+// which leave room for two workgroups a compute unit at the largest tile (a
+// third buffer, with the codes through LDS as well, measured no faster at 17 ..
+// 64 tokens: 16384 x 5120, n = 24: 17.0 against 16.8 us).  MODE: 0 linear, 1
 // gated (row groups alternate gate, up), 2 transposed weight, plain output.
 //
 // LDS layout of the slice: token t's 16-byte chunk c (8 columns) at
@@ -89,17 +90,13 @@ __device__ __forceinline__ unsigned lds_address(const void *p)
 // tokens' operand is one 16-byte read.  Against the 16-row form (whose operand
 // is two 8-byte reads) it halves the MFMA and LDS instructions that the
 // dequantisation has to share the issue slots with.
-template <int RG, int TB, int NB, int MODE>
+template <int RG, int TB, int MODE>
 __global__ __launch_bounds__(256, 2) void nvfp4_fused_gemm_kernel(FusedGemmParams p)
 {
     constexpr int BM = TB * 16;
-    constexpr bool kLdsCodes = NB > 2;
     constexpr int kSlice = BM / 4 * kQuad;         // LDS bytes of a step's token slice
-    constexpr int kCodes = kSlice + 4 * RG * 128;  // after the waves' scales
-    constexpr int kBuf = kCodes + (kLdsCodes ? 4 * RG * 1024 : 0);
+    constexpr int kBuf = kSlice + 4 * RG * 128;    // and of the waves' scales
     constexpr int XL = TB;                         // quads a wave stages: BM / 4 / 4 waves
-    constexpr int kLoads = XL + 1 + RG;            // loads of a step and wave
-    static_assert((NB - 2) * kLoads <= 63, "vmcnt is a 6-bit field");
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -127,7 +124,7 @@ __global__ __launch_bounds__(256, 2) void nvfp4_fused_gemm_kernel(FusedGemmParam
     const int ntok = min(BM, p.n - tok0);
     const int nrg = max(0, min(RG, p.RG - rg0)), rgb = min(rg0, p.RG);
     const int s0 = part * p.tp, s1 = min(p.T, s0 + p.tp);
-    __shared__ __align__(1024) char lds[NB][kBuf];
+    __shared__ __align__(1024) char lds[2][kBuf];
 
     // Loads past these ranges (tokens beyond n, row groups beyond RG) read
     // zeros without touching memory.
@@ -140,37 +137,25 @@ __global__ __launch_bounds__(256, 2) void nvfp4_fused_gemm_kernel(FusedGemmParam
     const unsigned soff = (unsigned)((lane >> 3) * p.T * 128 + (lane & 7) * 16);
     const unsigned ldsb = lds_address(lds) + wave * XL * kQuad;
     const unsigned ldss = lds_address(lds) + kSlice + wave * RG * 128;
-    const unsigned ldsc = lds_address(lds) + kCodes + wave * RG * 1024;
 
     u32x4 cw[RG];
-    // Loads of step s into LDS buffer `b`.  Steps past the part read zeros
-    // (every step issues the same loads, so that the waits can count them).
     auto issue = [&](int s, int b) {
         const unsigned buf = b * kBuf;
-        const bool live = s < s1;
-        const unsigned xv = live && s * kTileK + xcol < p.K ? xoff : kOutOfRange;
+        const unsigned xv = s * kTileK + xcol < p.K ? xoff : kOutOfRange;
 #pragma unroll
         for (int u = 0; u < XL; ++u)
             load_lds_b128(xrsrc, xv, (unsigned)(u * 4 * ldx2 + s * 256), ldsb + buf + u * kQuad);
         if (lane < 8 * RG)   // the wave's 128 RG bytes of scales
-            load_lds_b128(srsrc, live ? soff : kOutOfRange, (unsigned)(s * 128), ldss + buf);
+            load_lds_b128(srsrc, soff, (unsigned)(s * 128), ldss + buf);
 #pragma unroll
-        for (int r = 0; r < RG; ++r) {
-            const unsigned at = (unsigned)((r * p.T + s) * 1024);
-            if constexpr (kLdsCodes)
-                load_lds_b128(crsrc, live ? (unsigned)(lane * 16) : kOutOfRange, at, ldsc + buf + r * 1024);
-            else
-                cw[r] = buffer_load_b128_s(crsrc, (unsigned)(lane * 16), at);
-        }
+        for (int r = 0; r < RG; ++r)
+            cw[r] = buffer_load_b128_s(crsrc, (unsigned)(lane * 16), (unsigned)((r * p.T + s) * 1024));
     };
-    // Wait for the oldest step in flight, of NB - 1.
     auto land = [&]() {
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NB - 2) * kLoads) : "memory");
-        if constexpr (!kLdsCodes) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
-            for (int r = 0; r < RG; ++r)
-                asm volatile("" : "+v"(cw[r]));
-        }
+        for (int r = 0; r < RG; ++r)
+            asm volatile("" : "+v"(cw[r]));
         __syncthreads();
     };
 
@@ -252,36 +237,18 @@ __global__ __launch_bounds__(256, 2) void nvfp4_fused_gemm_kernel(FusedGemmParam
         });
     };
 
-    if constexpr (kLdsCodes) {
-        static_for<NB - 1>([&](auto q) { issue(s0 + decltype(q)::value, decltype(q)::value); });
-        land();
-        int b = 0;
-        for (int s = s0; s < s1; ++s) {
-            const int free = b == 0 ? NB - 1 : b - 1;   // the buffer computed from in the last step
-            issue(s + NB - 1, free);
-            u32x4 c[RG];
+    issue(s0, 0);
+    land();
+    for (int s = s0; s < s1; ++s) {
+        const int b = (s - s0) & 1;
+        u32x4 c[RG];
 #pragma unroll
-            for (int r = 0; r < RG; ++r)
-                c[r] = *reinterpret_cast<const u32x4 *>(lds[b] + kCodes + (wave * RG + r) * 1024 + lane * 16);
-            compute(b, c);
-            land();
-            b = b == NB - 1 ? 0 : b + 1;
-        }
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing still writes LDS
-    } else {
-        issue(s0, 0);
+        for (int r = 0; r < RG; ++r)
+            c[r] = cw[r];
+        if (s + 1 < s1)
+            issue(s + 1, b ^ 1);
+        compute(b, c);
         land();
-        for (int s = s0; s < s1; ++s) {
-            const int b = (s - s0) & 1;
-            u32x4 c[RG];
-#pragma unroll
-            for (int r = 0; r < RG; ++r)
-                c[r] = cw[r];
-            if (s + 1 < s1)
-                issue(s + 1, b ^ 1);
-            compute(b, c);
-            land();
-        }
     }
 
     // Components 4q .. 4q + 3 of acc[r][t]: weight rows 8q + 4h .. + 3 of the
@@ -351,7 +318,7 @@ __global__ __launch_bounds__(256, 2) void nvfp4_fused_gemm_kernel(FusedGemmParam
     }
 }
 
-template <int RG, int TB, int NB>
+template <int RG, int TB>
 int launch_one(FusedGemmParams p, int mode, hipStream_t stream)
 {
     p.tiles_x = (p.RG + 4 * RG - 1) / (4 * RG);
@@ -359,27 +326,44 @@ int launch_one(FusedGemmParams p, int mode, hipStream_t stream)
     const long long total = (long long)p.tiles_x * p.tiles_y * p.ks;
     if (total > INT32_MAX || (long long)p.T * RG * 1024 > INT32_MAX)
         return NVFP4_ERR_SHAPE;   // a wave's codes must stay within a 32-bit buffer offset
-    auto k = mode == 0 ? nvfp4_fused_gemm_kernel<RG, TB, NB, 0>
-                       : (mode == 1 ? nvfp4_fused_gemm_kernel<RG, TB, NB, 1> : nvfp4_fused_gemm_kernel<RG, TB, NB, 2>);
+    auto k = mode == 0 ? nvfp4_fused_gemm_kernel<RG, TB, 0>
+                       : (mode == 1 ? nvfp4_fused_gemm_kernel<RG, TB, 1> : nvfp4_fused_gemm_kernel<RG, TB, 2>);
     hipLaunchKernelGGL(k, dim3((unsigned)total), dim3(256), 0, stream, p);
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
 }
 
-// Tile shapes: row groups a wave, token blocks, and what a step of one
-// workgroup costs (ns) with one workgroup on its compute unit and with `full`
-// of them there (per workgroup).
+// Tile shapes: row groups a wave, 16-token blocks, workgroups that fit a
+// compute unit, and what a step of a workgroup costs (ns) with one workgroup
+// on its unit and, per workgroup, with the unit full.
 struct Tile {
     int rg, tb, full;
-    int alone, shared;
+    double alone, shared;
 };
 constexpr Tile kTiles[] = {
-    {2, 2, 2, 900, 500},
-    {2, 4, 2, 1000, 600},
-    {4, 8, 2, 2440, 1750},
+    {2, 2, 4, 610, 357},     //  128 rows x  32 tokens
+    {2, 4, 4, 710, 482},     //  128 x  64
+    {2, 8, 2, 1130, 888},    //  128 x 128
+    {4, 4, 3, 1240, 946},    //  256 x  64
+    {4, 8, 2, 1780, 1540},   //  256 x 128
 };
+constexpr int kParts[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16};
+constexpr double kStartSteps = 2.2;     // a workgroup's start and epilogue, in steps
+constexpr double kTail = 0.8;           // uneven end of a grid of several rounds, in workgroups a unit
+constexpr double kReduceNs = 5000;      // second launch (3 us on the device, 5 with the host's part)
+constexpr double kReduceSumNs = 8.2e-4; // a partial sum written and read again
 
 }  // namespace
 
+// The tile and part count of least modelled time.  More parts or smaller tiles
+// fill the chip where the largest tile leaves units idle, larger tiles
+// dequantise a weight for more tokens, fewer parts write fewer partial sums.
+// The constants were fitted to 50 shapes x every tile and part count measured
+// on MI355X (5120 .. 34816 rows, K 1024 .. 17408, n 17 .. 8000): over them the
+// choice is within 2% of the best measured one on average, 14% at worst.
+// Both sides, e.g. (us): 5120 x 6144, n = 17: 128 x 32 tile in 6 parts 11.3, 1
+// part 31.0; n = 1000: 256 x 128 in 3 parts 76, 1 part 97, 128 x 64 in 1 part
+// 88; 16384 x 5120, n = 512: 128 x 128 tile 91, 256 x 128 97; gated 2 x 17408 x
+// 5120, n = 300: 256 x 64 tile 127, 256 x 128 134; n = 2048: 625 and 692.
 nvfp4_fused_gemm_plan nvfp4_plan_fused_gemm(int n, int row_groups, int K)
 {
     const int T = (int)k_tiles(K);
@@ -387,24 +371,22 @@ nvfp4_fused_gemm_plan nvfp4_plan_fused_gemm(int n, int row_groups, int K)
     double best_cost = -1;
     for (int c = 0; c < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++c) {
         const Tile &t = kTiles[c];
-        if (t.tb > 2 && n <= 8 * t.tb)
-            continue;   // a smaller token tile holds them
-        const long long tiles = (long long)((row_groups + 4 * t.rg - 1) / (4 * t.rg)) * ((n + 16 * t.tb - 1) / (16 * t.tb));
-        for (int ks = 1; ks <= 16; ++ks) {
+        if (n <= 8 * t.tb && t.tb > 2)
+            continue;   // half its tokens would not exist
+        const long long tiles =
+            (long long)((row_groups + 4 * t.rg - 1) / (4 * t.rg)) * ((n + 16 * t.tb - 1) / (16 * t.tb));
+        for (const int ks : kParts) {
             const int tp = (T + ks - 1) / ks;
-            if (ks > 1 && (tp < 4 || (long long)(ks - 1) * tp >= T))
-                continue;
-            const long long units = tiles * ks, slots = 256LL * t.full;
-            const long long rest = units % slots;
-            const int r = (int)((rest + 255) / 256);
-            double cost = (double)(units / slots) * t.full * t.shared;
-            if (r == 1)
-                cost += t.alone;
-            else
-                cost += (double)r * t.shared;
-            cost = cost * tp + 3000;
+            if (ks > 1 && (tp < 2 || tiles >= 2048))
+                break;
+            if ((long long)(ks - 1) * tp >= T)
+                continue;   // the last part would be empty
+            const double load = (double)(tiles * ks) / 256;
+            const long long resident = (tiles * ks + 255) / 256;
+            const double step = resident <= t.full ? resident * t.shared : (load + kTail) * t.shared;
+            double cost = (tp + kStartSteps) * (step > t.alone ? step : t.alone);
             if (ks > 1)
-                cost += 3000 + (double)ks * n * row_groups * 16 * 8 / 5500;
+                cost += kReduceNs + (double)ks * n * row_groups * kRowsPerGroup * kReduceSumNs;
             if (best_cost < 0 || cost < best_cost) {
                 best_cost = cost;
                 best.tile = c;
@@ -436,8 +418,10 @@ int nvfp4_launch_fused_gemm(const nvfp4_fused_gemm_args &a, const nvfp4_fused_ge
     p.tp = plan.tp;
     p.partial = a.partial;
     switch (plan.tile) {
-    case 0: return launch_one<2, 2, 3>(p, a.mode, stream);
-    case 1: return launch_one<2, 4, 3>(p, a.mode, stream);
-    default: return launch_one<4, 8, 2>(p, a.mode, stream);
+    case 0: return launch_one<2, 2>(p, a.mode, stream);
+    case 1: return launch_one<2, 4>(p, a.mode, stream);
+    case 2: return launch_one<2, 8>(p, a.mode, stream);
+    case 3: return launch_one<4, 4>(p, a.mode, stream);
+    default: return launch_one<4, 8>(p, a.mode, stream);
     }
 }
