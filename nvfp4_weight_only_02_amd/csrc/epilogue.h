@@ -60,17 +60,27 @@ __device__ __forceinline__ float bf16_bits_to_f32(uint16_t b)
     return __builtin_bit_cast(float, (u32)b << 16);
 }
 
+// The two halves of an fp32 value, the lower one zero for bf16.
+struct Halves {
+    u32 lo, hi;
+    __device__ __forceinline__ float value() const { return __builtin_bit_cast(float, hi << 16 | lo); }
+};
+
 // Element i of an fp32 or bf16 array.  Both types go through the same load of
 // the upper 16 bits: a register that one of two branches loads looks, to the
 // build's check of loads in flight, as if both might.
-__device__ __forceinline__ float load_any(const void *p, long long i, int f32)
+__device__ __forceinline__ Halves load_halves(const void *p, long long i, int f32)
 {
     const uint16_t *h = static_cast<const uint16_t *>(p) + (f32 ? 2 * i : i);
     u32 lo = 0;
     if (f32)
         lo = h[0];
-    const u32 hi = h[f32 ? 1 : 0];
-    return __builtin_bit_cast(float, hi << 16 | lo);
+    return {lo, h[f32 ? 1 : 0]};
+}
+
+__device__ __forceinline__ float load_any(const void *p, long long i, int f32)
+{
+    return load_halves(p, i, f32).value();
 }
 
 __device__ __forceinline__ void store_any(void *p, long long i, int f32, float v)

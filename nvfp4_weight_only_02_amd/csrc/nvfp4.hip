@@ -75,6 +75,8 @@ template <int MT, int NV, bool EXACT, bool CHUNKED, bool SPLIT>
 __global__ __launch_bounds__(kWaves * 64) void nvfp4_gemv_kernel(GemvParams p)
 {
     constexpr int kGroups = 1;
+    constexpr bool kSpread = false;
+    auto reduce_batch = [](int, int) {};
 #include "gemv_product.inc"
 
     // Sum the K-slices of row group rg in wave order 0..W-1, scale by gscale,
