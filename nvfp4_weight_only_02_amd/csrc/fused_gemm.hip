@@ -65,8 +65,9 @@ __device__ __forceinline__ unsigned lds_address(const void *p)
     return (unsigned)(uintptr_t)(__attribute__((address_space(3))) const char *)p;
 }
 
-// One workgroup: 4 waves x RG row groups (64 * RG weight rows) times 16 * TB
-// tokens, over the steps of one K part.  A step covers 128 contracted columns:
+// One workgroup: RW waves x RG row groups (16 * RW * RG weight rows) times 16 *
+// TB tokens, over the steps of one K part, which KG groups of RW waves take in
+// turn and whose sums they add through LDS in the end, in group order.  A step covers 128 contracted columns:
 // the tokens' slice and the scales go straight to LDS, each wave turns its own
 // code tiles into MFMA operands in registers.  The loads of step s + 1 are
 // issued before step s is computed and waited for after it: two LDS buffers,
@@ -90,16 +91,18 @@ __device__ __forceinline__ unsigned lds_address(const void *p)
 // tokens' operand is one 16-byte read.  Against the 16-row form (whose operand
 // is two 8-byte reads) it halves the MFMA and LDS instructions that the
 // dequantisation has to share the issue slots with.
-template <int RG, int TB, int MODE>
-__global__ __launch_bounds__(256, 2) void nvfp4_fused_gemm_kernel(FusedGemmParams p)
+template <int RG, int TB, int RW, int KG, int MODE>
+__global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fused_gemm_kernel(FusedGemmParams p)
 {
     constexpr int BM = TB * 16;
+    constexpr int kThreads = 64 * RW * KG;
     constexpr int kSlice = BM / 4 * kQuad;         // LDS bytes of a step's token slice
-    constexpr int kBuf = kSlice + 4 * RG * 128;    // and of the waves' scales
-    constexpr int XL = TB;                         // quads a wave stages: BM / 4 / 4 waves
+    constexpr int kBuf = kSlice + RW * RG * 128;   // and of the waves' scales
+    constexpr int XL = BM / 4 / RW;                // quads a wave stages
     const int tid = threadIdx.x;
     const int lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) % RW;
+    const int kg = __builtin_amdgcn_readfirstlane(tid >> 6) / RW;
     const int i = lane & 15, g = lane >> 4;
 
     // Tile of this workgroup.  Consecutive workgroups go to the 8 XCDs in
@@ -119,12 +122,12 @@ __global__ __launch_bounds__(256, 2) void nvfp4_fused_gemm_kernel(FusedGemmParam
         tx = x0 + at % w;
         ty = at / w;
     }
-    const int rg0 = (tx * 4 + wave) * RG;
+    const int rg0 = (tx * RW + wave) * RG;
     const int tok0 = ty * BM;
     const int ntok = min(BM, p.n - tok0);
     const int nrg = max(0, min(RG, p.RG - rg0)), rgb = min(rg0, p.RG);
     const int s0 = part * p.tp, s1 = min(p.T, s0 + p.tp);
-    __shared__ __align__(1024) char lds[2][kBuf];
+    __shared__ __align__(1024) char lds[KG][2][kBuf];
 
     // Loads past these ranges (tokens beyond n, row groups beyond RG) read
     // zeros without touching memory.
@@ -135,8 +138,8 @@ __global__ __launch_bounds__(256, 2) void nvfp4_fused_gemm_kernel(FusedGemmParam
     const int xcol = 8 * (i ^ g);   // lane (i, g) stages chunk i ^ g of token 4 q + g
     const unsigned xoff = (unsigned)((wave * XL * 4 + g) * ldx2 + xcol * 2);
     const unsigned soff = (unsigned)((lane >> 3) * p.T * 128 + (lane & 7) * 16);
-    const unsigned ldsb = lds_address(lds) + wave * XL * kQuad;
-    const unsigned ldss = lds_address(lds) + kSlice + wave * RG * 128;
+    const unsigned ldsb = lds_address(lds[kg]) + wave * XL * kQuad;
+    const unsigned ldss = lds_address(lds[kg]) + kSlice + wave * RG * 128;
 
     u32x4 cw[RG];
     auto issue = [&](int s, int b) {
@@ -175,7 +178,7 @@ __global__ __launch_bounds__(256, 2) void nvfp4_fused_gemm_kernel(FusedGemmParam
     const int sa = kSlice + wave * RG * 128 + (g & 1) * 128 + (MODE == 2 ? h * 64 : i * 8);
 
     auto compute = [&](int b, const u32x4 *c) {
-        const char *buf = lds[b];
+        const char *buf = lds[kg][b];
         u32 lo[RP][4], hi[RP][4];   // columns 8h + 0..3 and 4..7 of each block
 #pragma unroll
         for (int r = 0; r < RP; ++r)
@@ -237,17 +240,20 @@ __global__ __launch_bounds__(256, 2) void nvfp4_fused_gemm_kernel(FusedGemmParam
         });
     };
 
-    issue(s0, 0);
+    if (s0 + kg < s1)
+        issue(s0 + kg, 0);
     land();
-    for (int s = s0; s < s1; ++s) {
-        const int b = (s - s0) & 1;
+    int b = 0;
+    for (int sb = s0; sb < s1; sb += KG, b ^= 1) {
+        const int s = sb + kg;
         u32x4 c[RG];
 #pragma unroll
         for (int r = 0; r < RG; ++r)
             c[r] = cw[r];
-        if (s + 1 < s1)
-            issue(s + 1, b ^ 1);
-        compute(b, c);
+        if (s + KG < s1)
+            issue(s + KG, b ^ 1);
+        if (KG == 1 || s < s1)
+            compute(b, c);
         land();
     }
 
@@ -257,17 +263,18 @@ __global__ __launch_bounds__(256, 2) void nvfp4_fused_gemm_kernel(FusedGemmParam
         constexpr int q = 4 * decltype(qc)::value;
         return f32x4{c[q], c[q + 1], c[q + 2], c[q + 3]};
     };
+    const int pitch = p.RG * kRowsPerGroup;
+    float *partial = p.partial + (long long)part * p.n * pitch;
 
     // A K part stores its sums as they are: nvfp4_fused_reduce_kernel adds the
     // parts in order and runs the epilogue.
-    if (p.ks > 1) {
-        const int pitch = p.RG * kRowsPerGroup;
+    if (KG == 1 && p.ks > 1) {
 #pragma unroll
         for (int t = 0; t < TP; ++t) {
             const int tok = tok0 + 32 * t + tl;
             if (tok >= p.n)
                 continue;
-            float *dst = p.partial + ((long long)part * p.n + tok) * pitch + rg0 * kRowsPerGroup + 4 * h;
+            float *dst = partial + (long long)tok * pitch + rg0 * kRowsPerGroup + 4 * h;
 #pragma unroll
             for (int r = 0; r < RP; ++r)
                 static_for<4>([&](auto qc) {
@@ -281,11 +288,18 @@ __global__ __launch_bounds__(256, 2) void nvfp4_fused_gemm_kernel(FusedGemmParam
 
     // Epilogue, one token block at a time through LDS, so that a wave writes
     // whole lines of consecutive outputs and the epilogue's code exists once.
-    constexpr int kRows = 64 * RG, kPitch = kRows + 4;
+    constexpr int kRows = 16 * RW * RG, kPitch = kRows + 4;
     constexpr int kOuts = MODE == 1 ? kRows / 2 : kRows;   // outputs a token
-    static_assert(32 * kPitch * 4 <= sizeof(lds), "the staged block fits the slice's LDS");
+    static_assert(KG * 32 * kPitch * 4 <= sizeof(lds), "the staged block fits the slices' LDS");
     float *stage = reinterpret_cast<float *>(lds);
-    const int out0 = tx * kOuts;
+    auto staged = [&](int t, int row) {
+        const float *src = stage + t * kPitch + row;
+        f32x4 v = *reinterpret_cast<const f32x4 *>(src);
+#pragma unroll
+        for (int k = 1; k < KG; ++k)
+            v += *reinterpret_cast<const f32x4 *>(src + k * 32 * kPitch);
+        return v;
+    };
 #pragma unroll 1
     for (int b = 0; b < TP && tok0 + 32 * b < p.n; ++b) {
         __syncthreads();
@@ -295,75 +309,88 @@ __global__ __launch_bounds__(256, 2) void nvfp4_fused_gemm_kernel(FusedGemmParam
 #pragma unroll
                 for (int r = 0; r < RP; ++r)
                     static_for<4>([&](auto qc) {
-                        *reinterpret_cast<f32x4 *>(stage + tl * kPitch + (wave * RG + 2 * r) * 16 + 8 * decltype(qc)::value +
-                                                   4 * h) = sums(acc[r][t], qc);
+                        *reinterpret_cast<f32x4 *>(stage + (kg * 32 + tl) * kPitch + (wave * RG + 2 * r) * 16 +
+                                                   8 * decltype(qc)::value + 4 * h) = sums(acc[r][t], qc);
                     });
             }
         });
         __syncthreads();
+        if (KG > 1 && p.ks > 1) {
 #pragma unroll 1
-        for (int q = tid * 4; q < 32 * kOuts; q += 1024) {
+            for (int q = tid * 4; q < 32 * kRows; q += 4 * kThreads) {
+                const int tok = tok0 + 32 * b + q / kRows, o = q % kRows;
+                if (tok < p.n && tx * kRows + o < pitch)
+                    *reinterpret_cast<f32x4 *>(partial + (long long)tok * pitch + tx * kRows + o) = staged(q / kRows, o);
+            }
+            continue;
+        }
+#pragma unroll 1
+        for (int q = tid * 4; q < 32 * kOuts; q += 4 * kThreads) {
             const int t = q / kOuts, o = q % kOuts;
             const int tok = tok0 + 32 * b + t;
             if (tok >= p.n)
                 break;
             if constexpr (MODE == 1) {
-                const float *src = stage + t * kPitch + (o >> 4) * 32 + (o & 15);
-                gated_out4(p.e, tok, out0 + o, *reinterpret_cast<const f32x4 *>(src),
-                           *reinterpret_cast<const f32x4 *>(src + 16));
+                const int row = (o >> 4) * 32 + (o & 15);
+                gated_out4(p.e, tok, tx * kOuts + o, staged(t, row), staged(t, row + 16));
             } else {
-                linear_out4(p.e, tok, out0 + o, *reinterpret_cast<const f32x4 *>(stage + t * kPitch + o));
+                linear_out4(p.e, tok, tx * kOuts + o, staged(t, o));
             }
         }
     }
 }
 
-template <int RG, int TB>
+template <int RG, int TB, int RW, int KG>
 int launch_one(FusedGemmParams p, int mode, hipStream_t stream)
 {
-    p.tiles_x = (p.RG + 4 * RG - 1) / (4 * RG);
+    p.tiles_x = (p.RG + RW * RG - 1) / (RW * RG);
     p.tiles_y = (p.n + TB * 16 - 1) / (TB * 16);
     const long long total = (long long)p.tiles_x * p.tiles_y * p.ks;
     if (total > INT32_MAX || (long long)p.T * RG * 1024 > INT32_MAX)
         return NVFP4_ERR_SHAPE;   // a wave's codes must stay within a 32-bit buffer offset
-    auto k = mode == 0 ? nvfp4_fused_gemm_kernel<RG, TB, 0>
-                       : (mode == 1 ? nvfp4_fused_gemm_kernel<RG, TB, 1> : nvfp4_fused_gemm_kernel<RG, TB, 2>);
-    hipLaunchKernelGGL(k, dim3((unsigned)total), dim3(256), 0, stream, p);
+    auto k = mode == 0 ? nvfp4_fused_gemm_kernel<RG, TB, RW, KG, 0>
+                       : (mode == 1 ? nvfp4_fused_gemm_kernel<RG, TB, RW, KG, 1> : nvfp4_fused_gemm_kernel<RG, TB, RW, KG, 2>);
+    hipLaunchKernelGGL(k, dim3((unsigned)total), dim3(64 * RW * KG), 0, stream, p);
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
 }
 
-// Tile shapes: row groups a wave, 16-token blocks, workgroups that fit a
-// compute unit, and what a step of a workgroup costs (ns) with one workgroup
-// on its unit and, per workgroup, with the unit full.
+// Tile shapes: row groups a wave, 16-token blocks, waves along the rows, K
+// groups, workgroups that fit a compute unit, and what an iteration (a step of
+// every K group) costs (ns) with one workgroup on its unit and, per workgroup,
+// with the unit full.
 struct Tile {
-    int rg, tb, full;
+    int rg, tb, rw, kg, full;
     double alone, shared;
 };
 constexpr Tile kTiles[] = {
-    {2, 2, 4, 610, 357},     //  128 rows x  32 tokens
-    {2, 4, 4, 710, 482},     //  128 x  64
-    {2, 8, 2, 1130, 888},    //  128 x 128
-    {4, 4, 3, 1240, 946},    //  256 x  64
-    {4, 8, 2, 1780, 1540},   //  256 x 128
+    {2, 2, 2, 4, 2, 820, 560},      //  64 rows x  32 tokens
+    {2, 2, 2, 8, 1, 1150, 1010},
+    {2, 4, 2, 4, 1, 1090, 1055},    //  64 x  64
+    {2, 4, 4, 2, 2, 1025, 760},     // 128 x  64
+    {4, 8, 4, 2, 1, 2630, 2515},    // 256 x 128
+    {4, 8, 4, 1, 2, 1785, 1230},
 };
-constexpr int kParts[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16};
-constexpr double kStartSteps = 2.2;     // a workgroup's start and epilogue, in steps
-constexpr double kTail = 0.8;           // uneven end of a grid of several rounds, in workgroups a unit
-constexpr double kReduceNs = 5000;      // second launch (3 us on the device, 5 with the host's part)
-constexpr double kReduceSumNs = 8.2e-4; // a partial sum written and read again
+constexpr int kParts[] = {1, 2, 3, 4, 6, 8, 12};
+constexpr double kStart = 3;            // a workgroup's start and epilogue, in iterations
+constexpr double kTail = 0.75;          // uneven end of a grid of several rounds, in workgroups a unit
+constexpr double kReduceNs = 3700;      // the second launch
+constexpr double kReduceSumNs = 9.1e-4; // a partial sum written and read again
 
 }  // namespace
 
-// The tile and part count of least modelled time.  More parts or smaller tiles
-// fill the chip where the largest tile leaves units idle, larger tiles
-// dequantise a weight for more tokens, fewer parts write fewer partial sums.
-// The constants were fitted to 50 shapes x every tile and part count measured
-// on MI355X (5120 .. 34816 rows, K 1024 .. 17408, n 17 .. 8000): over them the
-// choice is within 2% of the best measured one on average, 14% at worst.
-// Both sides, e.g. (us): 5120 x 6144, n = 17: 128 x 32 tile in 6 parts 11.3, 1
-// part 31.0; n = 1000: 256 x 128 in 3 parts 76, 1 part 97, 128 x 64 in 1 part
-// 88; 16384 x 5120, n = 512: 128 x 128 tile 91, 256 x 128 97; gated 2 x 17408 x
-// 5120, n = 300: 256 x 64 tile 127, 256 x 128 134; n = 2048: 625 and 692.
+// The tile and part count of least modelled time.  Smaller tiles, K groups and
+// K parts fill the chip where the largest tile leaves units idle; larger tiles
+// dequantise a weight for more tokens, K groups add their sums in LDS where
+// parts write them and need a second launch.  The constants were fitted to 91
+// shapes x 14 tiles x every part count measured on MI355X (64 .. 34816 rows, K
+// 1024 .. 34816, n 17 .. 8000): over them the choice is within 1.1% of the best
+// measured one on average, 13% at worst.  Both sides of some choices (us):
+//   5120 x 6144   n = 17    64 x 32 in 3 parts 9.9; without K groups 11.3 (6 parts), 32.3 (1 part)
+//   16384 x 5120  n = 24    64 x 32, 8 groups 13.7; without groups 17.7 (4 parts), 28.3
+//   1237 x 2064   n = 300   64 x 32, 4 groups 8.4; 128 x 32 without groups 16.0
+//   16384 x 5120  n = 128   128 x 64, 2 groups 31.1; 64 x 64 36.6, 256 x 128 84
+//   5120 x 6144   n = 1000  256 x 128 in 3 parts 78; 2 groups 85, 128 x 64 85, 1 part 104
+//   gated 2 x 17408 x 5120  n = 2048  256 x 128 611; 128 x 64 without groups 796
 nvfp4_fused_gemm_plan nvfp4_plan_fused_gemm(int n, int row_groups, int K)
 {
     const int T = (int)k_tiles(K);
@@ -371,20 +398,18 @@ nvfp4_fused_gemm_plan nvfp4_plan_fused_gemm(int n, int row_groups, int K)
     double best_cost = -1;
     for (int c = 0; c < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++c) {
         const Tile &t = kTiles[c];
-        if (n <= 8 * t.tb && t.tb > 2)
-            continue;   // half its tokens would not exist
         const long long tiles =
-            (long long)((row_groups + 4 * t.rg - 1) / (4 * t.rg)) * ((n + 16 * t.tb - 1) / (16 * t.tb));
+            (long long)((row_groups + t.rw * t.rg - 1) / (t.rw * t.rg)) * ((n + 16 * t.tb - 1) / (16 * t.tb));
         for (const int ks : kParts) {
             const int tp = (T + ks - 1) / ks;
             if (ks > 1 && (tp < 2 || tiles >= 2048))
                 break;
             if ((long long)(ks - 1) * tp >= T)
                 continue;   // the last part would be empty
-            const double load = (double)(tiles * ks) / 256;
-            const long long resident = (tiles * ks + 255) / 256;
-            const double step = resident <= t.full ? resident * t.shared : (load + kTail) * t.shared;
-            double cost = (tp + kStartSteps) * (step > t.alone ? step : t.alone);
+            const long long units = tiles * ks, resident = (units + 255) / 256;
+            const double per = resident <= t.full ? (double)resident : units * (1.0 / 256) + kTail;
+            const double step = per * t.shared > t.alone ? per * t.shared : t.alone;
+            double cost = ((tp + t.kg - 1) / t.kg + kStart) * step;
             if (ks > 1)
                 cost += kReduceNs + (double)ks * n * row_groups * kRowsPerGroup * kReduceSumNs;
             if (best_cost < 0 || cost < best_cost) {
@@ -418,10 +443,11 @@ int nvfp4_launch_fused_gemm(const nvfp4_fused_gemm_args &a, const nvfp4_fused_ge
     p.tp = plan.tp;
     p.partial = a.partial;
     switch (plan.tile) {
-    case 0: return launch_one<2, 2>(p, a.mode, stream);
-    case 1: return launch_one<2, 4>(p, a.mode, stream);
-    case 2: return launch_one<2, 8>(p, a.mode, stream);
-    case 3: return launch_one<4, 4>(p, a.mode, stream);
-    default: return launch_one<4, 8>(p, a.mode, stream);
+    case 0: return launch_one<2, 2, 2, 4>(p, a.mode, stream);
+    case 1: return launch_one<2, 2, 2, 8>(p, a.mode, stream);
+    case 2: return launch_one<2, 4, 2, 4>(p, a.mode, stream);
+    case 3: return launch_one<2, 4, 4, 2>(p, a.mode, stream);
+    case 4: return launch_one<4, 8, 4, 2>(p, a.mode, stream);
+    default: return launch_one<4, 8, 4, 1>(p, a.mode, stream);
     }
 }
