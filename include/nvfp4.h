@@ -320,7 +320,7 @@ typedef struct nvfp4_epilogue {
     const void *bias;        /* [N], added before the activation (gated: of the gate), or NULL */
     const void *up_bias;     /* gated only: [F], of the up projection, or NULL */
     const void *residual;    /* linear only: [n][ldr], added after the activation, or NULL */
-    uint16_t *preact;        /* receives the bf16 pre-activations for the backward pass, or NULL:
+    float *preact;           /* receives the pre-activations for the backward pass, or NULL:
                                 [n][ldp], ldp a multiple of 8, 16-byte aligned; linear: N columns;
                                 gated: nvfp4_gated_rows(F) columns in the gated weight's row order
                                 (columns of rows that do not exist are left as they were) */
@@ -390,7 +390,7 @@ size_t nvfp4_gemm_t_workspace_bytes(int n, int N, int K);
  * NVFP4_ACT_NONE).  Bias gradients need nvfp4_grad_workspace_bytes(n, N, 0)
  * bytes of workspace.  The residual's gradient is dY itself.  Errors: NULL,
  * RANGE, SHAPE, ALIGN, OVERLAP, WORKSPACE, DEVICE, LAUNCH. */
-int nvfp4_linear_grad(const void *dY, int dy_dtype, int64_t ldy, const uint16_t *preact, int64_t ldp,
+int nvfp4_linear_grad(const void *dY, int dy_dtype, int64_t ldy, const float *preact, int64_t ldp,
                       int activation, uint16_t *dZ, int64_t ldz, void *dbias, int bias_dtype, int n, int N,
                       void *workspace, size_t workspace_bytes, void *stream);
 
@@ -400,7 +400,7 @@ int nvfp4_linear_grad(const void *dY, int dy_dtype, int64_t ldy, const uint16_t 
  * nvfp4_gated_rows(F) on the transposed gated weight gives dX; the bias
  * gradients are sums of the unscaled values.  Workspace:
  * nvfp4_grad_workspace_bytes(n, F, 1). */
-int nvfp4_gated_grad(const void *dH, int dh_dtype, int64_t ldh, const uint16_t *preact, int64_t ldp,
+int nvfp4_gated_grad(const void *dH, int dh_dtype, int64_t ldh, const float *preact, int64_t ldp,
                      int activation, float gate_gscale, float up_gscale, uint16_t *dZ, int64_t ldz,
                      void *dgate_bias, void *dup_bias, int bias_dtype, int n, int F, void *workspace,
                      size_t workspace_bytes, void *stream);

@@ -114,7 +114,7 @@ __global__ __launch_bounds__(256) void nvfp4_fused_reduce_kernel(nvfp4_epi_param
 
 struct GradParams {
     const void *dy;
-    const uint16_t *z;       // bf16 pre-activations, or null (identity)
+    const float *z;          // pre-activations, or null (identity)
     uint16_t *dz;            // bf16, or null
     float *partial;          // [row blocks][halves][cols] column sums, or null
     void *db[2];             // bias gradients, or null
@@ -162,26 +162,31 @@ __global__ __launch_bounds__(256) void nvfp4_grad_kernel(GradParams p)
                 for (int e = 0; e < 8; ++e)
                     dy[e] = c0 + e < p.N ? load_any(p.dy, at + e, p.dy_f32) : 0.f;
             }
-            auto words = [&](long long col) {
-                return *reinterpret_cast<const u32x4 *>(p.z + t * p.ldz + col);
+            float z[2][8] = {};
+            auto fetch = [&](int half, long long col) {
+                const f32x4 *src = reinterpret_cast<const f32x4 *>(p.z + t * p.ldz + col);
+                const f32x4 a = src[0], b = src[1];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    z[half][e] = a[e];
+                    z[half][4 + e] = b[e];
+                }
             };
-            auto value = [](u32x4 w, int e) {
-                return __builtin_bit_cast(float, e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
-            };
+            if (p.z)
+                fetch(0, GATED ? gated_row(c0, 0) : c0);
+            if constexpr (GATED)
+                fetch(1, gated_row(c0, 1));
             u32x4 out[2];
-            const u32x4 z0 = p.z ? words(GATED ? gated_row(c0, 0) : c0) : u32x4{0u, 0u, 0u, 0u};
-            const u32x4 z1 = GATED ? words(gated_row(c0, 1)) : z0;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 float d[2];
                 // past the last output the pre-activations are not defined
                 const bool in = c0 + e < p.N;
                 if constexpr (GATED) {
-                    const float zg = value(z0, e);
-                    d[0] = in ? dy[e] * value(z1, e) * activate_grad(zg, p.act) : 0.f;
-                    d[1] = in ? dy[e] * activate(zg, p.act) : 0.f;
+                    d[0] = in ? dy[e] * z[1][e] * activate_grad(z[0][e], p.act) : 0.f;
+                    d[1] = in ? dy[e] * activate(z[0][e], p.act) : 0.f;
                 } else {
-                    d[0] = in ? (p.act == NVFP4_ACT_NONE ? dy[e] : dy[e] * activate_grad(value(z0, e), p.act)) : 0.f;
+                    d[0] = in ? (p.act == NVFP4_ACT_NONE ? dy[e] : dy[e] * activate_grad(z[0][e], p.act)) : 0.f;
                     d[1] = 0.f;
                 }
 #pragma unroll
@@ -309,7 +314,7 @@ int validate_forward(const uint8_t *Wq, const uint8_t *Wscale, const uint16_t *X
     // Workgroups read what others write unless the outputs lie apart.  The
     // residual may be the output itself: each element is read by the thread
     // that then writes it.
-    const size_t on = span(n, ldo, N, os), pn = ep->preact ? span(n, ep->ldp, pre_cols, 2) : 0;
+    const size_t on = span(n, ldo, N, os), pn = ep->preact ? span(n, ep->ldp, pre_cols, 4) : 0;
     const size_t xn = span(n, ldx, K, 2);
     const size_t bn = (size_t)N * dtype_size(ep->bias_dtype);
     const size_t wq = nvfp4_packed_codes_bytes(rows, K), ws = nvfp4_packed_scales_bytes(rows, K);
@@ -367,11 +372,23 @@ size_t parts_bytes(int n, int rows, int K)
     return ks > 1 ? (size_t)ks * n * padded_rows(rows) * sizeof(float) : 0;
 }
 
-int check_workspace(const void *workspace, size_t bytes, size_t need)
+// A workspace for the partial sums: large enough, aligned, apart from what the
+// second launch still reads or writes.
+int check_workspace(const void *workspace, size_t bytes, size_t need, const uint16_t *X, long long ldx, int n, int K,
+                    const nvfp4_epi_params &e, long long pre_cols)
 {
-    if (need && (!workspace || bytes < need))
+    if (!need)
+        return NVFP4_OK;
+    if (!workspace || bytes < need)
         return NVFP4_ERR_WORKSPACE;
-    return need && !is_aligned(workspace, 16) ? NVFP4_ERR_ALIGN : NVFP4_OK;
+    if (!is_aligned(workspace, 16))
+        return NVFP4_ERR_ALIGN;
+    if (overlap(workspace, need, X, span(n, ldx, K, 2)) ||
+        overlap(workspace, need, e.out, span(n, e.ldo, e.N, e.flags & kEpiOutF32 ? 4 : 2)) ||
+        overlap(workspace, need, e.residual, span(n, e.ldr, e.N, e.flags & kEpiResidualF32 ? 4 : 2)) ||
+        overlap(workspace, need, e.preact, span(n, e.ldp, pre_cols, 4)))
+        return NVFP4_ERR_OVERLAP;
+    return NVFP4_OK;
 }
 
 // The second launch of a call in K parts.
@@ -391,7 +408,8 @@ int launch_product(nvfp4_fused_gemm_args a, void *workspace, size_t workspace_by
 {
     const nvfp4_fused_gemm_plan plan = nvfp4_plan_fused_gemm(a.n, a.row_groups, a.K);
     const int pitch = a.row_groups * kRowsPerGroup;
-    int st = check_workspace(workspace, workspace_bytes, plan.ks > 1 ? (size_t)plan.ks * a.n * pitch * sizeof(float) : 0);
+    int st = check_workspace(workspace, workspace_bytes, plan.ks > 1 ? (size_t)plan.ks * a.n * pitch * sizeof(float) : 0,
+                             a.X, a.ldx, a.n, a.K, a.epi, a.mode == 1 ? pitch : a.epi.N);
     if (st != NVFP4_OK)
         return st;
     a.partial = static_cast<float *>(workspace);
@@ -422,7 +440,8 @@ int forward(const uint8_t *Wq, const uint8_t *Wscale, const uint16_t *X, int64_t
         a.epi = e;
         if (ks == 1)
             return gated ? nvfp4_launch_fused_gemv_gated(a, stream) : nvfp4_launch_fused_gemv_linear(a, stream);
-        int st = check_workspace(workspace, workspace_bytes, parts_bytes(n, rows, K));
+        int st = check_workspace(workspace, workspace_bytes, parts_bytes(n, rows, K), X, ldx, n, K, e,
+                                 gated ? rows : e.N);
         if (st != NVFP4_OK)
             return st;
         a.partials = static_cast<float *>(workspace);
@@ -504,7 +523,7 @@ int launch_grad(GradParams p, bool gated, void *workspace, size_t workspace_byte
     return NVFP4_OK;
 }
 
-int validate_grad(const void *dY, int dy_dtype, int64_t ldy, const uint16_t *preact, int64_t ldp, int activation,
+int validate_grad(const void *dY, int dy_dtype, int64_t ldy, const float *preact, int64_t ldp, int activation,
                   const uint16_t *dZ, int64_t ldz, const void *db0, const void *db1, int db_dtype, int n, int N,
                   int64_t pre_cols, int64_t dz_cols)
 {
@@ -523,7 +542,7 @@ int validate_grad(const void *dY, int dy_dtype, int64_t ldy, const uint16_t *pre
     if (!is_aligned(dY, ds) || (preact && (!is_aligned(preact, 16) || ldp % 8 != 0)) ||
         (dZ && (!is_aligned(dZ, 16) || ldz % 8 != 0)) || (db0 && !is_aligned(db0, bs)) || (db1 && !is_aligned(db1, bs)))
         return NVFP4_ERR_ALIGN;
-    const size_t yn = span(n, ldy, N, ds), pn = preact ? span(n, ldp, pre_cols, 2) : 0;
+    const size_t yn = span(n, ldy, N, ds), pn = preact ? span(n, ldp, pre_cols, 4) : 0;
     const size_t zn = dZ ? span(n, ldz, dz_cols, 2) : 0, bn = (size_t)N * bs;
     if (overlap(dZ, zn, dY, yn) || overlap(dZ, zn, preact, pn) || overlap(dZ, zn, db0, bn) || overlap(dZ, zn, db1, bn) ||
         overlap(db0, bn, dY, yn) || overlap(db1, bn, dY, yn) || overlap(db0, bn, preact, pn) ||
@@ -677,7 +696,7 @@ size_t nvfp4_grad_workspace_bytes(int n, int N, int gated)
     return gated ? grad_bytes(n, (int)(gated_rows(N) / 2), 2) : grad_bytes(n, (N + 7) / 8 * 8, 1);
 }
 
-int nvfp4_linear_grad(const void *dY, int dy_dtype, int64_t ldy, const uint16_t *preact, int64_t ldp, int activation,
+int nvfp4_linear_grad(const void *dY, int dy_dtype, int64_t ldy, const float *preact, int64_t ldp, int activation,
                       uint16_t *dZ, int64_t ldz, void *dbias, int bias_dtype, int n, int N, void *workspace,
                       size_t workspace_bytes, void *stream)
 {
@@ -706,7 +725,7 @@ int nvfp4_linear_grad(const void *dY, int dy_dtype, int64_t ldy, const uint16_t 
     return launch_grad(p, false, workspace, workspace_bytes, (hipStream_t)stream);
 }
 
-int nvfp4_gated_grad(const void *dH, int dh_dtype, int64_t ldh, const uint16_t *preact, int64_t ldp, int activation,
+int nvfp4_gated_grad(const void *dH, int dh_dtype, int64_t ldh, const float *preact, int64_t ldp, int activation,
                      float gate_gscale, float up_gscale, uint16_t *dZ, int64_t ldz, void *dgate_bias, void *dup_bias,
                      int bias_dtype, int n, int F, void *workspace, size_t workspace_bytes, void *stream)
 {

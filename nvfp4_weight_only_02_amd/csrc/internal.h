@@ -24,7 +24,7 @@ NVFP4_HIDDEN bool nvfp4_gemv_geometry_for(int N, int K, int cus, int ks, nvfp4_g
 struct nvfp4_epi_params {
     const void *bias, *up_bias;   // [N] (gated: of the gate and of the up rows), or null
     const void *residual;         // [n][ldr], or null
-    uint16_t *preact;             // bf16 [n][ldp], or null
+    float *preact;                // [n][ldp], or null
     void *out;                    // [n][ldo]
     int ldr, ldp, ldo;
     float gscale, up_gscale;

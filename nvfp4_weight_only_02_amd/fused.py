@@ -270,13 +270,13 @@ def _pad8(cols: int) -> int:
 
 
 def preact_columns(w) -> int:
-    """Columns of the bf16 pre-activation buffer of ``w`` (a PackedWeight or a
+    """Columns of the fp32 pre-activation buffer of ``w`` (a PackedWeight or a
     GatedWeight): the outputs up to a multiple of 8, or the gated weight's rows."""
     return gated_rows(w.F) if isinstance(w, GatedWeight) else _pad8(w.N)
 
 
 def _preact_arg(preact, w, n):
-    return None if preact is None else _mat(preact, (torch.bfloat16,), "preact", n, preact_columns(w))
+    return None if preact is None else _mat(preact, (torch.float32,), "preact", n, preact_columns(w))
 
 
 def _workspace_arg(workspace):
@@ -311,7 +311,7 @@ class _Linear(torch.autograd.Function):
         ctx.residual_dtype = None if residual is None else residual.dtype
         preact = None
         if act and (ctx.needs_input_grad[0] or ctx.needs_input_grad[1]):
-            preact = torch.empty(X.shape[0], _pad8(w.N), dtype=torch.bfloat16, device=X.device)
+            preact = torch.empty(X.shape[0], _pad8(w.N), dtype=torch.float32, device=X.device)
         ctx.save_for_backward(preact)
         return _linear_forward(w, X, bias, act, residual, None, out_dtype, preact, None, None)
 
@@ -332,7 +332,7 @@ class _Gated(torch.autograd.Function):
     def forward(ctx, X, gate_bias, up_bias, w, transposed, act, out_dtype):
         ctx.w, ctx.transposed, ctx.act = w, transposed, act
         ctx.bias_dtype = next((b.dtype for b in (gate_bias, up_bias) if b is not None), None)
-        preact = torch.empty(X.shape[0], gated_rows(w.F), dtype=torch.bfloat16, device=X.device)
+        preact = torch.empty(X.shape[0], gated_rows(w.F), dtype=torch.float32, device=X.device)
         ctx.save_for_backward(preact)
         return _gated_forward(w, X, act, gate_bias, up_bias, None, out_dtype, preact, None, None)
 
@@ -354,7 +354,7 @@ def linear(w: PackedWeight, X: torch.Tensor, bias: torch.Tensor = None, activati
 
     X: bf16 [n, K]; bias: bf16 or fp32 [N]; residual: bf16 or fp32 [n, N] (it
     may be ``out`` itself); Y: bf16, or fp32 with ``out_dtype``.  Rows may be
-    strided; X rows are 16-byte aligned.  ``preact`` (bf16 [n,
+    strided; X rows are 16-byte aligned.  ``preact`` (fp32 [n,
     preact_columns(w)]) receives the pre-activations ``linear_backward`` needs.
     ``workspace``: uint8, nvfp4_linear_workspace_bytes (allocated otherwise).
     Differentiable in X (given ``transposed``), bias and residual."""
@@ -484,7 +484,7 @@ def linear_backward(wt: TransposedWeight, dY: torch.Tensor, activation: str = No
     if act:
         if preact is None:
             raise ValueError("the gradient of an activation needs preact")
-        _mat(preact, (torch.bfloat16,), "preact", dY.shape[0], _pad8(dY.shape[-1]))
+        _mat(preact, (torch.float32,), "preact", dY.shape[0], _pad8(dY.shape[-1]))
     if out is not None:
         _mat(out, (torch.bfloat16,), "out", dY.shape[0], wt.K)
     return _linear_backward(wt, dY, act, preact if act else None, bias_dtype, out, stream)
@@ -495,7 +495,7 @@ def gated_backward(w: GatedWeight, wt: TransposedWeight, dH: torch.Tensor, preac
     """(dX, dgate_bias, dup_bias) of ``gated``; the bias gradients in
     ``bias_dtype`` (None without)."""
     act = _act(activation)
-    _mat(preact, (torch.bfloat16,), "preact", dH.shape[0], gated_rows(w.F))
+    _mat(preact, (torch.float32,), "preact", dH.shape[0], gated_rows(w.F))
     if wt is not None and (wt.N, wt.K) != (gated_rows(w.F), w.K):
         raise ValueError("wt is not the transposed copy of this gated weight")
     if out is not None:

@@ -88,9 +88,9 @@ def gated(X, Wg, Wu, bg=None, bu=None, kind="silu", out_f32=False):
 
 
 def _grad_parts(z, ez, kind):
-    """act'(z) and its bound when z is known within ez and then rounded to bf16."""
+    """act'(z) and its bound when z is known within ez and stored in fp32."""
     d = act_grad(z, kind)
-    e = ez + HALF_BF16 * (np.abs(z) + ez)
+    e = ez + HALF_F32 * (np.abs(z) + ez)
     if kind == "none":
         return d, np.zeros_like(d)
     if kind == "relu":
@@ -126,8 +126,8 @@ def gated_grads(X, Wg, Wu, dH, bg=None, bu=None, kind="silu", bias_f32=False):
     g, eg = pre(X, Wg, bg)
     u, eu = pre(X, Wu, bu)
     d, ed = _grad_parts(g, eg, kind)
-    rg = eg + HALF_BF16 * (np.abs(g) + eg)      # the stored pre-activations are rounded
-    ru = eu + HALF_BF16 * (np.abs(u) + eu)
+    rg = eg + HALF_F32 * (np.abs(g) + eg)      # the stored pre-activations
+    ru = eu + HALF_F32 * (np.abs(u) + eu)
     a, ea = _activated(g, rg, kind)
     dG, dU = dH * u * d, dH * a
     eG = np.abs(dH) * (np.abs(u) * ed + ru * np.abs(d) + ru * ed) + 3 * HALF_F32 * np.abs(dG)

@@ -72,6 +72,9 @@ def test_long_rows_need_a_workspace():
     assert linear(K=8208) == WORKSPACE
     assert linear(K=8208, work=at(7), size=need - 1) == WORKSPACE
     assert linear(K=8208, work=at(7) + 4, size=need) == ALIGN
+    for other in (2, 3):                             # X, Y
+        assert linear(K=8208, work=at(other) - 16, size=need) == OVERLAP
+    assert linear(K=8208, work=at(7), size=need, ep=epilogue(residual=at(7), ldr=64)) == OVERLAP
     assert linear(n=17, K=8208) == WORKSPACE        # many columns for one row tile: K parts here too
     assert fused._call("nvfp4_linear_workspace_bytes")(4, 64, 8192) == 0
     rows = nv.gated_rows(50)

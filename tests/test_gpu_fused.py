@@ -152,12 +152,12 @@ def test_gated_gradients(n, F, K, act, bias):
 
 @pytest.mark.parametrize("act", R.ACTS)
 def test_elementwise_gradient_tight(act):
-    """dZ from given bf16 pre-activations: one rounding, over a wide range of z."""
+    """Column sums of act'(z) over a wide range of z."""
     say("dZ", act)
     n, N, K = 40, 333, 16
     w, _ = weight(N, K, 23)
-    z = torch.zeros(n, 336, dtype=BF16, device="cuda")
-    z[:, :N] = randn((n, N), 24, std=4.0)
+    z = torch.zeros(n, 336, device="cuda")
+    z[:, :N] = randn((n, N), 24, F32, 4.0)
     z[:, N:] = float("nan")              # columns that do not exist
     dY = torch.ones(n, N, device="cuda", dtype=BF16)
     _, db = nv.linear_backward(None, dY, activation=act, preact=z, bias_dtype=F32)
@@ -195,22 +195,43 @@ def test_strides_guards_and_in_place_residual():
         assert (buf == 7.0).all()
 
 
-def test_results_do_not_depend_on_the_batch():
-    say("batch identity")
+def test_results_repeat_and_decode_does_not_depend_on_the_batch():
+    say("repeat, batch identity")
     N, K = 200, 656
     w, _ = weight(N, K, 29)
     gw = nv.GatedWeight.from_packed(w, w)
     wt = w.transpose()
     X, dY = randn((300, K), 30), randn((300, N), 31)
-    full = nv.linear(w, X, activation="silu"), nv.gated(gw, X), nv.gemm_t(wt, dY)
-    for a, b in ((0, 17), (100, 164), (37, 300), (283, 300)):
-        part = nv.linear(w, X[a:b], activation="silu"), nv.gated(gw, X[a:b]), nv.gemm_t(wt, dY[a:b])
-        for p, q in zip(part, full):
-            assert torch.equal(p, q[a:b]), (a, b)
+    for n in (17, 64, 300):
+        first = nv.linear(w, X[:n], activation="silu"), nv.gated(gw, X[:n]), nv.gemm_t(wt, dY[:n])
+        again = nv.linear(w, X[:n], activation="silu"), nv.gated(gw, X[:n]), nv.gemm_t(wt, dY[:n])
+        for p, q in zip(first, again):
+            assert torch.equal(p, q), n
     one = nv.linear(w, X[:16]), nv.gated(gw, X[:16])
     for a, b in ((0, 1), (3, 9), (15, 16)):
         assert torch.equal(nv.linear(w, X[a:b]), one[0][a:b])
         assert torch.equal(nv.gated(gw, X[a:b]), one[1][a:b])
+
+
+@pytest.mark.parametrize("n", [9, 33, 90, 300])
+def test_columns_that_do_not_exist_read_as_zero(n):
+    """After a call whose activations are NaN everywhere (its slices stay behind
+    in LDS), a K and an N that end inside a tile still give finite results."""
+    say("stale LDS", n)
+    big, _ = weight(2048, 1024, 70)
+    w, W = weight(328, 336, 71)
+    gw, wt = nv.GatedWeight.from_packed(w, w), w.transpose()
+    bt = big.transpose()
+    X, dY = randn((n, 336), 72), randn((n, 328), 73)
+    want = nv.linear(w, X), nv.gated(gw, X), nv.gemm_t(wt, dY)
+    for f, v in ((lambda: nv.linear(w, X), want[0]), (lambda: nv.gated(gw, X), want[1]),
+                 (lambda: nv.gemm_t(wt, dY), want[2])):
+        nan = torch.full((n, 2048), float("nan"), device="cuda", dtype=BF16)
+        nv.linear(big, nan[:, :1024])
+        nv.gemm_t(bt, nan)
+        got = f()
+        assert torch.isfinite(got).all()
+        assert torch.equal(got, v)
 
 
 def test_linear_without_epilogue_is_gemv():
@@ -287,8 +308,8 @@ def test_block_forward_and_backward(n):
             args = lambda s: (x + s * v, b) if which == 0 else (x, b + s * v)   # noqa: E731
             diff = (f(*args(t)).sum() - f(*args(-t)).sum()) / (2 * t)
             got = float((f64(grad) * v).sum())
-            # at most three roundings to bf16 (h's gradient, dZ, dX) and the
-            # rounded pre-activations on every term
+            # at most three roundings to bf16 (h's gradient, dZ, dX) and that of
+            # h itself, on every term
             assert abs(got - diff) <= 8 * R.HALF_BF16 * float((np.abs(f64(grad)) * np.abs(v)).sum()) + 1e-3, which
 
 
@@ -303,7 +324,7 @@ def test_graph_replays_match_eager():
 
     def step(X, dY, b):
         n = X.shape[0]
-        pre = torch.empty(n, nv.preact_columns(gw), dtype=BF16, device="cuda")
+        pre = torch.empty(n, nv.preact_columns(gw), device="cuda")
         H = nv.gated(gw, X, gate_bias=b, preact=pre)
         Y = nv.linear(d, H, residual=X)
         dH, _ = nv.linear_backward(dt, dY)
