@@ -294,7 +294,7 @@ int nvfp4_gemm_geometry(int n, int N, int K, int *rows_per_workgroup,
  * NVFP4 weight (to the activations, the biases and the residual).  Conventions
  * as above, and for all of them:
  *   - matrices are row-major with a row stride in elements (>= the columns);
- *     X and dY rows are 16-byte aligned (stride a multiple of 8, at most 2^22);
+ *     X rows are 16-byte aligned (stride a multiple of 8, at most 2^22);
  *   - n = 0 is a valid call that launches nothing (but zeroes bias gradients);
  *   - sums, biases, activations and products are fp32, rounded once when
  *     stored;
@@ -363,7 +363,7 @@ int nvfp4_gated(const uint8_t *Wq, const uint8_t *Wscale, float gate_gscale, flo
                 const nvfp4_epilogue *epilogue, void *workspace, size_t workspace_bytes, void *stream);
 size_t nvfp4_gated_workspace_bytes(int n, int F, int K);
 
-/* The transposed copy of a packed weight, which nvfp4_gemm_t reads: tiles of
+/* The transposed copy of a packed weight, which the gradients read: tiles of
  * 16 columns x 128 rows (rows padded with zero codes), codes in the lane order
  * of the packed layout, and beside each tile the scales of its 128 rows.
  * Another 9/16 byte a weight, made once, kept only where gradients are wanted. */
@@ -372,39 +372,37 @@ size_t nvfp4_transposed_scales_bytes(int N, int K);
 int nvfp4_pack_transposed(const uint8_t *codes_packed, const uint8_t *scales_packed, int N, int K,
                           uint8_t *codes_t, uint8_t *scales_t, void *stream);
 
-/* dX[n][K] = gscale dY[n][N] . dequant(W), bf16: the gradient of a projection
- * with respect to its input.  Where N is not a multiple of 8, the elements up
- * to the next multiple are read from each dY row and must be zero.  Workspace
- * as nvfp4_linear: nvfp4_gemm_t_workspace_bytes(n, N, K).  Errors: NULL, RANGE,
- * SHAPE, ALIGN, OVERLAP, WORKSPACE, DEVICE, LAUNCH. */
-int nvfp4_gemm_t(const uint8_t *codes_t, const uint8_t *scales_t, float gscale, const uint16_t *dY, int64_t ldy,
-                 uint16_t *dX, int64_t ldx, int n, int N, int K, void *workspace, size_t workspace_bytes,
-                 void *stream);
-size_t nvfp4_gemm_t_workspace_bytes(int n, int N, int K);
+/* The gradients of nvfp4_linear: with dZ = dY * act'(Z),
+ *     dX = gscale dZ . dequant(W)   bf16 [n][ldx], on the transposed copy (NULL: not wanted,
+ *                                   nor then the copy), dZ rounded to bf16 for the product;
+ *     dbias = column sums of dZ     unrounded, in a fixed order (NULL: not wanted).
+ * The residual's gradient is dY itself.  dY: bf16 or fp32, any stride and
+ * element alignment; preact: as nvfp4_linear stored it (NULL with
+ * NVFP4_ACT_NONE).  With no activation and no dbias this is the product the
+ * other way through the weight, the input gradient of any projection of this
+ * library.  Workspace (16-byte aligned): nvfp4_linear_backward_workspace_bytes
+ * with dx and dbias as they are wanted, copy = 0 only if dZ is dY as it stands:
+ * no activation, bf16, N a multiple of 8, dY 16-byte aligned, ldy a multiple of
+ * 8 and at most 2^22.  Errors: NULL, RANGE, SHAPE (K % 16, K > 262144, strides,
+ * N beyond 2^22), ALIGN, OVERLAP, WORKSPACE, DEVICE, LAUNCH. */
+int nvfp4_linear_backward(const uint8_t *codes_t, const uint8_t *scales_t, float gscale, const void *dY,
+                          int dy_dtype, int64_t ldy, const float *preact, int64_t ldp, int activation,
+                          uint16_t *dX, int64_t ldx, void *dbias, int bias_dtype, int n, int N, int K,
+                          void *workspace, size_t workspace_bytes, void *stream);
+size_t nvfp4_linear_backward_workspace_bytes(int n, int N, int K, int dx, int dbias, int copy);
 
-/* The elementwise half of nvfp4_linear's gradient: dZ = dY * act'(Z) in bf16
- * with columns N .. next multiple of 8 zero (ready for nvfp4_gemm_t; ldz a
- * multiple of 8, 16-byte aligned; NULL: not wanted) and dbias = column sums
- * (NULL: not wanted) of the unrounded values, in a fixed order.  dY: any
- * stride and alignment.  preact: as nvfp4_linear stored it (NULL with
- * NVFP4_ACT_NONE).  Bias gradients need nvfp4_grad_workspace_bytes(n, N, 0)
- * bytes of workspace.  The residual's gradient is dY itself.  Errors: NULL,
- * RANGE, SHAPE, ALIGN, OVERLAP, WORKSPACE, DEVICE, LAUNCH. */
-int nvfp4_linear_grad(const void *dY, int dy_dtype, int64_t ldy, const float *preact, int64_t ldp,
-                      int activation, uint16_t *dZ, int64_t ldz, void *dbias, int bias_dtype, int n, int N,
-                      void *workspace, size_t workspace_bytes, void *stream);
-
-/* The same for nvfp4_gated: dZ [n][nvfp4_gated_rows(F)] holds, in the gated
- * weight's row order, gate_gscale * dH * U * act'(G) and up_gscale * dH *
- * act(G), zeros where no row exists, so that nvfp4_gemm_t with gscale 1 and N =
- * nvfp4_gated_rows(F) on the transposed gated weight gives dX; the bias
- * gradients are sums of the unscaled values.  Workspace:
- * nvfp4_grad_workspace_bytes(n, F, 1). */
-int nvfp4_gated_grad(const void *dH, int dh_dtype, int64_t ldh, const float *preact, int64_t ldp,
-                     int activation, float gate_gscale, float up_gscale, uint16_t *dZ, int64_t ldz,
-                     void *dgate_bias, void *dup_bias, int bias_dtype, int n, int F, void *workspace,
-                     size_t workspace_bytes, void *stream);
-size_t nvfp4_grad_workspace_bytes(int n, int N, int gated);
+/* The gradients of nvfp4_gated, on the transposed copy of the gated weight
+ * (nvfp4_pack_transposed with N = nvfp4_gated_rows(F)): with dG = dH * U *
+ * act'(G) and dU = dH * act(G), dX = gate_gscale dG . Wg + up_gscale dU . Wu in
+ * one product (the scaled dG and dU rounded to bf16 for it), dgate_bias and
+ * dup_bias the column sums of dG and dU.  Arguments and errors as
+ * nvfp4_linear_backward. */
+int nvfp4_gated_backward(const uint8_t *codes_t, const uint8_t *scales_t, float gate_gscale, float up_gscale,
+                         const void *dH, int dh_dtype, int64_t ldh, const float *preact, int64_t ldp,
+                         int activation, uint16_t *dX, int64_t ldx, void *dgate_bias, void *dup_bias,
+                         int bias_dtype, int n, int F, int K, void *workspace, size_t workspace_bytes,
+                         void *stream);
+size_t nvfp4_gated_backward_workspace_bytes(int n, int F, int K, int dx, int dbias);
 
 /* Human-readable name of a status code (static storage). */
 const char *nvfp4_strerror(int status);

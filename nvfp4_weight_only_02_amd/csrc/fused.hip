@@ -488,24 +488,13 @@ size_t grad_bytes(int n, int cols, int halves)
     return by > 1 ? (size_t)by * halves * cols * sizeof(float) : 0;
 }
 
-int launch_grad(GradParams p, bool gated, void *workspace, size_t workspace_bytes, hipStream_t stream)
+int launch_grad(GradParams p, bool gated, hipStream_t stream)
 {
     const int halves = gated ? 2 : 1;
     const bool sums = p.db[0] || p.db[1];
     if (!sums && (!p.dz || p.n == 0))
         return NVFP4_OK;
     const int by = grad_blocks(p.n, p.cols);
-    if (sums && by > 1) {
-        if (!workspace || workspace_bytes < grad_bytes(p.n, p.cols, halves))
-            return NVFP4_ERR_WORKSPACE;
-        if (!is_aligned(workspace, 16))
-            return NVFP4_ERR_ALIGN;
-    }
-    int cus = 0;
-    const int st = nvfp4_device_cus(&cus);
-    if (st != NVFP4_OK)
-        return st;
-    p.partial = static_cast<float *>(workspace);
     p.rows_per_block = p.n > 0 ? grad_rows_per_block(p.n, p.cols) : 8;
     const dim3 grid((unsigned)((p.cols + kGradCols - 1) / kGradCols), (unsigned)by);
     if (gated)
@@ -523,32 +512,139 @@ int launch_grad(GradParams p, bool gated, void *workspace, size_t workspace_byte
     return NVFP4_OK;
 }
 
-int validate_grad(const void *dY, int dy_dtype, int64_t ldy, const float *preact, int64_t ldp, int activation,
-                  const uint16_t *dZ, int64_t ldz, const void *db0, const void *db1, int db_dtype, int n, int N,
-                  int64_t pre_cols, int64_t dz_cols)
+// A backward call: dZ (unless dY serves as it is), the bias gradients, dX.
+struct Backward {
+    const uint8_t *codes_t, *scales_t;   // needed with dX
+    float gscale;
+    const void *dy;
+    const float *preact;
+    uint16_t *dx;
+    void *db[2];
+    int64_t ldy, ldp, ldx;
+    int dy_dtype, db_dtype, act, n, N, K;
+    float gate_gscale, up_gscale;
+    bool gated;
+
+    int rows() const { return gated ? (int)gated_rows(N) : (N + 7) / 8 * 8; }   // columns of dZ
+};
+
+size_t round256(size_t bytes)
 {
-    if (n > 0 && (!dY || (!preact && activation != NVFP4_ACT_NONE)))
+    return (bytes + 255) / 256 * 256;
+}
+
+// Parts of the workspace, each on a multiple of 256 bytes.
+struct BackwardSpace {
+    size_t dz, sums, parts;
+    size_t total() const { return dz + sums + parts; }
+};
+
+BackwardSpace backward_space(int n, int N, int K, bool gated, bool dx, bool db, bool copy)
+{
+    const int rows = gated ? (int)gated_rows(N) : (N + 7) / 8 * 8;
+    BackwardSpace w = {};
+    if (n < 1)
+        return w;
+    if (dx && copy)
+        w.dz = round256((size_t)n * rows * 2);
+    if (db)
+        w.sums = round256(grad_bytes(n, gated ? rows / 2 : rows, gated ? 2 : 1));
+    if (dx) {
+        const int ks = nvfp4_plan_fused_gemm(n, K / 16, rows).ks;
+        w.parts = ks > 1 ? round256((size_t)ks * n * K * sizeof(float)) : 0;
+    }
+    return w;
+}
+
+// dY's rows can be loaded by the product as they are.
+bool usable_rows(const void *p, int dtype, int64_t ld, int n, int N)
+{
+    return dtype == NVFP4_DTYPE_BF16 && N % 8 == 0 && is_aligned(p, 16) && (n < 2 || (ld % 8 == 0 && ld <= kMaxStride));
+}
+
+int backward(const Backward &b, void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    const int n = b.n, N = b.N;
+    const bool sums = b.db[0] || b.db[1];
+    if (b.dx && (!b.codes_t || !b.scales_t))
         return NVFP4_ERR_NULL;
-    if (n < 0 || n > NVFP4_MAX_GEMM_TOKENS || N < 1 || N > (1 << 30))
+    if (n > 0 && (!b.dy || (!b.preact && (b.gated || b.act != NVFP4_ACT_NONE))))
+        return NVFP4_ERR_NULL;
+    if (n < 0 || n > NVFP4_MAX_GEMM_TOKENS || N < 1 || N > (1 << 29) || b.act < NVFP4_ACT_NONE ||
+        b.act > NVFP4_ACT_GELU_TANH || !valid_dtype(b.dy_dtype) || (sums && !valid_dtype(b.db_dtype)) ||
+        (b.dx && b.K < 1))
         return NVFP4_ERR_RANGE;
-    if (activation < NVFP4_ACT_NONE || activation > NVFP4_ACT_GELU_TANH || !valid_dtype(dy_dtype) ||
-        ((db0 || db1) && !valid_dtype(db_dtype)))
-        return NVFP4_ERR_RANGE;
-    if (ldy < N || (preact && ldp < pre_cols) || (dZ && ldz < dz_cols))
-        return NVFP4_ERR_RANGE;
-    if (ldy > INT32_MAX || ldp > INT32_MAX || ldz > INT32_MAX)
+    if (b.dx && (b.K % 16 != 0 || b.K > kMaxK))
         return NVFP4_ERR_SHAPE;
-    const int ds = dtype_size(dy_dtype), bs = dtype_size(db_dtype);
-    if (!is_aligned(dY, ds) || (preact && (!is_aligned(preact, 16) || ldp % 8 != 0)) ||
-        (dZ && (!is_aligned(dZ, 16) || ldz % 8 != 0)) || (db0 && !is_aligned(db0, bs)) || (db1 && !is_aligned(db1, bs)))
+    const int64_t pre_cols = b.gated ? b.rows() : N;
+    if (b.ldy < N || (b.preact && b.ldp < pre_cols) || (b.dx && b.ldx < b.K))
+        return NVFP4_ERR_RANGE;
+    if (b.ldy > INT32_MAX || b.ldp > INT32_MAX || b.ldx > INT32_MAX || (b.dx && b.rows() > kMaxStride))
+        return NVFP4_ERR_SHAPE;
+    const int ds = dtype_size(b.dy_dtype), bs = dtype_size(b.db_dtype);
+    if (!is_aligned(b.dy, ds) || (b.preact && (!is_aligned(b.preact, 16) || b.ldp % 8 != 0)) || !is_aligned(b.dx, 2) ||
+        !is_aligned(b.codes_t, 16) || !is_aligned(b.scales_t, 16) || !is_aligned(b.db[0], bs) || !is_aligned(b.db[1], bs))
         return NVFP4_ERR_ALIGN;
-    const size_t yn = span(n, ldy, N, ds), pn = preact ? span(n, ldp, pre_cols, 4) : 0;
-    const size_t zn = dZ ? span(n, ldz, dz_cols, 2) : 0, bn = (size_t)N * bs;
-    if (overlap(dZ, zn, dY, yn) || overlap(dZ, zn, preact, pn) || overlap(dZ, zn, db0, bn) || overlap(dZ, zn, db1, bn) ||
-        overlap(db0, bn, dY, yn) || overlap(db1, bn, dY, yn) || overlap(db0, bn, preact, pn) ||
-        overlap(db1, bn, preact, pn) || overlap(db0, bn, db1, bn))
-        return NVFP4_ERR_OVERLAP;
-    return NVFP4_OK;
+    const bool copy = b.gated || b.act != NVFP4_ACT_NONE || !usable_rows(b.dy, b.dy_dtype, b.ldy, n, N);
+    const BackwardSpace w = backward_space(n, N, b.K, b.gated, b.dx != nullptr, sums, copy);
+    if (w.total() && (!workspace || workspace_bytes < w.total()))
+        return NVFP4_ERR_WORKSPACE;
+    if (w.total() && !is_aligned(workspace, 16))
+        return NVFP4_ERR_ALIGN;
+    const size_t yn = span(n, b.ldy, N, ds), pn = b.preact ? span(n, b.ldp, pre_cols, 4) : 0, bn = (size_t)N * bs;
+    const size_t xn = b.dx ? span(n, b.ldx, b.K, 2) : 0;
+    const size_t ct = b.dx ? nvfp4_transposed_codes_bytes(b.rows(), b.K) : 0;
+    const size_t st = b.dx ? nvfp4_transposed_scales_bytes(b.rows(), b.K) : 0;
+    const struct { const void *p; size_t size; } out[] = {{b.dx, xn}, {b.db[0], bn}, {b.db[1], bn}, {workspace, w.total()}},
+        in[] = {{b.dy, yn}, {b.preact, pn}, {b.codes_t, ct}, {b.scales_t, st}};
+    for (int i = 0; i < 4; ++i) {
+        for (const auto &q : in)
+            if (overlap(out[i].p, out[i].size, q.p, q.size))
+                return NVFP4_ERR_OVERLAP;
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i].p, out[i].size, out[j].p, out[j].size))
+                return NVFP4_ERR_OVERLAP;
+    }
+    int cus = 0;
+    int status = nvfp4_device_cus(&cus);
+    if (status != NVFP4_OK)
+        return status;
+    char *ws = static_cast<char *>(workspace);
+    GradParams p = {};
+    p.dy = b.dy;
+    p.z = b.act == NVFP4_ACT_NONE && !b.gated ? nullptr : b.preact;
+    p.dz = w.dz ? reinterpret_cast<uint16_t *>(ws) : nullptr;
+    p.partial = reinterpret_cast<float *>(ws + w.dz);
+    p.db[0] = b.db[0];
+    p.db[1] = b.db[1];
+    p.ldy = b.ldy;
+    p.ldz = b.ldp;
+    p.lddz = b.rows();
+    p.n = n;
+    p.N = N;
+    p.cols = b.gated ? b.rows() / 2 : b.rows();
+    p.act = b.act;
+    p.dy_f32 = b.dy_dtype == NVFP4_DTYPE_F32;
+    p.db_f32 = b.db_dtype == NVFP4_DTYPE_F32;
+    p.vec = b.ldy % 4 == 0 && is_aligned(b.dy, 4 * ds);
+    p.gscale[0] = b.gate_gscale;
+    p.gscale[1] = b.up_gscale;
+    status = launch_grad(p, b.gated, stream);
+    if (status != NVFP4_OK || !b.dx || n == 0)
+        return status;
+    nvfp4_epilogue ep = {};
+    ep.out_dtype = ep.bias_dtype = ep.residual_dtype = NVFP4_DTYPE_BF16;
+    nvfp4_fused_gemm_args a = {};
+    a.mode = 2;
+    a.codes = b.codes_t;
+    a.scales = b.scales_t;
+    a.X = w.dz ? p.dz : static_cast<const uint16_t *>(b.dy);
+    a.ldx = w.dz ? p.lddz : b.ldy;
+    a.n = n;
+    a.K = b.rows();
+    a.row_groups = b.K / 16;
+    a.epi = epi_params(&ep, b.gscale, 0.f, b.dx, b.ldx, b.K, b.K);
+    return launch_product(a, w.parts ? ws + w.dz + w.sums : nullptr, w.parts, stream);
 }
 
 unsigned blocks_of(long long items)
@@ -689,120 +785,72 @@ int nvfp4_gated(const uint8_t *Wq, const uint8_t *Wscale, float gate_gscale, flo
 
 // ---- backward ----
 
-size_t nvfp4_grad_workspace_bytes(int n, int N, int gated)
+size_t nvfp4_linear_backward_workspace_bytes(int n, int N, int K, int dx, int dbias, int copy)
 {
-    if (n < 0 || n > NVFP4_MAX_GEMM_TOKENS || N < 1 || N > (1 << 29))
+    if (n < 1 || n > NVFP4_MAX_GEMM_TOKENS || N < 1 || N > (1 << 29) || (dx && (K < 1 || K % 16 != 0 || K > kMaxK)))
         return 0;
-    return gated ? grad_bytes(n, (int)(gated_rows(N) / 2), 2) : grad_bytes(n, (N + 7) / 8 * 8, 1);
+    return backward_space(n, N, K, false, dx != 0, dbias != 0, copy != 0).total();
 }
 
-int nvfp4_linear_grad(const void *dY, int dy_dtype, int64_t ldy, const float *preact, int64_t ldp, int activation,
-                      uint16_t *dZ, int64_t ldz, void *dbias, int bias_dtype, int n, int N, void *workspace,
-                      size_t workspace_bytes, void *stream)
+int nvfp4_linear_backward(const uint8_t *codes_t, const uint8_t *scales_t, float gscale, const void *dY, int dy_dtype,
+                          int64_t ldy, const float *preact, int64_t ldp, int activation, uint16_t *dX, int64_t ldx,
+                          void *dbias, int bias_dtype, int n, int N, int K, void *workspace, size_t workspace_bytes,
+                          void *stream)
 {
-    const int cols = N > 0 && N <= (1 << 29) ? (N + 7) / 8 * 8 : 0;
-    if (!cols)
-        return NVFP4_ERR_RANGE;
-    const int st = validate_grad(dY, dy_dtype, ldy, preact, ldp, activation, dZ, ldz, dbias, nullptr, bias_dtype, n, N,
-                                 N, cols);
-    if (st != NVFP4_OK)
-        return st;
-    GradParams p = {};
-    p.dy = dY;
-    p.z = activation == NVFP4_ACT_NONE ? nullptr : preact;
-    p.dz = dZ;
-    p.db[0] = dbias;
-    p.ldy = ldy;
-    p.ldz = ldp;
-    p.lddz = ldz;
-    p.n = n;
-    p.N = N;
-    p.cols = cols;
-    p.act = activation;
-    p.dy_f32 = dy_dtype == NVFP4_DTYPE_F32;
-    p.db_f32 = bias_dtype == NVFP4_DTYPE_F32;
-    p.vec = ldy % 4 == 0 && is_aligned(dY, 4 * dtype_size(dy_dtype));
-    return launch_grad(p, false, workspace, workspace_bytes, (hipStream_t)stream);
+    Backward b = {};
+    b.codes_t = codes_t;
+    b.scales_t = scales_t;
+    b.gscale = gscale;
+    b.dy = dY;
+    b.dy_dtype = dy_dtype;
+    b.ldy = ldy;
+    b.preact = preact;
+    b.ldp = ldp;
+    b.act = activation;
+    b.dx = dX;
+    b.ldx = ldx;
+    b.db[0] = dbias;
+    b.db_dtype = bias_dtype;
+    b.n = n;
+    b.N = N;
+    b.K = K;
+    return backward(b, workspace, workspace_bytes, (hipStream_t)stream);
 }
 
-int nvfp4_gated_grad(const void *dH, int dh_dtype, int64_t ldh, const float *preact, int64_t ldp, int activation,
-                     float gate_gscale, float up_gscale, uint16_t *dZ, int64_t ldz, void *dgate_bias, void *dup_bias,
-                     int bias_dtype, int n, int F, void *workspace, size_t workspace_bytes, void *stream)
+size_t nvfp4_gated_backward_workspace_bytes(int n, int F, int K, int dx, int dbias)
 {
-    if (F < 1 || F > (1 << 29))
-        return NVFP4_ERR_RANGE;
-    if (n > 0 && !preact)
-        return NVFP4_ERR_NULL;
-    const int64_t rows = gated_rows(F);
-    const int st = validate_grad(dH, dh_dtype, ldh, preact, ldp, activation, dZ, ldz, dgate_bias, dup_bias, bias_dtype,
-                                 n, F, rows, rows);
-    if (st != NVFP4_OK)
-        return st;
-    GradParams p = {};
-    p.dy = dH;
-    p.z = preact;
-    p.dz = dZ;
-    p.db[0] = dgate_bias;
-    p.db[1] = dup_bias;
-    p.ldy = ldh;
-    p.ldz = ldp;
-    p.lddz = ldz;
-    p.n = n;
-    p.N = F;
-    p.cols = (int)(rows / 2);
-    p.act = activation;
-    p.dy_f32 = dh_dtype == NVFP4_DTYPE_F32;
-    p.db_f32 = bias_dtype == NVFP4_DTYPE_F32;
-    p.vec = ldh % 4 == 0 && is_aligned(dH, 4 * dtype_size(dh_dtype));
-    p.gscale[0] = gate_gscale;
-    p.gscale[1] = up_gscale;
-    return launch_grad(p, true, workspace, workspace_bytes, (hipStream_t)stream);
-}
-
-size_t nvfp4_gemm_t_workspace_bytes(int n, int N, int K)
-{
-    if (n < 1 || n > NVFP4_MAX_GEMM_TOKENS || N < 1 || N > (1 << 30) || K < 1 || K % 16 != 0 || K > kMaxK)
+    if (n < 1 || n > NVFP4_MAX_GEMM_TOKENS || F < 1 || F > (1 << 29) || (dx && (K < 1 || K % 16 != 0 || K > kMaxK)))
         return 0;
-    const int ks = nvfp4_plan_fused_gemm(n, K / 16, (N + 7) / 8 * 8).ks;
-    return ks > 1 ? (size_t)ks * n * K * sizeof(float) : 0;
+    return backward_space(n, F, K, true, dx != 0, dbias != 0, true).total();
 }
 
-int nvfp4_gemm_t(const uint8_t *codes_t, const uint8_t *scales_t, float gscale, const uint16_t *dY, int64_t ldy,
-                 uint16_t *dX, int64_t ldx, int n, int N, int K, void *workspace, size_t workspace_bytes, void *stream)
+int nvfp4_gated_backward(const uint8_t *codes_t, const uint8_t *scales_t, float gate_gscale, float up_gscale,
+                         const void *dH, int dh_dtype, int64_t ldh, const float *preact, int64_t ldp, int activation,
+                         uint16_t *dX, int64_t ldx, void *dgate_bias, void *dup_bias, int bias_dtype, int n, int F,
+                         int K, void *workspace, size_t workspace_bytes, void *stream)
 {
-    if (!codes_t || !scales_t || (n > 0 && (!dY || !dX)))
-        return NVFP4_ERR_NULL;
-    if (n < 0 || n > NVFP4_MAX_GEMM_TOKENS || N < 1 || N > (1 << 30) || K < 1)
-        return NVFP4_ERR_RANGE;
-    if (K % 16 != 0 || K > kMaxK)
-        return NVFP4_ERR_SHAPE;
-    const int cols = (N + 7) / 8 * 8;
-    if (ldy < (n > 1 ? cols : N) || ldx < K)
-        return NVFP4_ERR_RANGE;
-    if (ldy > kMaxStride || ldx > INT32_MAX)
-        return NVFP4_ERR_SHAPE;
-    if (!is_aligned(codes_t, 16) || !is_aligned(scales_t, 16) || !is_aligned(dY, 16) || (n > 1 && ldy % 8 != 0) ||
-        !is_aligned(dX, 2))
-        return NVFP4_ERR_ALIGN;
-    const size_t yn = span(n, ldy, cols, 2), xn = span(n, ldx, K, 2);
-    if (overlap(dX, xn, dY, yn) || overlap(dX, xn, codes_t, nvfp4_transposed_codes_bytes(N, K)) ||
-        overlap(dX, xn, scales_t, nvfp4_transposed_scales_bytes(N, K)))
-        return NVFP4_ERR_OVERLAP;
-    if (n == 0)
-        return NVFP4_OK;
-    nvfp4_epilogue ep = {};
-    ep.out_dtype = ep.bias_dtype = ep.residual_dtype = NVFP4_DTYPE_BF16;
-    nvfp4_fused_gemm_args a = {};
-    a.mode = 2;
-    a.codes = codes_t;
-    a.scales = scales_t;
-    a.X = dY;
-    a.ldx = ldy;
-    a.n = n;
-    a.K = cols;
-    a.row_groups = K / 16;
-    a.epi = epi_params(&ep, gscale, 0.f, dX, ldx, K, K);
-    return launch_product(a, workspace, workspace_bytes, (hipStream_t)stream);
+    Backward b = {};
+    b.codes_t = codes_t;
+    b.scales_t = scales_t;
+    b.gscale = 1.0f;   // the gradient rows carry the two tensor scales
+    b.gate_gscale = gate_gscale;
+    b.up_gscale = up_gscale;
+    b.dy = dH;
+    b.dy_dtype = dh_dtype;
+    b.ldy = ldh;
+    b.preact = preact;
+    b.ldp = ldp;
+    b.act = activation;
+    b.dx = dX;
+    b.ldx = ldx;
+    b.db[0] = dgate_bias;
+    b.db[1] = dup_bias;
+    b.db_dtype = bias_dtype;
+    b.n = n;
+    b.N = F;
+    b.K = K;
+    b.gated = true;
+    return backward(b, workspace, workspace_bytes, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -47,12 +47,12 @@ _SIGNATURES = {
     "nvfp4_transposed_codes_bytes": (_SIZE, [_i32, _i32]),
     "nvfp4_transposed_scales_bytes": (_SIZE, [_i32, _i32]),
     "nvfp4_pack_transposed": (_i32, [_vp, _vp, _i32, _i32, _vp, _vp, _vp]),
-    "nvfp4_gemm_t": (_i32, [_vp, _vp, _F32, _vp, _i64, _vp, _i64, _i32, _i32, _i32, _vp, _SIZE, _vp]),
-    "nvfp4_gemm_t_workspace_bytes": (_SIZE, [_i32, _i32, _i32]),
-    "nvfp4_linear_grad": (_i32, [_vp, _i32, _i64, _vp, _i64, _i32, _vp, _i64, _vp, _i32, _i32, _i32, _vp, _SIZE, _vp]),
-    "nvfp4_gated_grad": (_i32, [_vp, _i32, _i64, _vp, _i64, _i32, _F32, _F32, _vp, _i64, _vp, _vp, _i32, _i32, _i32,
-                                _vp, _SIZE, _vp]),
-    "nvfp4_grad_workspace_bytes": (_SIZE, [_i32, _i32, _i32]),
+    "nvfp4_linear_backward": (_i32, [_vp, _vp, _F32, _vp, _i32, _i64, _vp, _i64, _i32, _vp, _i64, _vp, _i32, _i32, _i32,
+                                     _i32, _vp, _SIZE, _vp]),
+    "nvfp4_linear_backward_workspace_bytes": (_SIZE, [_i32] * 6),
+    "nvfp4_gated_backward": (_i32, [_vp, _vp, _F32, _F32, _vp, _i32, _i64, _vp, _i64, _i32, _vp, _i64, _vp, _vp, _i32,
+                                    _i32, _i32, _i32, _vp, _SIZE, _vp]),
+    "nvfp4_gated_backward_workspace_bytes": (_SIZE, [_i32] * 5),
 }
 
 
@@ -405,12 +405,6 @@ def gated(w: GatedWeight, X: torch.Tensor, activation: str = "silu", gate_bias: 
 
 # ---- backward ------------------------------------------------------------------------
 
-def _rows_ok(t) -> bool:
-    """Rows gemm_t can load as they are."""
-    return (t.dtype == torch.bfloat16 and t.shape[1] % 8 == 0 and t.data_ptr() % 16 == 0 and
-            (t.shape[0] < 2 or t.stride(0) % 8 == 0))
-
-
 def _incoming(dY, n, N, name):
     """A gradient as autograd hands it over: any strides."""
     if not isinstance(dY, torch.Tensor) or not dY.is_cuda:
@@ -420,47 +414,37 @@ def _incoming(dY, n, N, name):
     return _mat(dY, _FLOATS, name, n, N)
 
 
-def _gemm_t_launch(wt, dZ, out, at):
-    n = dZ.shape[0]
-    dX = out if out is not None else at.alloc(n, wt.K, dtype=torch.bfloat16)
-    ws, size, keep = at.workspace(None, int(_call("nvfp4_gemm_t_workspace_bytes")(n, wt.N, wt.K)))
-    _run("nvfp4_gemm_t", wt.codes.data_ptr(), wt.scales.data_ptr(), wt.gscale, dZ.data_ptr(), _ld(dZ),
-         dX.data_ptr(), _ld(dX), n, wt.N, wt.K, ws, size, at.handle)
-    return dX
-
-
 def _linear_backward(wt, dY, act, preact, bias_dtype, out, stream):
     dY = _incoming(dY, None, wt.N if wt is not None else dY.shape[-1], "dY")
     n, N = dY.shape
-    at = _Launch(stream, dY, preact, out, *((wt.codes, wt.scales) if wt is not None else ()))
-    db = at.alloc(N, dtype=bias_dtype) if bias_dtype is not None else None
-    dZ = None
-    if wt is not None and (act or not _rows_ok(dY)):
-        dZ = at.alloc(n, _pad8(N), dtype=torch.bfloat16)
-    if db is not None or dZ is not None:
-        need = int(_call("nvfp4_grad_workspace_bytes")(n, N, 0)) if db is not None else 0
-        ws, size, keep = at.workspace(None, need)
-        _run("nvfp4_linear_grad", dY.data_ptr(), _DTYPES[dY.dtype], _ld(dY), _ptr(preact),
-             _ld(preact) if preact is not None else 0, act, _ptr(dZ), _pad8(N), _ptr(db),
-             _DTYPES[bias_dtype] if db is not None else 1, n, N, ws, size, at.handle)
-    dX = _gemm_t_launch(wt, dY if dZ is None else dZ, out, at) if wt is not None else None
+    codes, scales, gscale, K = (wt.codes, wt.scales, wt.gscale, wt.K) if wt is not None else (None, None, 0.0, 0)
+    at = _Launch(stream, dY, preact, out, codes, scales)
+    dX = (at.alloc(n, K, dtype=torch.bfloat16) if out is None else out) if wt is not None else None
+    db = None if bias_dtype is None else at.alloc(N, dtype=bias_dtype)
+    ld, dtype, ptr = _ld(dY), _DTYPES[dY.dtype], dY.data_ptr()
+    copy = act or dtype == 0 or N % 8 or ptr % 16 or (n > 1 and (ld % 8 or ld > 1 << 22))
+    ws, size, keep = at.workspace(None, _call("nvfp4_linear_backward_workspace_bytes")(
+        n, N, K, wt is not None, db is not None, 1 if copy else 0))
+    _run("nvfp4_linear_backward", _ptr(codes), _ptr(scales), gscale, ptr, dtype, ld, _ptr(preact),
+         0 if preact is None else _ld(preact), act, _ptr(dX), K if dX is None else _ld(dX), _ptr(db),
+         1 if db is None else _DTYPES[bias_dtype], n, N, K, ws, size, at.handle)
     return dX, db
 
 
 def _gated_backward(w, wt, dH, act, preact, gate_dtype, up_dtype, out, stream):
     dH = _incoming(dH, None, w.F, "dH")
-    n, rows = dH.shape[0], gated_rows(w.F)
-    at = _Launch(stream, dH, preact, out, *((wt.codes, wt.scales) if wt is not None else ()))
-    dg = at.alloc(w.F, dtype=gate_dtype) if gate_dtype is not None else None
-    du = at.alloc(w.F, dtype=up_dtype) if up_dtype is not None else None
-    dZ = at.alloc(n, rows, dtype=torch.bfloat16) if wt is not None else None
+    n, F, K = dH.shape[0], w.F, w.K
+    codes, scales = (wt.codes, wt.scales) if wt is not None else (None, None)
+    at = _Launch(stream, dH, preact, out, codes, scales)
+    dX = (at.alloc(n, K, dtype=torch.bfloat16) if out is None else out) if wt is not None else None
+    dg = None if gate_dtype is None else at.alloc(F, dtype=gate_dtype)
+    du = None if up_dtype is None else at.alloc(F, dtype=up_dtype)
     some = gate_dtype if gate_dtype is not None else up_dtype
-    need = int(_call("nvfp4_grad_workspace_bytes")(n, w.F, 1)) if some is not None else 0
-    ws, size, keep = at.workspace(None, need)
-    _run("nvfp4_gated_grad", dH.data_ptr(), _DTYPES[dH.dtype], _ld(dH), preact.data_ptr(), _ld(preact), act,
-         w.gate_gscale, w.up_gscale, _ptr(dZ), rows, _ptr(dg), _ptr(du),
-         _DTYPES[some] if some is not None else 1, n, w.F, ws, size, at.handle)
-    dX = _gemm_t_launch(wt, dZ, out, at) if wt is not None else None
+    ws, size, keep = at.workspace(None, _call("nvfp4_gated_backward_workspace_bytes")(n, F, K, wt is not None,
+                                                                                     some is not None))
+    _run("nvfp4_gated_backward", _ptr(codes), _ptr(scales), w.gate_gscale, w.up_gscale, dH.data_ptr(),
+         _DTYPES[dH.dtype], _ld(dH), preact.data_ptr(), _ld(preact), act, _ptr(dX), K if dX is None else _ld(dX),
+         _ptr(dg), _ptr(du), 1 if some is None else _DTYPES[some], n, F, K, ws, size, at.handle)
     return dX, dg, du
 
 

@@ -91,29 +91,53 @@ def test_gated_refuses(kw, status):
     assert gated(**kw) == status
 
 
-@pytest.mark.parametrize("kw,status", [
-    (dict(c=None), NULL), (dict(dy=None), NULL), (dict(n=-1), RANGE), (dict(N=0), RANGE), (dict(K=40), SHAPE),
-    (dict(ldy=93), RANGE), (dict(ldy=100), ALIGN), (dict(dy=at(2) + 2), ALIGN), (dict(ldx=40), RANGE),
-    (dict(dx=at(2)), OVERLAP), (dict(dx=at(0)), OVERLAP), (dict(n=0), OK)])
-def test_gemm_t_refuses(kw, status):
-    a = dict(c=at(0), s=at(1), dy=at(2), ldy=96, dx=at(3), ldx=None, n=4, N=93, K=48)
+def linear_backward(**kw):
+    a = dict(c=at(0), s=at(1), dy=at(2), dt=1, ldy=93, z=at(3), ldp=96, act=2, dx=at(4), ldx=None, db=at(5), bt=0, n=4,
+             N=93, K=48, ws=at(6), size=1 << 30)
     a.update(kw)
     if a["ldx"] is None:
         a["ldx"] = a["K"]
-    assert fused._call("nvfp4_gemm_t")(a["c"], a["s"], 1.0, a["dy"], a["ldy"], a["dx"], a["ldx"], a["n"], a["N"],
-                                       a["K"], None, 0, None) == status
+    return fused._call("nvfp4_linear_backward")(a["c"], a["s"], 1.0, a["dy"], a["dt"], a["ldy"], a["z"], a["ldp"],
+                                                a["act"], a["dx"], a["ldx"], a["db"], a["bt"], a["n"], a["N"], a["K"],
+                                                a["ws"], a["size"], None)
+
+
+BACKWARD = [
+    (dict(dy=None), NULL), (dict(z=None), NULL), (dict(c=None), NULL), (dict(n=-1), RANGE), (dict(act=9), RANGE),
+    (dict(dt=3), RANGE), (dict(bt=2), RANGE), (dict(N=0), RANGE), (dict(K=0), RANGE), (dict(K=40), SHAPE),
+    (dict(ldy=90), RANGE), (dict(ldp=88), RANGE), (dict(ldx=40), RANGE), (dict(ldp=95), ALIGN), (dict(dx=at(4) + 1), ALIGN),
+    (dict(dy=at(2) + 1), ALIGN), (dict(db=at(5) + 2), ALIGN), (dict(ws=at(6) + 8), ALIGN), (dict(ws=None), WORKSPACE),
+    (dict(size=4 * 96 * 2 - 1), WORKSPACE), (dict(dx=at(2)), OVERLAP), (dict(dx=at(0)), OVERLAP), (dict(db=at(4)), OVERLAP),
+    (dict(db=at(3)), OVERLAP), (dict(ws=at(4) - 256), OVERLAP), (dict(ws=at(2) - 256), OVERLAP),
+    (dict(ldy=(1 << 31)), SHAPE), (dict(n=4000, N=2000, ldy=2000, ldp=2000, act=0, dx=None, size=15), WORKSPACE)]
+
+
+@pytest.mark.parametrize("kw,status", BACKWARD)
+def test_linear_backward_refuses(kw, status):
+    assert linear_backward(**kw) == status
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(dy=None), NULL), (dict(z=None), NULL), (dict(n=-1), RANGE), (dict(act=9), RANGE), (dict(dt=3), RANGE),
-    (dict(ldy=90), RANGE), (dict(ldz=88), RANGE), (dict(ldz=100), ALIGN), (dict(dz=at(4) + 2), ALIGN),
-    (dict(ldp=95), ALIGN), (dict(dz=at(2)), OVERLAP), (dict(db=at(4)), OVERLAP), (dict(db=at(3)), OVERLAP),
-    (dict(n=4000, N=2000, ldy=2000, ldp=2000, ldz=2000), WORKSPACE)])
-def test_linear_grad_refuses(kw, status):
-    a = dict(dy=at(2), dt=1, ldy=93, z=at(3), ldp=96, act=2, dz=at(4), ldz=96, db=at(5), bt=0, n=4, N=93)
+    (dict(z=None), NULL), (dict(F=0), RANGE), (dict(ldp=64), RANGE), (dict(dg=at(4)), OVERLAP), (dict(du=at(5)), OVERLAP),
+    (dict(ws=None), WORKSPACE), (dict(K=40), SHAPE), (dict(s=None), NULL), (dict(act=-1), RANGE)])
+def test_gated_backward_refuses(kw, status):
+    a = dict(c=at(0), s=at(1), dy=at(2), z=at(3), ldp=96, act=2, dx=at(4), dg=at(5), du=at(7), n=4, F=33, K=48, ws=at(6))
     a.update(kw)
-    assert fused._call("nvfp4_linear_grad")(a["dy"], a["dt"], a["ldy"], a["z"], a["ldp"], a["act"], a["dz"], a["ldz"],
-                                            a["db"], a["bt"], a["n"], a["N"], None, 0, None) == status
+    f = a["F"]
+    assert fused._call("nvfp4_gated_backward")(a["c"], a["s"], 1.0, 1.0, a["dy"], 1, f, a["z"], a["ldp"], a["act"],
+                                               a["dx"], a["K"], a["dg"], a["du"], 0, a["n"], f, a["K"], a["ws"],
+                                               1 << 20, None) == status
+
+
+def test_backward_workspace():
+    f = fused._call("nvfp4_linear_backward_workspace_bytes")
+    assert f(4, 96, 48, 1, 0, 0) == 0                # dY as it is, one part, no sums
+    assert f(4, 93, 48, 1, 0, 1) == 768              # dZ: 4 x 96 bf16
+    assert f(4, 93, 48, 0, 0, 1) == 0 and f(0, 93, 48, 1, 1, 1) == 0
+    assert f(4000, 2000, 48, 0, 1, 1) > 0            # column sums of row blocks
+    assert fused._call("nvfp4_gated_backward_workspace_bytes")(4, 33, 48, 1, 0) == 4 * 96 * 2
+    # no GPU, no tokens: refused only where memory would be touched
+    assert linear_backward(n=0, db=None, dx=None) in (OK, DEVICE)
 
 
 def test_pack_refuses():
