@@ -24,14 +24,38 @@ constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kTanhC = 1.5957691216057308f;    // 2 sqrt(2 / pi)
 constexpr float kTanhA = 0.044715f;
 
-// act(z).  gelu is z Phi(z) with Phi from erfc, so that its left tail keeps
-// its relative precision; gelu_tanh is 0.5 z (1 + tanh(u)) = z sigmoid(2u).
+// Phi(z), the normal distribution function, as 1 - erfc(x) / 2 for z = sqrt(2) x
+// >= 0 and erfc(x) / 2 for -z.  erfc(x) = t exp(p(t) - x^2) with t = 1 / (1 +
+// 0.4 x): p is a Chebyshev fit of degree 9, in t, of ln(erfc(x) exp(x^2) / t),
+// relative error 5e-8 before rounding and 9e-7 (x < 3.6) in fp32.  The math
+// library's erfc takes about four times the instructions: gelu added 22 us to
+// the 150 of 16384 x 5120 at n = 1024, and adds 10 this way.
+__device__ __forceinline__ float normal_cdf(float z)
+{
+    const float x = fabsf(z) * kSqrtHalf;
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.4f, x, 1.0f));
+    float p = 0.0683646575f;
+    p = __builtin_fmaf(p, t, -0.581891f);
+    p = __builtin_fmaf(p, t, 1.81158173f);
+    p = __builtin_fmaf(p, t, -2.67597985f);
+    p = __builtin_fmaf(p, t, 1.99297822f);
+    p = __builtin_fmaf(p, t, -0.977739036f);
+    p = __builtin_fmaf(p, t, 0.484770298f);
+    p = __builtin_fmaf(p, t, 0.360483378f);
+    p = __builtin_fmaf(p, t, 1.0063802f);
+    p = __builtin_fmaf(p, t, -1.48894858f);
+    const float half = 0.5f * t * __expf(__builtin_fmaf(-x, x, p));
+    return z < 0.0f ? half : 1.0f - half;
+}
+
+// act(z).  gelu is z Phi(z), whose left tail keeps its relative precision;
+// gelu_tanh is 0.5 z (1 + tanh(u)) = z sigmoid(2u).
 __device__ __forceinline__ float activate(float z, int act)
 {
     switch (act) {
     case NVFP4_ACT_RELU: return z < 0.0f ? 0.0f : z;   // NaN stays NaN
     case NVFP4_ACT_SILU: return z * sigmoid_f(z);
-    case NVFP4_ACT_GELU: return 0.5f * z * erfcf(-z * kSqrtHalf);
+    case NVFP4_ACT_GELU: return z * normal_cdf(z);
     case NVFP4_ACT_GELU_TANH: return z * sigmoid_f(kTanhC * (z + kTanhA * z * z * z));
     default: return z;
     }
@@ -47,7 +71,7 @@ __device__ __forceinline__ float activate_grad(float z, int act)
         return s * (1.0f + z * (1.0f - s));
     }
     case NVFP4_ACT_GELU:
-        return 0.5f * erfcf(-z * kSqrtHalf) + z * kInvSqrt2Pi * __expf(-0.5f * z * z);
+        return normal_cdf(z) + z * kInvSqrt2Pi * __expf(-0.5f * z * z);
     case NVFP4_ACT_GELU_TANH: {
         const float s = sigmoid_f(kTanhC * (z + kTanhA * z * z * z));
         return s + z * s * (1.0f - s) * kTanhC * (1.0f + 3.0f * kTanhA * z * z);
