@@ -44,19 +44,14 @@ __device__ __forceinline__ f32x2 scales2(u32 w)
 }
 
 // LDS-direct load: lane l's 16 bytes go to `lds` + 16 l (a wave-uniform LDS
-// address); offsets past the resource write zeros.  No register is written, so
-// only the vmcnt wait before the barrier orders it.
-__device__ __forceinline__ void load_lds_b128(u32x4 rsrc, unsigned voff, unsigned soff, unsigned lds)
+// address); offsets past the resource write zeros (the scalar offset stays 0:
+// the range check need not include it).  No register is written, so only the
+// vmcnt wait before the barrier orders it.  M0 is reserved, the compiler keeps
+// nothing in it; one wait state separates its write from the load.
+__device__ __forceinline__ void load_lds_b128(u32x4 rsrc, unsigned off, unsigned lds)
 {
-    asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-                 :: "v"(voff), "s"(rsrc), "s"(soff), "s"(lds) : "memory");   // M0 is reserved: the compiler keeps nothing in it
-}
-
-__device__ __forceinline__ u32x4 buffer_load_b128_s(u32x4 rsrc, unsigned voff, unsigned soff)
-{
-    u32x4 v;
-    asm volatile("buffer_load_dwordx4 %0, %1, %2, %3 offen" : "=v"(v) : "v"(voff), "s"(rsrc), "s"(soff));
-    return v;
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+                 :: "v"(off), "s"(rsrc), "s"(lds) : "memory");
 }
 
 // Byte address of LDS memory, as the M0 of an LDS-direct load takes it.
@@ -67,14 +62,15 @@ __device__ __forceinline__ unsigned lds_address(const void *p)
 
 // One workgroup: RW waves x RG row groups (16 * RW * RG weight rows) times 16 *
 // TB tokens, over the steps of one K part, which KG groups of RW waves take in
-// turn and whose sums they add through LDS in the end, in group order.  A step covers 128 contracted columns:
-// the tokens' slice and the scales go straight to LDS, each wave turns its own
-// code tiles into MFMA operands in registers.  The loads of step s + 1 are
-// issued before step s is computed and waited for after it: two LDS buffers,
-// which leave room for two workgroups a compute unit at the largest tile (a
-// third buffer, with the codes through LDS as well, measured no faster at 17 ..
-// 64 tokens: 16384 x 5120, n = 24: 17.0 against 16.8 us).  MODE: 0 linear, 1
-// gated (row groups alternate gate, up), 2 transposed weight, plain output.
+// turn and whose sums they add through LDS in the end, in group order.  A step
+// covers 128 contracted columns: the tokens' slice and the scales go straight
+// to LDS, each wave turns its own code tiles into MFMA operands in registers.
+// The loads of step s + 1 are issued before step s is computed and waited for
+// after it: two LDS buffers, which leave room for two workgroups a compute unit
+// at the largest tile (a third buffer, with the codes through LDS as well,
+// measured no faster at 17 .. 64 tokens: 16384 x 5120, n = 24: 17.0 against
+// 16.8 us).  MODE: 0 linear, 1 gated (row groups alternate gate, up), 2
+// transposed weight, plain output.
 //
 // LDS layout of the slice: token t's 16-byte chunk c (8 columns) at
 //     (t / 4) * kQuad + (t % 4) * 256 + (c ^ (t % 4)) * 16.
@@ -125,18 +121,25 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
     const int rg0 = (tx * RW + wave) * RG;
     const int tok0 = ty * BM;
     const int ntok = min(BM, p.n - tok0);
-    const int nrg = max(0, min(RG, p.RG - rg0)), rgb = min(rg0, p.RG);
     const int s0 = part * p.tp, s1 = min(p.T, s0 + p.tp);
     __shared__ __align__(1024) char lds[KG][2][kBuf];
 
-    // Loads past these ranges (tokens beyond n, row groups beyond RG) read
-    // zeros without touching memory.
-    const u32x4 xrsrc = uniform(buffer_rsrc(p.X + tok0 * p.ldx, (unsigned)(((ntok - 1) * p.ldx + p.K) * 2)));
+    // What lies past a resource (tokens beyond n, row groups beyond RG, and by an
+    // offset past all of them the columns beyond K) is read as zeros without
+    // touching memory.  Each quad of tokens has one of its own, so that a step
+    // needs one vector offset for all of them.
+    u32x4 xrsrc[XL];
+#pragma unroll
+    for (int u = 0; u < XL; ++u) {
+        const int t = tok0 + (wave * XL + u) * 4, live = min(4, p.n - t);
+        xrsrc[u] = uniform(live > 0 ? buffer_rsrc(p.X + t * p.ldx, (unsigned)(((live - 1) * p.ldx + p.K) * 2))
+                                    : buffer_rsrc(p.X, 0u));
+    }
+    const int nrg = max(0, min(RG, p.RG - rg0)), rgb = min(rg0, p.RG);
     const u32x4 crsrc = uniform(buffer_rsrc(p.codes + (size_t)rgb * p.T * 64, (unsigned)(nrg * p.T) * 1024u));
     const u32x4 srsrc = uniform(buffer_rsrc(p.scales + (size_t)rgb * p.T * 128, (unsigned)(nrg * p.T) * 128u));
-    const int ldx2 = (int)p.ldx * 2;
-    const int xcol = 8 * (i ^ g);   // lane (i, g) stages chunk i ^ g of token 4 q + g
-    const unsigned xoff = (unsigned)((wave * XL * 4 + g) * ldx2 + xcol * 2);
+    const int xcol = 8 * (i ^ g);   // lane (i, g) stages chunk i ^ g of token g of a quad
+    const unsigned xoff = (unsigned)(g * (int)p.ldx + xcol) * 2u;
     const unsigned soff = (unsigned)((lane >> 3) * p.T * 128 + (lane & 7) * 16);
     const unsigned ldsb = lds_address(lds[kg]) + wave * XL * kQuad;
     const unsigned ldss = lds_address(lds[kg]) + kSlice + wave * RG * 128;
@@ -144,15 +147,15 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
     u32x4 cw[RG];
     auto issue = [&](int s, int b) {
         const unsigned buf = b * kBuf;
-        const unsigned xv = s * kTileK + xcol < p.K ? xoff : kOutOfRange;
+        const unsigned xv = s * kTileK + xcol < p.K ? xoff + s * (kTileK * 2) : kOutOfRange;
 #pragma unroll
         for (int u = 0; u < XL; ++u)
-            load_lds_b128(xrsrc, xv, (unsigned)(u * 4 * ldx2 + s * 256), ldsb + buf + u * kQuad);
+            load_lds_b128(xrsrc[u], xv, ldsb + buf + u * kQuad);
         if (lane < 8 * RG)   // the wave's 128 RG bytes of scales
-            load_lds_b128(srsrc, soff, (unsigned)(s * 128), ldss + buf);
+            load_lds_b128(srsrc, soff + s * 128, ldss + buf);
 #pragma unroll
         for (int r = 0; r < RG; ++r)
-            cw[r] = buffer_load_b128_s(crsrc, (unsigned)(lane * 16), (unsigned)((r * p.T + s) * 1024));
+            cw[r] = buffer_load_b128(crsrc, (unsigned)((r * p.T + s) * 1024 + lane * 16));
     };
     auto land = [&]() {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");

@@ -8,8 +8,10 @@ to the activations, the biases and the residual).
 
 Both are differentiable when given the weight's transposed copy
 (``transposed=w.transpose()``, made once); ``linear_backward`` and
-``gated_backward`` are the same gradients without autograd, for captured
-graphs and programs that run their own backward pass.
+``gated_backward`` are the same gradients without autograd, for programs that
+run their own backward pass and for captured graphs (torch ends the process
+where an autograd pass is captured while an eager graph of the same leaves is
+alive; these functions have no such graph).
 
 Every launch goes to ``stream`` (the current stream by default).  Results and
 temporary memory are allocated on it, and tensors of the call are recorded on
@@ -306,7 +308,7 @@ def _check_grad(X, transposed, N, K, stream, *buffers):
 class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, X, bias, residual, w, transposed, act, out_dtype):
-        ctx.transposed, ctx.act, ctx.N = transposed, act, w.N
+        ctx.transposed, ctx.act = transposed, act
         ctx.bias_dtype = None if bias is None else bias.dtype
         ctx.residual_dtype = None if residual is None else residual.dtype
         preact = None
