@@ -343,6 +343,15 @@ int nvfp4_linear(const uint8_t *Wq, const uint8_t *Wscale, float gscale, const u
                  void *workspace, size_t workspace_bytes, void *stream);
 size_t nvfp4_linear_workspace_bytes(int n, int N, int K);
 
+/* The tile the fused operators take for n > 16 tokens on a packed weight of
+ * `rows` rows and K contracted columns (gated: nvfp4_gated_rows(F) rows; the
+ * gradients: the weight's K as rows, its rows up to a multiple of 8 as K):
+ * weight rows and tokens of a workgroup, K groups inside it, K parts of the
+ * launch (with more than one, fp32 partial sums and a second launch).  Pure
+ * host function; returns a status (RANGE, SHAPE). */
+int nvfp4_fused_geometry(int n, int rows, int K, int *rows_per_workgroup, int *tokens_per_workgroup,
+                         int *k_groups, int *k_parts);
+
 /* Rows of the packed weight of a gated block with F outputs: its 16-row groups
  * alternate gate, up, so gate row r is row (r / 16) * 32 + r % 16 and up row r
  * lies 16 further; F is padded to 16.  0 if F < 1. */

@@ -402,5 +402,5 @@ def gemv_qkv(w: PackedWeight, X: torch.Tensor, rows, out_off, ldy: int,
     return Y
 
 
-from .fused import (ACTIVATIONS, GatedWeight, TransposedWeight, gated, gated_backward, gated_rows, gemm_t,  # noqa: E402
-                    linear, linear_backward, preact_columns, transpose)
+from .fused import (ACTIVATIONS, GatedWeight, TransposedWeight, fused_geometry, gated, gated_backward,  # noqa: E402
+                    gated_rows, gemm_t, linear, linear_backward, preact_columns, transpose)

@@ -744,6 +744,21 @@ int nvfp4_pack_transposed(const uint8_t *codes_packed, const uint8_t *scales_pac
 
 // ---- forward ----
 
+int nvfp4_fused_geometry(int n, int rows, int K, int *rows_per_workgroup, int *tokens_per_workgroup, int *k_groups,
+                         int *k_parts)
+{
+    if (!rows_per_workgroup || !tokens_per_workgroup || !k_groups || !k_parts)
+        return NVFP4_ERR_NULL;
+    if (n <= NVFP4_MAX_TOKENS || n > NVFP4_MAX_GEMM_TOKENS || rows < 1 || rows > (1 << 30) || K < 1 || K > (1 << 30))
+        return NVFP4_ERR_RANGE;
+    if (K % 8 != 0)
+        return NVFP4_ERR_SHAPE;
+    const nvfp4_fused_gemm_plan plan = nvfp4_plan_fused_gemm(n, (int)row_groups(rows), K);
+    nvfp4_fused_gemm_tile(plan.tile, rows_per_workgroup, tokens_per_workgroup, k_groups);
+    *k_parts = plan.ks;
+    return NVFP4_OK;
+}
+
 size_t nvfp4_linear_workspace_bytes(int n, int N, int K)
 {
     if (n < 0 || n > NVFP4_MAX_GEMM_TOKENS || N < 1 || K < 1 || K % 16 != 0 || K > kMaxK)

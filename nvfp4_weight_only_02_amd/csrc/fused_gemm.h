@@ -21,6 +21,7 @@ struct nvfp4_fused_gemm_plan {
 };
 
 NVFP4_HIDDEN nvfp4_fused_gemm_plan nvfp4_plan_fused_gemm(int n, int row_groups, int K);
+NVFP4_HIDDEN void nvfp4_fused_gemm_tile(int tile, int *rows, int *tokens, int *k_groups);
 
 NVFP4_HIDDEN int nvfp4_launch_fused_gemm(const nvfp4_fused_gemm_args &a, const nvfp4_fused_gemm_plan &plan,
                                          hipStream_t stream);

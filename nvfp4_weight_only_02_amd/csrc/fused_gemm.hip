@@ -426,6 +426,14 @@ nvfp4_fused_gemm_plan nvfp4_plan_fused_gemm(int n, int row_groups, int K)
     return best;
 }
 
+void nvfp4_fused_gemm_tile(int tile, int *rows, int *tokens, int *k_groups)
+{
+    const Tile &t = kTiles[tile];
+    *rows = kRowsPerGroup * t.rw * t.rg;
+    *tokens = 16 * t.tb;
+    *k_groups = t.kg;
+}
+
 int nvfp4_launch_fused_gemm(const nvfp4_fused_gemm_args &a, const nvfp4_fused_gemm_plan &plan, hipStream_t stream)
 {
     int cus = 0;

@@ -43,6 +43,7 @@ _SIGNATURES = {
     "nvfp4_linear": (_i32, [_vp, _vp, _F32, _vp, _i64, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _SIZE, _vp]),
     "nvfp4_linear_workspace_bytes": (_SIZE, [_i32, _i32, _i32]),
     "nvfp4_gated_rows": (_SIZE, [_i32]),
+    "nvfp4_fused_geometry": (_i32, [_i32, _i32, _i32] + [ctypes.POINTER(_i32)] * 4),
     "nvfp4_pack_gated": (_i32, [_vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp]),
     "nvfp4_gated": (_i32, [_vp, _vp, _F32, _F32, _vp, _i64, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _SIZE, _vp]),
     "nvfp4_gated_workspace_bytes": (_SIZE, [_i32, _i32, _i32]),
@@ -188,6 +189,14 @@ def transpose(w: PackedWeight, stream=None) -> TransposedWeight:
 def gated_rows(F: int) -> int:
     """Rows of the packed weight of a gated block with F outputs."""
     return int(_call("nvfp4_gated_rows")(F))
+
+
+def fused_geometry(n: int, rows: int, K: int) -> tuple:
+    """(weight rows, tokens of a workgroup, K groups in it, K parts) the fused
+    operators take for n > 16 tokens (nvfp4_fused_geometry)."""
+    v = [_i32() for _ in range(4)]
+    _run("nvfp4_fused_geometry", n, rows, K, *(ctypes.byref(x) for x in v))
+    return tuple(x.value for x in v)
 
 
 @dataclass

@@ -2,6 +2,8 @@
 refusal comes before any HIP call."""
 import numpy as np
 import pytest
+from hypothesis import given, settings
+from hypothesis import strategies as st
 
 import fused_reference as R
 import nvfp4_weight_only_02_amd as nv
@@ -168,3 +170,24 @@ def test_reference_gradients_are_differences(kind):
     diff = (R.act(z + t, kind) - R.act(z - t, kind)) / (2 * t)
     assert np.abs(diff - R.act_grad(z, kind)).max() < 1e-8
     assert np.abs(R.act_grad(z, kind)).max() <= R.LIP
+
+
+@settings(max_examples=300, deadline=None)
+@given(n=st.integers(17, 1 << 20), rows=st.integers(1, 1 << 17), T=st.integers(1, 2048), tail=st.sampled_from([0, 8, 16, 112]))
+def test_fused_geometry_rule(n, rows, T, tail):
+    K = T * 128 - tail if T * 128 > tail else 8
+    r, t, kg, ks = nv.fused_geometry(n, rows, K)
+    assert (r, t, kg) in {(64, 32, 4), (64, 32, 8), (64, 64, 4), (128, 64, 2), (256, 128, 2), (256, 128, 1)}
+    tiles = -(-K // 128)
+    tp = -(-tiles // ks)
+    assert 1 <= ks <= 12 and (ks - 1) * tp < tiles        # no part is empty
+    if K % 16 == 0 and K <= 1 << 18:
+        need = fused._call("nvfp4_linear_workspace_bytes")(n, rows, K)
+        assert need == (ks * n * -(-rows // 16) * 16 * 4 if ks > 1 else 0)
+
+
+def test_fused_geometry_refuses():
+    for args, status in (((16, 64, 256), RANGE), ((17, 0, 256), RANGE), ((17, 64, 0), RANGE), ((17, 64, 260), SHAPE)):
+        with pytest.raises(nv.Nvfp4Error) as e:
+            nv.fused_geometry(*args)
+        assert e.value.status == status

@@ -413,3 +413,141 @@ def test_refusals():
     with pytest.raises(nv.Nvfp4Error) as e:
         nv.linear(w, X, out=X.view(-1)[:200].view(5, 40))
     assert e.value.status == 10
+
+
+# ---- every tile of the many-token product -------------------------------------------
+
+def device_weight(N, K, seed):
+    """(PackedWeight, its 64-bit values on the device), quantised there."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    codes, scales, ts = nv.quantize(torch.randn(N, K, generator=g, device="cuda") * 0.05)
+    lut = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64, device="cuda")
+    nib = torch.stack((codes & 15, codes >> 4), dim=2).view(N, K)
+    v = torch.where(nib >= 8, -lut[(nib & 7).long()], lut[(nib & 7).long()])
+    s = scales.view(torch.float8_e4m3fn).double().repeat_interleave(16, dim=1)
+    gscale = float(ts[0].item())
+    return nv.PackedWeight.from_canonical(codes, scales, gscale, N, K), v * s * gscale
+
+
+def device_check(got, ref, bound, what):
+    err = (got.double() - ref).abs()
+    assert torch.isfinite(got).all(), what
+    assert (err <= bound).all(), "%s: worst err/bound %.3g" % (what, float((err / bound).max()))
+
+
+# (n, rows, K) of each tile (rows, tokens, K groups), in one part and in several,
+# with n, rows and K that end inside a tile
+TILES = [((64, 32, 4), 1, (45, 336, 656)), ((64, 32, 4), 2, (17, 80, 3088)),
+         ((64, 32, 8), 1, (17, 4112, 3088)), ((64, 32, 8), 2, (17, 4624, 8208)),
+         ((64, 64, 4), 1, (70, 6160, 272)), ((64, 64, 4), 2, (33, 2576, 8208)),
+         ((128, 64, 2), 1, (201, 5136, 272)), ((128, 64, 2), 2, (33, 3088, 8208)),
+         ((256, 128, 2), 1, (701, 8208, 656)), ((256, 128, 2), 2, (401, 5136, 6160)),
+         ((256, 128, 1), 1, (257, 16400, 272)), ((256, 128, 1), 2, (1001, 5136, 6160))]
+
+
+@pytest.mark.parametrize("tile,parts,shape", TILES)
+def test_every_tile(tile, parts, shape):
+    n, rows, K = shape
+    say("tile", tile, parts, shape)
+    w, W = device_weight(rows, K, 80)
+    X = randn((n, K), 81)
+    F = rows // 32 * 16 - 3
+    for geo in (nv.fused_geometry(n, rows, K), nv.fused_geometry(n, nv.gated_rows(F), K)):
+        assert geo[:3] == tile and min(geo[3], 2) == parts, geo
+    mag = X.double().abs() @ W.abs().t()
+    ref = X.double() @ W.t()
+    sums = (K + 32) * R.HALF_F32 * mag
+    device_check(nv.linear(w, X, out_dtype=F32), ref, sums + R.HALF_F32 * ref.abs(), "linear")
+    # the gated weight of the same number of packed rows
+    (g, Wg), (u, Wu) = device_weight(F, K, 82), device_weight(F, K, 83)
+    gw = nv.GatedWeight.from_packed(g, u)
+    G, U = X.double() @ Wg.t(), X.double() @ Wu.t()
+    eg = (K + 32) * R.HALF_F32 * (X.double().abs() @ Wg.abs().t())
+    eu = (K + 32) * R.HALF_F32 * (X.double().abs() @ Wu.abs().t())
+    device_check(nv.gated(gw, X, activation="none", out_dtype=F32), G * U,
+                 G.abs() * eu + U.abs() * eg + eg * eu + 2 * R.HALF_F32 * (G * U).abs(), "gated")
+    # the other way: a weight of K rows and `rows` columns
+    t, Wt = device_weight(K - 5, rows, 84)
+    dY = randn((n, K - 5), 85)
+    ref = dY.double() @ Wt
+    b = (K + 32) * R.HALF_F32 * (dY.double().abs() @ Wt.abs())
+    device_check(nv.gemm_t(t.transpose(), dY), ref, b + R.HALF_BF16 * (ref.abs() + b) + 2.0 ** -133, "gemm_t")
+
+
+def test_offsets_beyond_32_bits():
+    """Rows of the output, the residual and the pre-activations that lie more
+    than 2^31 elements into their buffers."""
+    say("far rows")
+    n, N, K, ld = 1100, 72, 144, 1 << 21
+    w, W = device_weight(N, K, 86)
+    X = randn((n, K), 87)
+    r = randn((n, N), 88)
+    far = torch.empty_strided((n, N), (ld, 1), dtype=BF16, device="cuda")
+    out = torch.empty_strided((n, N), (ld, 1), dtype=BF16, device="cuda")
+    pre = torch.empty_strided((n, N), (ld, 1), dtype=F32, device="cuda")
+    far.copy_(r)
+    assert torch.equal(nv.linear(w, X, activation="silu", residual=far, out=out, preact=pre),
+                       nv.linear(w, X, activation="silu", residual=r))
+    dY = randn((n, N), 89)
+    far.copy_(dY)
+    near = torch.empty(n, N, device="cuda")
+    near.copy_(pre)
+    wt = w.transpose()
+    for a, b in zip(nv.linear_backward(wt, far, "silu", pre, F32), nv.linear_backward(wt, dY, "silu", near, F32)):
+        assert torch.equal(a, b)
+    Xf = torch.empty_strided((n, K), (ld, 1), dtype=BF16, device="cuda")
+    Xf.copy_(X)
+    assert torch.equal(nv.linear(w, Xf), nv.linear(w, X))
+    assert torch.equal(nv.linear(w, Xf[1090:]), nv.linear(w, X[1090:]))
+
+
+# ---- every specialisation of the decode product -----------------------------------------
+
+@pytest.mark.parametrize("n", [1, 6, 11, 16])
+@pytest.mark.parametrize("exact", [True, False])
+@pytest.mark.parametrize("tiles", range(1, 9))
+def test_every_decode_variant(tiles, exact, n):
+    """The linear form without an epilogue gives the plain projection's bits, the
+    gated form without an activation the product of two fp32 projections."""
+    K, N = 1024 * tiles - (0 if exact else 112), 83
+    say("decode", tiles, exact, n)
+    assert nv.gemv_variant(n, N, K)[:3] == (tiles, (n + 3) // 4, int(exact))
+    (g, _), (u, _) = device_weight(N, K, 90), device_weight(N, K, 91)
+    X = randn((n, K), 92)
+    assert torch.equal(nv.linear(g, X), nv.gemv(g, X))
+    want = nv.linear(g, X, out_dtype=F32) * nv.linear(u, X, out_dtype=F32)
+    assert torch.equal(nv.gated(nv.GatedWeight.from_packed(g, u), X, activation="none", out_dtype=F32), want)
+
+
+# (128-column tiles a wave, N, K) of calls in K parts
+PARTS = [(1, 83, 8208), (1, 83, 30000), (2, 20000, 20480), (3, 1000, 9216), (4, 1003, 13312), (5, 1000, 17408),
+         (6, 1000, 24576), (7, 877, 59072), (8, 1000, 30000)]
+
+
+@pytest.mark.parametrize("n", [1, 6, 11, 16])
+@pytest.mark.parametrize("tiles,N,K", PARTS)
+def test_every_decode_part_variant(tiles, N, K, n):
+    say("decode parts", tiles, N, K, n)
+    assert nv.gemv_variant(n, N, K, 0)[0] == tiles and nv.gemv_kparts(N, K) > 1
+    (g, _), (u, _) = device_weight(N, K, 93), device_weight(N, K, 94)
+    X = randn((n, K), 95)
+    assert torch.equal(nv.linear(g, X), nv.gemv_ws(g, X))
+    H = nv.gated(nv.GatedWeight.from_packed(g, u), X, activation="none", out_dtype=F32)
+    G, U = nv.linear(g, X, out_dtype=F32), nv.linear(u, X, out_dtype=F32)
+    # the gated weight has more rows, so maybe another number of parts: the order of the sums
+    e = 64 * R.HALF_F32 * (G.abs().max() * U.abs().max())
+    assert (H - G * U).abs().max() <= e * (K / 64)
+
+
+@pytest.mark.parametrize("n", [3, 16])
+def test_decode_with_many_row_groups(n):
+    """More row groups a workgroup than LDS has places for: several batches."""
+    say("many rows", n)
+    N, K = 70003, 144
+    (g, _), (u, _) = device_weight(N, K, 96), device_weight(N, K, 97)
+    X = randn((n, K), 98)
+    r = randn((n, N), 99)
+    assert torch.equal(nv.linear(g, X), nv.gemv(g, X))
+    G, U = nv.linear(g, X, out_dtype=F32), nv.linear(u, X, out_dtype=F32)
+    assert torch.equal(nv.linear(g, X, residual=r), (G + r.float()).to(BF16))
+    assert torch.equal(nv.gated(nv.GatedWeight.from_packed(g, u), X, activation="none", out_dtype=F32), G * U)
