@@ -92,18 +92,20 @@ def _typed(t, dtypes, name: str) -> None:
 def _mat(t, dtypes, name: str, n, cols) -> torch.Tensor:
     """A device matrix of n rows (None: any) and cols columns, unit stride
     along a row."""
-    _typed(t, dtypes, name)
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes):
+        _typed(t, dtypes, name)
     shape = t.shape
     if len(shape) != 2 or shape[1] != cols or (n is not None and shape[0] != n):
         raise ValueError("%s must be [%s, %d], got %s" % (name, "n" if n is None else n, cols, list(shape)))
-    if cols > 1 and shape[0] > 0 and t.stride(1) != 1:
+    if t.stride(1) != 1 and cols > 1 and shape[0] > 0:
         raise ValueError("%s must have unit stride along a row" % name)
     return t
 
 
 def _ld(t) -> int:
     """Row stride in elements; of no meaning with fewer than two rows."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    shape = t.shape
+    return t.stride(0) if shape[0] > 1 else shape[1]
 
 
 def _vec(t, dtypes, name: str, size: int):
