@@ -418,17 +418,23 @@ def gated(w: GatedWeight, X: torch.Tensor, activation: str = "silu", gate_bias: 
 
 # ---- backward ------------------------------------------------------------------------
 
-def _incoming(dY, n, N, name):
-    """A gradient as autograd hands it over: any strides."""
+def _incoming(dY, N, name, stream):
+    """A gradient as autograd hands it over: any strides.  A copy is made on
+    the launch stream, where the caller's ordering holds."""
     if not isinstance(dY, torch.Tensor) or not dY.is_cuda:
         raise TypeError("%s must be a CUDA (HIP) tensor" % name)
     if dY.dim() == 2 and (dY.stride(1) != 1 or dY.stride(0) < dY.shape[1]):
-        dY = dY.contiguous()
-    return _mat(dY, _FLOATS, name, n, N)
+        at = _Launch(stream, dY)
+        if at.stream is None:
+            dY = dY.contiguous()
+        else:
+            with torch.cuda.stream(stream):
+                dY = dY.contiguous()
+    return _mat(dY, _FLOATS, name, None, N)
 
 
 def _linear_backward(wt, dY, act, preact, bias_dtype, out, stream):
-    dY = _incoming(dY, None, wt.N if wt is not None else dY.shape[-1], "dY")
+    dY = _incoming(dY, wt.N if wt is not None else dY.shape[-1], "dY", stream)
     n, N = dY.shape
     codes, scales, gscale, K = (wt.codes, wt.scales, wt.gscale, wt.K) if wt is not None else (None, None, 0.0, 0)
     at = _Launch(stream, dY, preact, out, codes, scales)
@@ -445,7 +451,7 @@ def _linear_backward(wt, dY, act, preact, bias_dtype, out, stream):
 
 
 def _gated_backward(w, wt, dH, act, preact, gate_dtype, up_dtype, out, stream):
-    dH = _incoming(dH, None, w.F, "dH")
+    dH = _incoming(dH, w.F, "dH", stream)
     n, F, K = dH.shape[0], w.F, w.K
     codes, scales = (wt.codes, wt.scales) if wt is not None else (None, None)
     at = _Launch(stream, dH, preact, out, codes, scales)

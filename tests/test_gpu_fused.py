@@ -383,6 +383,36 @@ def test_unaligned_and_expanded_gradients():
     assert torch.equal(a, nv.gemm_t(wt, torch.ones(30, 40, device="cuda", dtype=BF16)))
 
 
+def test_gradient_copies_are_made_on_the_launch_stream():
+    # the current stream is kept busy (tens of ms): what a call on another
+    # stream computes may not wait for it, nor read what it has yet to write
+    w, W = weight(64, 144, 71)
+    wt = w.transpose()
+    gw = nv.GatedWeight.from_packed(w, w)
+    gt = gw.transpose()
+    big = randn((64, 21), 72, F32)
+    X = randn((21, 144), 73)
+    z = torch.empty(21, nv.preact_columns(gw), dtype=F32, device="cuda")
+    nv.gated(gw, X, preact=z)
+    s = torch.cuda.Stream()
+
+    def both(d, stream=None):
+        return (nv.linear_backward(wt, d, bias_dtype=F32, stream=stream) +
+                nv.gated_backward(gw, gt, d, z, bias_dtype=F32, stream=stream))
+
+    for stream in (None, s):        # memory that is used again holds another gradient's values
+        both(-big.t(), stream)
+        both((-big).t(), stream)
+    torch.cuda.synchronize()
+    say("gradients on another stream")
+    torch.cuda._sleep(50_000_000)
+    got = both(big.t(), s)
+    with torch.cuda.stream(s):
+        got = [t.cpu() for t in got]
+    for a, b in zip(got, both(big.t().contiguous())):
+        assert torch.equal(a, b.cpu())
+
+
 def test_refusals():
     say("refusals")
     w, _ = weight(40, 272, 63)
