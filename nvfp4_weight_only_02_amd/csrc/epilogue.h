@@ -73,8 +73,10 @@ __device__ __forceinline__ float activate_grad(float z, int act)
     case NVFP4_ACT_GELU:
         return normal_cdf(z) + z * kInvSqrt2Pi * __expf(-0.5f * z * z);
     case NVFP4_ACT_GELU_TANH: {
-        const float s = sigmoid_f(kTanhC * (z + kTanhA * z * z * z));
-        return s + z * s * (1.0f - s) * kTanhC * (1.0f + 3.0f * kTanhA * z * z);
+        // s (1 - s) is 0 well before |z| = 16: beyond it the square would only
+        // overflow, to 0 * inf
+        const float s = sigmoid_f(kTanhC * (z + kTanhA * z * z * z)), c = fminf(fabsf(z), 16.0f);
+        return s + z * s * (1.0f - s) * kTanhC * (1.0f + 3.0f * kTanhA * c * c);
     }
     default: return 1.0f;
     }

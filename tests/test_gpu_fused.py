@@ -166,6 +166,19 @@ def test_elementwise_gradient_tight(act):
     check(db, (s, b), "column sums")
 
 
+@pytest.mark.parametrize("act", R.ACTS)
+def test_gradient_of_huge_preactivations(act):
+    """act'(z) up to the end of fp32's range, where squares and cubes of z
+    overflow: 0 or 1 by then, so the bound is the one at |z| = 16."""
+    z = [s * v for v in (0.0, 1.0, 15.0, 17.0, 90.0, 1e4, 1e13, 1e19, 2e19, 3e38) for s in (1, -1)]
+    say("huge z", act)
+    z = torch.tensor([z], device="cuda", dtype=F32)
+    p = torch.zeros(1, 24, device="cuda")
+    p[:, :20] = z
+    _, db = nv.linear_backward(None, torch.ones(1, 20, device="cuda"), activation=act, preact=p, bias_dtype=F32)
+    check(db[None], (R.act_grad(f64(z), act), 4 * R.ACT_EPS * (1 + np.minimum(np.abs(f64(z)), 16))), "act'")
+
+
 def test_strides_guards_and_in_place_residual():
     """Strided X with NaN between its rows, an unaligned strided output whose
     surroundings stay as they were, the residual in place."""
