@@ -372,10 +372,12 @@ size_t parts_bytes(int n, int rows, int K)
     return ks > 1 ? (size_t)ks * n * padded_rows(rows) * sizeof(float) : 0;
 }
 
-// A workspace for the partial sums: large enough, aligned, apart from what the
-// second launch still reads or writes.
-int check_workspace(const void *workspace, size_t bytes, size_t need, const uint16_t *X, long long ldx, int n, int K,
-                    const nvfp4_epi_params &e, long long pre_cols)
+// A workspace for the partial sums of a product with a packed weight of
+// row_groups x T tiles: large enough, aligned, apart from what the two launches
+// read and write.
+int check_workspace(const void *workspace, size_t bytes, size_t need, const uint8_t *codes, const uint8_t *scales,
+                    long long tiles, const uint16_t *X, long long ldx, int n, int K, const nvfp4_epi_params &e,
+                    long long pre_cols)
 {
     if (!need)
         return NVFP4_OK;
@@ -383,7 +385,10 @@ int check_workspace(const void *workspace, size_t bytes, size_t need, const uint
         return NVFP4_ERR_WORKSPACE;
     if (!is_aligned(workspace, 16))
         return NVFP4_ERR_ALIGN;
-    if (overlap(workspace, need, X, span(n, ldx, K, 2)) ||
+    const size_t bn = (size_t)e.N * (e.flags & kEpiBiasF32 ? 4 : 2);
+    if (overlap(workspace, need, codes, tiles * 1024) || overlap(workspace, need, scales, tiles * 128) ||
+        overlap(workspace, need, X, span(n, ldx, K, 2)) || overlap(workspace, need, e.bias, bn) ||
+        overlap(workspace, need, e.up_bias, bn) ||
         overlap(workspace, need, e.out, span(n, e.ldo, e.N, e.flags & kEpiOutF32 ? 4 : 2)) ||
         overlap(workspace, need, e.residual, span(n, e.ldr, e.N, e.flags & kEpiResidualF32 ? 4 : 2)) ||
         overlap(workspace, need, e.preact, span(n, e.ldp, pre_cols, 4)))
@@ -409,7 +414,7 @@ int launch_product(nvfp4_fused_gemm_args a, void *workspace, size_t workspace_by
     const nvfp4_fused_gemm_plan plan = nvfp4_plan_fused_gemm(a.n, a.row_groups, a.K);
     const int pitch = a.row_groups * kRowsPerGroup;
     int st = check_workspace(workspace, workspace_bytes, plan.ks > 1 ? (size_t)plan.ks * a.n * pitch * sizeof(float) : 0,
-                             a.X, a.ldx, a.n, a.K, a.epi, a.mode == 1 ? pitch : a.epi.N);
+                             a.codes, a.scales, (long long)a.row_groups * k_tiles(a.K), a.X, a.ldx, a.n, a.K, a.epi, a.mode == 1 ? pitch : a.epi.N);
     if (st != NVFP4_OK)
         return st;
     a.partial = static_cast<float *>(workspace);
@@ -440,8 +445,8 @@ int forward(const uint8_t *Wq, const uint8_t *Wscale, const uint16_t *X, int64_t
         a.epi = e;
         if (ks == 1)
             return gated ? nvfp4_launch_fused_gemv_gated(a, stream) : nvfp4_launch_fused_gemv_linear(a, stream);
-        int st = check_workspace(workspace, workspace_bytes, parts_bytes(n, rows, K), X, ldx, n, K, e,
-                                 gated ? rows : e.N);
+        int st = check_workspace(workspace, workspace_bytes, parts_bytes(n, rows, K), Wq, Wscale,
+                                 row_groups(rows) * k_tiles(K), X, ldx, n, K, e, gated ? rows : e.N);
         if (st != NVFP4_OK)
             return st;
         a.partials = static_cast<float *>(workspace);

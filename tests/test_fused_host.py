@@ -77,6 +77,13 @@ def test_long_rows_need_a_workspace():
     for other in (2, 3):                             # X, Y
         assert linear(K=8208, work=at(other) - 16, size=need) == OVERLAP
     assert linear(K=8208, work=at(7), size=need, ep=epilogue(residual=at(7), ldr=64)) == OVERLAP
+    codes, scales = 4 * 65 * 1024, 4 * 65 * 128     # bytes of the weight
+    for q, size in ((at(0), codes), (at(1), scales)):
+        assert linear(K=8208, work=q - 16, size=need) == linear(K=8208, work=q + size - 16, size=need) == OVERLAP
+    for n in (4, 17):
+        big = fused._call("nvfp4_linear_workspace_bytes")(n, 64, 8208)
+        assert linear(n=n, K=8208, work=at(0), size=big) == OVERLAP
+        assert linear(n=n, K=8208, work=at(7), size=big, ep=epilogue(bias=at(7) + 64)) == OVERLAP
     assert linear(n=17, K=8208) == WORKSPACE        # many columns for one row tile: K parts here too
     assert fused._call("nvfp4_linear_workspace_bytes")(4, 64, 8192) == 0
     rows = nv.gated_rows(50)
