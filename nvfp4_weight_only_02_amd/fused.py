@@ -467,6 +467,15 @@ def _gated_backward(w, wt, dH, act, preact, gate_dtype, up_dtype, out, stream):
     return dX, dg, du
 
 
+def _grad_args(wt, bias_dtype, out, n):
+    if bias_dtype is not None and bias_dtype not in _DTYPES:
+        raise TypeError("bias_dtype must be torch.bfloat16 or torch.float32, got %s" % bias_dtype)
+    if out is not None:
+        if wt is None:
+            raise ValueError("out receives dX, which needs the transposed weight")
+        _mat(out, (torch.bfloat16,), "out", n, wt.K)
+
+
 def gemm_t(wt: TransposedWeight, dY: torch.Tensor, out: torch.Tensor = None, stream=None) -> torch.Tensor:
     """dX[n, K] = dY[n, N] . dequant(W) (bf16 in and out, fp32 accumulation):
     the gradient of ``gemv``, ``gemm`` or a plain ``linear`` with respect to
@@ -488,8 +497,7 @@ def linear_backward(wt: TransposedWeight, dY: torch.Tensor, activation: str = No
         if preact is None:
             raise ValueError("the gradient of an activation needs preact")
         _mat(preact, (torch.float32,), "preact", dY.shape[0], _pad8(dY.shape[-1]))
-    if out is not None:
-        _mat(out, (torch.bfloat16,), "out", dY.shape[0], wt.K)
+    _grad_args(wt, bias_dtype, out, dY.shape[0])
     return _linear_backward(wt, dY, act, preact if act else None, bias_dtype, out, stream)
 
 
@@ -501,6 +509,5 @@ def gated_backward(w: GatedWeight, wt: TransposedWeight, dH: torch.Tensor, preac
     _mat(preact, (torch.float32,), "preact", dH.shape[0], gated_rows(w.F))
     if wt is not None and (wt.N, wt.K) != (gated_rows(w.F), w.K):
         raise ValueError("wt is not the transposed copy of this gated weight")
-    if out is not None:
-        _mat(out, (torch.bfloat16,), "out", dH.shape[0], w.K)
+    _grad_args(wt, bias_dtype, out, dH.shape[0])
     return _gated_backward(w, wt, dH, act, preact, bias_dtype, bias_dtype, out, stream)

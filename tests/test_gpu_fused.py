@@ -426,6 +426,26 @@ def test_gradient_copies_are_made_on_the_launch_stream():
         assert torch.equal(a, b.cpu())
 
 
+def test_gradient_refusals():
+    w, _ = weight(40, 272, 63)
+    gw = nv.GatedWeight.from_packed(w, w)
+    wt, gt = w.transpose(), gw.transpose()
+    dY = randn((5, 40), 64)
+    z = torch.zeros(5, nv.preact_columns(gw), device="cuda")
+    out = torch.empty(5, 272, device="cuda", dtype=BF16)
+    for call in (lambda **k: nv.linear_backward(k.pop("wt"), dY, **k),
+                 lambda **k: nv.gated_backward(gw, gt if k.pop("wt") is wt else None, dY, z, **k)):
+        with pytest.raises(TypeError):
+            call(wt=wt, bias_dtype=torch.float16)
+        with pytest.raises(ValueError):
+            call(wt=None, bias_dtype=F32, out=out)       # no dX to receive
+        with pytest.raises(ValueError):
+            call(wt=wt, out=out[:4])
+        with pytest.raises(TypeError):
+            call(wt=wt, out=out.float())
+        assert call(wt=wt, out=out)[0] is out
+
+
 def test_refusals():
     say("refusals")
     w, _ = weight(40, 272, 63)
