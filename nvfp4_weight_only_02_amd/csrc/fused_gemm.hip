@@ -366,34 +366,41 @@ struct Tile {
     double alone, shared;
 };
 constexpr Tile kTiles[] = {
-    {2, 2, 2, 4, 2, 820, 560},      //  64 rows x  32 tokens
-    {2, 2, 2, 8, 1, 1150, 1010},
-    {2, 4, 2, 4, 1, 1090, 1055},    //  64 x  64
-    {2, 4, 4, 2, 2, 1025, 760},     // 128 x  64
-    {4, 8, 4, 2, 1, 2630, 2515},    // 256 x 128
-    {4, 8, 4, 1, 2, 1785, 1230},
+    {2, 2, 1, 4, 2, 750, 415},      //  32 rows x  32 tokens
+    {2, 2, 1, 8, 1, 1015, 885},
+    {2, 2, 2, 4, 2, 820, 680},      //  64 x  32
+    {2, 4, 2, 4, 1, 1315, 1170},    //  64 x  64
+    {2, 4, 4, 2, 2, 995, 805},      // 128 x  64
+    {4, 8, 4, 2, 1, 2655, 2530},    // 256 x 128
+    {4, 8, 4, 1, 2, 1680, 1235},
 };
 constexpr int kParts[] = {1, 2, 3, 4, 6, 8, 12};
-constexpr double kStart = 3;            // a workgroup's start and epilogue, in iterations
-constexpr double kTail = 0.75;          // uneven end of a grid of several rounds, in workgroups a unit
-constexpr double kReduceNs = 3700;      // the second launch
-constexpr double kReduceSumNs = 9.1e-4; // a partial sum written and read again
+constexpr double kStart = 2.55;         // a workgroup's start and epilogue, in iterations
+constexpr double kTail = 0.82;          // uneven end of a grid of several rounds, in workgroups a unit
+constexpr double kReduceNs = 4100;      // the second launch
+constexpr double kReduceSumNs = 9.2e-4; // a partial sum written and read again
 
 }  // namespace
 
 // The tile and part count of least modelled time.  Smaller tiles, K groups and
 // K parts fill the chip where the largest tile leaves units idle; larger tiles
 // dequantise a weight for more tokens, K groups add their sums in LDS where
-// parts write them and need a second launch.  The constants were fitted to 91
-// shapes x 14 tiles x every part count measured on MI355X (64 .. 34816 rows, K
-// 1024 .. 34816, n 17 .. 8000): over them the choice is within 1.1% of the best
-// measured one on average, 13% at worst.  Both sides of some choices (us):
-//   5120 x 6144   n = 17    64 x 32 in 3 parts 9.9; without K groups 11.3 (6 parts), 32.3 (1 part)
-//   16384 x 5120  n = 24    64 x 32, 8 groups 13.7; without groups 17.7 (4 parts), 28.3
-//   1237 x 2064   n = 300   64 x 32, 4 groups 8.4; 128 x 32 without groups 16.0
-//   16384 x 5120  n = 128   128 x 64, 2 groups 31.1; 64 x 64 36.6, 256 x 128 84
-//   5120 x 6144   n = 1000  256 x 128 in 3 parts 78; 2 groups 85, 128 x 64 85, 1 part 104
-//   gated 2 x 17408 x 5120  n = 2048  256 x 128 611; 128 x 64 without groups 796
+// parts write them and need a second launch.  A step of the small tiles is
+// bound by issue (64 rows x 32 tokens with 8 groups: 16 waves, 4 a SIMD, take
+// 2.0 us an iteration warm or cold, with 4 groups 1.0), so that a grid which
+// leaves units idle wants fewer waves a workgroup: 32 rows.  The constants were
+// fitted to 120 shapes x 8 tiles x every part count measured on MI355X with
+// weights that come from HBM (64 .. 34816 rows, K 1024 .. 34816, n 17 .. 8000):
+// over them the choice is within 0.8% of the best measured one on average, 17%
+// at worst.  Both sides of some choices (us):
+//   4096 x 1024   n = 20    32 x 32, 4 groups 4.9; 64 x 32 5.6, 128 x 64 8.6
+//   1237 x 2064   n = 47    32 x 32, 8 groups 7.0; 4 groups 7.2, 64 x 32 8.3
+//   5120 x 6144^T n = 24    32 x 32, 8 groups 12.4; 64 x 32 in 2 parts 13.1, 1 part 15.7
+//   16384 x 5120  n = 17    64 x 32 16.7; 32 x 32 18.5, 64 x 64 20.0
+//   16384 x 5120  n = 64    64 x 64 24.1; 64 x 32 25.5, 128 x 64 32.2
+//   16384 x 5120  n = 128   128 x 64 34.1; 64 x 64 42.5, 256 x 128 71
+//   5120 x 6144   n = 1000  256 x 128 in 3 parts 78; 2 groups 81, 128 x 64 86, 1 part 97
+//   gated 2 x 17408 x 5120  n = 1024  256 x 128 342; 2 groups 379, 128 x 64 402
 nvfp4_fused_gemm_plan nvfp4_plan_fused_gemm(int n, int row_groups, int K)
 {
     const int T = (int)k_tiles(K);
@@ -454,11 +461,12 @@ int nvfp4_launch_fused_gemm(const nvfp4_fused_gemm_args &a, const nvfp4_fused_ge
     p.tp = plan.tp;
     p.partial = a.partial;
     switch (plan.tile) {
-    case 0: return launch_one<2, 2, 2, 4>(p, a.mode, stream);
-    case 1: return launch_one<2, 2, 2, 8>(p, a.mode, stream);
-    case 2: return launch_one<2, 4, 2, 4>(p, a.mode, stream);
-    case 3: return launch_one<2, 4, 4, 2>(p, a.mode, stream);
-    case 4: return launch_one<4, 8, 4, 2>(p, a.mode, stream);
+    case 0: return launch_one<2, 2, 1, 4>(p, a.mode, stream);
+    case 1: return launch_one<2, 2, 1, 8>(p, a.mode, stream);
+    case 2: return launch_one<2, 2, 2, 4>(p, a.mode, stream);
+    case 3: return launch_one<2, 4, 2, 4>(p, a.mode, stream);
+    case 4: return launch_one<2, 4, 4, 2>(p, a.mode, stream);
+    case 5: return launch_one<4, 8, 4, 2>(p, a.mode, stream);
     default: return launch_one<4, 8, 4, 1>(p, a.mode, stream);
     }
 }

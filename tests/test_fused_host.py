@@ -184,7 +184,7 @@ def test_reference_gradients_are_differences(kind):
 def test_fused_geometry_rule(n, rows, T, tail):
     K = T * 128 - tail if T * 128 > tail else 8
     r, t, kg, ks = nv.fused_geometry(n, rows, K)
-    assert (r, t, kg) in {(64, 32, 4), (64, 32, 8), (64, 64, 4), (128, 64, 2), (256, 128, 2), (256, 128, 1)}
+    assert (r, t, kg) in {(32, 32, 4), (32, 32, 8), (64, 32, 4), (64, 64, 4), (128, 64, 2), (256, 128, 2), (256, 128, 1)}
     tiles = -(-K // 128)
     tp = -(-tiles // ks)
     assert 1 <= ks <= 12 and (ks - 1) * tp < tiles        # no part is empty

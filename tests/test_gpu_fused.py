@@ -500,11 +500,12 @@ def device_check(got, ref, bound, what):
 
 # (n, rows, K) of each tile (rows, tokens, K groups), in one part and in several,
 # with n, rows and K that end inside a tile
-TILES = [((64, 32, 4), 1, (45, 336, 656)), ((64, 32, 4), 2, (17, 80, 3088)),
-         ((64, 32, 8), 1, (17, 4112, 3088)), ((64, 32, 8), 2, (17, 4624, 8208)),
-         ((64, 64, 4), 1, (70, 6160, 272)), ((64, 64, 4), 2, (33, 2576, 8208)),
-         ((128, 64, 2), 1, (201, 5136, 272)), ((128, 64, 2), 2, (33, 3088, 8208)),
-         ((256, 128, 2), 1, (701, 8208, 656)), ((256, 128, 2), 2, (401, 5136, 6160)),
+TILES = [((32, 32, 4), 1, (45, 176, 272)), ((32, 32, 4), 2, (17, 80, 6160)),
+         ((32, 32, 8), 1, (17, 4112, 3088)), ((32, 32, 8), 2, (33, 80, 12304)),
+         ((64, 32, 4), 1, (33, 4624, 144)), ((64, 32, 4), 2, (33, 1040, 6160)),
+         ((64, 64, 4), 1, (100, 5136, 784)), ((64, 64, 4), 2, (193, 1328, 9232)),
+         ((128, 64, 2), 1, (201, 5136, 272)), ((128, 64, 2), 2, (33, 2576, 16400)),
+         ((256, 128, 2), 1, (701, 8208, 1552)), ((256, 128, 2), 2, (401, 5136, 6160)),
          ((256, 128, 1), 1, (257, 16400, 272)), ((256, 128, 1), 2, (1001, 5136, 6160))]
 
 
