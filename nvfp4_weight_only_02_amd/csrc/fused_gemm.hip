@@ -69,8 +69,9 @@ __device__ __forceinline__ unsigned lds_address(const void *p)
 // after it: two LDS buffers, which leave room for two workgroups a compute unit
 // at the largest tile (a third buffer, with the codes through LDS as well,
 // measured no faster at 17 .. 64 tokens: 16384 x 5120, n = 24: 17.0 against
-// 16.8 us).  MODE: 0 linear, 1 gated (row groups alternate gate, up), 2
-// transposed weight, plain output.
+// 16.8 us; weights alone two steps ahead 1 .. 4% slower at n = 17 .. 512: the
+// small tiles are bound by issue).  MODE: 0 linear, 1 gated (row groups
+// alternate gate, up), 2 transposed weight, plain output.
 //
 // LDS layout of the slice: token t's 16-byte chunk c (8 columns) at
 //     (t / 4) * kQuad + (t % 4) * 256 + (c ^ (t % 4)) * 16.
@@ -120,7 +121,6 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
     }
     const int rg0 = (tx * RW + wave) * RG;
     const int tok0 = ty * BM;
-    const int ntok = min(BM, p.n - tok0);
     const int s0 = part * p.tp, s1 = min(p.T, s0 + p.tp);
     __shared__ __align__(1024) char lds[KG][2][kBuf];
 
