@@ -272,16 +272,19 @@ class PackedWeight:
 
 # ---- the GEMV --------------------------------------------------------------
 
-def _x(X: torch.Tensor, K: int) -> torch.Tensor:
+def _x(w: PackedWeight, X: torch.Tensor) -> torch.Tensor:
+    # the other weights have fields of these names and layouts of other sizes
+    if isinstance(w, (TransposedWeight, GatedWeight)):
+        raise TypeError("w must be a PackedWeight, got %s" % type(w).__name__)
     _dev(X, torch.bfloat16, "X")
-    if X.dim() != 2 or X.shape[1] != K:
-        raise ValueError("X must be [n, %d]" % K)
+    if X.dim() != 2 or X.shape[1] != w.K:
+        raise ValueError("X must be [n, %d]" % w.K)
     return X
 
 
 def gemv(w: PackedWeight, X: torch.Tensor, out: torch.Tensor = None, stream=None) -> torch.Tensor:
     """Y[n, N] = X[n, K] . dequant(W)^T (bf16 in and out, fp32 accumulation)."""
-    _x(X, w.K)
+    _x(w, X)
     n = X.shape[0]
     Y = out if out is not None else torch.empty((n, w.N), dtype=torch.bfloat16, device=X.device)
     _dev(Y, torch.bfloat16, "out")
@@ -310,7 +313,7 @@ def gemv_ws(w: PackedWeight, X: torch.Tensor, ks: int = 0, workspace: torch.Tens
     """gemv with K cut into ``ks`` parts (0: the library's choice for the
     shape): fp32 partials in ``workspace`` (a uint8 device tensor, allocated
     here when not given), then a fixed-order sum of the parts."""
-    _x(X, w.K)
+    _x(w, X)
     n = X.shape[0]
     Y = out if out is not None else torch.empty((n, w.N), dtype=torch.bfloat16, device=X.device)
     _dev(Y, torch.bfloat16, "out")
@@ -332,7 +335,7 @@ def gemv_ws_static(w: PackedWeight, X: torch.Tensor, ks: int = 0, out: torch.Ten
     """gemv_ws with the partials in the library's fixed scratch memory: no
     device allocation by the library (``out`` may be given to avoid torch's).
     Calls that overlap on one GPU race."""
-    _x(X, w.K)
+    _x(w, X)
     n = X.shape[0]
     Y = out if out is not None else torch.empty((n, w.N), dtype=torch.bfloat16, device=X.device)
     _dev(Y, torch.bfloat16, "out")
@@ -352,7 +355,7 @@ def gemv_static_scratch_bytes() -> int:
 def gemv_sched(w: PackedWeight, X: torch.Tensor, tile_widths, out: torch.Tensor = None,
                stream=None) -> torch.Tensor:
     """gemv with an explicit token-tile schedule (one weight read per tile)."""
-    _x(X, w.K)
+    _x(w, X)
     n = X.shape[0]
     Y = out if out is not None else torch.empty((n, w.N), dtype=torch.bfloat16, device=X.device)
     _dev(Y, torch.bfloat16, "out")
@@ -368,7 +371,7 @@ def gemv_sched(w: PackedWeight, X: torch.Tensor, tile_widths, out: torch.Tensor 
 def gemm(w: PackedWeight, X: torch.Tensor, out: torch.Tensor = None, stream=None) -> torch.Tensor:
     """Prefill form: Y[n, N] = X[n, K] . dequant(W)^T for any n >= 1 (tiled
     MFMA GEMM; bf16 in and out, fp32 accumulation)."""
-    _x(X, w.K)
+    _x(w, X)
     n = X.shape[0]
     Y = out if out is not None else torch.empty((n, w.N), dtype=torch.bfloat16, device=X.device)
     _dev(Y, torch.bfloat16, "out")
@@ -383,7 +386,7 @@ def gemv_qkv(w: PackedWeight, X: torch.Tensor, rows, out_off, ldy: int,
              out: torch.Tensor = None, stream=None) -> torch.Tensor:
     """Fused q|k|v projection writing each projection at its offset of a
     token-major output with ``ldy`` elements per token."""
-    _x(X, w.K)
+    _x(w, X)
     n = X.shape[0]
     if len(rows) != 3 or len(out_off) != 3:
         raise ValueError("rows and out_off take three entries (q, k, v)")

@@ -108,6 +108,13 @@ def _ld(t) -> int:
     return t.stride(0) if shape[0] > 1 else shape[1]
 
 
+def _weight(w, cls, name: str = "w"):
+    """The classes of weights share field names over layouts of different sizes,
+    so one of another class would be read past its end."""
+    if not isinstance(w, cls):
+        raise TypeError("%s must be a %s, got %s" % (name, cls.__name__, type(w).__name__))
+
+
 def _vec(t, dtypes, name: str, size: int):
     _typed(t, dtypes, name)
     if t.dim() != 1 or t.shape[0] != size or not t.is_contiguous():
@@ -185,6 +192,7 @@ def _transpose(codes, scales, gscale, N, K, stream) -> TransposedWeight:
 
 def transpose(w: PackedWeight, stream=None) -> TransposedWeight:
     """The transposed copy of ``w`` (also ``w.transpose()``)."""
+    _weight(w, PackedWeight)
     return _transpose(w.codes, w.scales, w.gscale, w.N, w.K, stream)
 
 
@@ -214,6 +222,8 @@ class GatedWeight:
 
     @classmethod
     def from_packed(cls, gate: PackedWeight, up: PackedWeight, stream=None) -> "GatedWeight":
+        _weight(gate, PackedWeight, "gate")
+        _weight(up, PackedWeight, "up")
         if (gate.N, gate.K) != (up.N, up.K):
             raise ValueError("the gate and up weights must have one shape")
         at = _Launch(stream, gate.codes, gate.scales, up.codes, up.scales)
@@ -285,7 +295,11 @@ def _pad8(cols: int) -> int:
 def preact_columns(w) -> int:
     """Columns of the fp32 pre-activation buffer of ``w`` (a PackedWeight or a
     GatedWeight): the outputs up to a multiple of 8, or the gated weight's rows."""
-    return gated_rows(w.F) if isinstance(w, GatedWeight) else _pad8(w.N)
+    if isinstance(w, GatedWeight):
+        return gated_rows(w.F)
+    if not isinstance(w, PackedWeight):
+        raise TypeError("w must be a PackedWeight or a GatedWeight, got %s" % type(w).__name__)
+    return _pad8(w.N)
 
 
 def _preact_arg(preact, w, n):
@@ -372,6 +386,9 @@ def linear(w: PackedWeight, X: torch.Tensor, bias: torch.Tensor = None, activati
     ``workspace``: uint8, nvfp4_linear_workspace_bytes (allocated otherwise).
     Differentiable in X (given ``transposed``), bias and residual."""
     act = _act(activation)
+    _weight(w, PackedWeight)
+    if transposed is not None:
+        _weight(transposed, TransposedWeight, "transposed")
     _mat(X, (torch.bfloat16,), "X", None, w.K)
     n = X.shape[0]
     if bias is not None:
@@ -398,6 +415,9 @@ def gated(w: GatedWeight, X: torch.Tensor, activation: str = "silu", gate_bias: 
     as ``linear``; the biases have one dtype.  Differentiable in X (given
     ``transposed``) and the biases."""
     act = _act(activation)
+    _weight(w, GatedWeight)
+    if transposed is not None:
+        _weight(transposed, TransposedWeight, "transposed")
     _mat(X, (torch.bfloat16,), "X", None, w.K)
     n = X.shape[0]
     for b, name in ((gate_bias, "gate_bias"), (up_bias, "up_bias")):
@@ -481,6 +501,7 @@ def gemm_t(wt: TransposedWeight, dY: torch.Tensor, out: torch.Tensor = None, str
     the gradient of ``gemv``, ``gemm`` or a plain ``linear`` with respect to
     its input.  dY rows that are not 16-byte aligned, or an N that is no
     multiple of 8, cost a padded copy of dY."""
+    _weight(wt, TransposedWeight, "wt")
     _mat(dY, (torch.bfloat16,), "dY", None, wt.N)
     if out is not None:
         _mat(out, (torch.bfloat16,), "out", dY.shape[0], wt.K)
@@ -492,6 +513,8 @@ def linear_backward(wt: TransposedWeight, dY: torch.Tensor, activation: str = No
     """(dX, dbias) of ``linear``: dX bf16 [n, K] (None without ``wt``), dbias in
     ``bias_dtype`` (None without).  ``preact`` as ``linear`` filled it (not
     needed without an activation).  The residual's gradient is dY."""
+    if wt is not None:
+        _weight(wt, TransposedWeight, "wt")
     act = _act(activation)
     if act:
         if preact is None:
@@ -505,6 +528,9 @@ def gated_backward(w: GatedWeight, wt: TransposedWeight, dH: torch.Tensor, preac
                    activation: str = "silu", bias_dtype=None, out: torch.Tensor = None, stream=None):
     """(dX, dgate_bias, dup_bias) of ``gated``; the bias gradients in
     ``bias_dtype`` (None without)."""
+    _weight(w, GatedWeight)
+    if wt is not None:
+        _weight(wt, TransposedWeight, "wt")
     act = _act(activation)
     _mat(preact, (torch.float32,), "preact", dH.shape[0], gated_rows(w.F))
     if wt is not None and (wt.N, wt.K) != (gated_rows(w.F), w.K):

@@ -198,3 +198,56 @@ def test_fused_geometry_refuses():
         with pytest.raises(nv.Nvfp4Error) as e:
             nv.fused_geometry(*args)
         assert e.value.status == status
+
+
+# ---- weights of the wrong kind -------------------------------------------------------
+
+def weights(N=64, K=256):
+    """A weight of each class over host memory: refused for its class before any
+    of it is looked at."""
+    b = nv.torch.empty(16, dtype=nv.torch.uint8)
+    return {"PackedWeight": nv.PackedWeight(b, b, 1.0, N, K), "GatedWeight": nv.GatedWeight(b, b, 1.0, 1.0, N, K),
+            "TransposedWeight": nv.TransposedWeight(b, b, 1.0, N, K)}
+
+
+CALLS = [  # what the call takes, the call on a weight and a matrix
+    ("PackedWeight", lambda w, x: nv.linear(w, x)),
+    ("PackedWeight", lambda w, x: nv.transpose(w)),
+    ("PackedWeight", lambda w, x: nv.GatedWeight.from_packed(w, weights()["PackedWeight"])),
+    ("PackedWeight", lambda w, x: nv.GatedWeight.from_packed(weights()["PackedWeight"], w)),
+    ("GatedWeight", lambda w, x: nv.gated(w, x)),
+    ("GatedWeight", lambda w, x: nv.gated_backward(w, None, x, x)),
+    ("TransposedWeight", lambda w, x: nv.gemm_t(w, x)),
+    ("TransposedWeight", lambda w, x: nv.linear_backward(w, x)),
+    ("TransposedWeight", lambda w, x: nv.gated_backward(weights()["GatedWeight"], w, x, x)),
+    ("PackedWeight", lambda w, x: nv.gemv(w, x)),
+    ("PackedWeight", lambda w, x: nv.gemv_ws(w, x)),
+    ("PackedWeight", lambda w, x: nv.gemv_ws_static(w, x)),
+    ("PackedWeight", lambda w, x: nv.gemv_sched(w, x, [1])),
+    ("PackedWeight", lambda w, x: nv.gemm(w, x)),
+    ("PackedWeight", lambda w, x: nv.gemv_qkv(w, x, (32, 16, 16), (0, 32, 48), 64)),
+]
+
+
+@pytest.mark.parametrize("call", range(len(CALLS)))
+@pytest.mark.parametrize("kind", ["PackedWeight", "GatedWeight", "TransposedWeight", "other"])
+def test_weight_of_another_class_is_refused(call, kind):
+    """A transposed copy has the fields of a packed weight and other sizes: read
+    as one, its tiles would be read past their end."""
+    want, f = CALLS[call]
+    if kind == want or (kind == "other" and call >= 9):    # the projections look at no other class
+        return
+    w = object() if kind == "other" else weights()[kind]
+    x = nv.torch.empty(4, 256, dtype=nv.torch.bfloat16)
+    with pytest.raises(TypeError, match=want):
+        f(w, x)
+
+
+def test_transposed_argument_is_a_transposed_weight():
+    x = nv.torch.empty(4, 256, dtype=nv.torch.bfloat16)
+    for f, kind in ((nv.linear, "PackedWeight"), (nv.gated, "GatedWeight")):
+        for other in ("PackedWeight", "GatedWeight"):
+            with pytest.raises(TypeError, match="TransposedWeight"):
+                f(weights()[kind], x, transposed=weights()[other])
+    with pytest.raises(TypeError, match="PackedWeight or a GatedWeight"):
+        nv.preact_columns(weights()["TransposedWeight"])
