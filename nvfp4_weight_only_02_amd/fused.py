@@ -22,7 +22,8 @@ from __future__ import annotations
 import ctypes
 import functools
 import struct
-from dataclasses import dataclass
+import weakref
+from dataclasses import InitVar, dataclass
 
 import torch
 
@@ -179,15 +180,38 @@ class TransposedWeight:
     gscale: float
     N: int                   # rows of the packed weight
     K: int
+    gated: bool = False      # of a GatedWeight
+    # The packed codes the copy was made from, held weakly and only to refuse the
+    # copy of another weight; a copied or unpickled object has none.
+    source: InitVar[torch.Tensor] = None
+    _source = None
+
+    def __post_init__(self, source):
+        if source is not None:
+            self._source = weakref.ref(source)
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "_source"}
 
 
-def _transpose(codes, scales, gscale, N, K, stream) -> TransposedWeight:
+def _check_transposed(wt: TransposedWeight, w) -> None:
+    """wt is the transposed copy of w (a PackedWeight or a GatedWeight), as far
+    as sizes, kind, tensor scale and the codes it was made from tell."""
+    gated = isinstance(w, GatedWeight)
+    source = None if wt._source is None else wt._source()
+    if ((wt.gated, wt.N, wt.K, wt.gscale) != ((True, gated_rows(w.F), w.K, 1.0) if gated else
+                                              (False, w.N, w.K, w.gscale))
+            or (source is not None and source.data_ptr() != w.codes.data_ptr())):
+        raise ValueError("transposed is not the transposed copy of this weight (w.transpose())")
+
+
+def _transpose(codes, scales, gscale, N, K, stream, gated=False) -> TransposedWeight:
     at = _Launch(stream, codes, scales)
     ct = at.alloc(int(_call("nvfp4_transposed_codes_bytes")(N, K)), dtype=torch.uint8)
     st = at.alloc(int(_call("nvfp4_transposed_scales_bytes")(N, K)), dtype=torch.uint8)
     _run("nvfp4_pack_transposed", codes.data_ptr(), scales.data_ptr(), N, K, ct.data_ptr(), st.data_ptr(),
          at.handle)
-    return TransposedWeight(ct, st, gscale, N, K)
+    return TransposedWeight(ct, st, gscale, N, K, gated, codes)
 
 
 def transpose(w: PackedWeight, stream=None) -> TransposedWeight:
@@ -244,7 +268,7 @@ class GatedWeight:
     def transpose(self, stream=None) -> TransposedWeight:
         """The transposed copy, for gradients (its tensor scales are applied
         to the gradient rows, so its own is 1)."""
-        return _transpose(self.codes, self.scales, 1.0, gated_rows(self.F), self.K, stream)
+        return _transpose(self.codes, self.scales, 1.0, gated_rows(self.F), self.K, stream, gated=True)
 
 
 # ---- forward -------------------------------------------------------------------------
@@ -318,7 +342,7 @@ def _wants_grad(*tensors) -> bool:
     return False
 
 
-def _check_grad(X, transposed, N, K, stream, *buffers):
+def _check_grad(X, w, transposed, stream, *buffers):
     if any(b is not None for b in buffers):
         raise ValueError("out, preact and workspace go with calls that need no gradient")
     if stream is not None and stream != torch.cuda.current_stream():
@@ -326,8 +350,7 @@ def _check_grad(X, transposed, N, K, stream, *buffers):
     if X.requires_grad:
         if transposed is None:
             raise ValueError("a gradient of X needs the weight's transposed copy (transposed=w.transpose())")
-        if (transposed.N, transposed.K) != (N, K):
-            raise ValueError("transposed is not a copy of this weight's shape")
+        _check_transposed(transposed, w)
 
 
 class _Linear(torch.autograd.Function):
@@ -400,7 +423,7 @@ def linear(w: PackedWeight, X: torch.Tensor, bias: torch.Tensor = None, activati
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else torch.bfloat16
     if _wants_grad(X, bias, residual):
-        _check_grad(X, transposed, w.N, w.K, stream, out, preact, workspace)
+        _check_grad(X, w, transposed, stream, out, preact, workspace)
         return _Linear.apply(X, bias, residual, w, transposed, act, out_dtype)
     return _linear_forward(w, X, bias, act, residual, out, out_dtype, _preact_arg(preact, w, n),
                            _workspace_arg(workspace), stream)
@@ -430,7 +453,7 @@ def gated(w: GatedWeight, X: torch.Tensor, activation: str = "silu", gate_bias: 
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else torch.bfloat16
     if _wants_grad(X, gate_bias, up_bias):
-        _check_grad(X, transposed, gated_rows(w.F), w.K, stream, out, preact, workspace)
+        _check_grad(X, w, transposed, stream, out, preact, workspace)
         return _Gated.apply(X, gate_bias, up_bias, w, transposed, act, out_dtype)
     return _gated_forward(w, X, act, gate_bias, up_bias, out, out_dtype, _preact_arg(preact, w, n),
                           _workspace_arg(workspace), stream)
@@ -499,8 +522,9 @@ def _grad_args(wt, bias_dtype, out, n):
 def gemm_t(wt: TransposedWeight, dY: torch.Tensor, out: torch.Tensor = None, stream=None) -> torch.Tensor:
     """dX[n, K] = dY[n, N] . dequant(W) (bf16 in and out, fp32 accumulation):
     the gradient of ``gemv``, ``gemm`` or a plain ``linear`` with respect to
-    its input.  dY rows that are not 16-byte aligned, or an N that is no
-    multiple of 8, cost a padded copy of dY."""
+    its input.  (The copy of a GatedWeight has no tensor scale: W without its
+    two.)  dY rows that are not 16-byte aligned, or an N that is no multiple of
+    8, cost a padded copy of dY."""
     _weight(wt, TransposedWeight, "wt")
     _mat(dY, (torch.bfloat16,), "dY", None, wt.N)
     if out is not None:
@@ -515,6 +539,8 @@ def linear_backward(wt: TransposedWeight, dY: torch.Tensor, activation: str = No
     needed without an activation).  The residual's gradient is dY."""
     if wt is not None:
         _weight(wt, TransposedWeight, "wt")
+        if wt.gated:
+            raise ValueError("wt is the copy of a gated weight, which gated_backward takes")
     act = _act(activation)
     if act:
         if preact is None:
@@ -533,7 +559,7 @@ def gated_backward(w: GatedWeight, wt: TransposedWeight, dH: torch.Tensor, preac
         _weight(wt, TransposedWeight, "wt")
     act = _act(activation)
     _mat(preact, (torch.float32,), "preact", dH.shape[0], gated_rows(w.F))
-    if wt is not None and (wt.N, wt.K) != (gated_rows(w.F), w.K):
-        raise ValueError("wt is not the transposed copy of this gated weight")
+    if wt is not None:
+        _check_transposed(wt, w)
     _grad_args(wt, bias_dtype, out, dH.shape[0])
     return _gated_backward(w, wt, dH, act, preact, bias_dtype, bias_dtype, out, stream)

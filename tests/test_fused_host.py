@@ -251,3 +251,42 @@ def test_transposed_argument_is_a_transposed_weight():
                 f(weights()[kind], x, transposed=weights()[other])
     with pytest.raises(TypeError, match="PackedWeight or a GatedWeight"):
         nv.preact_columns(weights()["TransposedWeight"])
+
+
+def test_transposed_copy_of_another_weight_is_refused():
+    """What autograd and gated_backward can tell apart: the kind of weight, its
+    sizes, its tensor scale and the codes the copy was made from."""
+    import copy
+    import pickle
+    t = lambda: nv.torch.empty(16, dtype=nv.torch.uint8)     # noqa: E731
+    w = nv.PackedWeight(t(), t(), 0.5, 96, 64)
+    gw = nv.GatedWeight(t(), t(), 0.5, 0.25, 48, 64)
+    wt = nv.TransposedWeight(t(), t(), 0.5, 96, 64, source=w.codes)
+    gt = nv.TransposedWeight(t(), t(), 1.0, 96, 64, gated=True, source=gw.codes)
+    check = fused._check_transposed
+    check(wt, w)
+    check(gt, gw)
+    # the same memory in another object, and copies that go without a source
+    check(wt, nv.PackedWeight(w.codes[:], w.scales, 0.5, 96, 64))
+    for again in (copy.deepcopy(wt), pickle.loads(pickle.dumps(wt)), nv.TransposedWeight(t(), t(), 0.5, 96, 64)):
+        assert again.gscale == 0.5 and not again.gated
+        check(again, w)
+    for other, weight in ((gt, w), (wt, gw),                                           # the other kind
+                          (wt, nv.PackedWeight(t(), t(), 0.5, 96, 64)),                # other codes
+                          (gt, nv.GatedWeight(t(), t(), 0.5, 0.25, 48, 64)),
+                          (wt, nv.PackedWeight(w.codes, w.scales, 0.75, 96, 64)),      # another tensor scale
+                          (wt, nv.PackedWeight(w.codes, w.scales, 0.5, 80, 64)),       # other sizes
+                          (wt, nv.PackedWeight(w.codes, w.scales, 0.5, 96, 80))):
+        with pytest.raises(ValueError, match="transposed copy"):
+            check(other, weight)
+    # the copy does not keep the packed weight's memory, and outlives it
+    import gc
+    import weakref
+    alive = weakref.ref(w.codes)
+    del w, weight
+    gc.collect()
+    assert alive() is None
+    check(wt, nv.PackedWeight(t(), t(), 0.5, 96, 64))
+    x = nv.torch.empty(4, 96, dtype=nv.torch.bfloat16)
+    with pytest.raises(ValueError, match="gated weight"):
+        nv.linear_backward(gt, x)

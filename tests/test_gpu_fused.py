@@ -615,3 +615,27 @@ def test_decode_with_many_row_groups(n):
     G, U = nv.linear(g, X, out_dtype=F32), nv.linear(u, X, out_dtype=F32)
     assert torch.equal(nv.linear(g, X, residual=r), (G + r.float()).to(BF16))
     assert torch.equal(nv.gated(nv.GatedWeight.from_packed(g, u), X, activation="none", out_dtype=F32), G * U)
+
+
+# ---- transposed copies that belong to another weight ----------------------------------
+
+def test_transposed_copy_of_another_weight():
+    say("foreign transposed copies")
+    w, _ = weight(96, 144, 100)
+    other, _ = weight(96, 144, 101)
+    gw, go = nv.GatedWeight.from_packed(w, other), nv.GatedWeight.from_packed(other, w)
+    plain = nv.PackedWeight(gw.codes, gw.scales, 1.0, nv.gated_rows(96), 144)    # the gated rows as one weight
+    X = randn((5, 144), 102).requires_grad_()
+    for f, a, foreign in ((nv.linear, w, (other.transpose(),)), (nv.linear, plain, (gw.transpose(),)),
+                          (nv.gated, gw, (go.transpose(), plain.transpose()))):
+        for t in foreign:
+            with pytest.raises(ValueError, match="transposed copy"):
+                f(a, X, transposed=t)
+        assert torch.isfinite(torch.autograd.grad(f(a, X, transposed=a.transpose()).sum(), X)[0]).all()
+    z = torch.zeros(5, nv.preact_columns(gw), device="cuda")
+    dH = randn((5, 96), 103)
+    for t in (go.transpose(), plain.transpose()):
+        with pytest.raises(ValueError, match="transposed copy"):
+            nv.gated_backward(gw, t, dH, z)
+    with pytest.raises(ValueError, match="gated weight"):
+        nv.linear_backward(gw.transpose(), randn((5, nv.gated_rows(96)), 104))
