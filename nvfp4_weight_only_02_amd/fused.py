@@ -11,7 +11,9 @@ Both are differentiable when given the weight's transposed copy
 ``gated_backward`` are the same gradients without autograd, for programs that
 run their own backward pass and for captured graphs (torch ends the process
 where an autograd pass is captured while an eager graph of the same leaves is
-alive; these functions have no such graph).
+alive; these functions have no such graph, and with ``gemm_t`` they refuse
+tensors through which a gradient is wanted).  Forward-mode derivatives are
+refused everywhere.
 
 Every launch goes to ``stream`` (the current stream by default).  Results and
 temporary memory are allocated on it, and tensors of the call are recorded on
@@ -26,6 +28,7 @@ import weakref
 from dataclasses import InitVar, dataclass
 
 import torch
+from torch.autograd import forward_ad
 
 from . import (Nvfp4Error, PackedWeight, _dev, _i32, _i64, _vp, check_devices, lib, packed_codes_bytes,
                packed_scales_bytes)
@@ -334,12 +337,27 @@ def _workspace_arg(workspace):
     return None if workspace is None else _dev(workspace, torch.uint8, "workspace")
 
 
+def _refuse_tangents(tensors) -> None:
+    for t in tensors:
+        if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+            raise ValueError("forward-mode derivatives are not available")
+
+
 def _wants_grad(*tensors) -> bool:
+    if forward_ad._current_level >= 0:      # inside a dual_level
+        _refuse_tangents(tensors)
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:
                 return True
     return False
+
+
+def _no_graph(*tensors) -> None:
+    """Of a call that makes no graph: a gradient wanted through these would be
+    lost without a word."""
+    if _wants_grad(*tensors):
+        raise ValueError("a gradient through this call is not available (detach the argument, or torch.no_grad())")
 
 
 def _check_grad(X, w, transposed, stream, *buffers):
@@ -425,6 +443,8 @@ def linear(w: PackedWeight, X: torch.Tensor, bias: torch.Tensor = None, activati
     if _wants_grad(X, bias, residual):
         _check_grad(X, w, transposed, stream, out, preact, workspace)
         return _Linear.apply(X, bias, residual, w, transposed, act, out_dtype)
+    if out is not None or preact is not None:
+        _no_graph(out, preact)
     return _linear_forward(w, X, bias, act, residual, out, out_dtype, _preact_arg(preact, w, n),
                            _workspace_arg(workspace), stream)
 
@@ -455,6 +475,8 @@ def gated(w: GatedWeight, X: torch.Tensor, activation: str = "silu", gate_bias: 
     if _wants_grad(X, gate_bias, up_bias):
         _check_grad(X, w, transposed, stream, out, preact, workspace)
         return _Gated.apply(X, gate_bias, up_bias, w, transposed, act, out_dtype)
+    if out is not None or preact is not None:
+        _no_graph(out, preact)
     return _gated_forward(w, X, act, gate_bias, up_bias, out, out_dtype, _preact_arg(preact, w, n),
                           _workspace_arg(workspace), stream)
 
@@ -529,6 +551,7 @@ def gemm_t(wt: TransposedWeight, dY: torch.Tensor, out: torch.Tensor = None, str
     _mat(dY, (torch.bfloat16,), "dY", None, wt.N)
     if out is not None:
         _mat(out, (torch.bfloat16,), "out", dY.shape[0], wt.K)
+    _no_graph(dY, out)
     return _linear_backward(wt, dY, 0, None, None, out, stream)[0]
 
 
@@ -541,12 +564,14 @@ def linear_backward(wt: TransposedWeight, dY: torch.Tensor, activation: str = No
         _weight(wt, TransposedWeight, "wt")
         if wt.gated:
             raise ValueError("wt is the copy of a gated weight, which gated_backward takes")
+    _typed(dY, _FLOATS, "dY")
     act = _act(activation)
     if act:
         if preact is None:
             raise ValueError("the gradient of an activation needs preact")
         _mat(preact, (torch.float32,), "preact", dY.shape[0], _pad8(dY.shape[-1]))
     _grad_args(wt, bias_dtype, out, dY.shape[0])
+    _no_graph(dY, preact, out)
     return _linear_backward(wt, dY, act, preact if act else None, bias_dtype, out, stream)
 
 
@@ -557,9 +582,11 @@ def gated_backward(w: GatedWeight, wt: TransposedWeight, dH: torch.Tensor, preac
     _weight(w, GatedWeight)
     if wt is not None:
         _weight(wt, TransposedWeight, "wt")
+    _typed(dH, _FLOATS, "dH")
     act = _act(activation)
     _mat(preact, (torch.float32,), "preact", dH.shape[0], gated_rows(w.F))
     if wt is not None:
         _check_transposed(wt, w)
     _grad_args(wt, bias_dtype, out, dH.shape[0])
+    _no_graph(dH, preact, out)
     return _gated_backward(w, wt, dH, act, preact, bias_dtype, bias_dtype, out, stream)

@@ -639,3 +639,50 @@ def test_transposed_copy_of_another_weight():
             nv.gated_backward(gw, t, dH, z)
     with pytest.raises(ValueError, match="gated weight"):
         nv.linear_backward(gw.transpose(), randn((5, nv.gated_rows(96)), 104))
+
+
+# ---- derivatives that would be lost -----------------------------------------------------
+
+def test_derivatives_are_not_dropped():
+    """Calls without a graph refuse what asks for one, and forward-mode tangents."""
+    say("dropped derivatives")
+    from torch.autograd import forward_ad as fwd
+    w, _ = weight(40, 272, 105)
+    gw = nv.GatedWeight.from_packed(w, w)
+    wt, gt = w.transpose(), gw.transpose()
+    X, dY, r, b = randn((5, 272), 106), randn((5, 40), 107), randn((5, 40), 108), randn((40,), 109)
+    z = torch.zeros(5, nv.preact_columns(gw), device="cuda")
+    out = torch.empty(5, 40, device="cuda", dtype=BF16)
+    zl = torch.zeros(5, nv.preact_columns(w), device="cuda")
+    calls = {  # by the argument that carries the derivative
+        "gemm_t dY": (dY, lambda t: nv.gemm_t(wt, t)),
+        "linear_backward dY": (dY, lambda t: nv.linear_backward(wt, t, bias_dtype=F32)),
+        "linear_backward preact": (zl, lambda t: nv.linear_backward(wt, dY, "silu", t)),
+        "gated_backward dH": (dY, lambda t: nv.gated_backward(gw, gt, t, z)),
+        "gated_backward preact": (z, lambda t: nv.gated_backward(gw, gt, dY, t)),
+        "linear out": (out, lambda t: nv.linear(w, X, out=t)),
+        "gated out": (out, lambda t: nv.gated(gw, X, out=t)),
+        "linear preact": (zl, lambda t: nv.linear(w, X, preact=t)),
+    }
+    for name, (t, f) in calls.items():
+        leaf = t.clone().requires_grad_()
+        with pytest.raises(ValueError, match="gradient"):
+            f(leaf)
+        with torch.no_grad():
+            f(leaf)                                   # nothing is asked for
+        f(leaf.detach())
+    tangents = dict(calls, **{
+        "linear X": (X, lambda t: nv.linear(w, t)),
+        "linear bias": (b, lambda t: nv.linear(w, X, bias=t)),
+        "linear residual": (r, lambda t: nv.linear(w, X, residual=t)),
+        "gated X": (X, lambda t: nv.gated(gw, t)),
+        "gated bias": (b, lambda t: nv.gated(gw, X, up_bias=t)),
+    })
+    for name, (t, f) in tangents.items():
+        want = f(t.clone())
+        with fwd.dual_level():
+            with pytest.raises(ValueError, match="forward-mode"):
+                f(fwd.make_dual(t.clone(), torch.ones_like(t)))
+            got = f(t.clone())                        # no tangent, nothing lost
+        for p, q in zip(got if isinstance(got, tuple) else (got,), want if isinstance(want, tuple) else (want,)):
+            assert p is None or torch.equal(p, q), name
