@@ -29,6 +29,7 @@ from dataclasses import InitVar, dataclass
 
 import torch
 from torch.autograd import forward_ad
+from torch.autograd.graph import increment_version
 
 from . import (Nvfp4Error, PackedWeight, _dev, _i32, _i64, _vp, check_devices, lib, packed_codes_bytes,
                packed_scales_bytes)
@@ -360,6 +361,14 @@ def _no_graph(*tensors) -> None:
         raise ValueError("a gradient through this call is not available (detach the argument, or torch.no_grad())")
 
 
+def _written(*buffers) -> None:
+    """Tell autograd of buffers that a launch overwrites, for the graphs that
+    have saved them."""
+    for t in buffers:
+        if t is not None:
+            increment_version(t)
+
+
 def _check_grad(X, w, transposed, stream, *buffers):
     if any(b is not None for b in buffers):
         raise ValueError("out, preact and workspace go with calls that need no gradient")
@@ -445,6 +454,7 @@ def linear(w: PackedWeight, X: torch.Tensor, bias: torch.Tensor = None, activati
         return _Linear.apply(X, bias, residual, w, transposed, act, out_dtype)
     if out is not None or preact is not None:
         _no_graph(out, preact)
+        _written(out, preact)
     return _linear_forward(w, X, bias, act, residual, out, out_dtype, _preact_arg(preact, w, n),
                            _workspace_arg(workspace), stream)
 
@@ -477,6 +487,7 @@ def gated(w: GatedWeight, X: torch.Tensor, activation: str = "silu", gate_bias: 
         return _Gated.apply(X, gate_bias, up_bias, w, transposed, act, out_dtype)
     if out is not None or preact is not None:
         _no_graph(out, preact)
+        _written(out, preact)
     return _gated_forward(w, X, act, gate_bias, up_bias, out, out_dtype, _preact_arg(preact, w, n),
                           _workspace_arg(workspace), stream)
 
@@ -552,6 +563,7 @@ def gemm_t(wt: TransposedWeight, dY: torch.Tensor, out: torch.Tensor = None, str
     if out is not None:
         _mat(out, (torch.bfloat16,), "out", dY.shape[0], wt.K)
     _no_graph(dY, out)
+    _written(out)
     return _linear_backward(wt, dY, 0, None, None, out, stream)[0]
 
 
@@ -572,6 +584,7 @@ def linear_backward(wt: TransposedWeight, dY: torch.Tensor, activation: str = No
         _mat(preact, (torch.float32,), "preact", dY.shape[0], _pad8(dY.shape[-1]))
     _grad_args(wt, bias_dtype, out, dY.shape[0])
     _no_graph(dY, preact, out)
+    _written(out)
     return _linear_backward(wt, dY, act, preact if act else None, bias_dtype, out, stream)
 
 
@@ -589,4 +602,5 @@ def gated_backward(w: GatedWeight, wt: TransposedWeight, dH: torch.Tensor, preac
         _check_transposed(wt, w)
     _grad_args(wt, bias_dtype, out, dH.shape[0])
     _no_graph(dH, preact, out)
+    _written(out)
     return _gated_backward(w, wt, dH, act, preact, bias_dtype, bias_dtype, out, stream)

@@ -686,3 +686,36 @@ def test_derivatives_are_not_dropped():
             got = f(t.clone())                        # no tangent, nothing lost
         for p, q in zip(got if isinstance(got, tuple) else (got,), want if isinstance(want, tuple) else (want,)):
             assert p is None or torch.equal(p, q), name
+
+
+def test_written_buffers_are_modified_in_place():
+    """A buffer that a graph saved and a call then overwrote is an error of that
+    graph's backward pass, not another gradient."""
+    say("versions")
+    w, _ = weight(40, 272, 110)
+    gw = nv.GatedWeight.from_packed(w, w)
+    wt, gt = w.transpose(), gw.transpose()
+    X, dY = randn((5, 272), 111), randn((5, 40), 112)
+    z = torch.zeros(5, nv.preact_columns(gw), device="cuda")
+    calls = {
+        "linear out": ((5, 40), BF16, lambda t: nv.linear(w, X, out=t)),
+        "linear preact": ((5, nv.preact_columns(w)), F32, lambda t: nv.linear(w, X, preact=t)),
+        "gated out": ((5, 40), BF16, lambda t: nv.gated(gw, X, out=t)),
+        "gated preact": ((5, nv.preact_columns(gw)), F32, lambda t: nv.gated(gw, X, preact=t)),
+        "gemm_t out": ((5, 272), BF16, lambda t: nv.gemm_t(wt, dY, out=t)),
+        "linear_backward out": ((5, 272), BF16, lambda t: nv.linear_backward(wt, dY, out=t)),
+        "gated_backward out": ((5, 272), BF16, lambda t: nv.gated_backward(gw, gt, dY, z, out=t)),
+    }
+    for name, (shape, dtype, f) in calls.items():
+        buf = torch.zeros(shape, device="cuda", dtype=dtype)
+        f(buf)
+        leaf = torch.ones_like(buf).requires_grad_()
+        y = (leaf * buf).sum()
+        f(buf)
+        with pytest.raises(RuntimeError, match="inplace"):
+            y.backward()
+        f(buf)
+        (leaf * buf).sum().backward()
+        assert torch.equal(leaf.grad, buf), name
+        with torch.inference_mode():
+            f(torch.zeros(shape, device="cuda", dtype=dtype))
