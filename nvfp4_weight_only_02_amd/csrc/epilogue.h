@@ -27,13 +27,25 @@ constexpr float kTanhA = 0.044715f;
 // Phi(z), the normal distribution function, as 1 - erfc(x) / 2 for z = sqrt(2) x
 // >= 0 and erfc(x) / 2 for -z.  erfc(x) = t exp(p(t) - x^2) with t = 1 / (1 +
 // 0.4 x): p is a Chebyshev fit of degree 9, in t, of ln(erfc(x) exp(x^2) / t),
-// relative error 5e-8 before rounding and 9e-7 (x < 3.6) in fp32.  The math
+// relative error 9e-8 before rounding.  exp(-x^2) = 2^-(z^2 log2(e) / 2) takes
+// the remainders of the square and of the product: a rounding of the exponent y
+// would be a relative error of y 2^-24 (7e-6 of Phi(-8), 1.8e-5 of Phi(-13)).
+// Phi(z) is within 8e-7 of its value for every z, and 0 below 2^-126.  The math
 // library's erfc takes about four times the instructions: gelu added 22 us to
-// the 150 of 16384 x 5120 at n = 1024, and adds 10 this way.
-__device__ __forceinline__ float normal_cdf(float z)
+// the 158 of 16384 x 5120 at n = 1024, and adds 14 this way (9 without the
+// remainders).
+// *density receives exp(-z^2 / 2).
+__device__ __forceinline__ float normal_cdf(float z, float *density)
 {
-    const float x = fabsf(z) * kSqrtHalf;
-    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.4f, x, 1.0f));
+    constexpr float kC = 0.72134752044448170f;                              // log2(e) / 2
+    constexpr float kCLow = (float)(0.72134752044448170 - (double)kC);
+    const float a = fminf(fabsf(z), 16.0f);                                 // 0 by then
+    const float q = a * a, y = q * kC;
+    const float low = __builtin_fmaf(__builtin_fmaf(a, a, -q), kC, __builtin_fmaf(q, kCLow, __builtin_fmaf(q, kC, -y)));
+    const float e = __builtin_amdgcn_exp2f(-y);
+    const float d = __builtin_fmaf(-0.69314718f * low, e, e);               // 2^-low, low < 2^-16
+    *density = d;
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.4f * kSqrtHalf, a, 1.0f));
     float p = 0.0683646575f;
     p = __builtin_fmaf(p, t, -0.581891f);
     p = __builtin_fmaf(p, t, 1.81158173f);
@@ -44,7 +56,7 @@ __device__ __forceinline__ float normal_cdf(float z)
     p = __builtin_fmaf(p, t, 0.360483378f);
     p = __builtin_fmaf(p, t, 1.0063802f);
     p = __builtin_fmaf(p, t, -1.48894858f);
-    const float half = 0.5f * t * __expf(__builtin_fmaf(-x, x, p));
+    const float half = 0.5f * t * __expf(p) * d;
     return z < 0.0f ? half : 1.0f - half;
 }
 
@@ -55,7 +67,10 @@ __device__ __forceinline__ float activate(float z, int act)
     switch (act) {
     case NVFP4_ACT_RELU: return z < 0.0f ? 0.0f : z;   // NaN stays NaN
     case NVFP4_ACT_SILU: return z * sigmoid_f(z);
-    case NVFP4_ACT_GELU: return z * normal_cdf(z);
+    case NVFP4_ACT_GELU: {
+        float density;
+        return z * normal_cdf(z, &density);
+    }
     case NVFP4_ACT_GELU_TANH: return z * sigmoid_f(kTanhC * (z + kTanhA * z * z * z));
     default: return z;
     }
@@ -70,8 +85,11 @@ __device__ __forceinline__ float activate_grad(float z, int act)
         const float s = sigmoid_f(z);
         return s * (1.0f + z * (1.0f - s));
     }
-    case NVFP4_ACT_GELU:
-        return normal_cdf(z) + z * kInvSqrt2Pi * __expf(-0.5f * z * z);
+    case NVFP4_ACT_GELU: {
+        float density;
+        const float cdf = normal_cdf(z, &density);
+        return cdf + z * kInvSqrt2Pi * density;
+    }
     case NVFP4_ACT_GELU_TANH: {
         // s (1 - s) is 0 well before |z| = 16: beyond it the square would only
         // overflow, to 0 * inf

@@ -719,3 +719,36 @@ def test_written_buffers_are_modified_in_place():
         assert torch.equal(leaf.grad, buf), name
         with torch.inference_mode():
             f(torch.zeros(shape, device="cuda", dtype=dtype))
+
+
+# ---- the left tail of gelu ----------------------------------------------------------------
+
+# Phi(z) in units of 2^-24 of its value: t = 1 / (1 + 0.4 x) is off by 4 (x, the
+# sum, the reciprocal), the polynomial by 6, the two exponentials by 2 each, five
+# products by 1 each, the fit by 1.5: 20.5.  2^-126 is where they are flushed.
+PHI_EPS = 2.0 ** -19
+
+
+@pytest.mark.parametrize("n", [1, 20])
+def test_gelu_keeps_its_relative_precision(n):
+    say("gelu tail", n)
+    N, K = 4003, 16
+    w, _ = weight(N, K, 113)
+    z = torch.linspace(-14, 9, N, device="cuda")
+    Y = nv.linear(w, torch.zeros(n, K, device="cuda", dtype=BF16), bias=z, activation="gelu", out_dtype=F32)
+    z64 = f64(z)
+    ref = R.act(z64, "gelu")
+    bound = PHI_EPS * np.abs(ref) + np.abs(z64) * 2.0 ** -126
+    check(Y, (np.tile(ref, (n, 1)), np.tile(bound, (n, 1))), "gelu")
+
+
+def test_gelu_gradient_keeps_its_relative_precision():
+    """Phi(z) + z phi(z), against the sum of both terms' magnitudes."""
+    say("gelu gradient tail")
+    N = 4000
+    z = torch.linspace(-14, 9, N, device="cuda")[None]
+    _, db = nv.linear_backward(None, torch.ones(1, N, device="cuda"), "gelu", z, F32)
+    z64 = f64(z)[0]
+    phi = np.exp(-z64 * z64 / 2) / np.sqrt(2 * np.pi)
+    terms = 0.5 * R.special.erfc(-z64 / np.sqrt(2)) + np.abs(z64) * phi
+    check(db, (R.act_grad(z64, "gelu"), PHI_EPS * terms + np.abs(z64) * 2.0 ** -125), "gelu'")
