@@ -299,7 +299,10 @@ int nvfp4_gemm_geometry(int n, int N, int K, int *rows_per_workgroup,
  *   - sums, biases, activations and products are fp32, rounded once when
  *     stored;
  *   - outputs may not overlap other arguments (OVERLAP), except that the
- *     residual may be the output itself (same address, stride and type);
+ *     residual may be the output itself (same address, stride and type).
+ *     Matrices with one stride in bytes may be neighbouring columns of one
+ *     buffer; with different strides their spans, first to last element, lie
+ *     apart;
  *   - a call may run in K parts: fp32 partial sums in a workspace the caller
  *     owns (16-byte aligned, at least the bytes its _workspace_bytes function
  *     names, 0 for most sizes), added in part order by a second launch.  Calls

@@ -257,18 +257,51 @@ bool is_aligned(const void *p, size_t a)
     return ((uintptr_t)p % a) == 0;
 }
 
-// Bytes from the first to the last element of an [n][cols] matrix.
-size_t span(long long n, long long ld, long long cols, int size)
+// Memory an argument covers, in bytes: an array, or a matrix whose rows of
+// `width` bytes lie `ld` apart.
+struct Region {
+    const void *p;
+    size_t rows, ld, width;
+    size_t span() const { return rows ? (rows - 1) * ld + width : 0; }
+};
+
+Region array(const void *p, size_t bytes)
 {
-    return n > 0 ? (size_t)((n - 1) * ld + cols) * size : 0;
+    return {p, p && bytes ? 1u : 0u, 0, bytes};
+}
+
+Region matrix(const void *p, int n, int64_t ld, int64_t cols, int size)
+{
+    return {p, p && n > 0 ? (size_t)n : 0u, (size_t)ld * size, (size_t)cols * size};
+}
+
+// Rows that take turns in memory with one stride (neighbouring columns of one
+// buffer) lie apart although their spans do not.
+bool overlap(const Region &a, const Region &b)
+{
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    if (!a.rows || !b.rows || x >= y + b.span() || y >= x + a.span())
+        return false;
+    const size_t ld = a.rows > 1 ? a.ld : b.ld;   // one row fits any stride
+    if ((a.rows == 1 && b.rows == 1) || (a.rows > 1 && b.rows > 1 && a.ld != b.ld) || a.width > ld || b.width > ld)
+        return true;
+    const size_t from = (y % ld + ld - x % ld) % ld;   // b's first column, in a's rows
+    return from < a.width || from + b.width > ld;
 }
 
 bool overlap(const void *a, size_t an, const void *b, size_t bn)
 {
-    if (!a || !b || !an || !bn)
-        return false;
-    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-    return x < y + bn && y < x + an;
+    return overlap(array(a, an), array(b, bn));
+}
+
+// Whether an output overlaps an argument.
+template <int I>
+bool any_overlap(const Region &out, const Region (&args)[I])
+{
+    for (const Region &a : args)
+        if (overlap(out, a))
+            return true;
+    return false;
 }
 
 bool valid_dtype(int d)
@@ -314,17 +347,14 @@ int validate_forward(const uint8_t *Wq, const uint8_t *Wscale, const uint16_t *X
     // Workgroups read what others write unless the outputs lie apart.  The
     // residual may be the output itself: each element is read by the thread
     // that then writes it.
-    const size_t on = span(n, ldo, N, os), pn = ep->preact ? span(n, ep->ldp, pre_cols, 4) : 0;
-    const size_t xn = span(n, ldx, K, 2);
     const size_t bn = (size_t)N * dtype_size(ep->bias_dtype);
-    const size_t wq = nvfp4_packed_codes_bytes(rows, K), ws = nvfp4_packed_scales_bytes(rows, K);
-    const size_t rn = ep->residual ? span(n, ep->ldr, N, dtype_size(ep->residual_dtype)) : 0;
+    const Region y = matrix(out, n, ldo, N, os), z = matrix(ep->preact, n, ep->ldp, pre_cols, 4);
+    const Region residual = matrix(ep->residual, n, ep->ldr, N, dtype_size(ep->residual_dtype));
+    const Region in[] = {matrix(X, n, ldx, K, 2), array(Wq, nvfp4_packed_codes_bytes(rows, K)),
+                         array(Wscale, nvfp4_packed_scales_bytes(rows, K)), array(ep->bias, bn), array(ep->up_bias, bn)};
     const bool in_place = ep->residual == out && ep->ldr == ldo && ep->residual_dtype == ep->out_dtype;
-    if (overlap(out, on, X, xn) || overlap(out, on, Wq, wq) || overlap(out, on, Wscale, ws) ||
-        overlap(out, on, ep->bias, bn) || overlap(out, on, ep->up_bias, bn) || overlap(out, on, ep->preact, pn) ||
-        (!in_place && overlap(out, on, ep->residual, rn)) || overlap(ep->preact, pn, X, xn) ||
-        overlap(ep->preact, pn, Wq, wq) || overlap(ep->preact, pn, Wscale, ws) || overlap(ep->preact, pn, ep->bias, bn) ||
-        overlap(ep->preact, pn, ep->up_bias, bn) || overlap(ep->preact, pn, ep->residual, rn))
+    if (any_overlap(y, in) || any_overlap(z, in) || overlap(y, z) || overlap(z, residual) ||
+        (!in_place && overlap(y, residual)))
         return NVFP4_ERR_OVERLAP;
     return NVFP4_OK;
 }
@@ -386,12 +416,12 @@ int check_workspace(const void *workspace, size_t bytes, size_t need, const uint
     if (!is_aligned(workspace, 16))
         return NVFP4_ERR_ALIGN;
     const size_t bn = (size_t)e.N * (e.flags & kEpiBiasF32 ? 4 : 2);
-    if (overlap(workspace, need, codes, tiles * 1024) || overlap(workspace, need, scales, tiles * 128) ||
-        overlap(workspace, need, X, span(n, ldx, K, 2)) || overlap(workspace, need, e.bias, bn) ||
-        overlap(workspace, need, e.up_bias, bn) ||
-        overlap(workspace, need, e.out, span(n, e.ldo, e.N, e.flags & kEpiOutF32 ? 4 : 2)) ||
-        overlap(workspace, need, e.residual, span(n, e.ldr, e.N, e.flags & kEpiResidualF32 ? 4 : 2)) ||
-        overlap(workspace, need, e.preact, span(n, e.ldp, pre_cols, 4)))
+    const Region others[] = {array(codes, tiles * 1024), array(scales, tiles * 128), matrix(X, n, ldx, K, 2),
+                             array(e.bias, bn), array(e.up_bias, bn),
+                             matrix(e.out, n, e.ldo, e.N, e.flags & kEpiOutF32 ? 4 : 2),
+                             matrix(e.residual, n, e.ldr, e.N, e.flags & kEpiResidualF32 ? 4 : 2),
+                             matrix(e.preact, n, e.ldp, pre_cols, 4)};
+    if (any_overlap(array(workspace, need), others))
         return NVFP4_ERR_OVERLAP;
     return NVFP4_OK;
 }
@@ -596,18 +626,17 @@ int backward(const Backward &b, void *workspace, size_t workspace_bytes, hipStre
         return NVFP4_ERR_WORKSPACE;
     if (w.total() && !is_aligned(workspace, 16))
         return NVFP4_ERR_ALIGN;
-    const size_t yn = span(n, b.ldy, N, ds), pn = b.preact ? span(n, b.ldp, pre_cols, 4) : 0, bn = (size_t)N * bs;
-    const size_t xn = b.dx ? span(n, b.ldx, b.K, 2) : 0;
-    const size_t ct = b.dx ? nvfp4_transposed_codes_bytes(b.rows(), b.K) : 0;
-    const size_t st = b.dx ? nvfp4_transposed_scales_bytes(b.rows(), b.K) : 0;
-    const struct { const void *p; size_t size; } out[] = {{b.dx, xn}, {b.db[0], bn}, {b.db[1], bn}, {workspace, w.total()}},
-        in[] = {{b.dy, yn}, {b.preact, pn}, {b.codes_t, ct}, {b.scales_t, st}};
+    const size_t bn = (size_t)N * bs;
+    const Region in[] = {matrix(b.dy, n, b.ldy, N, ds), matrix(b.preact, n, b.ldp, pre_cols, 4),
+                         array(b.codes_t, b.dx ? nvfp4_transposed_codes_bytes(b.rows(), b.K) : 0),
+                         array(b.scales_t, b.dx ? nvfp4_transposed_scales_bytes(b.rows(), b.K) : 0)};
+    const Region out[] = {matrix(b.dx, n, b.ldx, b.K, 2), array(b.db[0], bn), array(b.db[1], bn),
+                          array(workspace, w.total())};
     for (int i = 0; i < 4; ++i) {
-        for (const auto &q : in)
-            if (overlap(out[i].p, out[i].size, q.p, q.size))
-                return NVFP4_ERR_OVERLAP;
+        if (any_overlap(out[i], in))
+            return NVFP4_ERR_OVERLAP;
         for (int j = 0; j < i; ++j)
-            if (overlap(out[i].p, out[i].size, out[j].p, out[j].size))
+            if (overlap(out[i], out[j]))
                 return NVFP4_ERR_OVERLAP;
     }
     int cus = 0;

@@ -290,3 +290,38 @@ def test_transposed_copy_of_another_weight_is_refused():
     x = nv.torch.empty(4, 96, dtype=nv.torch.bfloat16)
     with pytest.raises(ValueError, match="gated weight"):
         nv.linear_backward(gt, x)
+
+
+# ---- column slices of one buffer -----------------------------------------------------------
+
+def test_disjoint_columns_do_not_overlap():
+    """Matrices whose rows take turns in memory: neighbouring columns of one
+    row-major buffer."""
+    if nv.torch.cuda.is_available():
+        pytest.skip("needs a machine without a GPU")
+    base, ld = at(2), 512                                  # bf16 rows of 1 KiB
+    col = lambda c, size=2: base + c * size                # noqa: E731
+    # X in columns 0 .. 255, Y in 256 .. 319, residual in 320 .. 383
+    ep = epilogue(residual=col(320), ldr=ld)
+    assert linear(x=col(0), ldx=ld, y=col(256), ldy=ld, ep=ep) == DEVICE
+    assert linear(x=col(256), ldx=ld, y=col(0), ldy=ld, ep=epilogue(residual=col(64), ldr=ld)) == DEVICE
+    # Y reaches one column into X, into the residual, and around a row's end into X
+    assert linear(x=col(0), ldx=ld, y=col(255), ldy=ld) == OVERLAP
+    assert linear(x=col(0), ldx=ld, y=col(257), ldy=ld, ep=ep) == OVERLAP
+    assert linear(x=col(0), ldx=ld, y=col(449), ldy=ld) == OVERLAP
+    assert linear(x=col(0), ldx=ld, y=col(448), ldy=ld) == DEVICE
+    # a row further on the columns are the same ones; one row alone lies between rows
+    assert linear(x=col(0), ldx=ld, y=col(256 + 2 * ld), ldy=ld) == DEVICE
+    assert linear(x=col(0), ldx=ld, y=col(2 * ld), ldy=ld) == OVERLAP
+    assert linear(n=1, x=col(0), y=col(256), ep=epilogue(residual=col(320), ldr=64)) == DEVICE
+    # another stride in bytes: by their spans
+    assert linear(x=col(0), ldx=ld, y=col(256), ldy=ld, ep=epilogue(out_dtype=0)) == OVERLAP
+    assert linear(x=col(0), ldx=ld, y=col(256), ldy=ld // 2, ep=epilogue(out_dtype=0)) == DEVICE
+    # a bias between two rows of Y, a pre-activation buffer beside the output
+    assert linear(y=col(0), ldy=ld, x=at(4), ep=epilogue(bias=col(64))) == DEVICE
+    assert linear(y=col(0), ldy=ld, x=at(4), ep=epilogue(bias=col(449))) == OVERLAP
+    assert linear(y=col(0), ldy=ld, x=at(4), ep=epilogue(preact=col(256), ldp=ld // 2)) == DEVICE
+    assert linear(y=col(0), ldy=ld, x=at(4), ep=epilogue(preact=col(448), ldp=ld // 2)) == OVERLAP
+    # gradients: dX beside dY; dX over its columns
+    assert linear_backward(dy=col(48), ldy=ld, dx=col(0), ldx=ld) == DEVICE
+    assert linear_backward(dy=col(47), ldy=ld, dx=col(0), ldx=ld) == OVERLAP

@@ -752,3 +752,34 @@ def test_gelu_gradient_keeps_its_relative_precision():
     phi = np.exp(-z64 * z64 / 2) / np.sqrt(2 * np.pi)
     terms = 0.5 * R.special.erfc(-z64 / np.sqrt(2)) + np.abs(z64) * phi
     check(db, (R.act_grad(z64, "gelu"), PHI_EPS * terms + np.abs(z64) * 2.0 ** -125), "gelu'")
+
+
+# ---- column slices of one buffer ----------------------------------------------------------
+
+@pytest.mark.parametrize("n,N,K", [(5, 40, 272), (16, 93, 144), (40, 93, 272), (33, 72, 8208)])
+def test_neighbouring_columns_of_one_buffer(n, N, K):
+    """X, the residual and the output side by side in one buffer, the gradient's
+    dY and dX in another: what contiguous calls give, and nothing else moves."""
+    say("columns", n, N, K)
+    w, _ = weight(N, K, 114)
+    wt = w.transpose()
+    X, r, dY = randn((n, K), 115), randn((n, N), 116), randn((n, N), 117)
+    want = nv.linear(w, X, activation="silu", residual=r)
+    pad = 4 + (-(K + 2 * N + 4)) % 8
+    buf = torch.full((n, K + 2 * N + pad), 7.0, device="cuda", dtype=BF16)
+    x, res, out = buf[:, :K], buf[:, K:K + N], buf[:, K + N + 1:K + 2 * N + 1]
+    x.copy_(X)
+    res.copy_(r)
+    nv.linear(w, x, activation="silu", residual=res, out=out)
+    assert torch.equal(out, want) and torch.equal(x, X) and torch.equal(res, r)
+    assert (buf[:, K + N] == 7).all() and (buf[:, K + 2 * N + 1:] == 7).all()
+    dX, db = nv.linear_backward(wt, dY, bias_dtype=F32)
+    buf = torch.full((n, K + N + 8), 7.0, device="cuda", dtype=BF16)
+    dy, dx = buf[:, 1:1 + N], buf[:, 3 + N:3 + N + K]
+    dy.copy_(dY)
+    got = nv.linear_backward(wt, dy, bias_dtype=F32, out=dx)
+    assert torch.equal(dx, dX) and torch.equal(got[1], db) and torch.equal(dy, dY)
+    assert (buf[:, 0] == 7).all() and (buf[:, 1 + N:3 + N] == 7).all() and (buf[:, 3 + N + K:] == 7).all()
+    with pytest.raises(nv.Nvfp4Error) as e:
+        nv.linear_backward(wt, dy, out=buf[:, N:N + K])
+    assert e.value.status == 10
