@@ -335,9 +335,10 @@ typedef struct nvfp4_epilogue {
 } nvfp4_epilogue;
 
 /* Y = act(gscale X dequant(W)^T + bias) + residual for any n up to
- * NVFP4_MAX_GEMM_TOKENS, Wq / Wscale packed (nvfp4_pack).  Up to 16 tokens run
- * the decode product (K parts beyond K = 8192), more a token-tiled product (K
- * parts where its tiles alone would leave compute units idle).
+ * NVFP4_MAX_GEMM_TOKENS and N up to 2^30, Wq / Wscale packed (nvfp4_pack).  Up
+ * to 16 tokens run the decode product (K parts beyond K = 8192), more a
+ * token-tiled product (K parts where its tiles alone would leave compute units
+ * idle).
  * Errors: NULL, RANGE (n, N, K, strides, activation, types; up_bias set),
  * SHAPE (K % 16, K > 262144, strides), ALIGN, OVERLAP, WORKSPACE, DEVICE,
  * LAUNCH. */

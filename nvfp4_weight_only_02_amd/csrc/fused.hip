@@ -250,6 +250,7 @@ __global__ __launch_bounds__(256) void nvfp4_grad_sum_kernel(GradParams p, int b
 
 // ---- host side --------------------------------------------------------------------------
 
+constexpr int kMaxRows = 1 << 30;     // of a packed weight: rounded up to a tile they stay within 32 bits
 constexpr int kMaxStride = 1 << 22;   // elements between rows: keeps a token tile's offsets within 32 bits
 
 bool is_aligned(const void *p, size_t a)
@@ -321,7 +322,7 @@ int validate_forward(const uint8_t *Wq, const uint8_t *Wscale, const uint16_t *X
 {
     if (!Wq || !Wscale || !ep || (n > 0 && (!X || !out)))
         return NVFP4_ERR_NULL;
-    if (n < 0 || n > NVFP4_MAX_GEMM_TOKENS || N < 1 || K < 1)
+    if (n < 0 || n > NVFP4_MAX_GEMM_TOKENS || N < 1 || N > kMaxRows || K < 1)
         return NVFP4_ERR_RANGE;
     if (K % 16 != 0 || K > kMaxK)
         return NVFP4_ERR_SHAPE;
@@ -795,7 +796,7 @@ int nvfp4_fused_geometry(int n, int rows, int K, int *rows_per_workgroup, int *t
 
 size_t nvfp4_linear_workspace_bytes(int n, int N, int K)
 {
-    if (n < 0 || n > NVFP4_MAX_GEMM_TOKENS || N < 1 || K < 1 || K % 16 != 0 || K > kMaxK)
+    if (n < 0 || n > NVFP4_MAX_GEMM_TOKENS || N < 1 || N > kMaxRows || K < 1 || K % 16 != 0 || K > kMaxK)
         return 0;
     return parts_bytes(n, N, K);
 }

@@ -325,3 +325,15 @@ def test_disjoint_columns_do_not_overlap():
     # gradients: dX beside dY; dX over its columns
     assert linear_backward(dy=col(48), ldy=ld, dx=col(0), ldx=ld) == DEVICE
     assert linear_backward(dy=col(47), ldy=ld, dx=col(0), ldx=ld) == OVERLAP
+
+
+def test_rows_beyond_the_limit():
+    """2^30 rows, as the packing steps and the geometry take: beyond, a row count
+    rounded up to a tile would leave 32 bits."""
+    f, g = fused._call("nvfp4_linear_workspace_bytes"), fused._call("nvfp4_gated_workspace_bytes")
+    for N in ((1 << 30) + 1, (1 << 31) - 16, (1 << 31) - 1):
+        for n in (4, 40):
+            assert linear(n=n, N=N, K=16, y=at(60)) == RANGE
+            assert f(n, N, 16384) == 0
+    assert f(4, 1 << 30, 16384) == nv.gemv_kparts(1 << 30, 16384) * 4 * (1 << 30) * 4
+    assert gated(F=(1 << 29) + 1, h=at(60)) == RANGE and g(4, (1 << 29) + 1, 16384) == 0
