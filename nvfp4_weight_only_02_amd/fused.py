@@ -102,6 +102,8 @@ def _mat(t, dtypes, name: str, n, cols) -> torch.Tensor:
     shape = t.shape
     if len(shape) != 2 or shape[1] != cols or (n is not None and shape[0] != n):
         raise ValueError("%s must be [%s, %d], got %s" % (name, "n" if n is None else n, cols, list(shape)))
+    if shape[0] >> 31 or cols >> 31:         # the library's sizes are 32-bit
+        raise ValueError("%s must have fewer than 2^31 rows and columns, got %s" % (name, list(shape)))
     if t.stride(1) != 1 and cols > 1 and shape[0] > 0:
         raise ValueError("%s must have unit stride along a row" % name)
     return t

@@ -783,3 +783,18 @@ def test_neighbouring_columns_of_one_buffer(n, N, K):
     with pytest.raises(nv.Nvfp4Error) as e:
         nv.linear_backward(wt, dy, out=buf[:, N:N + K])
     assert e.value.status == 10
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    """A row or column count that the library's int would cut to a small one."""
+    say("sizes beyond 32 bits")
+    big = torch.zeros((1 << 32) + 64, device="cuda", dtype=BF16)
+    for dY in (big[:, None], big[None]):
+        with pytest.raises(ValueError, match="2\\^31"):
+            nv.linear_backward(None, dY, bias_dtype=F32)
+    w, _ = weight(1, 16, 118)
+    with pytest.raises(ValueError, match="2\\^31"):
+        nv.gemm_t(w.transpose(), big[:, None])
+    with pytest.raises(nv.Nvfp4Error) as e:
+        nv.gemm_t(w.transpose(), big[:(1 << 20) + 1, None])
+    assert e.value.status == 2
