@@ -261,8 +261,17 @@ class PackedWeight:
     @classmethod
     def from_float(cls, W: torch.Tensor, stream=None) -> "PackedWeight":
         """Quantise an fp32 or bf16 weight straight into the packed layout."""
-        cp, sp, ts = quantize_packed(W, stream)
-        gscale = float(ts[0].item())          # one host read at load time
+        if stream is None:
+            cp, sp, ts = quantize_packed(W)
+            gscale = float(ts[0].item())      # one host read at load time
+        else:
+            check_devices((), torch.cuda.current_device(), stream.device)
+            current = torch.cuda.current_stream()
+            with torch.cuda.stream(stream):   # the read too: on the current stream it would not wait
+                cp, sp, ts = quantize_packed(W)
+                gscale = float(ts[0].item())
+            for t in (cp, sp):
+                t.record_stream(current)      # memory of the launch stream, used on this one
         return cls(cp, sp, gscale, W.shape[0], W.shape[1])
 
     def transpose(self, stream=None) -> "TransposedWeight":

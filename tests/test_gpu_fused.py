@@ -798,3 +798,30 @@ def test_sizes_beyond_32_bits_are_refused():
     with pytest.raises(nv.Nvfp4Error) as e:
         nv.gemm_t(w.transpose(), big[:(1 << 20) + 1, None])
     assert e.value.status == 2
+
+
+def test_quantising_on_another_stream_reads_its_own_tensor_scale():
+    """The launch stream is behind (tens of ms) when the tensor scale is read."""
+    say("from_float on a stream")
+    W, V = randn((64, 256), 119, F32, 0.05), randn((64, 256), 120, F32, 0.02)
+    want, gated = nv.PackedWeight.from_float(W), nv.GatedWeight.from_float(W, V)
+    old = [torch.full((2,), 123.0, device="cuda") for _ in range(64)]
+    del old                               # what new small tensors find in their memory
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):            # the same for memory of that stream
+        old = [torch.full((2,), 123.0, device="cuda") for _ in range(64)]
+        del old
+    torch.cuda.synchronize()
+
+    def behind():
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(50_000_000)
+    behind()
+    w = nv.PackedWeight.from_float(W, stream=s)
+    assert w.gscale == want.gscale
+    behind()
+    g = nv.GatedWeight.from_float(W, V, stream=s)
+    assert (g.gate_gscale, g.up_gscale) == (gated.gate_gscale, gated.up_gscale)
+    s.synchronize()
+    assert torch.equal(w.codes, want.codes) and torch.equal(w.scales, want.scales)
+    assert torch.equal(g.codes, gated.codes) and torch.equal(g.scales, gated.scales)
