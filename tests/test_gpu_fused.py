@@ -825,3 +825,204 @@ def test_quantising_on_another_stream_reads_its_own_tensor_scale():
     s.synchronize()
     assert torch.equal(w.codes, want.codes) and torch.equal(w.scales, want.scales)
     assert torch.equal(g.codes, gated.codes) and torch.equal(g.scales, gated.scales)
+
+
+# ---- gradients in K parts, of many row blocks, of fp32 gradients; every tile's epilogue ---
+
+def linear_step(w, W, n, seed, act, out=BF16, bias=F32, what=""):
+    """A training step in two ways, with and without autograd, against 64 bits:
+    output, pre-activations, dX and the bias gradient."""
+    N, K = W.shape
+    wt = w.transpose()
+    X, b, r = randn((n, K), seed), randn((N,), seed + 1, bias), randn((n, N), seed + 2, out, 2.0)
+    dY = randn((n, N), seed + 3, out, 0.1)
+    z = torch.full((n, nv.preact_columns(w)), float("nan"), device="cuda")
+    Y = nv.linear(w, X, bias=b, activation=act, residual=r, out_dtype=out, preact=z)
+    x, bb = f64(X), f64(b)
+    check(Y, R.linear(x, W, bb, act, f64(r), out == F32), what + " Y")
+    p, ep = R.pre(x, W, bb)
+    check(z[:, :N], (p, ep + R.HALF_F32 * (np.abs(p) + ep)), what + " preact")
+    dX, db = nv.linear_backward(wt, dY, act, z, bias)
+    want_x, want_b = R.linear_grads(x, W, f64(dY), bb, act, bias == F32)
+    check(dX, want_x, what + " dX")
+    check(db, want_b, what + " db")
+    Xg, bg = X.clone().requires_grad_(), b.clone().requires_grad_()
+    Yg = nv.linear(w, Xg, bias=bg, activation=act, residual=r, out_dtype=out, transposed=wt)
+    for a, q in zip((Yg,) + torch.autograd.grad(Yg, [Xg, bg], dY), (Y, dX, db)):
+        assert torch.equal(a, q), what
+
+
+def gated_step(g, Wg, u, Wu, n, seed, act, out=BF16, bias=F32, what=""):
+    F, K = Wg.shape
+    w = nv.GatedWeight.from_packed(g, u)
+    wt = w.transpose()
+    X, bg, bu = randn((n, K), seed), randn((F,), seed + 1, bias), randn((F,), seed + 2, bias)
+    dH = randn((n, F), seed + 3, out, 0.1)
+    z = torch.full((n, nv.preact_columns(w)), float("nan"), device="cuda")
+    H = nv.gated(w, X, activation=act, gate_bias=bg, up_bias=bu, out_dtype=out, preact=z)
+    x, gb, ub = f64(X), f64(bg), f64(bu)
+    check(H, R.gated(x, Wg, Wu, gb, ub, act, out == F32), what + " H")
+    rows = torch.arange(F, device="cuda")
+    rows = rows // 16 * 32 + rows % 16
+    for W, b, at in ((Wg, gb, rows), (Wu, ub, rows + 16)):
+        p, ep = R.pre(x, W, b)
+        check(z[:, at], (p, ep + R.HALF_F32 * (np.abs(p) + ep)), what + " preact")
+    got = nv.gated_backward(w, wt, dH, z, act, bias)
+    for a, want, name in zip(got, R.gated_grads(x, Wg, Wu, f64(dH), gb, ub, act, bias == F32), ("dX", "dbg", "dbu")):
+        check(a, want, what + " " + name)
+    leaves = [t.clone().requires_grad_() for t in (X, bg, bu)]
+    Hg = nv.gated(w, leaves[0], activation=act, gate_bias=leaves[1], up_bias=leaves[2], out_dtype=out, transposed=wt)
+    for a, q in zip((Hg,) + torch.autograd.grad(Hg, leaves, dH), (H,) + got):
+        assert torch.equal(a, q), what
+
+
+@pytest.mark.parametrize("n", [1, 7, 16])
+@pytest.mark.parametrize("act,out,bias", [("silu", BF16, F32), ("gelu", F32, BF16)])
+def test_training_step_with_a_decode_product_in_parts(n, act, out, bias):
+    """K > 8192 at few tokens: the second launch stores the pre-activations."""
+    say("step, decode parts", n, act)
+    N, K = 83, 8208
+    assert nv.gemv_kparts(N, K) > 1 and nv.gemv_kparts(nv.gated_rows(N), K) > 1
+    (g, Wg), (u, Wu) = weight(N, K, 121), weight(N, K, 122, 0.02)
+    linear_step(g, Wg, n, 123, act, out, bias, "linear")
+    gated_step(g, Wg, u, Wu, n, 127, act, out, bias, "gated")
+
+
+@pytest.mark.parametrize("n,N,K", [(33, 5140, 8208), (100, 5140, 4112)])
+def test_training_step_in_parts_both_ways(n, N, K):
+    """Forward and backward products in K parts, with bias gradients of several
+    row blocks: the workspace holds dZ, column sums and partial sums."""
+    say("step, parts", n, N, K)
+    F = N // 2
+    for rows, k in ((N, K), (nv.gated_rows(F), K), (K, N + (-N) % 8), (K, nv.gated_rows(F))):
+        assert nv.fused_geometry(n, rows, k)[3] > 1
+    w, W = device_weight(N, K, 131)
+    linear_step(w, f64(W), n, 132, "gelu_tanh", what="linear")
+    (g, Wg), (u, Wu) = device_weight(F, K, 136), device_weight(F, K, 137)
+    gated_step(g, f64(Wg), u, f64(Wu), n, 138, "silu", what="gated")
+
+
+@pytest.mark.parametrize("n,N", [(450, 16400), (1001, 8210), (40000, 40)])
+def test_column_sums_of_many_rows_a_block(n, N):
+    """More token rows a block of the gradient kernel than its eight at a time
+    (2048 blocks in all, 256 columns each), and the same bits again."""
+    say("rows a block", n, N)
+    K = 48
+    assert n > 8 * -(-2048 // -(-N // 256))
+    (g, Wg), (u, Wu) = weight(N, K, 142), weight(N, K, 143, 0.02)
+    linear_step(g, Wg, n, 144, "silu", what="linear")
+    gated_step(g, Wg, u, Wu, n, 148, "gelu", what="gated")
+    wt, dY, z = g.transpose(), randn((n, N), 152), randn((n, nv.preact_columns(g)), 153, F32)
+    first = nv.linear_backward(wt, dY, "gelu", z, F32)
+    for _ in range(3):
+        for a, b in zip(first, nv.linear_backward(wt, dY, "gelu", z, F32)):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("n,N,K", [(1, 93, 144), (16, 200, 656), (33, 93, 144), (150, 330, 272), (33, 5140, 4112)])
+def test_fp32_gradients(n, N, K):
+    """dY and dH in fp32, rows unaligned, without an activation and with one."""
+    say("fp32 dY", n, N, K)
+    (w, W), (u, U) = device_weight(N, K, 154), device_weight(N, K, 155)
+    W, U = f64(W), f64(U)
+    X = randn((n, K), 156)
+    buf = randn((n, N + 3), 157, F32, 0.1)
+    dY = buf[:, 1:N + 1]
+    z = torch.empty(n, nv.preact_columns(w), device="cuda")
+    for act in ("none", "gelu"):
+        nv.linear(w, X, activation=act, preact=z)
+        dX, db = nv.linear_backward(w.transpose(), dY, act, z, BF16)
+        want_x, want_b = R.linear_grads(f64(X), W, f64(dY), None, act, False)
+        check(dX, want_x, "dX " + act)
+        check(db, want_b, "db " + act)
+    gw = nv.GatedWeight.from_packed(w, u)
+    z = torch.empty(n, nv.preact_columns(gw), device="cuda")
+    nv.gated(gw, X, preact=z)
+    for a, want in zip(nv.gated_backward(gw, gw.transpose(), dY, z, "silu", F32),
+                       R.gated_grads(f64(X), W, U, f64(dY), None, None, "silu", True)):
+        check(a, want, "gated")
+
+
+@pytest.mark.parametrize("tile,parts,shape", TILES)
+def test_every_tile_with_an_epilogue(tile, parts, shape):
+    """Bias, activation, residual and pre-activations in each tile, in one part
+    and in several; the bounds of fused_reference.linear and gated."""
+    n, rows, K = shape
+    say("tile epilogue", tile, parts, shape)
+    F = rows // 32 * 16 - 3
+    for geo in (nv.fused_geometry(n, rows, K), nv.fused_geometry(n, nv.gated_rows(F), K)):
+        assert geo[:3] == tile and min(geo[3], 2) == parts, geo
+    X = randn((n, K), 158)
+    x = X.double()
+
+    def pre(W, b):
+        p = x @ W.t() + b.double()
+        return p, (K + 32) * R.HALF_F32 * (x.abs() @ W.abs().t() + b.double().abs())
+
+    def silu(p, e):
+        a = p * torch.sigmoid(p)
+        return a, R.LIP * e + R.ACT_EPS * (1 + a.abs())
+
+    w, W = device_weight(rows, K, 159)
+    b, r = randn((rows,), 160), randn((n, rows), 161, F32, 2.0)
+    z = torch.full((n, nv.preact_columns(w)), float("nan"), device="cuda")
+    Y = nv.linear(w, X, bias=b, activation="silu", residual=r, preact=z)
+    p, e = pre(W, b)
+    device_check(z[:, :rows], p, e + R.HALF_F32 * (p.abs() + e), "preact")
+    y, e = silu(p, e)
+    y = y + r.double()
+    e = e + R.HALF_F32 * y.abs()
+    device_check(Y, y, e + R.HALF_BF16 * (y.abs() + e) + 2.0 ** -133, "linear")
+    del W, y, p, e
+    (g, Wg), (u, Wu) = device_weight(F, K, 162), device_weight(F, K, 163)
+    gw = nv.GatedWeight.from_packed(g, u)
+    bg, bu = randn((F,), 164, F32), randn((F,), 165, F32)
+    z = torch.full((n, nv.preact_columns(gw)), float("nan"), device="cuda")
+    H = nv.gated(gw, X, gate_bias=bg, up_bias=bu, preact=z)
+    at = torch.arange(F, device="cuda")
+    at = at // 16 * 32 + at % 16
+    (pg, eg), (pu, eu) = pre(Wg, bg), pre(Wu, bu)
+    device_check(z[:, at], pg, eg + R.HALF_F32 * (pg.abs() + eg), "gate preact")
+    device_check(z[:, at + 16], pu, eu + R.HALF_F32 * (pu.abs() + eu), "up preact")
+    a, ea = silu(pg, eg)
+    h = a * pu
+    e = a.abs() * eu + pu.abs() * ea + ea * eu + R.HALF_F32 * h.abs()
+    device_check(H, h, e + R.HALF_BF16 * (h.abs() + e) + 2.0 ** -133, "gated")
+
+
+def test_graphs_of_steps_in_parts():
+    """Captured training steps whose products run in K parts, each with workspaces
+    of its graph, replayed in turn between eager calls."""
+    say("graphs, parts")
+    N, K = 83, 8208
+    (g, _), (u, _) = weight(N, K, 166), weight(N, K, 167, 0.02)
+    gw = nv.GatedWeight.from_packed(g, u)
+    wt, gt = g.transpose(), gw.transpose()
+    assert nv.fused_geometry(70, N, K)[3] > 1 and nv.fused_geometry(70, nv.gated_rows(N), K)[3] > 1
+
+    def step(X, dY, b):
+        z = torch.empty(X.shape[0], nv.preact_columns(g), device="cuda")
+        zg = torch.empty(X.shape[0], nv.preact_columns(gw), device="cuda")
+        Y = nv.linear(g, X, bias=b, activation="silu", preact=z)
+        H = nv.gated(gw, X, gate_bias=b, preact=zg)
+        return (Y, H) + nv.linear_backward(wt, dY, "silu", z, F32) + nv.gated_backward(gw, gt, dY, zg, "silu", F32)
+
+    graphs = []
+    for n in (5, 70):
+        args = randn((n, K), 168), randn((n, N), 169), randn((N,), 170, F32)
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            step(*args)
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step(*args)
+        graphs.append((args, graph, out))
+    for trip in range(4):
+        for args, graph, out in graphs:
+            args[0].copy_(randn(args[0].shape, 171 + trip))
+            args[1].copy_(randn(args[1].shape, 175 + trip))
+            graph.replay()
+            torch.cuda.synchronize()
+            for o, e in zip(out, step(*args)):
+                assert torch.equal(o, e), trip
