@@ -308,8 +308,10 @@ int nvfp4_gemm_geometry(int n, int N, int K, int *rows_per_workgroup,
  *     names, 0 for most sizes), added in part order by a second launch.  Calls
  *     that share a workspace must be ordered (one stream); graphs captured with
  *     one must not run at the same time;
- *   - the order of every sum depends on the sizes (n, N, K) alone, and for n <=
- *     16 on (N, K) alone: results do not vary from run to run. */
+ *   - the order of every sum depends on the sizes (n, N, K) alone, so results do
+ *     not vary from run to run; nvfp4_linear and nvfp4_gated take one order for
+ *     all n <= 16 of an (N, K), so a token's result does not depend on the batch
+ *     there (the gradients' products have no such form). */
 
 /* Activations: z; max(z, 0); z / (1 + exp(-z)); z Phi(z) (erf form);
  * 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))). */

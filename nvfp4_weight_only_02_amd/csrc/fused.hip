@@ -135,10 +135,15 @@ __device__ __forceinline__ void store_db(const GradParams &p, int half, int col,
 
 // dZ = dY act'(Z) (linear), or of a gate and up row (dH U act'(G), dH act(G))
 // times its tensor scale (gated, so that one product with the gated weight
-// serves both), each rounded to bf16 for that product; and the column sums of
-// the unrounded, unscaled values.  Memory bound: dY and Z in, dZ out, 6 bytes
-// (gated 10) an output.  A block sums 8 * rows_per_block / 8 rows in a fixed
-// order, blocks are added in order: no atomics.
+// serves both), each rounded to bf16; and the column sums of the unrounded,
+// unscaled values.  The rounding makes dZ an operand of the bf16 matrix
+// instructions: dX is then off by 2.3e-3 of its norm, of which its own rounding
+// to bf16 is 1.7e-3 (linear 16384 x 5120, n = 1536; gated 2 x 17408 x 5120, n =
+// 1024).  A second operand for the remainder would double the matrix
+// instructions of that product, seven eighths of the backward pass.  Memory
+// bound: dY (bf16) and Z (fp32) in, dZ out, 8 bytes an output (gated 14).  A
+// block takes rows_per_block rows, eight at a time, sums them in a fixed order,
+// and blocks are added in order: no atomics.
 template <bool GATED>
 __global__ __launch_bounds__(256) void nvfp4_grad_kernel(GradParams p)
 {
