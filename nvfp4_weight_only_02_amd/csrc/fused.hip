@@ -168,13 +168,20 @@ __global__ __launch_bounds__(256) void nvfp4_grad_kernel(GradParams p)
                     dy[e] = c0 + e < p.N ? load_any(p.dy, at + e, p.dy_f32) : 0.f;
             }
             float z[2][8] = {};
+            // (a gated row has all the columns up to a multiple of 16)
             auto fetch = [&](int half, long long col) {
-                const f32x4 *src = reinterpret_cast<const f32x4 *>(p.z + t * p.ldz + col);
-                const f32x4 a = src[0], b = src[1];
+                const float *row = p.z + t * p.ldz + col;
+                if (GATED || c0 + 8 <= p.N) {
+                    const f32x4 a = reinterpret_cast<const f32x4 *>(row)[0], b = reinterpret_cast<const f32x4 *>(row)[1];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    z[half][e] = a[e];
-                    z[half][4 + e] = b[e];
+                    for (int e = 0; e < 4; ++e) {
+                        z[half][e] = a[e];
+                        z[half][4 + e] = b[e];
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        z[half][e] = c0 + e < p.N ? row[e] : 0.f;
                 }
             };
             if (p.z)

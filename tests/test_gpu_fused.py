@@ -8,7 +8,7 @@ import torch
 import fused_reference as R
 import nvfp4_weight_only_02_amd as nv
 import oracle as O
-from nvfp4_weight_only_02_amd import inputs
+from nvfp4_weight_only_02_amd import fused, inputs
 
 pytestmark = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
@@ -1026,3 +1026,30 @@ def test_graphs_of_steps_in_parts():
             torch.cuda.synchronize()
             for o, e in zip(out, step(*args)):
                 assert torch.equal(o, e), trip
+
+
+@pytest.mark.parametrize("n,N,ldp,col", [(3, 92, 192, 100), (20, 93, 192, 96), (9, 1, 8, 4), (300, 332, 440, 108)])
+def test_preactivations_in_the_last_columns_of_a_buffer(n, N, ldp, col):
+    """Through the C entry points: nothing behind column N of the last row is
+    theirs to read."""
+    say("last columns", n, N, ldp, col)
+    K = 144
+    w, W = weight(N, K, 180)
+    wt = w.transpose()
+    X, dY = randn((n, K), 181), randn((n, N), 182)
+    whole = torch.full((n * ldp,), float("nan"), device="cuda")
+    whole = whole[:(n - 1) * ldp + col + N]
+    stream = torch.cuda.current_stream().cuda_stream
+    Y, dX, db = (torch.empty(s, device="cuda", dtype=t) for s, t in (((n, N), BF16), ((n, K), BF16), ((N,), F32)))
+    ep = fused._EPILOGUE.pack(0, 0, 0, whole.data_ptr() + 4 * col, 0, ldp, 2, 1, 1, 1)
+    ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    fused._run("nvfp4_linear", w.codes.data_ptr(), w.scales.data_ptr(), w.gscale, X.data_ptr(), K, Y.data_ptr(), N, n,
+               N, K, ep, ws.data_ptr(), ws.numel(), stream)
+    fused._run("nvfp4_linear_backward", wt.codes.data_ptr(), wt.scales.data_ptr(), wt.gscale, dY.data_ptr(), 1, N,
+               whole.data_ptr() + 4 * col, ldp, 2, dX.data_ptr(), K, db.data_ptr(), 0, n, N, K, ws.data_ptr(),
+               ws.numel(), stream)
+    check(Y, R.linear(f64(X), W, None, "silu"), "Y")
+    want_x, want_b = R.linear_grads(f64(X), W, f64(dY), None, "silu", True)
+    check(dX, want_x, "dX")
+    check(db, want_b, "db")
+    assert torch.isnan(whole[:col]).all()
