@@ -419,6 +419,121 @@ int nvfp4_gated_backward(const uint8_t *codes_t, const uint8_t *scales_t, float 
                          void *stream);
 size_t nvfp4_gated_backward_workspace_bytes(int n, int F, int K, int dx, int dbias);
 
+/* ---- expert layer -----------------------------------------------------------
+ *
+ * A router from logits to each token's experts and their weights, and the whole
+ * layer of gated NVFP4 experts that reads them, with gradients (the experts are
+ * frozen: gradients go to the activations, the weights and the logits).
+ * Conventions as for the fused operators above. */
+
+#define NVFP4_SCORE_SOFTMAX 0
+#define NVFP4_SCORE_SIGMOID 1
+
+/* The k experts of each token with the largest scores, largest first, ties to
+ * the lowest index, and their weights:
+ *     p = softmax(logits) or sigmoid(logits);   chosen by p + bias (bias NULL: by p);
+ *     weights = scale p  or, with normalize, scale p / (sum of the chosen p).
+ * logits: [n][ldl] fp32 or bf16; bias: [E] fp32, of the choice alone; weights
+ * [n][k] fp32 and experts [n][k], contiguous.  E up to 1024, k up to 32 and E.
+ * A logit of -infinity masks an expert: it is never chosen, and slots for which
+ * no expert is left have expert -1 and weight 0.  A NaN logit counts as the
+ * largest (with a softmax and a bias every score of its row is NaN: the experts
+ * are then the first ones that are not masked) and makes the weights that
+ * depend on it NaN.  Scores that are compared with a bias are 64-bit.
+ * Errors: NULL, RANGE, ALIGN, OVERLAP, DEVICE, LAUNCH. */
+int nvfp4_moe_route(const void *logits, int dtype, int64_t ldl, const float *bias, int n, int E, int k,
+                    int scoring, int normalize, float scale, float *weights, int32_t *experts, void *stream);
+
+/* dlogits [n][ldd] (every element of a row's E; the logits' type) from dweights
+ * [n][k], with the experts that nvfp4_moe_route chose; the choice and its bias
+ * have no gradient.  Experts outside [0, E) are skipped. */
+int nvfp4_moe_route_backward(const void *logits, int dtype, int64_t ldl, const int32_t *experts,
+                             const float *dweights, int n, int E, int k, int scoring, int normalize, float scale,
+                             void *dlogits, int64_t ldd, void *stream);
+
+/* E experts of one shape, each part of the E experts in turn in one buffer
+ * (16-byte aligned): gated weights (nvfp4_pack_gated, F outputs, K columns) and
+ * packed down weights (K rows, F columns), or for nvfp4_moe_backward the
+ * transposed copies of both (nvfp4_pack_transposed).  F and K are multiples of
+ * 16 up to 262144, E up to 1024.  gscale: DEVICE fp32 [3][E], the tensor scales
+ * of the gate, up and down weights. */
+typedef struct nvfp4_experts {
+    const uint8_t *gate_up_codes, *gate_up_scales;
+    const uint8_t *down_codes, *down_scales;
+    const float *gscale;
+    int32_t E, F, K;
+} nvfp4_experts;
+
+/* Y[t] = sum over s < k of weights[t][s] FFN(experts[t][s], X[t]) + residual[t],
+ *     FFN(e, x) = (act(gate_e x Wg_e^T) * (up_e x Wu_e^T)) (down_e Wd_e)^T,
+ * for n = 0 .. NVFP4_MAX_GEMM_TOKENS tokens.  experts int32 and weights fp32
+ * [n][k], contiguous, k up to 32; an expert outside [0, E) is no expert (its
+ * weight is not read into the sum), so a row may be empty; the same expert twice
+ * counts twice.  X rows as nvfp4_linear's, ldx at most 2^18.  epilogue: activation,
+ * residual (it may be Y itself), out_dtype, and preact: fp32 [n k][ldp >= 2 F]
+ * receives the pre-activations for nvfp4_moe_backward, its rows in the order of
+ * the experts (rows of slots without an expert are left as they were); biases
+ * NULL.  h = act() * () is rounded to bf16, an operand of the matrix
+ * instructions; all sums are fp32.
+ * Up to 16 tokens (K up to 8192, no preact) take two launches, and a token's
+ * result does not depend on the others there; more are sorted by expert, 2^16
+ * pairs at a time.  Workspace: nvfp4_moe_workspace_bytes, 16-byte aligned, with
+ * preact 1 where it is given.
+ * Errors: NULL, RANGE, SHAPE, ALIGN, OVERLAP, WORKSPACE, DEVICE, LAUNCH. */
+int nvfp4_moe(const nvfp4_experts *w, const uint16_t *X, int64_t ldx, const int32_t *experts,
+              const float *weights, int n, int k, void *Y, int64_t ldy, const nvfp4_epilogue *epilogue,
+              void *workspace, size_t workspace_bytes, void *stream);
+size_t nvfp4_moe_workspace_bytes(int n, int k, int E, int F, int K, int preact);
+
+/* The gradients of nvfp4_moe, on the transposed copies: dX bf16 [n][ldx] (NULL:
+ * not wanted) and dweights fp32 [n][k] (NULL: not wanted; 0 where there is no
+ * expert).  dY fp32 or bf16 [n][ldy], ldy at most 2^18; it is rounded to bf16, and
+ * so are the gradients of the pre-activations, as operands of the products.
+ * preact as nvfp4_moe stored it.  The residual's gradient is dY itself.
+ * Workspace: nvfp4_moe_backward_workspace_bytes with dx as it is wanted, copy =
+ * 0 only if dY is bf16, 16-byte aligned and ldy a multiple of 8. */
+int nvfp4_moe_backward(const nvfp4_experts *wt, const void *dY, int dy_dtype, int64_t ldy,
+                       const int32_t *experts, const float *weights, const float *preact, int64_t ldp,
+                       int activation, int n, int k, uint16_t *dX, int64_t ldx, float *dweights, void *workspace,
+                       size_t workspace_bytes, void *stream);
+size_t nvfp4_moe_backward_workspace_bytes(int n, int k, int E, int F, int K, int dx, int copy);
+
+/* ---- 8-bit projection --------------------------------------------------------
+ *
+ * For layers that do not stand four bits: weight and activations in 8-bit
+ * integers, one fp32 scale for each weight row (channel) and each token.  Sums
+ * are exact 32-bit integers, so a result depends on its own row and token alone.
+ * Conventions as for the fused operators above.  K: a multiple of 16 up to
+ * 131056 (128 * 128 * K stays below 2^31). */
+
+/* The packed layout of codes [N][K]: 16-row x 64-column tiles in the lane order
+ * of the matrix instructions, rows padded to 16 and columns to 128 with zeros. */
+size_t nvfp4_int8_packed_bytes(int N, int K);
+int nvfp4_int8_pack(const int8_t *codes, int N, int K, int8_t *packed, void *stream);
+
+/* Rows of X (bf16 or fp32 [n][ldx]) to 8 bits: scale = amax / 127 and
+ * q = 127 x / amax rounded to the nearest integer, halves to the even one (for
+ * bf16 exactly; fp32 after one rounding of each operation), amax the row's largest
+ * magnitude.  A row of zeros has scale 0; a row that holds a NaN or an infinity
+ * scale NaN and q 0.  X and q rows are 16-byte aligned.  Errors: NULL, RANGE,
+ * SHAPE (K % 16), ALIGN, OVERLAP, DEVICE, LAUNCH. */
+int nvfp4_int8_quantize(const void *X, int dtype, int64_t ldx, int n, int K, int8_t *q, int64_t ldq,
+                        float *scale, void *stream);
+
+/* Y[t][r] = act(xscale[t] wscale[r] sum_k Xq[t][k] Wq[r][k] + bias[r]) + residual[t][r]
+ * for n = 0 .. NVFP4_MAX_GEMM_TOKENS.  Wq packed.  xscale [n] with X int8
+ * [n][ldx]; or xscale NULL with X bf16 [n][ldx], which is then quantised as by
+ * nvfp4_int8_quantize into the workspace.  X rows are 16-byte aligned, ldx at most
+ * 2^22.  epilogue: bias, activation, residual (it may be Y itself), out_dtype;
+ * up_bias and preact NULL (a quantised product has no derivative).  Workspace:
+ * nvfp4_int8_linear_workspace_bytes (0 for some calls with xscale), quantize = 1
+ * where xscale is NULL; 16-byte aligned.
+ * Errors: NULL, RANGE, SHAPE, ALIGN, OVERLAP, WORKSPACE, DEVICE, LAUNCH. */
+int nvfp4_int8_linear(const int8_t *Wq, const float *wscale, const void *X, int64_t ldx, const float *xscale,
+                      void *Y, int64_t ldy, int n, int N, int K, const nvfp4_epilogue *epilogue,
+                      void *workspace, size_t workspace_bytes, void *stream);
+size_t nvfp4_int8_linear_workspace_bytes(int n, int N, int K, int quantize);
+
 /* Human-readable name of a status code (static storage). */
 const char *nvfp4_strerror(int status);
 

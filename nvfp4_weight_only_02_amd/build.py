@@ -24,7 +24,8 @@ PROBES_LIB = os.path.join(PKG, "libnvfp4_probes.so")
 # (library, its sources)
 TARGETS = [(LIB, [os.path.join(PKG, "csrc", f) for f in
                   ("nvfp4.hip", "fused.hip", "fused_gemm.hip", "fused_gemv_linear.hip",
-                   "fused_gemv_gated.hip", "fused_gemv_partial.hip")]),
+                   "fused_gemv_gated.hip", "fused_gemv_partial.hip", "moe.hip", "moe_few.hip",
+                   "moe_gemm.hip", "int8.hip", "int8_gemm.hip")]),
            (PROBES_LIB, [os.path.join(PKG, "csrc", "probes.hip")])]
 ARCH = "gfx950"
 

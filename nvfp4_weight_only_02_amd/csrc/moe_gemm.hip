@@ -1,0 +1,70 @@
+// Products of rows grouped by expert with the experts' NVFP4 weights: the
+// many-token form of the expert layer and its gradients.
+#include "fused_gemm_kernel.h"
+#include "moe.h"
+
+namespace {
+
+template <int RG, int TB, int RW, int KG>
+int launch_grouped(GroupedGemmParams p, const nvfp4_moe_gemm_args &a, hipStream_t stream)
+{
+    p.tiles_x = (p.RG + RW * RG - 1) / (RW * RG);
+    p.tiles_y = (int)nvfp4_moe_max_tiles(a.rows, a.E);
+    const long long total = (long long)p.tiles_x * p.tiles_y;
+    if (total > INT32_MAX || (long long)p.T * RG * 1024 > INT32_MAX)
+        return NVFP4_ERR_SHAPE;   // a wave's codes must stay within a 32-bit buffer offset
+    // (the XCDs' shares differ by one workgroup at most: 8 more cover every share)
+    const dim3 grid((unsigned)((total + 7) / 8 * 8)), block(64 * RW * KG);
+    if (a.mode == 1)
+        hipLaunchKernelGGL((nvfp4_fused_gemm_kernel<RG, TB, RW, KG, 1, 1>), grid, block, 0, stream, p);
+    else if (a.mode == 0)
+        hipLaunchKernelGGL((nvfp4_fused_gemm_kernel<RG, TB, RW, KG, 0, 2>), grid, block, 0, stream, p);
+    else if (a.gather)
+        hipLaunchKernelGGL((nvfp4_fused_gemm_kernel<RG, TB, RW, KG, 2, 1>), grid, block, 0, stream, p);
+    else
+        hipLaunchKernelGGL((nvfp4_fused_gemm_kernel<RG, TB, RW, KG, 2, 2>), grid, block, 0, stream, p);
+    return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
+}
+
+}  // namespace
+
+int nvfp4_moe_tile_tokens(int rows, int E)
+{
+    const int each = (rows + E - 1) / E;   // rows of an expert where all are chosen alike
+    return each <= 32 ? 32 : (each <= 64 ? 64 : 128);
+}
+
+long long nvfp4_moe_max_tiles(int rows, int E)
+{
+    return rows / nvfp4_moe_tile_tokens(rows, E) + (rows < E ? rows : E);
+}
+
+int nvfp4_launch_moe_gemm(const nvfp4_moe_gemm_args &a, hipStream_t stream)
+{
+    GroupedGemmParams p = {};
+    p.codes = reinterpret_cast<const u32x4 *>(a.codes);
+    p.scales = reinterpret_cast<const char *>(a.scales);
+    p.X = a.X;
+    p.ldx = a.ldx;
+    p.n = a.rows;
+    p.K = a.K;
+    p.T = (int)k_tiles(a.K);
+    p.RG = a.row_groups;
+    p.ks = 1;
+    p.tp = p.T;
+    p.e = a.epi;
+    p.tile = a.order.tile;
+    p.offset = a.order.offset;
+    p.pair = a.order.pair;
+    p.k = a.k;
+    p.xrows = a.xrows;
+    p.gscale = a.gscale;
+    p.up_gscale = a.up_gscale;
+    p.cstride = a.cstride;
+    p.sstride = a.sstride;
+    switch (nvfp4_moe_tile_tokens(a.rows, a.E)) {
+    case 32: return launch_grouped<2, 2, 2, 4>(p, a, stream);
+    case 64: return launch_grouped<2, 4, 4, 2>(p, a, stream);
+    default: return launch_grouped<4, 8, 4, 1>(p, a, stream);
+    }
+}
