@@ -61,7 +61,7 @@ def check_resources(remarks: str) -> None:
         if m:
             kernel = m.group(1)
             continue
-        if kernel is None or ("gemv_kernel" not in kernel and "gemm_kernel" not in kernel):
+        if kernel is None or not re.search(r"(gemv|gemm|moe_down)_kernel", kernel):
             continue
         m = re.search(r"(ScratchSize \[bytes/lane\]|VGPRs Spill|SGPRs Spill): (\d+)", line)
         if m and int(m.group(2)) != 0:

@@ -171,6 +171,32 @@ __device__ __forceinline__ u32x4 dequant_pair(u32 w, u32 sw)
                  __builtin_bit_cast(u32, o3)};
 }
 
+// LDS-direct load: lane l's 16 bytes go to `lds` + 16 l (a wave-uniform LDS
+// address); offsets past the resource write zeros (the scalar offset stays 0:
+// the range check need not include it).  No register is written, so only the
+// vmcnt wait before the barrier orders it.  M0 is reserved, the compiler keeps
+// nothing in it; one wait state separates its write from the load.
+__device__ __forceinline__ void load_lds_b128(u32x4 rsrc, unsigned off, unsigned lds)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+                 :: "v"(off), "s"(rsrc), "s"(lds) : "memory");
+}
+
+// Byte address of LDS memory, as the M0 of an LDS-direct load takes it.
+__device__ __forceinline__ unsigned lds_address(const void *p)
+{
+    return (unsigned)(uintptr_t)(__attribute__((address_space(3))) const char *)p;
+}
+
+// Raw buffer over [base, base + bytes), for loads whose waits the compiler counts.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void *base, unsigned bytes)
+{
+    const unsigned long long a = (unsigned long long)base;
+    const unsigned lo = __builtin_amdgcn_readfirstlane((int)(u32)a), hi = __builtin_amdgcn_readfirstlane((int)(u32)(a >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc((void *)((unsigned long long)hi << 32 | lo), 0,
+                                             __builtin_amdgcn_readfirstlane((int)bytes), kBufferWord3);
+}
+
 }  // namespace
 
 #endif  // NVFP4_DEVICE_H

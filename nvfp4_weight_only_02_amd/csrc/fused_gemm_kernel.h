@@ -58,23 +58,6 @@ __device__ __forceinline__ f32x2 scales2(u32 w)
     return f32x2{s[0], s[1]};
 }
 
-// LDS-direct load: lane l's 16 bytes go to `lds` + 16 l (a wave-uniform LDS
-// address); offsets past the resource write zeros (the scalar offset stays 0:
-// the range check need not include it).  No register is written, so only the
-// vmcnt wait before the barrier orders it.  M0 is reserved, the compiler keeps
-// nothing in it; one wait state separates its write from the load.
-__device__ __forceinline__ void load_lds_b128(u32x4 rsrc, unsigned off, unsigned lds)
-{
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-                 :: "v"(off), "s"(rsrc), "s"(lds) : "memory");
-}
-
-// Byte address of LDS memory, as the M0 of an LDS-direct load takes it.
-__device__ __forceinline__ unsigned lds_address(const void *p)
-{
-    return (unsigned)(uintptr_t)(__attribute__((address_space(3))) const char *)p;
-}
-
 // One workgroup: RW waves x RG row groups (16 * RW * RG weight rows) times 16 *
 // TB tokens, over the steps of one K part, which KG groups of RW waves take in
 // turn and whose sums they add through LDS in the end, in group order.  A step

@@ -168,20 +168,20 @@ __global__ __launch_bounds__(kWaves * 64) void nvfp4_int8_gemv_kernel(Int8GemvPa
     u32x4 c[U][R], x[U];
     auto load = [&](int tile, int u) {
         const int col = tile * 64 + 16 * g;
+        const int behind = tile < p.T2 ? 0 : 1 << 30;   // past the resource: no memory is touched
         x[u] = __builtin_amdgcn_raw_buffer_load_b128(xr, i < p.n && col < p.K ? (int)(i * p.ldx + col) : (int)kOutOfRange, 0, 0);
 #pragma unroll
         for (int r = 0; r < R; ++r)
-            c[u][r] = __builtin_amdgcn_raw_buffer_load_b128(cr, (r * p.T2 + tile) * 1024 + lane * 16, 0, 2);
+            c[u][r] = __builtin_amdgcn_raw_buffer_load_b128(cr, (r * p.T2 + tile) * 1024 + lane * 16 + behind, 0, 2);
     };
     i32x4 acc[R];
 #pragma unroll
     for (int r = 0; r < R; ++r)
         acc[r] = i32x4{0, 0, 0, 0};
-    int tile = wave * U;
+    int tile = wave;
 #pragma unroll
     for (int u = 0; u < U; ++u)
-        load(tile + u, u);
-    // (a tile behind the last one multiplies tokens' zeros)
+        load(tile + u * W, u);
     for (; tile < p.T2; tile += W * U) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -189,7 +189,7 @@ __global__ __launch_bounds__(kWaves * 64) void nvfp4_int8_gemv_kernel(Int8GemvPa
             for (int r = 0; r < R; ++r)
                 acc[r] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, x[u]), __builtin_bit_cast(i32x4, c[u][r]),
                                                                acc[r], 0, 0, 0);
-            load(tile + W * U + u, u);
+            load(tile + W * (U + u), u);
             __builtin_amdgcn_sched_barrier(0);
         }
     }

@@ -21,28 +21,6 @@ struct Int8GemmParams {
 
 constexpr int kStep = 128;              // columns of a step, bytes of a token's slice
 
-// LDS-direct load: lane l's 16 bytes go to `lds` + 16 l (a wave-uniform LDS
-// address); offsets past the resource write zeros.  M0 is reserved, the compiler
-// keeps nothing in it; one wait state separates its write from the load.
-__device__ __forceinline__ void load_lds_b128(u32x4 rsrc, unsigned off, unsigned lds)
-{
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-                 :: "v"(off), "s"(rsrc), "s"(lds) : "memory");
-}
-
-__device__ __forceinline__ unsigned lds_address(const void *p)
-{
-    return (unsigned)(uintptr_t)(__attribute__((address_space(3))) const char *)p;
-}
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void *base, unsigned bytes)
-{
-    const unsigned long long a = (unsigned long long)base;
-    const u32 lo = __builtin_amdgcn_readfirstlane((int)(u32)a), hi = __builtin_amdgcn_readfirstlane((int)(u32)(a >> 32));
-    return __builtin_amdgcn_make_buffer_rsrc((void *)((unsigned long long)hi << 32 | lo), 0,
-                                             __builtin_amdgcn_readfirstlane((int)bytes), kBufferWord3);
-}
-
 // One workgroup: RW x TW waves of RG row groups x TB 16-token blocks, times KG
 // groups that take the 128-column steps of a K part in turn and add their sums
 // through LDS in the end (integers: exact in any order).  Tokens' slices go

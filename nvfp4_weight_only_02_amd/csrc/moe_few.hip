@@ -31,57 +31,56 @@ struct MoeFewParams {
     uint16_t *h;                  // [n k][128 Td], columns of a tile in the lanes' order
     int ldx, n, k, E, F, K, act;
     int T, Td, P;                 // 128-column tiles of K and of F, pairs of row groups of a gated weight
-    int ws, tpw;                  // waves that share an expert's down projection, and the tiles of each
+    int ws, tpw;                  // parts of an expert's F in the down projection, and the tiles of each
     nvfp4_epi_params e;
 };
 
 // The choices of the batch in LDS.
 struct Routes {
     int expert[kMaxPairs];                   // of each pair, -1 if none
-    unsigned short first[kMaxPairs];         // the token's first pair with the same expert
     unsigned short list[kMaxPairs];          // the distinct experts, ascending
-    unsigned tokens[kMaxPairs];              // of each of them: its tokens, a bit each
-    unsigned short pair[kMaxPairs][kFewTokens];   // and the pair of its j-th token
     u32 bits[kMaxExperts / 32];
     int count;
 };
 
-// All threads of the workgroup; a barrier ends it.
-__device__ __forceinline__ void build_routes(Routes &r, const MoeFewParams &p, bool pairs)
+// The expert of thread tid's pair, -1 if none.
+__device__ __forceinline__ int load_choice(const MoeFewParams &p)
+{
+    int e = -1;
+    if (threadIdx.x < (unsigned)(p.n * p.k))
+        e = p.experts[threadIdx.x];
+    return e;
+}
+
+// All threads of the workgroup, e from load_choice; a barrier ends it.  Returns
+// the place of this thread's expert in the list if it is the first pair of its
+// token with that expert, else -1; *first is that pair.
+__device__ __forceinline__ int build_routes(Routes &r, const MoeFewParams &p, int e, int *first)
 {
     const int tid = threadIdx.x, nk = p.n * p.k, words = (p.E + 31) / 32;
-    int e = -1;
-    if (tid < nk) {
-        e = p.experts[tid];
-        if (e < 0 || e >= p.E)
-            e = -1;
+    if (e < 0 || e >= p.E)
+        e = -1;
+    if (tid < nk)
         r.expert[tid] = e;
-        r.tokens[tid] = 0;
-    }
     if (tid < words)
         r.bits[tid] = 0;
     __syncthreads();
-    const int t = tid / p.k;
-    bool first = e >= 0;
-    if (first) {
-        int f = tid;
-        for (int q = tid - 1; q >= t * p.k; --q)
+    int f = tid;
+    if (e >= 0) {
+        for (int q = tid - 1; q >= tid / p.k * p.k; --q)
             if (r.expert[q] == e)
                 f = q;
-        first = f == tid;
-        r.first[tid] = (unsigned short)f;
-        if (first)
+        if (f == tid)
             atomicOr(&r.bits[e >> 5], 1u << (e & 31));
     }
+    *first = f;
     __syncthreads();
-    int a = 0;
-    if (first) {
+    int a = -1;
+    if (e >= 0 && f == tid) {
+        a = __popc(r.bits[e >> 5] & ((1u << (e & 31)) - 1));
         for (int w = 0; w < e >> 5; ++w)
             a += __popc(r.bits[w]);
-        a += __popc(r.bits[e >> 5] & ((1u << (e & 31)) - 1));
         r.list[a] = (unsigned short)e;
-        if (pairs)
-            atomicOr(&r.tokens[a], 1u << t);
     }
     if (tid == kThreads - 1) {
         int c = 0;
@@ -90,23 +89,9 @@ __device__ __forceinline__ void build_routes(Routes &r, const MoeFewParams &p, b
         r.count = c;
     }
     __syncthreads();
-    if (pairs) {
-        if (first)
-            r.pair[a][__popc(r.tokens[a] & ((1u << t) - 1))] = (unsigned short)tid;
-        __syncthreads();
-    }
+    return a;
 }
 
-// Raw buffer over [base, base + bytes), for loads whose waits the compiler counts.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void *base, unsigned bytes)
-{
-    const unsigned long long a = (unsigned long long)base;
-    const unsigned lo = __builtin_amdgcn_readfirstlane((int)(u32)a), hi = __builtin_amdgcn_readfirstlane((int)(u32)(a >> 32));
-    return __builtin_amdgcn_make_buffer_rsrc((void *)((unsigned long long)hi << 32 | lo), 0,
-                                             __builtin_amdgcn_readfirstlane((int)bytes), kBufferWord3);
-}
-
-constexpr unsigned kBehind = 0x40000000u;   // added to an offset: behind any h
 constexpr int kNt = 2;   // read once: streamed past the caches
 
 __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, unsigned off, int more = 0)
@@ -181,34 +166,9 @@ __global__ __launch_bounds__(kThreads) void nvfp4_moe_up_kernel(MoeFewParams p)
     __shared__ Routes routes;
     __shared__ f32x4 part[kSlots][W][64];
 
-    // Lane (i, g) loads 16-byte chunks (block 2j + g % 2, half g / 2) of its
-    // token's tile; a swap between lane groups then leaves columns 4g .. 4g + 3
-    // of both blocks.
-    const int tok = 4 * (i & 3) + (i >> 2);
-    u32x2 x[MT][kBlocksPerTile];
-    {
-        const auto xr = resource(p.X, (unsigned)(((p.n - 1) * p.ldx + p.K) * 2));
-        u32x4 raw[MT][4];
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int col = (wave + W * t) * kTileK + 32 * j + 16 * (g & 1) + 8 * (g >> 1);
-                raw[t][j] = load16(xr, tok < p.n && col < p.K ? (unsigned)(tok * p.ldx + col) * 2u : kOutOfRange);
-            }
-        build_routes(routes, p, false);
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const u32x4 r = raw[t][j];
-                const auto a = __builtin_amdgcn_permlane16_swap(r[0], r[2], false, false);
-                const auto b = __builtin_amdgcn_permlane16_swap(r[1], r[3], false, false);
-                x[t][2 * j] = u32x2{a[0], b[0]};
-                x[t][2 * j + 1] = u32x2{a[1], b[1]};
-            }
-    }
-
+    const int choice = load_choice(p);
+    int first;
+    build_routes(routes, p, choice, &first);
     const int units = __builtin_amdgcn_readfirstlane(routes.count) * p.P;
     const int per = units / (int)gridDim.x, rem = units % (int)gridDim.x, wg = blockIdx.x;
     const int u0 = wg * per + min(wg, rem), u1 = u0 + per + (wg < rem ? 1 : 0);
@@ -228,6 +188,20 @@ __global__ __launch_bounds__(kThreads) void nvfp4_moe_up_kernel(MoeFewParams p)
         return resource(p.gu_scales + rg * sb, in ? sb : 0u);
     };
     const unsigned coff = (unsigned)(wave * 1024 + lane * 16), soff = (unsigned)(wave * 128 + i * 8);
+    // Lane (i, g) loads 16-byte chunks (block 2j + g % 2, half g / 2) of its
+    // token's tile; a swap between lane groups then leaves columns 4g .. 4g + 3
+    // of both blocks.
+    const int tok = 4 * (i & 3) + (i >> 2);
+    u32x4 raw[MT][4];
+    const auto xr = resource(p.X, (unsigned)(((p.n - 1) * p.ldx + p.K) * 2));
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int col = (wave + W * t) * kTileK + 32 * j + 16 * (g & 1) + 8 * (g >> 1);
+            raw[t][j] = load16(xr, tok < p.n && col < p.K ? (unsigned)(tok * p.ldx + col) * 2u : kOutOfRange);
+        }
+    __builtin_amdgcn_sched_barrier(0);
     {
         const auto cr = codes_of(u0, 0, true), sr = scales_of(u0, 0, true);
 #pragma unroll
@@ -236,6 +210,18 @@ __global__ __launch_bounds__(kThreads) void nvfp4_moe_up_kernel(MoeFewParams p)
             c[t] = load16_nt(cr, coff + t * (W * 1024));
         }
     }
+    __builtin_amdgcn_sched_barrier(0);
+    u32x2 x[MT][kBlocksPerTile];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const u32x4 r = raw[t][j];
+            const auto a = __builtin_amdgcn_permlane16_swap(r[0], r[2], false, false);
+            const auto b = __builtin_amdgcn_permlane16_swap(r[1], r[3], false, false);
+            x[t][2 * j] = u32x2{a[0], b[0]};
+            x[t][2 * j + 1] = u32x2{a[1], b[1]};
+        }
     for (int b0 = u0; b0 < u1; b0 += kSlots / 2) {
         const int b1 = min(b0 + kSlots / 2, u1);
         for (int q = 2 * b0; q < 2 * b1; ++q) {
@@ -285,105 +271,158 @@ __global__ __launch_bounds__(kThreads) void nvfp4_moe_up_kernel(MoeFewParams p)
     }
 }
 
-// Down: a workgroup has 16 outputs of every token, its waves an expert each in
-// turn (ws of them share one expert's F where a token has fewer experts than
-// that takes); the rows of an expert's own tokens are its operand.  The sums of
-// all pairs meet in LDS, and a thread adds those of its token, weighted, in slot
-// order.
-template <int TP>
-__global__ __launch_bounds__(kThreads) void nvfp4_moe_down_kernel(MoeFewParams p)
+// A piece of the down projection of 16 outputs: up to four tokens of an expert,
+// over a part of F.
+struct Unit {
+    unsigned short expert, part;
+    unsigned short tile, end;
+    unsigned short pair[4];       // 0xFFFF: none
+};
+constexpr int kNoPair = 0xFFFF;
+
+// Down: a workgroup has 16 outputs of every token.  Its waves take units from a
+// queue: an expert with up to four of its tokens (an expert with more has several
+// units, whose weights come from cache after the first; four tokens cost the
+// matrix instruction one component and 1 KiB of LDS a tile), or a part of its F
+// where a token has few experts.  A unit's tiles of weights go to registers and
+// its tokens' rows straight to LDS, D tiles ahead: three loads a tile, always in
+// the same order, so that the wait for a tile is the constant count of the newer
+// ones, across the units' ends too.  The sums of all pairs meet in LDS, and a
+// thread adds those of its token, weighted, in slot order.
+template <int D>
+__global__ __launch_bounds__(kThreads, 4) void nvfp4_moe_down_kernel(MoeFewParams p)
 {
     constexpr int W = kWaves;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int i = lane & 15, g = lane >> 4;
     const int rg = blockIdx.x, nk = p.n * p.k;
     __shared__ Routes routes;
-    __shared__ float mix[kMaxPairs];
-    extern __shared__ float sums[];   // [n k][ws][16]
-    build_routes(routes, p, true);
-    if (tid < nk) {
-        const int e = routes.expert[tid];
-        mix[tid] = e < 0 ? 0.f : p.weights[tid] * p.gscale[2 * p.E + e];
-    }
-    const int units = __builtin_amdgcn_readfirstlane(routes.count) * p.ws;
-    const long long groups = p.K / kRowsPerGroup;
-    const unsigned tb = p.Td * 1024u, sb = p.Td * 128u;
-    const auto hr = resource(p.h, (unsigned)(nk * p.Td * kTileK * 2));
-
-    // This wave's units, an expert or its part each, in steps of TP tiles; the
-    // operands of a step are loaded while the one before is computed.
-    u32x4 c[TP], h[TP][4];
-    u32x2 s[TP];
-    int unit = wave, tile = 0, end = 0, cnt = 0;   // of the step that is loaded next
-    unsigned row = kOutOfRange;                    // this lane's operand row in h, bytes
-    auto open = [&](int u) {
-        unit = u;
-        if (u >= units)
-            return;
-        const int a = u / p.ws;
-        tile = u % p.ws * p.tpw;
-        end = min(p.Td, tile + p.tpw);
-        cnt = __builtin_amdgcn_readfirstlane(__popc(routes.tokens[a]));
-        const int j = 4 * (i & 3) + (i >> 2);
-        row = j < cnt ? (unsigned)(routes.pair[a][j] * p.Td * kTileK + 32 * g) * 2u : kOutOfRange;
-    };
-    // A unit's tiles end where its resources do: what lies behind reads zeros.
-    auto codes_of = [&](int u) {
-        const long long at = u < units ? (long long)routes.list[u / p.ws] * groups + rg : 0;
-        return resource(p.d_codes + at * tb, u < units ? end * 1024u : 0u);
-    };
-    auto scales_of = [&](int u) {
-        const long long at = u < units ? (long long)routes.list[u / p.ws] * groups + rg : 0;
-        return resource(p.d_scales + at * sb, u < units ? end * 128u : 0u);
-    };
-    auto load = [&](__amdgpu_buffer_rsrc_t cr, __amdgpu_buffer_rsrc_t sr, auto tc) {
-        constexpr int t = decltype(tc)::value;
-        s[t] = load8_nt(sr, (unsigned)((tile + t) * 128 + i * 8));
-        c[t] = load16_nt(cr, (unsigned)((tile + t) * 1024 + lane * 16));
-        const unsigned at = row + (tile + t) * (kTileK * 2) + (tile + t < end ? 0u : kBehind);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            h[t][q] = load16(hr, at, 16 * q);
-    };
-    open(wave);
-    if (unit < units) {
-        {
-            const auto cr = codes_of(unit), sr = scales_of(unit);
-            static_for<TP>([&](auto tc) { load(cr, sr, tc); });
+    __shared__ unsigned tokens[kMaxPairs];        // of each expert of the list: its tokens, a bit each
+    __shared__ unsigned short firsts[kMaxPairs];  // of each pair: the token's first pair with its expert
+    __shared__ float mix[kMaxPairs];              // of each pair: its weight times the tensor scale
+    __shared__ int queue, count;                  // next unit, units
+    extern __shared__ __align__(1024) char dynamic[];
+    char *rows = dynamic;                                                      // [W][D] KiB
+    Unit *table = reinterpret_cast<Unit *>(dynamic + W * D * 1024);            // [n k ws]
+    float *sums = reinterpret_cast<float *>(table + nk * p.ws);                // [n k][ws][16]
+    unsigned short *pairs = reinterpret_cast<unsigned short *>(sums + nk * p.ws * 16);   // [n k][16]
+    {
+        const int e = load_choice(p);
+        const float w = tid < nk ? p.weights[tid] : 0.f;
+        if (tid < nk)
+            tokens[tid] = 0;
+        if (tid == 0) {
+            queue = W;
+            count = 0;
         }
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-        while (true) {
-            const int done = unit, had = cnt;
-            tile += TP;
-            const bool last = tile >= end;
-            if (last)
-                open(unit + W);
-            const auto cr = codes_of(unit), sr = scales_of(unit);
-            static_for<TP>([&](auto tc) {
-                constexpr int t = decltype(tc)::value;
-                const u32x2 x[8] = {{h[t][0][0], h[t][0][1]}, {h[t][0][2], h[t][0][3]}, {h[t][1][0], h[t][1][1]},
-                                    {h[t][1][2], h[t][1][3]}, {h[t][2][0], h[t][2][1]}, {h[t][2][2], h[t][2][3]},
-                                    {h[t][3][0], h[t][3][1]}, {h[t][3][2], h[t][3][3]}};
-                if (had <= 4)
-                    tile_product<1>(acc, c[t], s[t], x);
-                else
-                    tile_product<4>(acc, c[t], s[t], x);
-                load(cr, sr, tc);
-                __builtin_amdgcn_sched_barrier(0);
-            });
-            if (last) {
+        int first;
+        const int a = build_routes(routes, p, e, &first), t = tid / p.k;
+        if (a >= 0)
+            atomicOr(&tokens[a], 1u << t);
+        if (tid < nk)
+            firsts[tid] = (unsigned short)first;
+        const float scale = tid < nk && routes.expert[tid] >= 0 ? p.gscale[2 * p.E + routes.expert[tid]] : 0.f;
+        __syncthreads();
+        const int j = a >= 0 ? __popc(tokens[a] & ((1u << t) - 1)) : 0;
+        if (a >= 0)
+            pairs[a * kFewTokens + j] = (unsigned short)tid;
+        __syncthreads();
+        // the first of each four tokens makes their units
+        if (a >= 0 && j % 4 == 0) {
+            const int n = __popc(tokens[a]);
+            for (int part = 0; part < p.ws; ++part) {
+                Unit u;
+                u.expert = routes.list[a];
+                u.part = (unsigned short)part;
+                u.tile = (unsigned short)(part * p.tpw);
+                u.end = (unsigned short)min(p.Td, (part + 1) * p.tpw);
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const int j = 4 * v + g;
-                    if (j < had)
-                        sums[(routes.pair[done / p.ws][j] * p.ws + done % p.ws) * 16 + i] = acc[v];
-                    acc[v] = 0.f;
-                }
+                for (int q = 0; q < 4; ++q)
+                    u.pair[q] = j + q < n ? pairs[a * kFewTokens + j + q] : kNoPair;
+                table[atomicAdd(&count, 1)] = u;
             }
-            if (unit >= units)
-                break;
         }
+        if (tid < nk)
+            mix[tid] = routes.expert[tid] < 0 ? 0.f : w * scale;
+        __syncthreads();
     }
+    const int units = __builtin_amdgcn_readfirstlane(count);
+    const unsigned tb = p.Td * 1024u, sb = p.Td * 128u;
+    const u32x4 hrsrc = uniform(buffer_rsrc(p.h, (unsigned)(nk * p.Td * kTileK * 2)));
+    const unsigned slots = lds_address(rows) + wave * (D * 1024);
+
+    u32x4 c[D];
+    u32x2 s[D];
+    int unit = wave, tile = 0, end = 0;   // of the tile that is loaded next
+    u32x4 crsrc, srsrc;
+    unsigned row;                         // this lane's 16 bytes of its row of the unit's h
+    auto begin = [&]() {
+        const bool in = unit < units;
+        const Unit &u = table[in ? unit : 0];
+        const int expert = in ? __builtin_amdgcn_readfirstlane(u.expert) : 0;
+        tile = in ? __builtin_amdgcn_readfirstlane(u.tile) : 0;
+        end = in ? __builtin_amdgcn_readfirstlane(u.end) : 1 << 30;
+        const int pair = u.pair[g];
+        const long long place = (long long)expert * (p.K / kRowsPerGroup) + rg;
+        crsrc = uniform(buffer_rsrc(p.d_codes + place * tb, in ? tb : 0u));
+        srsrc = uniform(buffer_rsrc(p.d_scales + place * sb, in ? sb : 0u));
+        // row g's chunk i ^ g goes to slot i of the row: the operand's reads (chunk
+        // 4 g + q of row i / 4) then fall into 16 different 16-byte slots
+        row = in && pair != kNoPair ? (unsigned)(pair * p.Td * (kTileK * 2) + 16 * (i ^ g)) : kOutOfRange;
+    };
+    auto load = [&](auto tc) {
+        constexpr int t = decltype(tc)::value;
+        load_lds_b128(hrsrc, row + tile * (kTileK * 2), slots + t * 1024);
+        s[t] = buffer_load_b64_nt(srsrc, (unsigned)(tile * 128 + i * 8));
+        c[t] = buffer_load_b128_nt(crsrc, (unsigned)(tile * 1024 + lane * 16));
+    };
+    // The tile after; its unit, if another begins, from the queue.
+    auto advance = [&]() {
+        if (++tile < end)
+            return;
+        int next = 0;
+        if (lane == 0)
+            next = atomicAdd(&queue, 1);
+        unit = __builtin_amdgcn_readfirstlane(next);
+        begin();
+    };
+    const char *mine = rows + wave * (D * 1024) + (i >> 2) * 256;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    begin();
+    int what[D];                  // of each slot: twice its unit, and 1 on the unit's last tile; -1: none
+    static_for<D>([&](auto tc) {
+        constexpr int t = decltype(tc)::value;
+        what[t] = unit < units ? unit * 2 + (tile + 1 == end) : -1;
+        load(tc);
+        advance();
+    });
+    while (what[0] >= 0) {
+        static_for<D>([&](auto tc) {
+            constexpr int t = decltype(tc)::value;
+            asm volatile("s_waitcnt vmcnt(%2)" : "+v"(c[t]), "+v"(s[t]) : "n"(3 * (D - 1)) : "memory");
+            u32x2 x[8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const u32x4 v = *reinterpret_cast<const u32x4 *>(mine + t * 1024 + ((4 * g + q) ^ (i >> 2)) * 16);
+                x[2 * q] = u32x2{v[0], v[1]};
+                x[2 * q + 1] = u32x2{v[2], v[3]};
+            }
+            tile_product<1>(acc, c[t], s[t], x);
+            if (what[t] >= 0 && (what[t] & 1)) {
+                const Unit &u = table[what[t] >> 1];
+                const int pair = u.pair[g];
+                if (pair != kNoPair)
+                    sums[(pair * p.ws + u.part) * 16 + i] = acc[0];
+                acc[0] = 0.f;
+            }
+            what[t] = unit < units ? unit * 2 + (tile + 1 == end) : -1;
+            // the slot has been read before the next tile's rows are sent to it
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            load(tc);
+            advance();
+        });
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (tid < p.n * 16) {
         const int t = tid >> 4, r = tid & 15;
@@ -392,7 +431,7 @@ __global__ __launch_bounds__(kThreads) void nvfp4_moe_down_kernel(MoeFewParams p
             const int q = t * p.k + sl;
             if (routes.expert[q] < 0)
                 continue;
-            const float *src = sums + routes.first[q] * p.ws * 16 + r;
+            const float *src = sums + firsts[q] * p.ws * 16 + r;
             float o = src[0];
             for (int w = 1; w < p.ws; ++w)
                 o += src[w * 16];
@@ -462,6 +501,7 @@ int nvfp4_launch_moe_few(const nvfp4_moe_few_args &a, hipStream_t stream)
     p.P = a.F / kRowsPerGroup;
     p.ws = down_split(a.k, p.Td);
     p.tpw = (p.Td + p.ws - 1) / p.ws;
+    p.ws = (p.Td + p.tpw - 1) / p.tpw;   // no part is empty
     p.e = a.epi;
     const int mt = (p.T + kWaves - 1) / kWaves;
     constexpr auto mts = std::make_integer_sequence<int, kMaxTilesPerWave>{};
@@ -470,7 +510,10 @@ int nvfp4_launch_moe_few(const nvfp4_moe_few_args &a, hipStream_t stream)
     hipLaunchKernelGGL(up, dim3((unsigned)(most < cus ? most : cus)), dim3(kThreads), 0, stream, p);
     if (hipGetLastError() != hipSuccess)
         return NVFP4_ERR_LAUNCH;
-    hipLaunchKernelGGL(nvfp4_moe_down_kernel<4>, dim3((unsigned)(a.K / kRowsPerGroup)), dim3(kThreads),
-                       (unsigned)(a.n * a.k * p.ws * 16 * sizeof(float)), stream, p);
+    constexpr int kAhead = 6;
+    const int nk = a.n * a.k;
+    hipLaunchKernelGGL(nvfp4_moe_down_kernel<kAhead>, dim3((unsigned)(a.K / kRowsPerGroup)), dim3(kThreads),
+                       (unsigned)(kWaves * kAhead * 1024 + nk * p.ws * (sizeof(Unit) + 64) + nk * kFewTokens * 2),
+                       stream, p);
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
 }
