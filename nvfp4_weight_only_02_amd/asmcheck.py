@@ -218,7 +218,7 @@ def check_function(instrs: list, stats: dict = None) -> list:
     return [(a,) + violations[a] for a in sorted(violations)]
 
 
-def check_library(lib: str, pattern: str = r"nvfp4_((fused_)?gem[mv]|moe_down)_kernel") -> dict:
+def check_library(lib: str, pattern: str = r"nvfp4_((fused_)?gem[mv]|moe_down|int8_gemm)_kernel") -> dict:
     """{kernel: violations} for every function of `lib` whose name matches
     `pattern`; raises if no function matches."""
     funcs = parse(disassemble(lib))

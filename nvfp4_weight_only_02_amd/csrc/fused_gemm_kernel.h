@@ -221,6 +221,9 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
             for (int v = 0; v < 16; ++v)
                 acc[r][t][v] = 0.f;
 
+    // 32-token blocks with rows (an expert's last tile is seldom full: the others
+    // would cost their matrix instructions and the power these are bound by)
+    const int blocks = GROUP ? __builtin_amdgcn_readfirstlane(min(TP, (tok1 - tok0 + 31) >> 5)) : TP;
     const int h = lane >> 5, tl = lane & 31;   // column half, token of the operand
     const int xa = (tl >> 2) * kQuad + (tl & 3) * 256;
     const int x0 = xa + (h ^ (tl & 3)) * 16, x1 = xa + ((h | 2) ^ (tl & 3)) * 16;
@@ -276,6 +279,8 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
                 dequant(std::integral_constant<int, j + 1>{}, (j + 1) & 1);
 #pragma unroll
             for (int t = 0; t < TP; ++t) {
+                if (GROUP && TP > 1 && t >= blocks)
+                    break;
                 const bf16x8 a = *reinterpret_cast<const bf16x8 *>(buf + x0 + t * 8 * kQuad + 64 * j);
                 const bf16x8 d = *reinterpret_cast<const bf16x8 *>(buf + x1 + t * 8 * kQuad + 64 * j);
 #pragma unroll

@@ -20,16 +20,17 @@ struct nvfp4_moe_gemm_args {
     long long ldx;
     int xrows, k;                 // rows of X (gather), experts of a token
     int rows, E;                  // at most so many rows
+    int tile_tokens;              // of a tile (nvfp4_moe_tile_tokens)
     int K, row_groups;            // of an expert's weight
     const float *gscale, *up_gscale;
     nvfp4_moe_order order;
     nvfp4_epi_params epi;
 };
 
-// The tile of a grouped product, from the sizes alone: its tokens, and the most
-// token tiles that `rows` rows of E experts can take.
-NVFP4_HIDDEN int nvfp4_moe_tile_tokens(int rows, int E);
-NVFP4_HIDDEN long long nvfp4_moe_max_tiles(int rows, int E);
+// The tokens of a tile of the grouped products (32 or 64), from the layer's sizes,
+// and the most tiles that `rows` rows of E experts can take.
+NVFP4_HIDDEN int nvfp4_moe_tile_tokens(int rows, int E, int F);
+NVFP4_HIDDEN long long nvfp4_moe_max_tiles(int rows, int E, int tokens);
 NVFP4_HIDDEN int nvfp4_launch_moe_gemm(const nvfp4_moe_gemm_args &a, hipStream_t stream);
 
 // The layer for a few tokens (moe_few.hip).

@@ -422,7 +422,10 @@ __global__ __launch_bounds__(kThreads, 4) void nvfp4_moe_down_kernel(MoeFewParam
             advance();
         });
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    // (the loads behind the last tile still write their registers)
+#pragma unroll
+    for (int t = 0; t < D; ++t)
+        asm volatile("s_waitcnt vmcnt(0)" : "+v"(c[t]), "+v"(s[t])::"memory");
     __syncthreads();
     if (tid < p.n * 16) {
         const int t = tid >> 4, r = tid & 15;

@@ -9,7 +9,7 @@ template <int RG, int TB, int RW, int KG>
 int launch_grouped(GroupedGemmParams p, const nvfp4_moe_gemm_args &a, hipStream_t stream)
 {
     p.tiles_x = (p.RG + RW * RG - 1) / (RW * RG);
-    p.tiles_y = (int)nvfp4_moe_max_tiles(a.rows, a.E);
+    p.tiles_y = (int)nvfp4_moe_max_tiles(a.rows, a.E, a.tile_tokens);
     const long long total = (long long)p.tiles_x * p.tiles_y;
     if (total > INT32_MAX || (long long)p.T * RG * 1024 > INT32_MAX)
         return NVFP4_ERR_SHAPE;   // a wave's codes must stay within a 32-bit buffer offset
@@ -28,15 +28,27 @@ int launch_grouped(GroupedGemmParams p, const nvfp4_moe_gemm_args &a, hipStream_
 
 }  // namespace
 
-int nvfp4_moe_tile_tokens(int rows, int E)
+// Measured on MI355X, weights cold (us, the whole layer, with gradients where
+// marked; E experts of F x K with k a token):
+//                                              128 x 32   128 x 64   256 x 64   256 x 128
+//   n = 30    E = 64  k = 8  F = 1408 K = 5120      150        175        166         204
+//   n = 100                                         184        197        194         254
+//   n = 1500                                       1009        776        750         786
+//   n = 700   E = 32  k = 4  F = 1280 K = 2048 *    252        235        249         305
+//   n = 4000  *                                    1060        820        802         823
+//   n = 300   E = 8   k = 2  F = 1024 K = 4096 *    123        143        188         271
+// A larger tile dequantises a weight for more rows, but an expert's last tile is
+// seldom full, and the smaller ones leave room for four workgroups a compute unit.
+int nvfp4_moe_tile_tokens(int rows, int E, int F)
 {
     const int each = (rows + E - 1) / E;   // rows of an expert where all are chosen alike
-    return each <= 32 ? 32 : (each <= 64 ? 64 : 128);
+    const long long workgroups = (rows / 64 + (E + 1) / 2) * (2LL * F + 127) / 128;
+    return each <= 40 || workgroups < 384 ? 32 : 64;
 }
 
-long long nvfp4_moe_max_tiles(int rows, int E)
+long long nvfp4_moe_max_tiles(int rows, int E, int tokens)
 {
-    return rows / nvfp4_moe_tile_tokens(rows, E) + (rows < E ? rows : E);
+    return rows / tokens + (rows < E ? rows : E);
 }
 
 int nvfp4_launch_moe_gemm(const nvfp4_moe_gemm_args &a, hipStream_t stream)
@@ -62,9 +74,9 @@ int nvfp4_launch_moe_gemm(const nvfp4_moe_gemm_args &a, hipStream_t stream)
     p.up_gscale = a.up_gscale;
     p.cstride = a.cstride;
     p.sstride = a.sstride;
-    switch (nvfp4_moe_tile_tokens(a.rows, a.E)) {
-    case 32: return launch_grouped<2, 2, 2, 4>(p, a, stream);
-    case 64: return launch_grouped<2, 4, 4, 2>(p, a, stream);
-    default: return launch_grouped<4, 8, 4, 1>(p, a, stream);
-    }
+    if (a.tile_tokens == 32)
+        return launch_grouped<2, 2, 4, 2>(p, a, stream);
+    if (a.rows / a.E >= 128)
+        return launch_grouped<4, 4, 4, 1>(p, a, stream);
+    return launch_grouped<2, 4, 4, 1>(p, a, stream);
 }

@@ -195,9 +195,10 @@ def test_results_repeat_and_do_not_depend_on_the_batch(n):
     say("int8 batch", n)
     w, _, _ = weight(200, 2064, 17)
     X = randn((600, 2064), 18)
-    whole = nv.int8_linear(w, X, activation="silu", out_dtype=F32)
-    for a in (0, 31, 600 - n):
-        assert torch.equal(nv.int8_linear(w, X[a:a + n], activation="silu", out_dtype=F32), whole[a:a + n])
+    for bias in (None, randn((200,), 30, F32)):
+        whole = nv.int8_linear(w, X, bias=bias, activation="silu", out_dtype=F32)
+        for a in (0, 31, 600 - n):
+            assert torch.equal(nv.int8_linear(w, X[a:a + n], bias=bias, activation="silu", out_dtype=F32), whole[a:a + n])
 
 
 @pytest.mark.parametrize("n", [6, 80, 530])
