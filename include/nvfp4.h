@@ -523,11 +523,11 @@ int nvfp4_int8_quantize(const void *X, int dtype, int64_t ldx, int n, int K, int
 /* Y[t][r] = act(xscale[t] wscale[r] sum_k Xq[t][k] Wq[r][k] + bias[r]) + residual[t][r]
  * for n = 0 .. NVFP4_MAX_GEMM_TOKENS.  Wq packed.  xscale [n] with X int8
  * [n][ldx]; or xscale NULL with X bf16 [n][ldx], which is then quantised as by
- * nvfp4_int8_quantize into the workspace.  X rows are 16-byte aligned, ldx at most
+ * nvfp4_int8_quantize.  X rows are 16-byte aligned, ldx at most
  * 2^22.  epilogue: bias, activation, residual (it may be Y itself), out_dtype;
  * up_bias and preact NULL (a quantised product has no derivative).  Workspace:
- * nvfp4_int8_linear_workspace_bytes (0 for some calls with xscale), quantize = 1
- * where xscale is NULL; 16-byte aligned.
+ * nvfp4_int8_linear_workspace_bytes (0 for some calls), quantize = 1 where xscale is
+ * NULL; 16-byte aligned.
  * Errors: NULL, RANGE, SHAPE, ALIGN, OVERLAP, WORKSPACE, DEVICE, LAUNCH. */
 int nvfp4_int8_linear(const int8_t *Wq, const float *wscale, const void *X, int64_t ldx, const float *xscale,
                       void *Y, int64_t ldy, int n, int N, int K, const nvfp4_epilogue *epilogue,

@@ -78,6 +78,19 @@ __device__ __forceinline__ float activate(float z, int act)
     }
 }
 
+// f(std::integral_constant<int, act>): the choice made once for a loop of outputs.
+template <typename F>
+__device__ __forceinline__ void with_activation(int act, F &&f)
+{
+    switch (act) {
+    case NVFP4_ACT_RELU: f(std::integral_constant<int, NVFP4_ACT_RELU>{}); break;
+    case NVFP4_ACT_SILU: f(std::integral_constant<int, NVFP4_ACT_SILU>{}); break;
+    case NVFP4_ACT_GELU: f(std::integral_constant<int, NVFP4_ACT_GELU>{}); break;
+    case NVFP4_ACT_GELU_TANH: f(std::integral_constant<int, NVFP4_ACT_GELU_TANH>{}); break;
+    default: f(std::integral_constant<int, NVFP4_ACT_NONE>{}); break;
+    }
+}
+
 // act'(z)
 __device__ __forceinline__ float activate_grad(float z, int act)
 {

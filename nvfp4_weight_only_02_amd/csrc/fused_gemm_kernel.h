@@ -378,6 +378,44 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
             }
             continue;
         }
+        // GROUP: sums as they are, in rows of their own (whole vectors: outputs come
+        // in sixteens), or h with the activation chosen once.
+        if constexpr (GROUP && MODE != 1) {
+#pragma unroll 2
+            for (int q = tid * 4; q < 32 * kOuts; q += 4 * kThreads) {
+                const int t = q / kOuts, o = q % kOuts, tok = tok0 + 32 * b + t;
+                if (tok >= tok1)
+                    break;
+                if (tx * kOuts + o < p.e.N)
+                    *reinterpret_cast<f32x4 *>(static_cast<float *>(p.e.out) + (long long)tok * p.e.ldo + tx * kOuts + o) =
+                        p.e.gscale * staged(t, o);
+            }
+            continue;
+        } else if constexpr (GROUP) {
+            with_activation(p.e.flags & kEpiAct, [&](auto act) {
+#pragma unroll 2
+                for (int q = tid * 4; q < 32 * kOuts; q += 4 * kThreads) {
+                    const int t = q / kOuts, o = q % kOuts, tok = tok0 + 32 * b + t, r = tx * kOuts + o;
+                    if (tok >= tok1)
+                        break;
+                    if (r >= p.e.N)
+                        continue;
+                    const int row = (o >> 4) * 32 + (o & 15);
+                    const f32x4 z = p.e.gscale * staged(t, row), u = p.e.up_gscale * staged(t, row + 16);
+                    if (p.e.preact) {
+                        float *pre = p.e.preact + (long long)tok * p.e.ldp;
+                        *reinterpret_cast<f32x4 *>(pre + gated_row(r, 0)) = z;
+                        *reinterpret_cast<f32x4 *>(pre + gated_row(r, 1)) = u;
+                    }
+                    f32x4 y;
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        y[v] = activate(z[v], decltype(act)::value) * u[v];
+                    store_any4(p.e.out, (long long)tok * p.e.ldo + r, 0, y);
+                }
+            });
+            continue;
+        }
 #pragma unroll 1
         for (int q = tid * 4; q < 32 * kOuts; q += 4 * kThreads) {
             const int t = q / kOuts, o = q % kOuts;

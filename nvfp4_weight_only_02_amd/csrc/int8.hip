@@ -38,17 +38,48 @@ __global__ __launch_bounds__(256) void nvfp4_int8_pack_kernel(const int8_t *src,
 
 // ---- quantisation ------------------------------------------------------------------
 
-// Rows of bf16 or fp32 to 8-bit integers: scale = amax / 127, q = rint(127 x /
-// amax), halves to the even integer.  For bf16 the quotient of two 8-bit
+// A row's quantisation: scale = amax / 127, q = rint(127 x / amax), halves to the
+// even integer.  `top`: the bits of amax.  For bf16 the quotient of two 8-bit
 // mantissas (one times 127) is either a half-integer exactly or at least 2^-17 of
-// its value away from one, so the correctly rounded fp32 division decides as
-// exact arithmetic would.  A row that holds a NaN or an infinity has scale NaN
-// and q = 0; a row of zeros has scale 0.  One workgroup a row, whose values stay
-// in registers between the maximum and the division (the first kHeld vectors of a
-// thread; a longer row is read again).
-constexpr int kQuantThreads = 256, kHeld = 4;
+// its value away from one; the product with the reciprocal and one correction by
+// its exact remainder is within 2^-23 of it, and gives a representable quotient
+// itself: rounding decides as exact arithmetic would.  fp32 rows are divided.
+// Both sides of the quotient are first scaled by a power of two that keeps 127 x
+// and the reciprocal in range.  A row that holds a NaN or an infinity has scale
+// NaN and q = 0; a row of zeros has scale 0.
+struct RowScale {
+    float mul, div, rcp, scale;
+    bool finite;
+    __device__ __forceinline__ explicit RowScale(u32 top)
+    {
+        finite = top < 0x7F800000u;
+        const float amax = __builtin_bit_cast(float, top);
+        scale = finite ? amax / 127.0f : __builtin_nanf("");
+        const float by = amax > 0x1p60f ? 0x1p-64f : (amax < 0x1p-60f ? 0x1p100f : 1.0f);
+        mul = 127.0f * by;
+        div = finite && top ? amax * by : 1.0f;
+        rcp = __builtin_amdgcn_rcpf(div);
+    }
+    template <bool F32>
+    __device__ __forceinline__ int quantize(u32 bits) const
+    {
+        const float t = __builtin_bit_cast(float, bits) * mul;
+        float q;
+        if constexpr (F32) {
+            q = t / div;
+        } else {
+            const float q0 = t * rcp;
+            q = __builtin_fmaf(__builtin_fmaf(-q0, div, t), rcp, q0);
+        }
+        return finite ? (int)__builtin_rintf(q) : 0;
+    }
+};
 
-template <bool F32>
+// One workgroup a row, whose values stay in registers between the maximum and the
+// division (the first kHeld vectors of a thread; a longer row is read again).
+constexpr int kHeld = 4;
+
+template <bool F32, int kQuantThreads>
 __global__ __launch_bounds__(kQuantThreads) void nvfp4_int8_quantize_kernel(const void *src, long long ldx, int K, int8_t *q,
                                                                            long long ldq, float *scale)
 {
@@ -109,20 +140,14 @@ __global__ __launch_bounds__(kQuantThreads) void nvfp4_int8_quantize_kernel(cons
 #pragma unroll
     for (int w = 0; w < kQuantThreads / 64; ++w)
         top = max(top, tops[w]);
-    const bool finite = top < 0x7F800000u;
-    const float amax = __builtin_bit_cast(float, top);
+    const RowScale row_scale(top);
     if (tid == 0)
-        scale[t] = finite ? amax / 127.0f : __builtin_nanf("");
-    // 127 x must not overflow; both sides of the quotient by a power of two
-    const float down = amax > 0x1p100f ? 0x1p-64f : 1.0f;
-    const float mul = 127.0f * down, div = finite && top ? amax * down : 1.0f;
+        scale[t] = row_scale.scale;
     auto store = [&](int c, const Vec &r) {
         u32 w[2] = {0u, 0u};
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float x = __builtin_bit_cast(float, r.v[e]);
-            const int v = finite ? (int)__builtin_rintf(x * mul / div) : 0;
-            w[e / 4] |= (u32)(v & 255) << (8 * (e % 4));
+            w[e / 4] |= (u32)(row_scale.quantize<F32>(r.v[e]) & 255) << (8 * (e % 4));
         }
         *reinterpret_cast<u32x2 *>(q + t * ldq + c * 8) = u32x2{w[0], w[1]};
     };
@@ -141,55 +166,147 @@ __global__ __launch_bounds__(kQuantThreads) void nvfp4_int8_quantize_kernel(cons
 struct Int8GemvParams {
     const char *codes;
     const float *wscale, *xscale;
-    const int8_t *X;
+    const void *X;        // int8, or bf16 that the launch quantises
     long long ldx;
     int n, K, T2, RG;     // T2: 64-column tiles
+    int rows;             // of a workgroup
     nvfp4_epi_params e;
 };
 
-// A workgroup has R row groups; its eight waves take U consecutive 64-column
-// tiles in turn.  A tile's 1 KiB is one 16-byte load a lane and the operand of one
-// v_mfma_i32_16x16x64_i8 as it stands; the tokens' operand is loaded beside it
-// (16 rows x 64 bytes, from L2) once for the R row groups.  Bound by the weight
-// stream.
-template <int R, int U>
+constexpr int kQuantInside = 49152;   // most activations a decode launch quantises itself
+
+// A workgroup has p.rows weight rows, in R windows of 16 (of which the last may use
+// fewer, and which need not begin with a row group); its eight waves take
+// 64-column tiles in turn.  A window's 1 KiB is one 16-byte load a lane and the
+// operand of one v_mfma_i32_16x16x64_i8 as it stands; the tokens' operand is read
+// beside it once for the R windows.  Bound by the weight stream; rows are dealt
+// out evenly, in fours, since a compute unit reads no faster than its share of the
+// memory's bandwidth (5120 x 6144, n = 1, 16 rows a workgroup: 320 of them on 256
+// units took 9.4 us).
+//
+// QUANT: every workgroup quantises the bf16 activations itself, into LDS, while
+// its first weights are under way; a launch for it costs 4.4 us more (5120 x 6144,
+// n = 1).  Up to eight tokens, a wave each, and kQuantInside values: beyond, the
+// arithmetic outlasts the loads that it hides behind.
+template <int R, int U, bool QUANT>
 __global__ __launch_bounds__(kWaves * 64) void nvfp4_int8_gemv_kernel(Int8GemvParams p)
 {
     constexpr int W = kWaves;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int i = lane & 15, g = lane >> 4;
-    const int rg0 = blockIdx.x * R, nrg = min(R, p.RG - rg0);
+    const int row0 = blockIdx.x * p.rows;
     __shared__ i32x4 part[R][W][64];
-    auto resource = [&](const void *base, unsigned bytes) {
-        return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, (int)bytes, kBufferWord3);
-    };
+    __shared__ u32 tops[W];
+    __shared__ float xs[W];
+    extern __shared__ __align__(16) char xq[];   // QUANT: [n][64 T2]
+    // This lane's row of each window: its offset from the first row group.
+    const int rg0 = row0 >> 4, nrg = min((row0 + p.rows + 15) >> 4, p.RG) - rg0;
     const auto cr = resource(p.codes + (size_t)rg0 * p.T2 * 1024, (unsigned)(nrg * p.T2) * 1024u);
-    const auto xr = resource(p.X, (unsigned)((p.n - 1) * p.ldx + p.K));
+    unsigned off[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int at = 16 * r + i, row = row0 + at;
+        off[r] = at < p.rows ? (unsigned)(((row >> 4) - rg0) * p.T2 * 1024 + (g * 16 + (row & 15)) * 16) : kOutOfRange;
+    }
     u32x4 c[U][R], x[U];
-    auto load = [&](int tile, int u) {
-        const int col = tile * 64 + 16 * g;
-        const int behind = tile < p.T2 ? 0 : 1 << 30;   // past the resource: no memory is touched
-        x[u] = __builtin_amdgcn_raw_buffer_load_b128(xr, i < p.n && col < p.K ? (int)(i * p.ldx + col) : (int)kOutOfRange, 0, 0);
+    auto load_codes = [&](int tile, int u) {
+        const unsigned behind = tile < p.T2 ? 0 : 1u << 30;   // past the resource: no memory is touched
 #pragma unroll
         for (int r = 0; r < R; ++r)
-            c[u][r] = __builtin_amdgcn_raw_buffer_load_b128(cr, (r * p.T2 + tile) * 1024 + lane * 16 + behind, 0, 2);
+            c[u][r] = __builtin_amdgcn_raw_buffer_load_b128(cr, (int)(off[r] + tile * 1024 + behind), 0, 2);
     };
+    const auto xr = resource(p.X, (unsigned)((p.n - 1) * p.ldx + p.K));   // int8
+    auto load_x = [&](int tile, int u) {
+        const int col = tile * 64 + 16 * g;
+        if constexpr (QUANT)
+            x[u] = i < p.n && tile < p.T2 ? *reinterpret_cast<const u32x4 *>(xq + i * (p.T2 * 64) + col) : u32x4{0u, 0u, 0u, 0u};
+        else
+            x[u] = __builtin_amdgcn_raw_buffer_load_b128(xr, i < p.n && col < p.K ? (int)(i * p.ldx + col) : (int)kOutOfRange, 0, 0);
+    };
+    int tile = wave;
+    // QUANT: 8, 4, 2 or 1 waves a token; what a lane reads for the maximum it keeps
+    // for the division (a long row's rest is read again).  Loads come back in order:
+    // the activations first, the weights while they are quantised.
+    constexpr int kHold = 8;
+    const int share = p.n == 1 ? 8 : (p.n == 2 ? 4 : (p.n <= 4 ? 2 : 1)), sub = wave % share, t = wave / share;
+    const int chunks = p.K / 8, step = 64 * share, c0 = sub * 64 + lane;
+    const u32x4 *row = reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(p.X) + (QUANT && t < p.n ? t : 0) * p.ldx);
+    u32x4 held[QUANT ? kHold : 1];
+    if constexpr (QUANT) {
+#pragma unroll
+        for (int j = 0; j < kHold; ++j)
+            held[j] = t < p.n && c0 + j * step < chunks ? row[c0 + j * step] : u32x4{0u, 0u, 0u, 0u};
+        __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        load_codes(tile + u * W, u);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (QUANT) {
+        u32 top = 0;
+        auto largest = [&](const u32x4 v) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                top = max(top, max((v[q] << 16) & 0x7FFF0000u, v[q] & 0x7FFF0000u));
+        };
+        if (t < p.n) {
+#pragma unroll
+            for (int j = 0; j < kHold; ++j)
+                largest(held[j]);
+            for (int c = c0 + kHold * step; c < chunks; c += step)
+                largest(row[c]);
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2)
+                top = max(top, (u32)__shfl_xor((int)top, d));
+            if (lane == 0)
+                tops[wave] = top;
+        }
+        __syncthreads();
+        if (t < p.n) {
+            for (int w = 0; w < share; ++w)
+                top = max(top, tops[t * share + w]);
+            const RowScale scale(top);
+            if (sub == 0 && lane == 0)
+                xs[t] = scale.scale;
+            auto store = [&](int c, const u32x4 v) {
+                u32 w[2] = {0u, 0u};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const u32 lo = scale.quantize<false>(v[q] << 16) & 255, hi = scale.quantize<false>(v[q] & 0xFFFF0000u) & 255;
+                    w[q / 2] |= (lo | hi << 8) << (16 * (q % 2));
+                }
+                *reinterpret_cast<u32x2 *>(xq + t * (p.T2 * 64) + c * 8) = u32x2{w[0], w[1]};
+            };
+#pragma unroll
+            for (int j = 0; j < kHold; ++j)
+                if (c0 + j * step < p.T2 * 8)      // (the columns behind K are zeros)
+                    store(c0 + j * step, held[j]);
+            for (int c = c0 + kHold * step; c < p.T2 * 8; c += step)
+                store(c, c < chunks ? row[c] : u32x4{0u, 0u, 0u, 0u});
+        }
+        __syncthreads();
+    }
     i32x4 acc[R];
 #pragma unroll
     for (int r = 0; r < R; ++r)
         acc[r] = i32x4{0, 0, 0, 0};
-    int tile = wave;
+    if constexpr (!QUANT) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-        load(tile + u * W, u);
+        for (int u = 0; u < U; ++u)
+            load_x(tile + u * W, u);
+    }
     for (; tile < p.T2; tile += W * U) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+            if constexpr (QUANT)
+                load_x(tile + u * W, u);
 #pragma unroll
             for (int r = 0; r < R; ++r)
                 acc[r] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, x[u]), __builtin_bit_cast(i32x4, c[u][r]),
                                                                acc[r], 0, 0, 0);
-            load(tile + W * (U + u), u);
+            load_codes(tile + W * (U + u), u);
+            if constexpr (!QUANT)
+                load_x(tile + W * (U + u), u);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
@@ -200,38 +317,58 @@ __global__ __launch_bounds__(kWaves * 64) void nvfp4_int8_gemv_kernel(Int8GemvPa
     // lane (i, g), component v: token 4 g + v, weight row i
     for (int o = tid; o < R * 256; o += kWaves * 64) {
         const int r = o >> 8, l = (o >> 2) & 63, v = o & 3;
-        const int tok = 4 * (l >> 4) + v, row = (rg0 + r) * kRowsPerGroup + (l & 15);
-        if (tok >= p.n || row >= p.e.N)
+        const int tok = 4 * (l >> 4) + v, at = 16 * r + (l & 15), row = row0 + at;
+        if (tok >= p.n || at >= p.rows || row >= p.e.N)
             continue;
         int s = 0;
 #pragma unroll
         for (int w = 0; w < W; ++w)
             s += reinterpret_cast<const int *>(&part[r][w][l])[v];
-        linear_out(p.e, tok, row, (float)s * p.xscale[tok] * p.wscale[row]);
+        linear_out(p.e, tok, row, (float)s * (QUANT ? xs[tok] : p.xscale[tok]) * p.wscale[row]);
     }
 }
 
-int launch_gemv(const nvfp4_int8_args &a, hipStream_t stream)
+// Whether a decode launch quantises its activations itself.
+bool quant_inside(int n, int K)
+{
+    return n <= kWaves && (long long)n * K <= kQuantInside;
+}
+
+template <bool QUANT>
+int launch_gemv(Int8GemvParams p, hipStream_t stream)
+{
+    int cus = 0;
+    const int st = nvfp4_device_cus(&cus);
+    if (st != NVFP4_OK)
+        return st;
+    // one workgroup a compute unit, or as many as keep them at 64 rows
+    const long long units = ((long long)p.e.N + 64LL * cus - 1) / (64LL * cus) * cus;
+    p.rows = (int)((p.e.N + 4 * units - 1) / (4 * units) * 4);
+    const dim3 grid((unsigned)((p.e.N + p.rows - 1) / p.rows)), block(kWaves * 64);
+    const unsigned lds = QUANT ? (unsigned)(p.n * p.T2 * 64) : 0u;
+    switch ((p.rows + 15) / 16) {
+    case 1: hipLaunchKernelGGL((nvfp4_int8_gemv_kernel<1, 8, QUANT>), grid, block, lds, stream, p); break;
+    case 2: hipLaunchKernelGGL((nvfp4_int8_gemv_kernel<2, 6, QUANT>), grid, block, lds, stream, p); break;
+    case 3: hipLaunchKernelGGL((nvfp4_int8_gemv_kernel<3, 4, QUANT>), grid, block, lds, stream, p); break;
+    default: hipLaunchKernelGGL((nvfp4_int8_gemv_kernel<4, 4, QUANT>), grid, block, lds, stream, p); break;
+    }
+    return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
+}
+
+int launch_gemv(const nvfp4_int8_args &a, const void *X, long long ldx, hipStream_t stream)
 {
     Int8GemvParams p = {};
     p.codes = reinterpret_cast<const char *>(a.codes);
     p.wscale = a.wscale;
     p.xscale = a.xscale;
-    p.X = a.X;
-    p.ldx = a.ldx;
+    p.X = X;
+    p.ldx = ldx;
     p.n = a.n;
     p.K = a.K;
     p.T2 = 2 * (int)k_tiles(a.K);
     p.RG = (int)row_groups(a.N);
     p.e = a.epi;
-    const dim3 block(kWaves * 64);
-    if (p.RG >= 1024)
-        hipLaunchKernelGGL((nvfp4_int8_gemv_kernel<4, 4>), dim3((unsigned)((p.RG + 3) / 4)), block, 0, stream, p);
-    else if (p.RG >= 512)
-        hipLaunchKernelGGL((nvfp4_int8_gemv_kernel<2, 6>), dim3((unsigned)((p.RG + 1) / 2)), block, 0, stream, p);
-    else
-        hipLaunchKernelGGL((nvfp4_int8_gemv_kernel<1, 8>), dim3((unsigned)p.RG), block, 0, stream, p);
-    return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
+    return a.xscale ? launch_gemv<false>(p, stream) : launch_gemv<true>(p, stream);
 }
 
 // K parts added, then the epilogue: four outputs of a token a thread.
@@ -270,7 +407,7 @@ Space space_of(int n, int N, int K, bool quantize)
     Space s = {};
     if (n < 1)
         return s;
-    if (quantize) {
+    if (quantize && !quant_inside(n, K)) {
         s.q = round256((size_t)n * K);
         s.scale = round256((size_t)n * 4);
     }
@@ -290,10 +427,16 @@ int check_shape(int n, int N, int K)
 
 int launch_quantize(const void *X, int dtype, long long ldx, int n, int K, int8_t *q, long long ldq, float *scale, hipStream_t s)
 {
-    if (dtype == NVFP4_DTYPE_F32)
-        hipLaunchKernelGGL(nvfp4_int8_quantize_kernel<true>, dim3((unsigned)n), dim3(kQuantThreads), 0, s, X, ldx, K, q, ldq, scale);
-    else
-        hipLaunchKernelGGL(nvfp4_int8_quantize_kernel<false>, dim3((unsigned)n), dim3(kQuantThreads), 0, s, X, ldx, K, q, ldq, scale);
+    // (a row of 8192 stays in the registers of 256 threads; n = 300, K = 17408: 7.7 us
+    // with 256, LONG with 1024)
+    const bool f32 = dtype == NVFP4_DTYPE_F32;
+    if (K <= 8192) {
+        auto k = f32 ? nvfp4_int8_quantize_kernel<true, 256> : nvfp4_int8_quantize_kernel<false, 256>;
+        hipLaunchKernelGGL(k, dim3((unsigned)n), dim3(256), 0, s, X, ldx, K, q, ldq, scale);
+    } else {
+        auto k = f32 ? nvfp4_int8_quantize_kernel<true, 1024> : nvfp4_int8_quantize_kernel<false, 1024>;
+        hipLaunchKernelGGL(k, dim3((unsigned)n), dim3(1024), 0, s, X, ldx, K, q, ldq, scale);
+    }
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
 }
 
@@ -405,7 +548,7 @@ int nvfp4_int8_linear(const int8_t *Wq, const float *wscale, const void *X, int6
     a.n = n;
     a.N = N;
     a.K = K;
-    if (quantize) {
+    if (w.q) {
         int8_t *q = reinterpret_cast<int8_t *>(ws);
         float *scale = reinterpret_cast<float *>(ws + w.q);
         st = launch_quantize(X, NVFP4_DTYPE_BF16, ldx, n, K, q, K, scale, s);
@@ -434,7 +577,7 @@ int nvfp4_int8_linear(const int8_t *Wq, const float *wscale, const void *X, int6
         (!ep.residual || (ep.ldr % 4 == 0 && is_aligned(ep.residual, 4 * rs))))
         e.flags |= kEpiVec;
     if (n <= NVFP4_MAX_TOKENS)
-        return launch_gemv(a, s);
+        return w.q || !quantize ? launch_gemv(a, a.X, a.ldx, s) : launch_gemv(a, X, ldx, s);
     const nvfp4_int8_plan plan = nvfp4_plan_int8(n, (int)row_groups(N), K);
     st = nvfp4_launch_int8_gemm(a, plan, s);
     if (st != NVFP4_OK || plan.ks == 1)

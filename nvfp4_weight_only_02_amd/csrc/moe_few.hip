@@ -32,6 +32,7 @@ struct MoeFewParams {
     int ldx, n, k, E, F, K, act;
     int T, Td, P;                 // 128-column tiles of K and of F, pairs of row groups of a gated weight
     int ws, tpw;                  // parts of an expert's F in the down projection, and the tiles of each
+    int rows;                     // outputs of a workgroup of the down projection
     nvfp4_epi_params e;
 };
 
@@ -82,7 +83,7 @@ __device__ __forceinline__ int build_routes(Routes &r, const MoeFewParams &p, in
             a += __popc(r.bits[w]);
         r.list[a] = (unsigned short)e;
     }
-    if (tid == kThreads - 1) {
+    if (tid == kMaxPairs - 1) {
         int c = 0;
         for (int w = 0; w < words; ++w)
             c += __popc(r.bits[w]);
@@ -280,22 +281,32 @@ struct Unit {
 };
 constexpr int kNoPair = 0xFFFF;
 
-// Down: a workgroup has 16 outputs of every token.  Its waves take units from a
-// queue: an expert with up to four of its tokens (an expert with more has several
-// units, whose weights come from cache after the first; four tokens cost the
-// matrix instruction one component and 1 KiB of LDS a tile), or a part of its F
-// where a token has few experts.  A unit's tiles of weights go to registers and
-// its tokens' rows straight to LDS, D tiles ahead: three loads a tile, always in
-// the same order, so that the wait for a tile is the constant count of the newer
-// ones, across the units' ends too.  The sums of all pairs meet in LDS, and a
-// thread adds those of its token, weighted, in slot order.
-template <int D>
+// Down: a workgroup has p.rows outputs of every token, in NW windows of 16 rows
+// (of which the last may use fewer, and which need not begin with a row group).
+// Its waves take units from a queue: an expert with up to four of its tokens (an
+// expert with more has several units, whose weights come from cache after the
+// first; four tokens cost the matrix instruction one component and 1 KiB of LDS a
+// tile), or a part of its F where a token has few experts.  A unit's tiles of
+// weights go to registers and its tokens' rows straight to LDS, D tiles ahead:
+// always the same loads a tile in the same order, so that the wait for a tile is
+// the constant count of the newer ones, across the units' ends too.  The sums of
+// all pairs meet in LDS, and a thread adds those of its token, weighted, in slot
+// order.
+//
+// Rows are dealt out evenly over the compute units, in fours (64 bytes of each
+// column quarter of a tile): a unit reads little faster than its share of the
+// memory's bandwidth (24 KB/us were measured with most others done, against 25 for
+// 6.4 TB/s over 256), so a second workgroup on some of them would be what the
+// launch waits for.  13 experts 400 x 1040, n = 7: 10.2 us with 16 rows a
+// workgroup, 7.5 with 8; E = 64, F = 1408, K = 5120, k = 8, n = 16 (225 MB): 53 us,
+// of which the codes alone take 42.
+template <int NW, int D>
 __global__ __launch_bounds__(kThreads, 4) void nvfp4_moe_down_kernel(MoeFewParams p)
 {
     constexpr int W = kWaves;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int i = lane & 15, g = lane >> 4;
-    const int rg = blockIdx.x, nk = p.n * p.k;
+    const int row0 = blockIdx.x * p.rows, nk = p.n * p.k;
     __shared__ Routes routes;
     __shared__ unsigned tokens[kMaxPairs];        // of each expert of the list: its tokens, a bit each
     __shared__ unsigned short firsts[kMaxPairs];  // of each pair: the token's first pair with its expert
@@ -304,8 +315,8 @@ __global__ __launch_bounds__(kThreads, 4) void nvfp4_moe_down_kernel(MoeFewParam
     extern __shared__ __align__(1024) char dynamic[];
     char *rows = dynamic;                                                      // [W][D] KiB
     Unit *table = reinterpret_cast<Unit *>(dynamic + W * D * 1024);            // [n k ws]
-    float *sums = reinterpret_cast<float *>(table + nk * p.ws);                // [n k][ws][16]
-    unsigned short *pairs = reinterpret_cast<unsigned short *>(sums + nk * p.ws * 16);   // [n k][16]
+    float *sums = reinterpret_cast<float *>(table + nk * p.ws);                // [n k][ws][16 NW]
+    unsigned short *pairs = reinterpret_cast<unsigned short *>(sums + nk * p.ws * 16 * NW);   // [n k][16]
     {
         const int e = load_choice(p);
         const float w = tid < nk ? p.weights[tid] : 0.f;
@@ -351,8 +362,17 @@ __global__ __launch_bounds__(kThreads, 4) void nvfp4_moe_down_kernel(MoeFewParam
     const u32x4 hrsrc = uniform(buffer_rsrc(p.h, (unsigned)(nk * p.Td * kTileK * 2)));
     const unsigned slots = lds_address(rows) + wave * (D * 1024);
 
-    u32x4 c[D];
-    u32x2 s[D];
+    // This lane's row of each window: its offsets within an expert's codes and scales.
+    unsigned coff[NW], soff[NW];
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        const int at = 16 * w + i, r = row0 + at;
+        const bool in = at < p.rows && r < p.K;
+        coff[w] = in ? (unsigned)(r >> 4) * tb + (unsigned)((g * 16 + (r & 15)) * 16) : kOutOfRange;
+        soff[w] = in ? (unsigned)(r >> 4) * sb + (unsigned)((r & 15) * 8) : kOutOfRange;
+    }
+    u32x4 c[D][NW];
+    u32x2 s[D][NW];
     int unit = wave, tile = 0, end = 0;   // of the tile that is loaded next
     u32x4 crsrc, srsrc;
     unsigned row;                         // this lane's 16 bytes of its row of the unit's h
@@ -363,9 +383,9 @@ __global__ __launch_bounds__(kThreads, 4) void nvfp4_moe_down_kernel(MoeFewParam
         tile = in ? __builtin_amdgcn_readfirstlane(u.tile) : 0;
         end = in ? __builtin_amdgcn_readfirstlane(u.end) : 1 << 30;
         const int pair = u.pair[g];
-        const long long place = (long long)expert * (p.K / kRowsPerGroup) + rg;
-        crsrc = uniform(buffer_rsrc(p.d_codes + place * tb, in ? tb : 0u));
-        srsrc = uniform(buffer_rsrc(p.d_scales + place * sb, in ? sb : 0u));
+        const unsigned groups = p.K / kRowsPerGroup;
+        crsrc = uniform(buffer_rsrc(p.d_codes + (long long)expert * groups * tb, in ? groups * tb : 0u));
+        srsrc = uniform(buffer_rsrc(p.d_scales + (long long)expert * groups * sb, in ? groups * sb : 0u));
         // row g's chunk i ^ g goes to slot i of the row: the operand's reads (chunk
         // 4 g + q of row i / 4) then fall into 16 different 16-byte slots
         row = in && pair != kNoPair ? (unsigned)(pair * p.Td * (kTileK * 2) + 16 * (i ^ g)) : kOutOfRange;
@@ -373,8 +393,11 @@ __global__ __launch_bounds__(kThreads, 4) void nvfp4_moe_down_kernel(MoeFewParam
     auto load = [&](auto tc) {
         constexpr int t = decltype(tc)::value;
         load_lds_b128(hrsrc, row + tile * (kTileK * 2), slots + t * 1024);
-        s[t] = buffer_load_b64_nt(srsrc, (unsigned)(tile * 128 + i * 8));
-        c[t] = buffer_load_b128_nt(crsrc, (unsigned)(tile * 1024 + lane * 16));
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            s[t][w] = buffer_load_b64_nt(srsrc, soff[w] + tile * 128);
+            c[t][w] = buffer_load_b128_nt(crsrc, coff[w] + tile * 1024);
+        }
     };
     // The tile after; its unit, if another begins, from the queue.
     auto advance = [&]() {
@@ -387,7 +410,10 @@ __global__ __launch_bounds__(kThreads, 4) void nvfp4_moe_down_kernel(MoeFewParam
         begin();
     };
     const char *mine = rows + wave * (D * 1024) + (i >> 2) * 256;
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    f32x4 acc[NW];
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
+        acc[w] = f32x4{0.f, 0.f, 0.f, 0.f};
     begin();
     int what[D];                  // of each slot: twice its unit, and 1 on the unit's last tile; -1: none
     static_for<D>([&](auto tc) {
@@ -399,7 +425,11 @@ __global__ __launch_bounds__(kThreads, 4) void nvfp4_moe_down_kernel(MoeFewParam
     while (what[0] >= 0) {
         static_for<D>([&](auto tc) {
             constexpr int t = decltype(tc)::value;
-            asm volatile("s_waitcnt vmcnt(%2)" : "+v"(c[t]), "+v"(s[t]) : "n"(3 * (D - 1)) : "memory");
+            if constexpr (NW == 1)
+                asm volatile("s_waitcnt vmcnt(%2)" : "+v"(c[t][0]), "+v"(s[t][0]) : "n"(3 * (D - 1)) : "memory");
+            else
+                asm volatile("s_waitcnt vmcnt(%4)" : "+v"(c[t][0]), "+v"(s[t][0]), "+v"(c[t][1]), "+v"(s[t][1])
+                             : "n"(5 * (D - 1)) : "memory");
             u32x2 x[8];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -407,13 +437,18 @@ __global__ __launch_bounds__(kThreads, 4) void nvfp4_moe_down_kernel(MoeFewParam
                 x[2 * q] = u32x2{v[0], v[1]};
                 x[2 * q + 1] = u32x2{v[2], v[3]};
             }
-            tile_product<1>(acc, c[t], s[t], x);
+#pragma unroll
+            for (int w = 0; w < NW; ++w)
+                tile_product<1>(acc[w], c[t][w], s[t][w], x);
             if (what[t] >= 0 && (what[t] & 1)) {
                 const Unit &u = table[what[t] >> 1];
                 const int pair = u.pair[g];
-                if (pair != kNoPair)
-                    sums[(pair * p.ws + u.part) * 16 + i] = acc[0];
-                acc[0] = 0.f;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) {
+                    if (pair != kNoPair)
+                        sums[(pair * p.ws + u.part) * (16 * NW) + 16 * w + i] = acc[w][0];
+                    acc[w][0] = 0.f;
+                }
             }
             what[t] = unit < units ? unit * 2 + (tile + 1 == end) : -1;
             // the slot has been read before the next tile's rows are sent to it
@@ -425,24 +460,28 @@ __global__ __launch_bounds__(kThreads, 4) void nvfp4_moe_down_kernel(MoeFewParam
     // (the loads behind the last tile still write their registers)
 #pragma unroll
     for (int t = 0; t < D; ++t)
-        asm volatile("s_waitcnt vmcnt(0)" : "+v"(c[t]), "+v"(s[t])::"memory");
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+            asm volatile("s_waitcnt vmcnt(0)" : "+v"(c[t][w]), "+v"(s[t][w])::"memory");
     __syncthreads();
-    if (tid < p.n * 16) {
-        const int t = tid >> 4, r = tid & 15;
+    const int t = tid / (16 * NW), r = tid % (16 * NW);
+    if (t < p.n && r < p.rows && row0 + r < p.K) {
         float y = 0.f;
         for (int sl = 0; sl < p.k; ++sl) {
             const int q = t * p.k + sl;
             if (routes.expert[q] < 0)
                 continue;
-            const float *src = sums + firsts[q] * p.ws * 16 + r;
+            const float *src = sums + firsts[q] * p.ws * (16 * NW) + r;
             float o = src[0];
             for (int w = 1; w < p.ws; ++w)
-                o += src[w * 16];
+                o += src[w * (16 * NW)];
             y = __builtin_fmaf(mix[q], o, y);
         }
-        linear_out(p.e, t, rg * 16 + r, y);
+        linear_out(p.e, t, row0 + r, y);
     }
 }
+
+static_assert(kFewTokens * 32 <= kThreads, "a thread for each output of a workgroup");
 
 typedef void (*UpKernel)(MoeFewParams);
 
@@ -513,10 +552,17 @@ int nvfp4_launch_moe_few(const nvfp4_moe_few_args &a, hipStream_t stream)
     hipLaunchKernelGGL(up, dim3((unsigned)(most < cus ? most : cus)), dim3(kThreads), 0, stream, p);
     if (hipGetLastError() != hipSuccess)
         return NVFP4_ERR_LAUNCH;
+    // Rows in fours, so that every compute unit has a workgroup; up to K = 8192, 32 of them.
+    p.rows = (a.K + 4 * cus - 1) / (4 * cus) * 4;
+    const int nk = a.n * a.k, nw = (p.rows + 15) / 16;
     constexpr int kAhead = 6;
-    const int nk = a.n * a.k;
-    hipLaunchKernelGGL(nvfp4_moe_down_kernel<kAhead>, dim3((unsigned)(a.K / kRowsPerGroup)), dim3(kThreads),
-                       (unsigned)(kWaves * kAhead * 1024 + nk * p.ws * (sizeof(Unit) + 64) + nk * kFewTokens * 2),
-                       stream, p);
+    const dim3 grid((unsigned)((a.K + p.rows - 1) / p.rows));
+    const unsigned lds = (unsigned)(kWaves * kAhead * 1024 + nk * p.ws * (sizeof(Unit) + 64 * nw) + nk * kFewTokens * 2);
+    if (nw == 1)
+        hipLaunchKernelGGL((nvfp4_moe_down_kernel<1, kAhead>), grid, dim3(kThreads), lds, stream, p);
+    else if (nw == 2)
+        hipLaunchKernelGGL((nvfp4_moe_down_kernel<2, kAhead>), grid, dim3(kThreads), lds, stream, p);
+    else
+        return NVFP4_ERR_SHAPE;
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
 }

@@ -126,12 +126,12 @@ def int8_linear(**kw):
     (dict(n=-1), RANGE), (dict(n=(1 << 20) + 1), RANGE), (dict(N=0), RANGE), (dict(N=(1 << 30) + 1), RANGE), (dict(K=0), RANGE),
     (dict(K=72), SHAPE), (dict(K=131072), SHAPE), (dict(ldx=56), RANGE), (dict(ldy=39), RANGE), (dict(ldx=(1 << 22) + 16), SHAPE),
     (dict(ldx=68), ALIGN), (dict(xs=at(5), ldx=72), ALIGN), (dict(x=at(2) + 8), ALIGN), (dict(wq=at(0) + 8), ALIGN),
-    (dict(ws=at(1) + 2), ALIGN), (dict(xs=at(5) + 2), ALIGN), (dict(y=at(3) + 1), ALIGN), (dict(work=None), WORKSPACE),
-    (dict(size=255), WORKSPACE), (dict(work=at(4) + 8), ALIGN), (dict(ep=epilogue(up_bias=at(5))), RANGE),
+    (dict(ws=at(1) + 2), ALIGN), (dict(xs=at(5) + 2), ALIGN), (dict(y=at(3) + 1), ALIGN), (dict(n=20, work=None), WORKSPACE),
+    (dict(n=20, size=255), WORKSPACE), (dict(n=20, work=at(4) + 8), ALIGN), (dict(ep=epilogue(up_bias=at(5))), RANGE),
     (dict(ep=epilogue(preact=at(5), ldp=64)), RANGE), (dict(ep=epilogue(activation=7)), RANGE), (dict(ep=epilogue(out_dtype=2)), RANGE),
     (dict(ep=epilogue(residual=at(5), ldr=39)), RANGE), (dict(ep=epilogue(bias=at(5) + 1)), ALIGN), (dict(y=at(2)), OVERLAP),
     (dict(y=at(0)), OVERLAP), (dict(y=at(1) + 156), OVERLAP), (dict(xs=at(3)), OVERLAP), (dict(ep=epilogue(bias=at(3))), OVERLAP),
-    (dict(work=at(3)), OVERLAP), (dict(work=at(2)), OVERLAP), (dict(ep=epilogue(residual=at(4), ldr=40)), OVERLAP),
+    (dict(n=20, work=at(3)), OVERLAP), (dict(n=20, work=at(2)), OVERLAP), (dict(n=20, ep=epilogue(residual=at(4), ldr=40)), OVERLAP),
     (dict(ep=epilogue(residual=at(3) + 2, ldr=40)), OVERLAP)])
 def test_int8_linear_refuses(kw, status):
     assert int8_linear(**kw) == status
@@ -160,7 +160,9 @@ def test_int8_sizes_and_pack_refusals():
     assert pack(at(0), 4, 72, at(1), None) == SHAPE and pack(at(0), 0, 64, at(1), None) == RANGE
     assert pack(at(0), 4, 64, at(1) + 8, None) == ALIGN and pack(at(0), 4, 64, at(0) + 16, None) == OVERLAP
     need = nv.int8_linear_workspace_bytes
-    assert need(4, 40, 64) == 512 and need(4, 40, 64, False) == 0 and need(0, 40, 64) == 0 and need(4, 40, 72) == 0
+    assert need(20, 40, 64) == 20 * 64 + 256 and need(20, 40, 64, False) == 0 and need(0, 40, 64) == 0 and need(20, 40, 72) == 0
+    # a decode launch quantises few activations itself
+    assert need(4, 40, 64) == need(8, 40, 6144) == 0 and need(8, 40, 6160) == 8 * 6160 + 128 + 256 and need(9, 40, 64) == 9 * 64 + 192 + 256
     assert need(17, 40, 8192, False) > 0           # K parts: one row tile alone
 
 

@@ -266,7 +266,7 @@ def test_refusals():
         (ValueError, lambda: nv.int8_linear(w, X, bias=torch.zeros(40, device="cuda", requires_grad=True))),
         (ValueError, lambda: nv.int8_quantize(X.clone().requires_grad_())), (TypeError, lambda: nv.int8_quantize(q)),
         (nv.Nvfp4Error, lambda: nv.int8_quantize(X[:, :40])), (nv.Nvfp4Error, lambda: nv.int8_quantize(X[:, 4:20])),
-        (nv.Nvfp4Error, lambda: nv.int8_linear(w, X, out=torch.empty(5, 40, device="cuda"), residual=None, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))),
+        (nv.Nvfp4Error, lambda: nv.int8_linear(w, randn((20, 64), 1), workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))),
         (ValueError, lambda: nv.Int8Weight.from_int8(codes((4, 40), 1), torch.ones(4, device="cuda"))),
         (ValueError, lambda: nv.Int8Weight.from_int8(codes((1, 131072), 1), torch.ones(1, device="cuda"))),
         (ValueError, lambda: nv.Int8Weight.from_int8(codes((4, 64), 1), torch.ones(3, device="cuda"))),
