@@ -220,6 +220,22 @@ __device__ __forceinline__ u16x4 to_bf16x4(const f32x4 v)
     return u16x4{f32_to_bf16_bits(v[0]), f32_to_bf16_bits(v[1]), f32_to_bf16_bits(v[2]), f32_to_bf16_bits(v[3])};
 }
 
+// v as the sum of two bf16 values, 16 significant bits, at p and p + at: an operand
+// of a further product.  In one bf16 it would add as much to the result's error as
+// the rounding of a bf16 result does.  (Infinities and NaN are in the first alone.)
+__device__ __forceinline__ float bf16_rest(float v, uint16_t high)
+{
+    return (high & 0x7F80) == 0x7F80 ? 0.f : v - bf16_bits_to_f32(high);
+}
+
+__device__ __forceinline__ void split_bf16(uint16_t *p, long long at, const f32x4 v)
+{
+    const u16x4 high = to_bf16x4(v);
+    *reinterpret_cast<u16x4 *>(p) = high;
+    *reinterpret_cast<u16x4 *>(p + at) = to_bf16x4(f32x4{bf16_rest(v[0], high[0]), bf16_rest(v[1], high[1]),
+                                                         bf16_rest(v[2], high[2]), bf16_rest(v[3], high[3])});
+}
+
 __device__ __forceinline__ void store_any4(void *p, long long i, int f32, const f32x4 v)
 {
     if (f32)

@@ -77,7 +77,9 @@ __device__ __forceinline__ f32x2 scales2(u32 w)
 // rows of X are gathered through `pair`, by the vector offset of the LDS-direct
 // loads (no copy of X in the experts' order: 168 MB of it for 1500 tokens of
 // 5120 columns with 8 experts each); 2: X's rows are in the experts' order
-// themselves.
+// themselves, values between two products in two bf16 parts (split_bf16), of which
+// the second lies a.K columns behind the first: a weight operand is dequantised
+// once for both.
 //
 // LDS layout of the slice: token t's 16-byte chunk c (8 columns) at
 //     (t / 4) * kQuad + (t % 4) * 256 + (c ^ (t % 4)) * 16.
@@ -99,7 +101,9 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
 {
     constexpr int BM = TB * 16;
     constexpr int kThreads = 64 * RW * KG;
-    constexpr int kSlice = BM / 4 * kQuad;         // LDS bytes of a step's token slice
+    constexpr int kPlanes = GROUP == 2 ? 2 : 1;    // parts of a value of X
+    constexpr int kPlane = BM / 4 * kQuad;
+    constexpr int kSlice = kPlanes * kPlane;       // LDS bytes of a step's token slice
     constexpr int kBuf = kSlice + RW * RG * 128;   // and of the waves' scales
     constexpr int XL = BM / 4 / RW;                // quads a wave stages
     const int tid = threadIdx.x;
@@ -171,7 +175,7 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
 #pragma unroll
         for (int u = 0; u < XL; ++u) {
             const int t = tok0 + (wave * XL + u) * 4, live = min(4, tok1 - t);
-            xrsrc[u] = uniform(live > 0 ? buffer_rsrc(p.X + t * p.ldx, (unsigned)(((live - 1) * p.ldx + p.K) * 2))
+            xrsrc[u] = uniform(live > 0 ? buffer_rsrc(p.X + t * p.ldx, (unsigned)(((live - 1) * p.ldx + kPlanes * p.K) * 2))
                                         : buffer_rsrc(p.X, 0u));
         }
     }
@@ -196,6 +200,12 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
 #pragma unroll
             for (int u = 0; u < XL; ++u)
                 load_lds_b128(xrsrc[u], xv, ldsb + buf + u * kQuad);
+            if constexpr (kPlanes == 2) {
+                const unsigned xl = in ? xoff + s * (kTileK * 2) + p.K * 2 : kOutOfRange;
+#pragma unroll
+                for (int u = 0; u < XL; ++u)
+                    load_lds_b128(xrsrc[u], xl, ldsb + buf + kPlane + u * kQuad);
+            }
         }
         if (lane < 8 * RG)   // the wave's 128 RG bytes of scales
             load_lds_b128(srsrc, soff + s * 128, ldss + buf);
@@ -281,14 +291,17 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
             for (int t = 0; t < TP; ++t) {
                 if (GROUP && TP > 1 && t >= blocks)
                     break;
-                const bf16x8 a = *reinterpret_cast<const bf16x8 *>(buf + x0 + t * 8 * kQuad + 64 * j);
-                const bf16x8 d = *reinterpret_cast<const bf16x8 *>(buf + x1 + t * 8 * kQuad + 64 * j);
 #pragma unroll
-                for (int r = 0; r < RP; ++r)
-                    acc[r][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j & 1][r][0], a, acc[r][t], 0, 0, 0);
+                for (int q = 0; q < kPlanes; ++q) {
+                    const bf16x8 a = *reinterpret_cast<const bf16x8 *>(buf + q * kPlane + x0 + t * 8 * kQuad + 64 * j);
+                    const bf16x8 d = *reinterpret_cast<const bf16x8 *>(buf + q * kPlane + x1 + t * 8 * kQuad + 64 * j);
 #pragma unroll
-                for (int r = 0; r < RP; ++r)
-                    acc[r][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j & 1][r][1], d, acc[r][t], 0, 0, 0);
+                    for (int r = 0; r < RP; ++r)
+                        acc[r][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j & 1][r][0], a, acc[r][t], 0, 0, 0);
+#pragma unroll
+                    for (int r = 0; r < RP; ++r)
+                        acc[r][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j & 1][r][1], d, acc[r][t], 0, 0, 0);
+                }
             }
             __builtin_amdgcn_sched_barrier(0);   // one substep's operands live at a time
         });
@@ -411,7 +424,7 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
                         y[v] = activate(z[v], decltype(act)::value) * u[v];
-                    store_any4(p.e.out, (long long)tok * p.e.ldo + r, 0, y);
+                    split_bf16(static_cast<uint16_t *>(p.e.out) + (long long)tok * p.e.ldo + r, p.e.N, y);
                 }
             });
             continue;

@@ -13,7 +13,8 @@ struct nvfp4_moe_order {
 
 struct nvfp4_moe_gemm_args {
     int mode;                     // 1 gated, 2 transposed, 0 linear, as nvfp4_fused_gemm_args
-    bool gather;                  // X's rows are the tokens; else the rows in the experts' order
+    bool gather;                  // X's rows are the tokens; else the rows in the experts' order, each
+                                  // value in two bf16 parts, K columns apart (split_bf16)
     const uint8_t *codes, *scales;
     long long cstride, sstride;   // bytes of an expert's
     const uint16_t *X;

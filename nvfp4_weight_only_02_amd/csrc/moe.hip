@@ -453,9 +453,9 @@ __global__ __launch_bounds__(256) void nvfp4_moe_combine_kernel(nvfp4_epi_params
 
 // One workgroup a pair: with d = dY . Wd (for weight one), the weight's gradient
 // is the dot product of d with h = act(G) U, unrounded; dG = w d U act'(G) and dU
-// = w d act(G), times their tensor scales, are rounded to bf16 as operands of the
-// next product (dX is then off by 2.3e-3 of its norm, of which its own rounding
-// is 1.7e-3).
+// = w d act(G), times their tensor scales, become operands of the next product in
+// two bf16 parts (in one, dX was off by 2.3e-3 of its norm, of which its own
+// rounding is 1.7e-3).
 __global__ __launch_bounds__(256) void nvfp4_moe_grad_kernel(const float *d, const float *preact, const int *position,
                                                              const int *experts, const float *weights, const float *gscale,
                                                              float *dweights, uint16_t *dz, long long ldp, int E, int F, int act)
@@ -470,7 +470,7 @@ __global__ __launch_bounds__(256) void nvfp4_moe_grad_kernel(const float *d, con
     const int e = experts[q];
     const float w = weights[q], gg = gscale[e], gu = gscale[E + e];
     const float *src = preact + (long long)row * ldp;
-    uint16_t *dst = dz + (long long)row * 2 * F;
+    uint16_t *dst = dz + (long long)row * 4 * F;
     float dot = 0.f;
     for (int c = tid * 4; c < F; c += 1024) {
         const f32x4 dh = *reinterpret_cast<const f32x4 *>(d + (long long)row * F + c);
@@ -485,8 +485,8 @@ __global__ __launch_bounds__(256) void nvfp4_moe_grad_kernel(const float *d, con
             du[j] = w * dh[j] * a * gu;
         }
         if (dz) {
-            *reinterpret_cast<u16x4 *>(dst + gated_row(c, 0)) = to_bf16x4(dg);
-            *reinterpret_cast<u16x4 *>(dst + gated_row(c, 1)) = to_bf16x4(du);
+            split_bf16(dst + gated_row(c, 0), 2LL * F, dg);
+            split_bf16(dst + gated_row(c, 1), 2LL * F, du);
         }
     }
     if (!dweights)
@@ -607,7 +607,7 @@ Bytes expert_bytes(const nvfp4_experts *w, bool transposed)
 size_t forward_bytes(int n, int k, const nvfp4_experts *w)
 {
     const int by_pairs = kChunkPairs / k, m = n < by_pairs ? n : by_pairs, pairs = m * k;
-    return order_bytes(pairs, w->E) + round256((size_t)pairs * w->F * 2) + round256((size_t)pairs * w->K * 4);
+    return order_bytes(pairs, w->E) + round256((size_t)pairs * w->F * 4) + round256((size_t)pairs * w->K * 4);
 }
 
 size_t backward_bytes(int n, int k, const nvfp4_experts *w, bool dx, bool copy)
@@ -617,7 +617,7 @@ size_t backward_bytes(int n, int k, const nvfp4_experts *w, bool dx, bool copy)
     if (copy)
         b += round256((size_t)m * w->K * 2);
     if (dx)
-        b += round256((size_t)pairs * w->F * 4) + round256((size_t)pairs * w->K * 4);
+        b += round256((size_t)pairs * w->F * 8) + round256((size_t)pairs * w->K * 4);
     return b;
 }
 
@@ -801,7 +801,7 @@ int nvfp4_moe(const nvfp4_experts *w, const uint16_t *X, int64_t ldx, const int3
         const Order o = order_at(ws, pairs, E);
         ws += order_bytes(pairs, E);
         uint16_t *h = reinterpret_cast<uint16_t *>(ws);
-        float *rows = reinterpret_cast<float *>(ws + round256((size_t)pairs * F * 2));
+        float *rows = reinterpret_cast<float *>(ws + round256((size_t)pairs * F * 4));
         st = launch_sort(o, experts + (size_t)t0 * k, pairs, E, tokens, s);
         if (st != NVFP4_OK)
             break;
@@ -824,7 +824,7 @@ int nvfp4_moe(const nvfp4_experts *w, const uint16_t *X, int64_t ldx, const int3
         a.gscale = w->gscale;
         a.up_gscale = w->gscale + E;
         a.order = {o.tile, o.offset, o.pair};
-        a.epi = plain_out(h, F, false, F);
+        a.epi = plain_out(h, 2 * F, false, F);
         a.epi.flags |= ep.activation;
         if (ep.preact) {
             a.epi.preact = ep.preact + (size_t)t0 * k * ep.ldp;
@@ -840,7 +840,7 @@ int nvfp4_moe(const nvfp4_experts *w, const uint16_t *X, int64_t ldx, const int3
         a.cstride = (long long)b.d_codes;
         a.sstride = (long long)b.d_scales;
         a.X = h;
-        a.ldx = F;
+        a.ldx = 2 * F;
         a.K = F;
         a.row_groups = K / kRowsPerGroup;
         a.gscale = w->gscale + 2 * (size_t)E;
@@ -938,7 +938,7 @@ int nvfp4_moe_backward(const nvfp4_experts *wt, const void *dY, int dy_dtype, in
             ld = K;
         }
         uint16_t *dz = dX ? reinterpret_cast<uint16_t *>(ws) : nullptr;
-        ws += dX ? round256((size_t)pairs * F * 4) : 0;
+        ws += dX ? round256((size_t)pairs * F * 8) : 0;
         float *rows = reinterpret_cast<float *>(ws);
         const int *ids = experts + (size_t)t0 * k;
         st = launch_sort(o, ids, pairs, E, tokens, s);
@@ -978,7 +978,7 @@ int nvfp4_moe_backward(const nvfp4_experts *wt, const void *dY, int dy_dtype, in
         a.cstride = (long long)b.gu_codes;
         a.sstride = (long long)b.gu_scales;
         a.X = dz;
-        a.ldx = 2 * (long long)F;
+        a.ldx = 4 * (long long)F;
         a.K = 2 * F;
         a.row_groups = K / kRowsPerGroup;
         a.gscale = nullptr;   // dz carries the tensor scales

@@ -28,7 +28,8 @@ struct MoeFewParams {
     const uint16_t *X;
     const int *experts;           // [n][k]
     const float *weights;         // [n][k]
-    uint16_t *h;                  // [n k][128 Td], columns of a tile in the lanes' order
+    uint16_t *h;                  // [n k][Td][2][128]: the two bf16 parts of a value (split_bf16),
+                                  // columns of a tile in the lanes' order
     int ldx, n, k, E, F, K, act;
     int T, Td, P;                 // 128-column tiles of K and of F, pairs of row groups of a gated weight
     int ws, tpw;                  // parts of an expert's F in the down projection, and the tiles of each
@@ -148,9 +149,10 @@ __device__ __forceinline__ void tile_product(f32x4 &acc, const u32x4 c, const u3
 
 // Position of column r of a 128-column tile in the order of the lanes' operands:
 // lane group g of block b takes columns 16 b + 4 g + 0 .. 3, eight blocks in turn.
+// Each tile's columns come twice: the values' first parts, then the second ones.
 __device__ __forceinline__ int operand_order(int r)
 {
-    return (r & ~127) + 32 * ((r >> 2) & 3) + 4 * ((r >> 4) & 7) + (r & 3);
+    return 2 * (r & ~127) + 32 * ((r >> 2) & 3) + 4 * ((r >> 4) & 7) + (r & 3);
 }
 
 // Gate and up: the row groups of all chosen experts as one sequence, gate and up
@@ -257,12 +259,14 @@ __global__ __launch_bounds__(kThreads) void nvfp4_moe_up_kernel(MoeFewParams p)
                 for (int sl = 0; sl < p.k; ++sl) {
                     if (routes.expert[t * p.k + sl] != e)
                         continue;
-                    uint16_t *row = p.h + (long long)(t * p.k + sl) * (p.Td * kTileK);
-                    row[operand_order(pr * 16 + i)] = f32_to_bf16_bits(hv);
+                    uint16_t *row = p.h + (long long)(t * p.k + sl) * (p.Td * 2 * kTileK);
+                    const uint16_t high = f32_to_bf16_bits(hv);
+                    row[operand_order(pr * 16 + i)] = high;
+                    row[operand_order(pr * 16 + i) + kTileK] = f32_to_bf16_bits(bf16_rest(hv, high));
                     // the columns behind the last one, up to a whole tile
                     if (pr == p.P - 1)
                         for (int r = p.P * 16 + i; r < p.Td * kTileK; r += 16)
-                            row[operand_order(r)] = 0;
+                            row[operand_order(r)] = row[operand_order(r) + kTileK] = 0;
                     break;
                 }
             }
@@ -285,8 +289,9 @@ constexpr int kNoPair = 0xFFFF;
 // (of which the last may use fewer, and which need not begin with a row group).
 // Its waves take units from a queue: an expert with up to four of its tokens (an
 // expert with more has several units, whose weights come from cache after the
-// first; four tokens cost the matrix instruction one component and 1 KiB of LDS a
-// tile), or a part of its F where a token has few experts.  A unit's tiles of
+// first; four tokens, whose values are two bf16 parts each, cost the matrix
+// instruction two components and 2 KiB of LDS a tile), or a part of its F where a
+// token has few experts.  A unit's tiles of
 // weights go to registers and its tokens' rows straight to LDS, D tiles ahead:
 // always the same loads a tile in the same order, so that the wait for a tile is
 // the constant count of the newer ones, across the units' ends too.  The sums of
@@ -313,10 +318,11 @@ __global__ __launch_bounds__(kThreads, 4) void nvfp4_moe_down_kernel(MoeFewParam
     __shared__ float mix[kMaxPairs];              // of each pair: its weight times the tensor scale
     __shared__ int queue, count;                  // next unit, units
     extern __shared__ __align__(1024) char dynamic[];
-    char *rows = dynamic;                                                      // [W][D] KiB
-    Unit *table = reinterpret_cast<Unit *>(dynamic + W * D * 1024);            // [n k ws]
+    char *rows = dynamic;                                                      // [W][D][2] KiB
+    Unit *table = reinterpret_cast<Unit *>(dynamic + W * D * 2048);            // [n k ws]
     float *sums = reinterpret_cast<float *>(table + nk * p.ws);                // [n k][ws][16 NW]
-    unsigned short *pairs = reinterpret_cast<unsigned short *>(sums + nk * p.ws * 16 * NW);   // [n k][16]
+    unsigned short *pairs = reinterpret_cast<unsigned short *>(rows);          // [n k][16], before the rows come
+    static_assert(W * D * 2048 >= kMaxPairs * kFewTokens * 2, "the pairs fit the rows");
     {
         const int e = load_choice(p);
         const float w = tid < nk ? p.weights[tid] : 0.f;
@@ -359,8 +365,8 @@ __global__ __launch_bounds__(kThreads, 4) void nvfp4_moe_down_kernel(MoeFewParam
     }
     const int units = __builtin_amdgcn_readfirstlane(count);
     const unsigned tb = p.Td * 1024u, sb = p.Td * 128u;
-    const u32x4 hrsrc = uniform(buffer_rsrc(p.h, (unsigned)(nk * p.Td * kTileK * 2)));
-    const unsigned slots = lds_address(rows) + wave * (D * 1024);
+    const u32x4 hrsrc = uniform(buffer_rsrc(p.h, (unsigned)(nk * p.Td * kTileK * 4)));
+    const unsigned slots = lds_address(rows) + wave * (D * 2048);
 
     // This lane's row of each window: its offsets within an expert's codes and scales.
     unsigned coff[NW], soff[NW];
@@ -375,7 +381,7 @@ __global__ __launch_bounds__(kThreads, 4) void nvfp4_moe_down_kernel(MoeFewParam
     u32x2 s[D][NW];
     int unit = wave, tile = 0, end = 0;   // of the tile that is loaded next
     u32x4 crsrc, srsrc;
-    unsigned row;                         // this lane's 16 bytes of its row of the unit's h
+    unsigned high, low;                   // this lane's 16 bytes of its row of the unit's h, of each part
     auto begin = [&]() {
         const bool in = unit < units;
         const Unit &u = table[in ? unit : 0];
@@ -386,13 +392,17 @@ __global__ __launch_bounds__(kThreads, 4) void nvfp4_moe_down_kernel(MoeFewParam
         const unsigned groups = p.K / kRowsPerGroup;
         crsrc = uniform(buffer_rsrc(p.d_codes + (long long)expert * groups * tb, in ? groups * tb : 0u));
         srsrc = uniform(buffer_rsrc(p.d_scales + (long long)expert * groups * sb, in ? groups * sb : 0u));
-        // row g's chunk i ^ g goes to slot i of the row: the operand's reads (chunk
-        // 4 g + q of row i / 4) then fall into 16 different 16-byte slots
-        row = in && pair != kNoPair ? (unsigned)(pair * p.Td * (kTileK * 2) + 16 * (i ^ g)) : kOutOfRange;
+        // chunk c of token g's part j goes to slot c ^ (2 g + j) of its 256 bytes: the
+        // operand's reads (chunk 4 g + q of part i % 2 of token i / 4) then fall into
+        // eight different 16-byte slots a lane group
+        const unsigned row = pair * p.Td * (kTileK * 4);
+        high = in && pair != kNoPair ? row + 16 * (i ^ 2 * g) : kOutOfRange;
+        low = in && pair != kNoPair ? row + 256 + 16 * (i ^ (2 * g + 1)) : kOutOfRange;
     };
     auto load = [&](auto tc) {
         constexpr int t = decltype(tc)::value;
-        load_lds_b128(hrsrc, row + tile * (kTileK * 2), slots + t * 1024);
+        load_lds_b128(hrsrc, high + tile * (kTileK * 4), slots + t * 2048);
+        load_lds_b128(hrsrc, low + tile * (kTileK * 4), slots + t * 2048 + 1024);
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
             s[t][w] = buffer_load_b64_nt(srsrc, soff[w] + tile * 128);
@@ -409,7 +419,8 @@ __global__ __launch_bounds__(kThreads, 4) void nvfp4_moe_down_kernel(MoeFewParam
         unit = __builtin_amdgcn_readfirstlane(next);
         begin();
     };
-    const char *mine = rows + wave * (D * 1024) + (i >> 2) * 256;
+    const char *mine = rows + wave * (D * 2048) + (i & 1) * 1024 + (i >> 2) * 256;
+    const int turn = 2 * (i >> 2) + (i & 1);
     f32x4 acc[NW];
 #pragma unroll
     for (int w = 0; w < NW; ++w)
@@ -426,28 +437,28 @@ __global__ __launch_bounds__(kThreads, 4) void nvfp4_moe_down_kernel(MoeFewParam
         static_for<D>([&](auto tc) {
             constexpr int t = decltype(tc)::value;
             if constexpr (NW == 1)
-                asm volatile("s_waitcnt vmcnt(%2)" : "+v"(c[t][0]), "+v"(s[t][0]) : "n"(3 * (D - 1)) : "memory");
+                asm volatile("s_waitcnt vmcnt(%2)" : "+v"(c[t][0]), "+v"(s[t][0]) : "n"(4 * (D - 1)) : "memory");
             else
                 asm volatile("s_waitcnt vmcnt(%4)" : "+v"(c[t][0]), "+v"(s[t][0]), "+v"(c[t][1]), "+v"(s[t][1])
-                             : "n"(5 * (D - 1)) : "memory");
+                             : "n"(6 * (D - 1)) : "memory");
             u32x2 x[8];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const u32x4 v = *reinterpret_cast<const u32x4 *>(mine + t * 1024 + ((4 * g + q) ^ (i >> 2)) * 16);
+                const u32x4 v = *reinterpret_cast<const u32x4 *>(mine + t * 2048 + ((4 * g + q) ^ turn) * 16);
                 x[2 * q] = u32x2{v[0], v[1]};
                 x[2 * q + 1] = u32x2{v[2], v[3]};
             }
 #pragma unroll
             for (int w = 0; w < NW; ++w)
-                tile_product<1>(acc[w], c[t][w], s[t][w], x);
+                tile_product<2>(acc[w], c[t][w], s[t][w], x);
             if (what[t] >= 0 && (what[t] & 1)) {
                 const Unit &u = table[what[t] >> 1];
                 const int pair = u.pair[g];
 #pragma unroll
                 for (int w = 0; w < NW; ++w) {
                     if (pair != kNoPair)
-                        sums[(pair * p.ws + u.part) * (16 * NW) + 16 * w + i] = acc[w][0];
-                    acc[w][0] = 0.f;
+                        sums[(pair * p.ws + u.part) * (16 * NW) + 16 * w + i] = acc[w][0] + acc[w][1];
+                    acc[w][0] = acc[w][1] = 0.f;
                 }
             }
             what[t] = unit < units ? unit * 2 + (tile + 1 == end) : -1;
@@ -483,12 +494,12 @@ __global__ __launch_bounds__(kThreads, 4) void nvfp4_moe_down_kernel(MoeFewParam
 
 static_assert(kFewTokens * 32 <= kThreads, "a thread for each output of a workgroup");
 
-typedef void (*UpKernel)(MoeFewParams);
+typedef void (*FewKernel)(MoeFewParams);
 
 template <int NV, int... MT>
-UpKernel pick_up(int mt, std::integer_sequence<int, MT...>)
+FewKernel pick_up(int mt, std::integer_sequence<int, MT...>)
 {
-    UpKernel k = nullptr;
+    FewKernel k = nullptr;
     ((mt == MT + 1 ? (void)(k = nvfp4_moe_up_kernel<MT + 1, NV>) : (void)0), ...);
     return k;
 }
@@ -512,7 +523,7 @@ bool nvfp4_moe_is_few(int n, int K)
 
 size_t nvfp4_moe_few_bytes(int n, int k, int F)
 {
-    return (size_t)n * k * k_tiles(F) * kTileK * 2;
+    return (size_t)n * k * k_tiles(F) * kTileK * 4;
 }
 
 int nvfp4_launch_moe_few(const nvfp4_moe_few_args &a, hipStream_t stream)
@@ -547,7 +558,7 @@ int nvfp4_launch_moe_few(const nvfp4_moe_few_args &a, hipStream_t stream)
     p.e = a.epi;
     const int mt = (p.T + kWaves - 1) / kWaves;
     constexpr auto mts = std::make_integer_sequence<int, kMaxTilesPerWave>{};
-    const UpKernel up = a.n <= 4 ? pick_up<1>(mt, mts) : (a.n <= 8 ? pick_up<2>(mt, mts) : pick_up<4>(mt, mts));
+    const FewKernel up = a.n <= 4 ? pick_up<1>(mt, mts) : (a.n <= 8 ? pick_up<2>(mt, mts) : pick_up<4>(mt, mts));
     const long long most = (long long)(a.n * a.k < a.E ? a.n * a.k : a.E) * p.P;
     hipLaunchKernelGGL(up, dim3((unsigned)(most < cus ? most : cus)), dim3(kThreads), 0, stream, p);
     if (hipGetLastError() != hipSuccess)
@@ -555,14 +566,16 @@ int nvfp4_launch_moe_few(const nvfp4_moe_few_args &a, hipStream_t stream)
     // Rows in fours, so that every compute unit has a workgroup; up to K = 8192, 32 of them.
     p.rows = (a.K + 4 * cus - 1) / (4 * cus) * 4;
     const int nk = a.n * a.k, nw = (p.rows + 15) / 16;
-    constexpr int kAhead = 6;
-    const dim3 grid((unsigned)((a.K + p.rows - 1) / p.rows));
-    const unsigned lds = (unsigned)(kWaves * kAhead * 1024 + nk * p.ws * (sizeof(Unit) + 64 * nw) + nk * kFewTokens * 2);
-    if (nw == 1)
-        hipLaunchKernelGGL((nvfp4_moe_down_kernel<1, kAhead>), grid, dim3(kThreads), lds, stream, p);
-    else if (nw == 2)
-        hipLaunchKernelGGL((nvfp4_moe_down_kernel<2, kAhead>), grid, dim3(kThreads), lds, stream, p);
-    else
+    if (nw > 2)
         return NVFP4_ERR_SHAPE;
+    const dim3 grid((unsigned)((a.K + p.rows - 1) / p.rows));
+    // Six tiles ahead where the sums leave the LDS for it (of 160 KiB, of which the
+    // kernel's own arrays take less than 10), else four.
+    const unsigned units = (unsigned)(nk * p.ws * (sizeof(Unit) + 64 * nw));
+    const bool six = units + kWaves * 6 * 2048 <= 150 * 1024;
+    const unsigned lds = units + kWaves * (six ? 6 : 4) * 2048;
+    const FewKernel down = nw == 1 ? (six ? nvfp4_moe_down_kernel<1, 6> : nvfp4_moe_down_kernel<1, 4>)
+                                  : (six ? nvfp4_moe_down_kernel<2, 6> : nvfp4_moe_down_kernel<2, 4>);
+    hipLaunchKernelGGL(down, grid, dim3(kThreads), lds, stream, p);
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
 }

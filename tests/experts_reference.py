@@ -87,10 +87,17 @@ def _live(experts, E):
     return (experts >= 0) & (experts < E)
 
 
+def _kept(v, e):
+    """Bound of rows v, known within e, as operands of the next product."""
+    a = np.abs(v) + e
+    return e + 2.0 ** -12 * a + 2.0 ** -25 * a.max(1, keepdims=True)
+
+
 def moe(X, Wg, Wu, Wd, experts, weights, kind="silu", residual=None, out_f32=False):
-    """(Y, bound): h rounded to bf16 and its down projection, k weighted terms
-    (a weight is multiplied by the tensor scale first: 3 steps), the residual, the
-    last rounding."""
+    """(Y, bound): h kept to 11 bits at least (half a step of 2^-11 relative, or of
+    2^-24 of the row's largest) and its down projection, k weighted terms (a weight
+    is multiplied by the tensor scale first: 3 steps), the residual, the last
+    rounding."""
     n, k = experts.shape
     F, K = Wg.shape[1:]
     y, b, m = np.zeros((n, K)), np.zeros((n, K)), np.zeros((n, K))
@@ -99,7 +106,8 @@ def moe(X, Wg, Wu, Wd, experts, weights, kind="silu", residual=None, out_f32=Fal
         t, s = np.nonzero(ok & (experts == e))
         if not len(t):
             continue
-        h, eh = R.gated(X[t], Wg[e], Wu[e], kind=kind)
+        h, eh = R.gated(X[t], Wg[e], Wu[e], kind=kind, out_f32=True)
+        eh = _kept(h, eh)
         o = h @ Wd[e].T
         eo = eh @ np.abs(Wd[e]).T + (F + 32) * STEP * ((np.abs(h) + eh) @ np.abs(Wd[e]).T)
         w = weights[t, s][:, None]
@@ -141,8 +149,9 @@ def moe_grads(X, Wg, Wu, Wd, experts, weights, dY, kind="silu", dy_f32=False):
         dG, dU = weights[t, s][:, None] * dh * u * d, weights[t, s][:, None] * dh * a
         eG = w * (eh * np.abs(u * d) + (np.abs(dh) + eh) * (np.abs(u) * ed + ru * np.abs(d) + ru * ed)) + 6 * STEP * np.abs(dG)
         eU = w * (eh * np.abs(a) + (np.abs(dh) + eh) * ea) + 6 * STEP * np.abs(dU)
-        for v, ev, W in ((dG, eG, Wg[e]), (dU, eU, Wu[e])):
-            ev = ev + R.HALF_BF16 * (np.abs(v) + ev)
+        kept = _kept(np.hstack((dG, dU)), np.hstack((eG, eU)))
+        F = dG.shape[1]
+        for v, ev, W in ((dG, kept[:, :F], Wg[e]), (dU, kept[:, F:], Wu[e])):
             p = (np.abs(v) + ev) @ np.abs(W)
             np.add.at(dx, t, v @ W)
             np.add.at(bx, t, ev @ np.abs(W) + (2 * F + 32) * STEP * p)
