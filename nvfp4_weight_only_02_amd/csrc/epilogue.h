@@ -220,20 +220,59 @@ __device__ __forceinline__ u16x4 to_bf16x4(const f32x4 v)
     return u16x4{f32_to_bf16_bits(v[0]), f32_to_bf16_bits(v[1]), f32_to_bf16_bits(v[2]), f32_to_bf16_bits(v[3])};
 }
 
-// v as the sum of two bf16 values, 16 significant bits, at p and p + at: an operand
-// of a further product.  In one bf16 it would add as much to the result's error as
-// the rounding of a bf16 result does.  (Infinities and NaN are in the first alone.)
+// What is left of v, rounded to the bf16 number `high`: both hold 16 significant bits
+// of v, an operand of a further product.  One bf16 number would add as much to the
+// result's error as the rounding of a bf16 result does.  (Infinities and NaN are in
+// the first alone.)
 __device__ __forceinline__ float bf16_rest(float v, uint16_t high)
 {
     return (high & 0x7F80) == 0x7F80 ? 0.f : v - bf16_bits_to_f32(high);
 }
 
-__device__ __forceinline__ void split_bf16(uint16_t *p, long long at, const f32x4 v)
+// The same for many rows, in half the matrix instructions: a block of values of a row
+// as fp16 with a common exponent, 11 significant bits of those not far below its
+// largest, whose fp16 is between 2^14 and 2^15.
+
+// Bits of the largest magnitude.
+__device__ __forceinline__ u32 top_bits(const f32x4 v)
 {
-    const u16x4 high = to_bf16x4(v);
-    *reinterpret_cast<u16x4 *>(p) = high;
-    *reinterpret_cast<u16x4 *>(p + at) = to_bf16x4(f32x4{bf16_rest(v[0], high[0]), bf16_rest(v[1], high[1]),
-                                                         bf16_rest(v[2], high[2]), bf16_rest(v[3], high[3])});
+    u32 m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        m = max(m, __builtin_bit_cast(u32, fabsf(v[j])));
+    return m;
+}
+
+// The largest of L (8 or 16) lanes, in all of them; lanes that are switched off count as none.
+template <int L>
+__device__ __forceinline__ u32 row_max(u32 m)
+{
+    static_assert(L == 8 || L == 16, "lanes of a row");
+    m = max(m, (u32)__builtin_amdgcn_update_dpp((int)m, (int)m, 0xB1, 0xF, 0xF, false));    // lane ^ 1
+    m = max(m, (u32)__builtin_amdgcn_update_dpp((int)m, (int)m, 0x4E, 0xF, 0xF, false));    // lane ^ 2
+    m = max(m, (u32)__builtin_amdgcn_update_dpp((int)m, (int)m, 0x141, 0xF, 0xF, false));   // 7 - lane of eight
+    if (L == 16)
+        m = max(m, (u32)__builtin_amdgcn_update_dpp((int)m, (int)m, 0x140, 0xF, 0xF, false));   // 15 - lane of sixteen
+    return m;
+}
+
+constexpr int kNoExponent = -1000;   // of a block of zeros
+
+// (beside an infinity or NaN the finite values of the block do not matter)
+__device__ __forceinline__ int block_exponent(u32 top)
+{
+    if (top == 0)
+        return kNoExponent;
+    return top >= 0x7F800000u ? 113 : __builtin_amdgcn_frexp_expf(__builtin_bit_cast(float, top)) - 15;
+}
+
+__device__ __forceinline__ void store_block(uint16_t *p, const f32x4 v, int exponent)
+{
+    u16x4 h;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        h[j] = __builtin_bit_cast(uint16_t, (_Float16)__builtin_amdgcn_ldexpf(v[j], -exponent));
+    *reinterpret_cast<u16x4 *>(p) = h;
 }
 
 __device__ __forceinline__ void store_any4(void *p, long long i, int f32, const f32x4 v)

@@ -28,6 +28,9 @@ struct GroupedGemmParams : FusedGemmParams {
     const int *pair;              // [rows]: the pair of each row; the token of pair q is q / k
     int k, xrows;                 // GROUP 1: X's rows are the tokens
     const float *gscale, *up_gscale;   // [E], or null (1)
+    const int *xexp;              // GROUP 2: exponents of X's rows, [rows][nexp]
+    int *hexp;                    // MODE 1: of the rows it writes, likewise
+    int nexp;                     // an even number
     long long cstride, sstride;   // bytes of an expert's codes and scales
 };
 
@@ -49,6 +52,24 @@ __device__ __forceinline__ u32x2 dequant4(u32 w, f32x2 sa, f32x2 sb)
     const bf16x2 x = {(__bf16)(a[0] * sa[0]), (__bf16)(a[1] * sa[1])};
     const bf16x2 y = {(__bf16)(b[0] * sb[0]), (__bf16)(b[1] * sb[1])};
     return u32x2{__builtin_bit_cast(u32, x), __builtin_bit_cast(u32, y)};
+}
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+// The same in fp16 (between 2^-10 and 2688: exact too), scales s.
+template <int H>
+__device__ __forceinline__ u32x2 dequant4(u32 w, f16x2 sa, f16x2 sb)
+{
+    const f16x2 a = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2 * H));
+    const f16x2 b = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2 * H + 1));
+    return u32x2{__builtin_bit_cast(u32, a * sa), __builtin_bit_cast(u32, b * sb)};
+}
+
+template <bool H>
+__device__ __forceinline__ f16x2 half_scales2(u32 w)
+{
+    return __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w, 1.0f, H));
 }
 
 template <bool H>
@@ -77,9 +98,14 @@ __device__ __forceinline__ f32x2 scales2(u32 w)
 // rows of X are gathered through `pair`, by the vector offset of the LDS-direct
 // loads (no copy of X in the experts' order: 168 MB of it for 1500 tokens of
 // 5120 columns with 8 experts each); 2: X's rows are in the experts' order
-// themselves, values between two products in two bf16 parts (split_bf16), of which
-// the second lies a.K columns behind the first: a weight operand is dequantised
-// once for both.
+// themselves, values between two products as fp16 with an exponent for each 64
+// columns (store_block).  A lane multiplies its operands by 2 to the difference from
+// the row's largest exponent, at most 1 and exact down to 2^-25 of the row's largest
+// value, and the sums are scaled by the latter.  One bf16 number for a value adds as
+// much to the result's error as the result's own rounding (2.3e-3 of the norm against
+// 1.7e-3); two bf16 parts, added by a second matrix instruction, take twice the
+// tokens' LDS: E = 64, F = 1408, K = 5120, n = 1500, k = 8: 833 us for the layer
+// against 711, 692 with one bf16 number.
 //
 // LDS layout of the slice: token t's 16-byte chunk c (8 columns) at
 //     (t / 4) * kQuad + (t % 4) * 256 + (c ^ (t % 4)) * 16.
@@ -101,9 +127,7 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
 {
     constexpr int BM = TB * 16;
     constexpr int kThreads = 64 * RW * KG;
-    constexpr int kPlanes = GROUP == 2 ? 2 : 1;    // parts of a value of X
-    constexpr int kPlane = BM / 4 * kQuad;
-    constexpr int kSlice = kPlanes * kPlane;       // LDS bytes of a step's token slice
+    constexpr int kSlice = BM / 4 * kQuad;         // LDS bytes of a step's token slice
     constexpr int kBuf = kSlice + RW * RG * 128;   // and of the waves' scales
     constexpr int XL = BM / 4 / RW;                // quads a wave stages
     const int tid = threadIdx.x;
@@ -175,7 +199,7 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
 #pragma unroll
         for (int u = 0; u < XL; ++u) {
             const int t = tok0 + (wave * XL + u) * 4, live = min(4, tok1 - t);
-            xrsrc[u] = uniform(live > 0 ? buffer_rsrc(p.X + t * p.ldx, (unsigned)(((live - 1) * p.ldx + kPlanes * p.K) * 2))
+            xrsrc[u] = uniform(live > 0 ? buffer_rsrc(p.X + t * p.ldx, (unsigned)(((live - 1) * p.ldx + p.K) * 2))
                                         : buffer_rsrc(p.X, 0u));
         }
     }
@@ -186,6 +210,46 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
     const unsigned soff = (unsigned)((lane >> 3) * p.T * 128 + (lane & 7) * 16);
     const unsigned ldsb = lds_address(lds[kg]) + wave * XL * kQuad;
     const unsigned ldss = lds_address(lds[kg]) + kSlice + wave * RG * 128;
+
+    // GROUP 2: the tokens of this lane's operands, and the largest exponent of each
+    constexpr int NE = GROUP == 2 ? TB / 2 : 1;
+    const int *xexp[NE];
+    int top[NE], ex[NE][2];
+    __shared__ int tops[GROUP == 2 ? BM : 1];
+    if constexpr (GROUP == 2) {
+#pragma unroll
+        for (int t = 0; t < NE; ++t)
+            xexp[t] = p.xexp + (long long)min(tok0 + 32 * t + (lane & 31), tok1 - 1) * p.nexp;
+    }
+    // (lanes l and l + 32 take every other pair of a token's, eight loads at a time)
+    auto find_tops = [&]() {
+        const int used = (p.K + 63) / 64, last = (used - 1) & ~1;
+#pragma unroll
+        for (int t = 0; t < NE; ++t)
+            top[t] = kNoExponent;
+        for (int b0 = 2 * (lane >> 5); b0 < used; b0 += 32) {
+            u32x2 v[NE][8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+#pragma unroll
+                for (int t = 0; t < NE; ++t)
+                    v[t][q] = *reinterpret_cast<const u32x2 *>(xexp[t] + min(b0 + 4 * q, last));
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+#pragma unroll
+                for (int t = 0; t < NE; ++t) {
+                    top[t] = max(top[t], (int)v[t][q][0]);
+                    if (min(b0 + 4 * q, last) + 1 < used)
+                        top[t] = max(top[t], (int)v[t][q][1]);
+                }
+        }
+#pragma unroll
+        for (int t = 0; t < NE; ++t) {
+            top[t] = max(top[t], __shfl_xor(top[t], 32));
+            if (tid < 32)
+                tops[32 * t + tid] = top[t];
+        }
+    };
 
     u32x4 cw[RG];
     auto issue = [&](int s, int b) {
@@ -200,24 +264,31 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
 #pragma unroll
             for (int u = 0; u < XL; ++u)
                 load_lds_b128(xrsrc[u], xv, ldsb + buf + u * kQuad);
-            if constexpr (kPlanes == 2) {
-                const unsigned xl = in ? xoff + s * (kTileK * 2) + p.K * 2 : kOutOfRange;
-#pragma unroll
-                for (int u = 0; u < XL; ++u)
-                    load_lds_b128(xrsrc[u], xl, ldsb + buf + kPlane + u * kQuad);
-            }
         }
         if (lane < 8 * RG)   // the wave's 128 RG bytes of scales
             load_lds_b128(srsrc, soff + s * 128, ldss + buf);
 #pragma unroll
         for (int r = 0; r < RG; ++r)
             cw[r] = buffer_load_b128(crsrc, (unsigned)((r * p.T + s) * 1024 + lane * 16));
+        if constexpr (GROUP == 2) {
+#pragma unroll
+            for (int t = 0; t < NE; ++t) {
+                const u32x2 v = *reinterpret_cast<const u32x2 *>(xexp[t] + 2 * s);
+                ex[t][0] = (int)v[0];
+                ex[t][1] = (int)v[1];
+            }
+        }
     };
     auto land = [&]() {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
         for (int r = 0; r < RG; ++r)
             asm volatile("" : "+v"(cw[r]));
+        if constexpr (GROUP == 2) {
+#pragma unroll
+            for (int t = 0; t < NE; ++t)
+                asm volatile("" : "+v"(ex[t][0]), "+v"(ex[t][1]));
+        }
         __syncthreads();
     };
 
@@ -239,7 +310,7 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
     const int x0 = xa + (h ^ (tl & 3)) * 16, x1 = xa + ((h | 2) ^ (tl & 3)) * 16;
     const int sa = kSlice + wave * RG * 128 + (g & 1) * 128 + (MODE == 2 ? h * 64 : i * 8);
 
-    auto compute = [&](int b, const u32x4 *c) {
+    auto compute = [&](int b, const u32x4 *c, const f16x2 (*factor)[2]) {
         const char *buf = lds[kg][b];
         u32 lo[RP][4], hi[RP][4];   // columns 8h + 0..3 and 4..7 of each block
 #pragma unroll
@@ -256,13 +327,27 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
             for (int r = 0; r < RP; ++r)
                 sw[r] = *reinterpret_cast<const u32x2 *>(buf + sa + r * 256);
         }
-        bf16x8 w[2][RP][2];   // of substep j: blocks 2j and 2j + 1
+        u32x4 w[2][RP][2];   // of substep j: blocks 2j and 2j + 1
         auto dequant = [&](auto jc, int q) {
             constexpr int j = decltype(jc)::value;
 #pragma unroll
             for (int r = 0; r < RP; ++r) {
                 u32x2 l0, l1, h0, h1;
-                if constexpr (MODE == 2) {
+                if constexpr (MODE == 2 && GROUP == 2) {
+                    const u32x2 s = *reinterpret_cast<const u32x2 *>(buf + sa + r * 256 + 8 * j);
+                    const u32x2 t = *reinterpret_cast<const u32x2 *>(buf + sa + r * 256 + 8 * j + 32);
+                    l0 = dequant4<0>(lo[r][j], half_scales2<false>(s[0]), half_scales2<true>(s[0]));
+                    h0 = dequant4<0>(hi[r][j], half_scales2<false>(t[0]), half_scales2<true>(t[0]));
+                    l1 = dequant4<1>(lo[r][j], half_scales2<false>(s[1]), half_scales2<true>(s[1]));
+                    h1 = dequant4<1>(hi[r][j], half_scales2<false>(t[1]), half_scales2<true>(t[1]));
+                } else if constexpr (GROUP == 2) {
+                    const f16x2 s = half_scales2<(j & 1) != 0>(sw[r][j >> 1]);
+                    const f16x2 s0 = {s[0], s[0]}, s1 = {s[1], s[1]};
+                    l0 = dequant4<0>(lo[r][j], s0, s0);
+                    h0 = dequant4<0>(hi[r][j], s0, s0);
+                    l1 = dequant4<1>(lo[r][j], s1, s1);
+                    h1 = dequant4<1>(hi[r][j], s1, s1);
+                } else if constexpr (MODE == 2) {
                     // a scale for each contracted row: of columns 8h + 0..3, and 4..7
                     const u32x2 s = *reinterpret_cast<const u32x2 *>(buf + sa + r * 256 + 8 * j);
                     const u32x2 t = *reinterpret_cast<const u32x2 *>(buf + sa + r * 256 + 8 * j + 32);
@@ -278,8 +363,8 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
                     l1 = dequant4<1>(lo[r][j], s1, s1);
                     h1 = dequant4<1>(hi[r][j], s1, s1);
                 }
-                w[q][r][0] = __builtin_bit_cast(bf16x8, u32x4{l0[0], l0[1], h0[0], h0[1]});
-                w[q][r][1] = __builtin_bit_cast(bf16x8, u32x4{l1[0], l1[1], h1[0], h1[1]});
+                w[q][r][0] = u32x4{l0[0], l0[1], h0[0], h0[1]};
+                w[q][r][1] = u32x4{l1[0], l1[1], h1[0], h1[1]};
             }
         };
         dequant(std::integral_constant<int, 0>{}, 0);
@@ -291,16 +376,29 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
             for (int t = 0; t < TP; ++t) {
                 if (GROUP && TP > 1 && t >= blocks)
                     break;
-#pragma unroll
-                for (int q = 0; q < kPlanes; ++q) {
-                    const bf16x8 a = *reinterpret_cast<const bf16x8 *>(buf + q * kPlane + x0 + t * 8 * kQuad + 64 * j);
-                    const bf16x8 d = *reinterpret_cast<const bf16x8 *>(buf + q * kPlane + x1 + t * 8 * kQuad + 64 * j);
+                const u32x4 a = *reinterpret_cast<const u32x4 *>(buf + x0 + t * 8 * kQuad + 64 * j);
+                const u32x4 d = *reinterpret_cast<const u32x4 *>(buf + x1 + t * 8 * kQuad + 64 * j);
+                if constexpr (GROUP == 2) {
+                    const f16x2 f = factor[t][j >> 1];
+                    const f16x8 f8 = {f[0], f[1], f[0], f[1], f[0], f[1], f[0], f[1]};
+                    const f16x8 af = __builtin_bit_cast(f16x8, a) * f8, df = __builtin_bit_cast(f16x8, d) * f8;
 #pragma unroll
                     for (int r = 0; r < RP; ++r)
-                        acc[r][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j & 1][r][0], a, acc[r][t], 0, 0, 0);
+                        acc[r][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, w[j & 1][r][0]), af,
+                                                                           acc[r][t], 0, 0, 0);
 #pragma unroll
                     for (int r = 0; r < RP; ++r)
-                        acc[r][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j & 1][r][1], d, acc[r][t], 0, 0, 0);
+                        acc[r][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, w[j & 1][r][1]), df,
+                                                                           acc[r][t], 0, 0, 0);
+                } else {
+#pragma unroll
+                    for (int r = 0; r < RP; ++r)
+                        acc[r][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w[j & 1][r][0]),
+                                                                            __builtin_bit_cast(bf16x8, a), acc[r][t], 0, 0, 0);
+#pragma unroll
+                    for (int r = 0; r < RP; ++r)
+                        acc[r][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w[j & 1][r][1]),
+                                                                            __builtin_bit_cast(bf16x8, d), acc[r][t], 0, 0, 0);
                 }
             }
             __builtin_amdgcn_sched_barrier(0);   // one substep's operands live at a time
@@ -309,6 +407,8 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
 
     if (s0 + kg < s1)
         issue(s0 + kg, 0);
+    if constexpr (GROUP == 2)
+        find_tops();
     land();
     int b = 0;
     for (int sb = s0; sb < s1; sb += KG, b ^= 1) {
@@ -317,10 +417,21 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
 #pragma unroll
         for (int r = 0; r < RG; ++r)
             c[r] = cw[r];
+        f16x2 factor[NE][2];
+        if constexpr (GROUP == 2) {
+#pragma unroll
+            for (int t = 0; t < NE; ++t)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    // (an exponent behind the last column is none: its columns are zeros)
+                    const _Float16 f = (_Float16)__builtin_amdgcn_ldexpf(1.0f, min(max(ex[t][q] - top[t], -30), 0));
+                    factor[t][q] = f16x2{f, f};
+                }
+        }
         if (s + KG < s1)
             issue(s + KG, b ^ 1);
         if (KG == 1 || s < s1)
-            compute(b, c);
+            compute(b, c, factor);
         land();
     }
 
@@ -399,23 +510,34 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
                 const int t = q / kOuts, o = q % kOuts, tok = tok0 + 32 * b + t;
                 if (tok >= tok1)
                     break;
-                if (tx * kOuts + o < p.e.N)
-                    *reinterpret_cast<f32x4 *>(static_cast<float *>(p.e.out) + (long long)tok * p.e.ldo + tx * kOuts + o) =
-                        p.e.gscale * staged(t, o);
+                if (tx * kOuts + o >= p.e.N)
+                    continue;
+                f32x4 v = staged(t, o);
+                if constexpr (GROUP == 2) {
+                    const int top = tops[32 * b + t];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        v[j] = __builtin_amdgcn_ldexpf(p.e.gscale * v[j], top);
+                } else {
+                    v = p.e.gscale * v;
+                }
+                *reinterpret_cast<f32x4 *>(static_cast<float *>(p.e.out) + (long long)tok * p.e.ldo + tx * kOuts + o) = v;
             }
             continue;
         } else if constexpr (GROUP) {
             with_activation(p.e.flags & kEpiAct, [&](auto act) {
-#pragma unroll 2
-                for (int q = tid * 4; q < 32 * kOuts; q += 4 * kThreads) {
+                constexpr int kTurns = 8 * kOuts / kThreads;
+                static_assert(kTurns * kThreads == 8 * kOuts && kOuts % 64 == 0, "sixteen lanes: a block of 64 columns");
+#pragma unroll
+                for (int turn = 0; turn < kTurns; ++turn) {
+                    const int q = tid * 4 + turn * 4 * kThreads;
                     const int t = q / kOuts, o = q % kOuts, tok = tok0 + 32 * b + t, r = tx * kOuts + o;
                     if (tok >= tok1)
                         break;
-                    if (r >= p.e.N)
-                        continue;
+                    const bool in = r < p.e.N;
                     const int row = (o >> 4) * 32 + (o & 15);
                     const f32x4 z = p.e.gscale * staged(t, row), u = p.e.up_gscale * staged(t, row + 16);
-                    if (p.e.preact) {
+                    if (p.e.preact && in) {
                         float *pre = p.e.preact + (long long)tok * p.e.ldp;
                         *reinterpret_cast<f32x4 *>(pre + gated_row(r, 0)) = z;
                         *reinterpret_cast<f32x4 *>(pre + gated_row(r, 1)) = u;
@@ -423,8 +545,13 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
                     f32x4 y;
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
-                        y[v] = activate(z[v], decltype(act)::value) * u[v];
-                    split_bf16(static_cast<uint16_t *>(p.e.out) + (long long)tok * p.e.ldo + r, p.e.N, y);
+                        y[v] = in ? activate(z[v], decltype(act)::value) * u[v] : 0.f;
+                    const int exponent = block_exponent(row_max<16>(top_bits(y)));
+                    if (in) {
+                        store_block(static_cast<uint16_t *>(p.e.out) + (long long)tok * p.e.ldo + r, y, exponent);
+                        if (r % 64 == 0)
+                            p.hexp[(long long)tok * p.nexp + r / 64] = exponent;
+                    }
                 }
             });
             continue;

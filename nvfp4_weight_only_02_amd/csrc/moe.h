@@ -13,11 +13,14 @@ struct nvfp4_moe_order {
 
 struct nvfp4_moe_gemm_args {
     int mode;                     // 1 gated, 2 transposed, 0 linear, as nvfp4_fused_gemm_args
-    bool gather;                  // X's rows are the tokens; else the rows in the experts' order, each
-                                  // value in two bf16 parts, K columns apart (split_bf16)
+    bool gather;                  // X's rows are the tokens; else the rows in the experts' order, in
+                                  // fp16 with exponents (store_block)
     const uint8_t *codes, *scales;
     long long cstride, sstride;   // bytes of an expert's
     const uint16_t *X;
+    const int *xexp;              // of X, and of the rows of mode 1's output
+    int *hexp;
+    int nexp;                     // of a row
     long long ldx;
     int xrows, k;                 // rows of X (gather), experts of a token
     int rows, E;                  // at most so many rows

@@ -453,12 +453,13 @@ __global__ __launch_bounds__(256) void nvfp4_moe_combine_kernel(nvfp4_epi_params
 
 // One workgroup a pair: with d = dY . Wd (for weight one), the weight's gradient
 // is the dot product of d with h = act(G) U, unrounded; dG = w d U act'(G) and dU
-// = w d act(G), times their tensor scales, become operands of the next product in
-// two bf16 parts (in one, dX was off by 2.3e-3 of its norm, of which its own
-// rounding is 1.7e-3).
+// = w d act(G), times their tensor scales, become operands of the next product,
+// fp16 with an exponent for each 64 (as bf16, dX was off by 2.3e-3 of its norm, of
+// which its own rounding is 1.7e-3).
 __global__ __launch_bounds__(256) void nvfp4_moe_grad_kernel(const float *d, const float *preact, const int *position,
                                                              const int *experts, const float *weights, const float *gscale,
-                                                             float *dweights, uint16_t *dz, long long ldp, int E, int F, int act)
+                                                             float *dweights, uint16_t *dz, int *dzexp, int nexp, long long ldp,
+                                                             int E, int F, int act)
 {
     const int q = blockIdx.x, tid = threadIdx.x;
     const int row = position[q];
@@ -470,7 +471,7 @@ __global__ __launch_bounds__(256) void nvfp4_moe_grad_kernel(const float *d, con
     const int e = experts[q];
     const float w = weights[q], gg = gscale[e], gu = gscale[E + e];
     const float *src = preact + (long long)row * ldp;
-    uint16_t *dst = dz + (long long)row * 4 * F;
+    uint16_t *dst = dz + (long long)row * 2 * F;
     float dot = 0.f;
     for (int c = tid * 4; c < F; c += 1024) {
         const f32x4 dh = *reinterpret_cast<const f32x4 *>(d + (long long)row * F + c);
@@ -485,8 +486,12 @@ __global__ __launch_bounds__(256) void nvfp4_moe_grad_kernel(const float *d, con
             du[j] = w * dh[j] * a * gu;
         }
         if (dz) {
-            split_bf16(dst + gated_row(c, 0), 2LL * F, dg);
-            split_bf16(dst + gated_row(c, 1), 2LL * F, du);
+            // eight lanes: 32 columns of both
+            const int exponent = block_exponent(row_max<8>(max(top_bits(dg), top_bits(du))));
+            store_block(dst + gated_row(c, 0), dg, exponent);
+            store_block(dst + gated_row(c, 1), du, exponent);
+            if (c % 32 == 0)
+                dzexp[(long long)row * nexp + c / 32] = exponent;
         }
     }
     if (!dweights)
@@ -603,11 +608,24 @@ Bytes expert_bytes(const nvfp4_experts *w, bool transposed)
                               nvfp4_packed_codes_bytes(w->K, w->F), nvfp4_packed_scales_bytes(w->K, w->F)};
 }
 
-// Workspace of a forward call of several tokens: the order, h and the rows.
+// Exponents of a row of `cols` values between two products: one for 64, an even number.
+int exponents(int cols)
+{
+    return (cols + 127) / 128 * 2;
+}
+
+size_t exponents_bytes(int rows, int cols)
+{
+    return round256((size_t)rows * exponents(cols) * 4);
+}
+
+// Workspace of a forward call of several tokens: the order, h with its exponents and
+// the rows.
 size_t forward_bytes(int n, int k, const nvfp4_experts *w)
 {
     const int by_pairs = kChunkPairs / k, m = n < by_pairs ? n : by_pairs, pairs = m * k;
-    return order_bytes(pairs, w->E) + round256((size_t)pairs * w->F * 4) + round256((size_t)pairs * w->K * 4);
+    return order_bytes(pairs, w->E) + round256((size_t)pairs * w->F * 2) + exponents_bytes(pairs, w->F) +
+           round256((size_t)pairs * w->K * 4);
 }
 
 size_t backward_bytes(int n, int k, const nvfp4_experts *w, bool dx, bool copy)
@@ -617,7 +635,7 @@ size_t backward_bytes(int n, int k, const nvfp4_experts *w, bool dx, bool copy)
     if (copy)
         b += round256((size_t)m * w->K * 2);
     if (dx)
-        b += round256((size_t)pairs * w->F * 8) + round256((size_t)pairs * w->K * 4);
+        b += round256((size_t)pairs * w->F * 4) + exponents_bytes(pairs, 2 * w->F) + round256((size_t)pairs * w->K * 4);
     return b;
 }
 
@@ -801,7 +819,9 @@ int nvfp4_moe(const nvfp4_experts *w, const uint16_t *X, int64_t ldx, const int3
         const Order o = order_at(ws, pairs, E);
         ws += order_bytes(pairs, E);
         uint16_t *h = reinterpret_cast<uint16_t *>(ws);
-        float *rows = reinterpret_cast<float *>(ws + round256((size_t)pairs * F * 4));
+        ws += round256((size_t)pairs * F * 2);
+        int *hexp = reinterpret_cast<int *>(ws);
+        float *rows = reinterpret_cast<float *>(ws + exponents_bytes(pairs, F));
         st = launch_sort(o, experts + (size_t)t0 * k, pairs, E, tokens, s);
         if (st != NVFP4_OK)
             break;
@@ -824,7 +844,9 @@ int nvfp4_moe(const nvfp4_experts *w, const uint16_t *X, int64_t ldx, const int3
         a.gscale = w->gscale;
         a.up_gscale = w->gscale + E;
         a.order = {o.tile, o.offset, o.pair};
-        a.epi = plain_out(h, 2 * F, false, F);
+        a.hexp = hexp;
+        a.nexp = exponents(F);
+        a.epi = plain_out(h, F, false, F);
         a.epi.flags |= ep.activation;
         if (ep.preact) {
             a.epi.preact = ep.preact + (size_t)t0 * k * ep.ldp;
@@ -840,7 +862,8 @@ int nvfp4_moe(const nvfp4_experts *w, const uint16_t *X, int64_t ldx, const int3
         a.cstride = (long long)b.d_codes;
         a.sstride = (long long)b.d_scales;
         a.X = h;
-        a.ldx = 2 * F;
+        a.xexp = hexp;
+        a.ldx = F;
         a.K = F;
         a.row_groups = K / kRowsPerGroup;
         a.gscale = w->gscale + 2 * (size_t)E;
@@ -938,7 +961,9 @@ int nvfp4_moe_backward(const nvfp4_experts *wt, const void *dY, int dy_dtype, in
             ld = K;
         }
         uint16_t *dz = dX ? reinterpret_cast<uint16_t *>(ws) : nullptr;
-        ws += dX ? round256((size_t)pairs * F * 8) : 0;
+        ws += dX ? round256((size_t)pairs * F * 4) : 0;
+        int *dzexp = reinterpret_cast<int *>(ws);
+        ws += dX ? exponents_bytes(pairs, 2 * F) : 0;
         float *rows = reinterpret_cast<float *>(ws);
         const int *ids = experts + (size_t)t0 * k;
         st = launch_sort(o, ids, pairs, E, tokens, s);
@@ -968,7 +993,8 @@ int nvfp4_moe_backward(const nvfp4_experts *wt, const void *dY, int dy_dtype, in
             break;
         hipLaunchKernelGGL(nvfp4_moe_grad_kernel, dim3((unsigned)pairs), dim3(256), 0, s, d, preact + (size_t)t0 * k * ldp,
                            o.position, ids, weights + (size_t)t0 * k, wt->gscale,
-                           dweights ? dweights + (size_t)t0 * k : nullptr, dz, (long long)ldp, E, F, activation);
+                           dweights ? dweights + (size_t)t0 * k : nullptr, dz, dzexp, exponents(2 * F), (long long)ldp, E, F,
+                           activation);
         st = hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
         if (!dX || st != NVFP4_OK)
             continue;
@@ -978,7 +1004,9 @@ int nvfp4_moe_backward(const nvfp4_experts *wt, const void *dY, int dy_dtype, in
         a.cstride = (long long)b.gu_codes;
         a.sstride = (long long)b.gu_scales;
         a.X = dz;
-        a.ldx = 4 * (long long)F;
+        a.xexp = dzexp;
+        a.nexp = exponents(2 * F);
+        a.ldx = 2 * (long long)F;
         a.K = 2 * F;
         a.row_groups = K / kRowsPerGroup;
         a.gscale = nullptr;   // dz carries the tensor scales

@@ -28,7 +28,7 @@ struct MoeFewParams {
     const uint16_t *X;
     const int *experts;           // [n][k]
     const float *weights;         // [n][k]
-    uint16_t *h;                  // [n k][Td][2][128]: the two bf16 parts of a value (split_bf16),
+    uint16_t *h;                  // [n k][Td][2][128]: the two bf16 parts of a value (bf16_rest),
                                   // columns of a tile in the lanes' order
     int ldx, n, k, E, F, K, act;
     int T, Td, P;                 // 128-column tiles of K and of F, pairs of row groups of a gated weight

@@ -70,6 +70,9 @@ int nvfp4_launch_moe_gemm(const nvfp4_moe_gemm_args &a, hipStream_t stream)
     p.pair = a.order.pair;
     p.k = a.k;
     p.xrows = a.xrows;
+    p.xexp = a.xexp;
+    p.hexp = a.hexp;
+    p.nexp = a.nexp;
     p.gscale = a.gscale;
     p.up_gscale = a.up_gscale;
     p.cstride = a.cstride;

@@ -88,16 +88,19 @@ def _live(experts, E):
 
 
 def _kept(v, e):
-    """Bound of rows v, known within e, as operands of the next product."""
+    """Bound of rows v, known within e, as operands of the next product: fp16 numbers
+    with an exponent for each 64 (half of a step of 2^-10: 2^-11 relative), whose
+    largest is between 2^14 and 2^15.  A block's numbers are scaled by a power of two
+    to the row's exponent, and lost where it is below 2^-24: numbers below 2^15 2^-25,
+    against 2^14 at least of the row's largest."""
     a = np.abs(v) + e
-    return e + 2.0 ** -12 * a + 2.0 ** -25 * a.max(1, keepdims=True)
+    return e + 2.0 ** -11 * a + 2.0 ** -24 * a.max(1, keepdims=True)
 
 
 def moe(X, Wg, Wu, Wd, experts, weights, kind="silu", residual=None, out_f32=False):
-    """(Y, bound): h kept to 11 bits at least (half a step of 2^-11 relative, or of
-    2^-24 of the row's largest) and its down projection, k weighted terms (a weight
-    is multiplied by the tensor scale first: 3 steps), the residual, the last
-    rounding."""
+    """(Y, bound): h kept to 11 bits (_kept) and its down projection, k weighted terms
+    (a weight is multiplied by the tensor scale first: 3 steps), the residual, the
+    last rounding."""
     n, k = experts.shape
     F, K = Wg.shape[1:]
     y, b, m = np.zeros((n, K)), np.zeros((n, K)), np.zeros((n, K))
