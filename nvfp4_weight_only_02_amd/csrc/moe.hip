@@ -28,14 +28,44 @@ struct RouteParams {
     float scale;
 };
 
-// v combined over the wave in a fixed order; every lane has the result.
+// Dword v of another lane: STEP 0 and 1 of the lane 1 and 2 away, 2 and 3 of the
+// mirror of its eight and sixteen, 4 and 5 of the other sixteen and half of the wave.
+// Without LDS: the router's rounds wait for one reduction after another (8000 x 256
+// with bias, k = 8: 22 us through __shfl_xor).
+template <int STEP>
+__device__ __forceinline__ int other_lane(int v)
+{
+    if constexpr (STEP < 4) {
+        constexpr int kControl[] = {0xB1, 0x4E, 0x141, 0x140};
+        return __builtin_amdgcn_update_dpp(v, v, kControl[STEP], 0xF, 0xF, false);
+    } else {
+        const auto s = STEP == 4 ? __builtin_amdgcn_permlane16_swap(v, v, false, false)
+                                 : __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return (threadIdx.x & (STEP == 4 ? 16 : 32)) ? s[0] : s[1];
+    }
+}
+
+// v combined over the wave (all lanes on) in a fixed order; every lane has the result.
 template <typename T, typename F>
 __device__ __forceinline__ T wave_all(T v, F f)
 {
+    static_for<6>([&](auto sc) {
+        constexpr int kStep = decltype(sc)::value;
+        struct Dwords {
+            int d[sizeof(T) / 4];
+        } w = __builtin_bit_cast(Dwords, v);
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2)
-        v = f(v, __shfl_xor(v, d));
+        for (int j = 0; j < (int)(sizeof(T) / 4); ++j)
+            w.d[j] = other_lane<kStep>(w.d[j]);
+        v = f(v, __builtin_bit_cast(T, w));
+    });
     return v;
+}
+
+// v of lane `at`, the same in all lanes.
+__device__ __forceinline__ float of_lane(float v, int at)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), at));
 }
 
 __device__ __forceinline__ float wave_sum(float v)
@@ -154,7 +184,7 @@ __global__ __launch_bounds__(256) void nvfp4_moe_route_kernel(RouteParams p)
             const unsigned long long mask = __ballot(is && !found);
             if (mask && !found) {
                 const int at = __ffsll((long long)mask) - 1;
-                const float v = __shfl(l[r], at);
+                const float v = of_lane(l[r], at);
                 if (lane == s) {
                     mine = r * 64 + at;
                     logit = v;
@@ -235,16 +265,22 @@ __global__ __launch_bounds__(256) void nvfp4_moe_route_grad_kernel(RouteParams p
     if (p.sigmoid)
         d *= 1.0f / (1.0f + expf(logit));
     d = live ? d : 0.0f;
+    float out[NE];
+#pragma unroll
+    for (int r = 0; r < NE; ++r)
+        out[r] = 0.0f;
+    for (int s = 0; s < p.k; ++s) {
+        const int es = __builtin_amdgcn_readlane(chosen, s);
+        const float ds = of_lane(d, s);
+#pragma unroll
+        for (int r = 0; r < NE; ++r)
+            if (es == r * 64 + lane)
+                out[r] += ds;
+    }
 #pragma unroll
     for (int r = 0; r < NE; ++r) {
         const int e = r * 64 + lane;
-        float v = 0.0f;
-        for (int s = 0; s < p.k; ++s) {
-            const int es = __shfl(chosen, s);
-            const float ds = __shfl(d, s);
-            if (es == e)
-                v += ds;
-        }
+        float v = out[r];
         if (dense)
             v = l[r] == -__builtin_inff() ? 0.0f : expf(l[r] - m) * inv * (v - dot);
         if (e < p.E)
