@@ -473,8 +473,9 @@ typedef struct nvfp4_experts {
  * residual (it may be Y itself), out_dtype, and preact: fp32 [n k][ldp >= 2 F]
  * receives the pre-activations for nvfp4_moe_backward, its rows in the order of
  * the experts (rows of slots without an expert are left as they were); biases
- * NULL.  h = act() * () is rounded to bf16, an operand of the matrix
- * instructions; all sums are fp32.
+ * NULL.  h = act() * (), an operand of the matrix instructions, is held to 16
+ * significant bits up to 16 tokens, else to 11, down to 2^-24 of its row's largest
+ * value; all sums are fp32.
  * Up to 16 tokens (K up to 8192, no preact) take two launches, and a token's
  * result does not depend on the others there; more are sorted by expert, 2^16
  * pairs at a time.  Workspace: nvfp4_moe_workspace_bytes, 16-byte aligned, with
@@ -485,10 +486,15 @@ int nvfp4_moe(const nvfp4_experts *w, const uint16_t *X, int64_t ldx, const int3
               void *workspace, size_t workspace_bytes, void *stream);
 size_t nvfp4_moe_workspace_bytes(int n, int k, int E, int F, int K, int preact);
 
+/* The tile of the grouped products for more than 16 tokens (or with preact):
+ * weight rows and tokens of a workgroup.  Pure host function; returns a status
+ * (NULL, RANGE, SHAPE). */
+int nvfp4_moe_geometry(int n, int k, int E, int F, int K, int *rows_per_workgroup, int *tokens_per_workgroup);
+
 /* The gradients of nvfp4_moe, on the transposed copies: dX bf16 [n][ldx] (NULL:
  * not wanted) and dweights fp32 [n][k] (NULL: not wanted; 0 where there is no
- * expert).  dY fp32 or bf16 [n][ldy], ldy at most 2^18; it is rounded to bf16, and
- * so are the gradients of the pre-activations, as operands of the products.
+ * expert).  dY fp32 or bf16 [n][ldy], ldy at most 2^18; it is rounded to bf16, an
+ * operand of the products; the gradients of the pre-activations are held as h is.
  * preact as nvfp4_moe stored it.  The residual's gradient is dY itself.
  * Workspace: nvfp4_moe_backward_workspace_bytes with dx as it is wanted, copy =
  * 0 only if dY is bf16, 16-byte aligned and ldy a multiple of 8. */
@@ -533,6 +539,11 @@ int nvfp4_int8_linear(const int8_t *Wq, const float *wscale, const void *X, int6
                       void *Y, int64_t ldy, int n, int N, int K, const nvfp4_epilogue *epilogue,
                       void *workspace, size_t workspace_bytes, void *stream);
 size_t nvfp4_int8_linear_workspace_bytes(int n, int N, int K, int quantize);
+
+/* The tile of nvfp4_int8_linear for n > 16 tokens, as nvfp4_fused_geometry gives
+ * it.  Pure host function; returns a status (NULL, RANGE, SHAPE). */
+int nvfp4_int8_geometry(int n, int N, int K, int *rows_per_workgroup, int *tokens_per_workgroup, int *k_groups,
+                        int *k_parts);
 
 /* Human-readable name of a status code (static storage). */
 const char *nvfp4_strerror(int status);

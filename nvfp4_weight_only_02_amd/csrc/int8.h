@@ -22,6 +22,7 @@ struct nvfp4_int8_plan {
     int tile, ks, tp;             // K parts of tp 64-column steps
 };
 NVFP4_HIDDEN nvfp4_int8_plan nvfp4_plan_int8(int n, int row_groups, int K);
+NVFP4_HIDDEN void nvfp4_int8_tile(int tile, int *rows, int *tokens, int *k_groups);
 NVFP4_HIDDEN int nvfp4_launch_int8_gemm(const nvfp4_int8_args &a, const nvfp4_int8_plan &plan, hipStream_t stream);
 
 #endif  // NVFP4_INT8_H

@@ -494,6 +494,21 @@ int nvfp4_int8_quantize(const void *X, int dtype, int64_t ldx, int n, int K, int
     return st != NVFP4_OK ? st : launch_quantize(X, dtype, ldx, n, K, q, ldq, scale, (hipStream_t)stream);
 }
 
+int nvfp4_int8_geometry(int n, int N, int K, int *rows_per_workgroup, int *tokens_per_workgroup, int *k_groups, int *k_parts)
+{
+    if (!rows_per_workgroup || !tokens_per_workgroup || !k_groups || !k_parts)
+        return NVFP4_ERR_NULL;
+    if (n <= NVFP4_MAX_TOKENS)
+        return NVFP4_ERR_RANGE;
+    const int st = check_shape(n, N, K);
+    if (st != NVFP4_OK)
+        return st;
+    const nvfp4_int8_plan plan = nvfp4_plan_int8(n, (int)row_groups(N), K);
+    nvfp4_int8_tile(plan.tile, rows_per_workgroup, tokens_per_workgroup, k_groups);
+    *k_parts = plan.ks;
+    return NVFP4_OK;
+}
+
 size_t nvfp4_int8_linear_workspace_bytes(int n, int N, int K, int quantize)
 {
     return check_shape(n, N, K) == NVFP4_OK ? space_of(n, N, K, quantize != 0).total() : 0;

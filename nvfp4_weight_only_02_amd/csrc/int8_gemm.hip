@@ -430,6 +430,14 @@ nvfp4_int8_plan nvfp4_plan_int8(int n, int row_groups, int K)
     return best;
 }
 
+void nvfp4_int8_tile(int tile, int *rows, int *tokens, int *k_groups)
+{
+    const Tile &t = kTiles[tile];
+    *rows = t.rows;
+    *tokens = t.tokens;
+    *k_groups = t.kg;
+}
+
 int nvfp4_launch_int8_gemm(const nvfp4_int8_args &a, const nvfp4_int8_plan &plan, hipStream_t stream)
 {
     Int8GemmParams p = {};

@@ -31,9 +31,10 @@ struct nvfp4_moe_gemm_args {
     nvfp4_epi_params epi;
 };
 
-// The tokens of a tile of the grouped products (32 or 64), from the layer's sizes,
-// and the most tiles that `rows` rows of E experts can take.
+// The tile of the grouped products, from the layer's sizes: its tokens (32 or 64) and
+// weight rows; and the most tiles that `rows` rows of E experts can take.
 NVFP4_HIDDEN int nvfp4_moe_tile_tokens(int rows, int E, int F);
+NVFP4_HIDDEN int nvfp4_moe_tile_rows(int rows, int E, int tokens);
 NVFP4_HIDDEN long long nvfp4_moe_max_tiles(int rows, int E, int tokens);
 NVFP4_HIDDEN int nvfp4_launch_moe_gemm(const nvfp4_moe_gemm_args &a, hipStream_t stream);
 

@@ -770,6 +770,23 @@ size_t nvfp4_moe_workspace_bytes(int n, int k, int E, int F, int K, int preact)
     return !preact && is_few(n, K) ? nvfp4_moe_few_bytes(n, k, F) : forward_bytes(n, k, &w);
 }
 
+int nvfp4_moe_geometry(int n, int k, int E, int F, int K, int *rows_per_workgroup, int *tokens_per_workgroup)
+{
+    if (!rows_per_workgroup || !tokens_per_workgroup)
+        return NVFP4_ERR_NULL;
+    nvfp4_experts w = {};
+    w.E = E;
+    w.F = F;
+    w.K = K;
+    const int st = n < 1 ? NVFP4_ERR_RANGE : check_sizes(&w, n, k);
+    if (st != NVFP4_OK)
+        return st;
+    const int by_pairs = kChunkPairs / k, pairs = (n < by_pairs ? n : by_pairs) * k;   // (a shorter last chunk may differ)
+    *tokens_per_workgroup = nvfp4_moe_tile_tokens(pairs, E, F);
+    *rows_per_workgroup = nvfp4_moe_tile_rows(pairs, E, *tokens_per_workgroup);
+    return NVFP4_OK;
+}
+
 int nvfp4_moe(const nvfp4_experts *w, const uint16_t *X, int64_t ldx, const int32_t *experts, const float *weights, int n, int k,
               void *Y, int64_t ldy, const nvfp4_epilogue *epilogue, void *workspace, size_t workspace_bytes, void *stream)
 {

@@ -46,6 +46,11 @@ int nvfp4_moe_tile_tokens(int rows, int E, int F)
     return each <= 40 || workgroups < 384 ? 32 : 64;
 }
 
+int nvfp4_moe_tile_rows(int rows, int E, int tokens)
+{
+    return tokens == 64 && rows / E >= 128 ? 256 : 128;
+}
+
 long long nvfp4_moe_max_tiles(int rows, int E, int tokens)
 {
     return rows / tokens + (rows < E ? rows : E);
@@ -79,7 +84,7 @@ int nvfp4_launch_moe_gemm(const nvfp4_moe_gemm_args &a, hipStream_t stream)
     p.sstride = a.sstride;
     if (a.tile_tokens == 32)
         return launch_grouped<2, 2, 4, 2>(p, a, stream);
-    if (a.rows / a.E >= 128)
+    if (nvfp4_moe_tile_rows(a.rows, a.E, a.tile_tokens) == 256)
         return launch_grouped<4, 4, 4, 1>(p, a, stream);
     return launch_grouped<2, 4, 4, 1>(p, a, stream);
 }

@@ -13,6 +13,7 @@ without autograd.  Streams, memory and refusals as in ``fused.py``.
 """
 from __future__ import annotations
 
+import ctypes
 import functools
 import math
 import struct
@@ -38,6 +39,7 @@ _SIGNATURES = {
     "nvfp4_moe_route_backward": (_i32, [_vp, _i32, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _F32, _vp, _i64, _vp]),
     "nvfp4_moe": (_i32, [_vp, _vp, _i64, _vp, _vp, _i32, _i32, _vp, _i64, _vp, _vp, _SIZE, _vp]),
     "nvfp4_moe_workspace_bytes": (_SIZE, [_i32] * 6),
+    "nvfp4_moe_geometry": (_i32, [_i32] * 5 + [ctypes.POINTER(_i32)] * 2),
     "nvfp4_moe_backward": (_i32, [_vp, _vp, _i32, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _SIZE, _vp]),
     "nvfp4_moe_backward_workspace_bytes": (_SIZE, [_i32] * 7),
 }
@@ -405,6 +407,14 @@ def moe_backward(wt: TransposedExperts, dY: torch.Tensor, experts: torch.Tensor,
     _no_graph(dY, weights, preact, out)
     _written(out)
     return _moe_backward(wt, dY, experts, weights, preact, act, True, True, out, stream)
+
+
+def moe_geometry(n: int, k: int, E: int, F: int, K: int) -> tuple:
+    """(weight rows, tokens of a workgroup) of the grouped products of ``moe`` for
+    more than 16 tokens, or with pre-activations (nvfp4_moe_geometry)."""
+    v = [_i32() for _ in range(2)]
+    _run("nvfp4_moe_geometry", n, k, E, F, K, *(ctypes.byref(x) for x in v))
+    return tuple(x.value for x in v)
 
 
 def moe_workspace_bytes(n: int, k: int, w: ExpertWeights, preact: bool = False) -> int:

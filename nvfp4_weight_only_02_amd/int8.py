@@ -11,6 +11,7 @@ refusals as in ``fused.py``.
 """
 from __future__ import annotations
 
+import ctypes
 import functools
 from dataclasses import dataclass
 
@@ -26,6 +27,7 @@ _SIGNATURES = {
     "nvfp4_int8_quantize": (_i32, [_vp, _i32, _i64, _i32, _i32, _vp, _i64, _vp, _vp]),
     "nvfp4_int8_linear": (_i32, [_vp, _vp, _vp, _i64, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _SIZE, _vp]),
     "nvfp4_int8_linear_workspace_bytes": (_SIZE, [_i32] * 4),
+    "nvfp4_int8_geometry": (_i32, [_i32, _i32, _i32] + [ctypes.POINTER(_i32)] * 4),
 }
 
 
@@ -129,6 +131,14 @@ def int8_linear(w: Int8Weight, X: torch.Tensor, scale: torch.Tensor = None, bias
     _run("nvfp4_int8_linear", w.codes.data_ptr(), w.scale.data_ptr(), X.data_ptr(), _ld(X), _ptr(scale), Y.data_ptr(), _ld(Y), n,
          w.N, w.K, ep, ws, size, at.handle)
     return Y
+
+
+def int8_geometry(n: int, N: int, K: int) -> tuple:
+    """(weight rows, tokens of a workgroup, K groups in it, K parts) that
+    ``int8_linear`` takes for n > 16 tokens (nvfp4_int8_geometry)."""
+    v = [_i32() for _ in range(4)]
+    _run("nvfp4_int8_geometry", n, N, K, *(ctypes.byref(x) for x in v))
+    return tuple(x.value for x in v)
 
 
 def int8_linear_workspace_bytes(n: int, N: int, K: int, quantize: bool = True) -> int:

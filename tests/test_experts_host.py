@@ -1,6 +1,7 @@
 """Argument checks and host functions of the router, the expert layer and the
 8-bit projection, no GPU: every refusal comes before any HIP call."""
 import pytest
+from hypothesis import given, settings, strategies as st
 
 import nvfp4_weight_only_02_amd as nv
 from nvfp4_weight_only_02_amd import experts, int8
@@ -181,3 +182,28 @@ def test_valid_calls_reach_the_device_check():
     assert route(n=0, l=None, w=None, e=None) == route_backward(n=0, l=None) == quantize(n=0, x=None) == OK
     assert moe(n=0, x=None, y=None, e=None, w=None, ws=None) == moe_backward(n=0, x=None, e=None, w=None, z=None) == OK
     assert moe_backward(dx=None, dw=None, ws=None) == int8_linear(n=0, x=None, y=None, work=None) == OK
+
+
+def test_geometry():
+    assert nv.moe_geometry(1, 1, 1, 16, 16) == (128, 32) and nv.moe_geometry(1 << 20, 32, 1024, 16, 16) == (128, 64)
+    for a, status in (((0, 1, 1, 16, 16), RANGE), ((1, 33, 40, 16, 16), RANGE), ((1, 1, 0, 16, 16), RANGE), ((1, 1, 1, 8, 16), SHAPE)):
+        with pytest.raises(nv.Nvfp4Error) as e:
+            nv.moe_geometry(*a)
+        assert e.value.status == status
+    for a, status in (((16, 64, 64), RANGE), ((17, 0, 64), RANGE), ((17, 64, 72), SHAPE), ((17, 64, 131072), SHAPE)):
+        with pytest.raises(nv.Nvfp4Error) as e:
+            nv.int8_geometry(*a)
+        assert e.value.status == status
+    assert int8._call("nvfp4_int8_geometry")(17, 64, 64, None, None, None, None) == NULL
+    assert experts._call("nvfp4_moe_geometry")(17, 1, 1, 64, 64, None, None) == NULL
+
+
+@settings(max_examples=300, deadline=None)
+@given(n=st.integers(17, 1 << 20), N=st.integers(1, 1 << 17), T=st.integers(1, 1023), tail=st.sampled_from([0, 16, 112]))
+def test_int8_geometry_rule(n, N, T, tail):
+    K = T * 128 - tail
+    r, t, kg, ks = nv.int8_geometry(n, N, K)
+    assert (r, t, kg) in {(64, 32, 4), (128, 64, 2), (128, 64, 1), (128, 128, 1), (256, 128, 1), (256, 256, 1)}
+    tp = -(-2 * T // ks)
+    assert 1 <= ks <= 8 and (ks - 1) * tp < 2 * T        # no part is empty
+    assert (nv.int8_linear_workspace_bytes(n, N, K, False) > 0) == (ks > 1)

@@ -201,6 +201,57 @@ def test_moe(n, E, F, K, k, act, residual, out, empty):
     check(Y, X8.moe(f64(X), Wg, Wu, Wd, e.cpu().numpy(), f64(c), act, None if r is None else f64(r), out == F32), "Y")
 
 
+@pytest.mark.parametrize("n,E,F,K,k,tile", [(60, 6, 80, 144, 2, (128, 32)), (450, 8, 2576, 144, 1, (128, 64)),
+                                            (800, 2, 2064, 144, 1, (256, 64))])
+@pytest.mark.parametrize("act", ["silu", "none"])
+def test_every_tile_of_the_grouped_products(n, E, F, K, k, tile, act):
+    say("moe tile", n, E, F, K, k, tile, act)
+    assert nv.moe_geometry(n, k, E, F, K) == tile
+    w, Wg, Wu, Wd = weights(E, F, K, 60)
+    X = randn((n, K), 61).requires_grad_()
+    e, c = choices(n, k, E, 62)
+    c.requires_grad_()
+    dY = randn((n, K), 63, BF16, 0.1)
+    Y = nv.moe(w, X, e, c, act, transposed=w.transpose())
+    args = (f64(X), Wg, Wu, Wd, e.cpu().numpy(), f64(c))
+    check(Y, X8.moe(*args, act), "Y")
+    dX, dc = torch.autograd.grad(Y, [X, c], dY)
+    x, d = X8.moe_grads(*args, f64(dY), act)
+    check(dX, x, "dX")
+    check(dc, d, "dweights")
+
+
+@pytest.mark.parametrize("n", [9, 40])
+def test_values_between_the_products_of_any_size(n):
+    """Rows of h from 2^-60 to 2^60, whose columns spread over another 2^32: what is
+    kept of a value depends on its own row alone."""
+    say("moe sizes", n)
+    E, F, K, k = 3, 208, 144, 2
+    g = torch.Generator(device="cuda").manual_seed(70)
+    spread = 2.0 ** torch.randint(-8, 9, (E, F, 1), generator=g, device="cuda").float()
+    packed, dense = ([], [], []), ([], [], [])
+    for j, (N, C, m) in enumerate(((F, K, spread), (F, K, spread), (K, F, torch.ones(E, K, 1, device="cuda")))):
+        W = torch.randn(E, N, C, generator=g, device="cuda") * 0.1
+        for i in range(E):
+            codes, scales, t = O.quantize((W[i] * m[i]).cpu().numpy())
+            packed[j].append(nv.PackedWeight.from_canonical(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), t, N, C))
+            dense[j].append(np.asarray(O.dequant(codes, scales, t), dtype=np.float64))
+    w, (Wg, Wu, Wd) = nv.ExpertWeights.from_packed(*packed), (np.stack(d) for d in dense)
+    X = (randn((n, K), 71, F32) * 2.0 ** torch.linspace(-30, 30, n, device="cuda").round()[:, None]).to(BF16).requires_grad_()
+    e, c = choices(n, k, E, 72)
+    c.requires_grad_()
+    dY = (randn((n, K), 73, F32) * 2.0 ** torch.linspace(20, -20, n, device="cuda").round()[:, None]).to(BF16)
+    args = (f64(X), Wg, Wu, Wd, e.cpu().numpy(), f64(c))
+    with torch.no_grad():
+        check(nv.moe(w, X, e, c, "none"), X8.moe(*args, "none"), "Y")
+    Y = nv.moe(w, X, e, c, "none", transposed=w.transpose())
+    check(Y, X8.moe(*args, "none"), "Y")
+    dX, dc = torch.autograd.grad(Y, [X, c], dY)
+    x, d = X8.moe_grads(*args, f64(dY), "none")
+    check(dX, x, "dX")
+    check(dc, d, "dweights")
+
+
 @pytest.mark.parametrize("K,F,n", [(8192, 32, 16), (8208, 32, 3), (7184, 128, 2), (32, 8208, 5), (1040, 144, 16)])
 def test_moe_long_rows(K, F, n):
     """Every wave's share of K up to 8192, the form beyond, long F."""

@@ -130,6 +130,25 @@ def test_linear(n, N, K, quantized, act, bias, residual, out):
     check(Y, X8.int8_linear(rq, rs, wq, ws, None if b is None else f64(b), act, None if r is None else f64(r), out == F32), "Y")
 
 
+@pytest.mark.parametrize("n,N,K,geometry", [
+    (60, 330, 2064, (64, 32, 4, 1)), (40, 40, 8208, (64, 32, 4, 8)), (70, 9000, 144, (128, 64, 1, 1)),
+    (75, 2000, 8208, (128, 64, 1, 8)), (520, 1040, 1040, (128, 64, 2, 1)), (40, 9000, 8208, (128, 64, 2, 3)),
+    (520, 4090, 144, (128, 128, 1, 1)), (150, 4096, 8208, (128, 128, 1, 4)), (2000, 4090, 272, (256, 128, 1, 1)),
+    (2050, 5120, 400, (256, 256, 1, 1)), (520, 4090, 8208, (256, 128, 1, 3))])
+def test_every_tile(n, N, K, geometry):
+    """Every tile of the many-token product, with K parts where it takes them, the
+    sizes no multiple of the tile's."""
+    say("int8 tile", n, N, K, geometry)
+    assert nv.int8_geometry(n, N, K) == geometry
+    w, wq, ws = weight(N, K, 40, -128)
+    q, s = codes((n, K), 41, -128), randn((n,), 42, F32).abs() * 0.01
+    b, r = randn((N,), 43, F32), randn((n, N), 44, BF16, 3.0)
+    # (sums below 2^31: exact in 64-bit floats too)
+    args = f64(q), f64(s), wq.astype(np.float64), ws, f64(b)
+    check(nv.int8_linear(w, q, s, b, "silu", r), X8.int8_linear(*args, "silu", f64(r)), "Y")
+    check(nv.int8_linear(w, q, s, b, "none", out_dtype=F32), X8.int8_linear(*args, "none", None, True), "Y")
+
+
 @pytest.mark.parametrize("N,n", [(16384, 3), (9000, 16), (2000, 1), (16001, 5), (5120, 700)])
 def test_many_rows(N, n):
     say("int8 rows", N, n)
