@@ -38,6 +38,10 @@ constexpr int kStep = 64;               // columns of a step, bytes of a token's
 // The MFMA is v_mfma_i32_32x32x32_i8, weights as rows: one permlane16 swap a
 // dword of two row groups' tiles gives lane (row 16 (g % 2) + i, half h = g / 2)
 // columns 32 h + 0 .. 15 and 32 h + 16 .. 31 of the 64.
+//
+// The large tiles have the weights in LDS too (WL), where the waves that share row
+// groups read them once.  16384 x 5120, n = 4096: 327 us on 256 x 256, 2.1 POP/s,
+// bound by the matrix instructions and power (a library product: 2.2).
 constexpr int kRing = 4;
 
 // a * b, a + b, rounded: the compiler makes no fma of them.  A result has the same

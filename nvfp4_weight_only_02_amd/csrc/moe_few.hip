@@ -159,7 +159,9 @@ __device__ __forceinline__ int operand_order(int r)
 // in turn, cut into equal shares for the workgroups; the eight waves split K.
 // All tokens' rows stay in registers as MFMA operands (rows that an expert was
 // not chosen for cost nothing: the matrix instruction has 16 rows anyway), and
-// the weights stream past them, a row group ahead.
+// the weights stream past them, a row group ahead.  Bound by the weights' bytes and
+// the start: E = 64, F = 1408, K = 5120, k = 8: 15.7 us for n = 1 (65 MB), 79 for 16
+// (450 MB, 5.7 TB/s).
 template <int MT, int NV>
 __global__ __launch_bounds__(kThreads) void nvfp4_moe_up_kernel(MoeFewParams p)
 {
@@ -303,8 +305,8 @@ constexpr int kNoPair = 0xFFFF;
 // memory's bandwidth (24 KB/us were measured with most others done, against 25 for
 // 6.4 TB/s over 256), so a second workgroup on some of them would be what the
 // launch waits for.  13 experts 400 x 1040, n = 7: 10.2 us with 16 rows a
-// workgroup, 7.5 with 8; E = 64, F = 1408, K = 5120, k = 8, n = 16 (225 MB): 53 us,
-// of which the codes alone take 42.
+// workgroup, 7.5 with 8; E = 64, F = 1408, K = 5120, k = 8, n = 16 (225 MB): 59 us,
+// 53 with one bf16 number for a value; the codes alone take 42.
 template <int NW, int D>
 __global__ __launch_bounds__(kThreads, 4) void nvfp4_moe_down_kernel(MoeFewParams p)
 {

@@ -283,6 +283,17 @@ def test_every_split_of_the_down_projection(k, n):
     check(nv.moe(w, X, e, c), X8.moe(f64(X), Wg, Wu, Wd, e.cpu().numpy(), f64(c)), "Y")
 
 
+@pytest.mark.parametrize("k", [8, 24, 25, 32])
+def test_most_pairs_of_the_down_projection(k):
+    """Up to 512 pairs and two windows of rows: the sums take the most LDS there, and
+    beyond 384 pairs fewer tiles are fetched ahead."""
+    say("moe most pairs", k)
+    n, E, F, K = 16, 40, 144, 4112
+    w, Wg, Wu, Wd = weights(E, F, K, 85)
+    X, (e, c) = randn((n, K), 86), choices(n, k, E, 87)
+    check(nv.moe(w, X, e, c, out_dtype=F32), X8.moe(f64(X), Wg, Wu, Wd, e.cpu().numpy(), f64(c), out_f32=True), "Y")
+
+
 @pytest.mark.parametrize("n", [1, 6, 16, 30, 200])
 def test_empty_repeated_and_foreign_experts(n):
     """No expert at all; one expert for all tokens, in every slot; experts that
