@@ -243,17 +243,13 @@ __device__ __forceinline__ u32 top_bits(const f32x4 v)
     return m;
 }
 
-// The largest of L (8 or 16) lanes, in all of them; lanes that are switched off count as none.
-template <int L>
+// The largest of sixteen lanes, in all of them; lanes that are switched off count as none.
 __device__ __forceinline__ u32 row_max(u32 m)
 {
-    static_assert(L == 8 || L == 16, "lanes of a row");
     m = max(m, (u32)__builtin_amdgcn_update_dpp((int)m, (int)m, 0xB1, 0xF, 0xF, false));    // lane ^ 1
     m = max(m, (u32)__builtin_amdgcn_update_dpp((int)m, (int)m, 0x4E, 0xF, 0xF, false));    // lane ^ 2
     m = max(m, (u32)__builtin_amdgcn_update_dpp((int)m, (int)m, 0x141, 0xF, 0xF, false));   // 7 - lane of eight
-    if (L == 16)
-        m = max(m, (u32)__builtin_amdgcn_update_dpp((int)m, (int)m, 0x140, 0xF, 0xF, false));   // 15 - lane of sixteen
-    return m;
+    return max(m, (u32)__builtin_amdgcn_update_dpp((int)m, (int)m, 0x140, 0xF, 0xF, false));
 }
 
 constexpr int kNoExponent = -1000;   // of a block of zeros

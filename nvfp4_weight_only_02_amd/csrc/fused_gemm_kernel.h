@@ -28,7 +28,7 @@ struct GroupedGemmParams : FusedGemmParams {
     const int *pair;              // [rows]: the pair of each row; the token of pair q is q / k
     int k, xrows;                 // GROUP 1: X's rows are the tokens
     const float *gscale, *up_gscale;   // [E], or null (1)
-    const int *xexp;              // GROUP 2: exponents of X's rows, [rows][nexp]
+    const int *xexp;              // GROUP 2: exponents of X's rows, [rows][nexp], or MODE 2: [rows]
     int *hexp;                    // MODE 1: of the rows it writes, likewise
     int nexp;                     // an even number
     long long cstride, sstride;   // bytes of an expert's codes and scales
@@ -99,7 +99,8 @@ __device__ __forceinline__ f32x2 scales2(u32 w)
 // loads (no copy of X in the experts' order: 168 MB of it for 1500 tokens of
 // 5120 columns with 8 experts each); 2: X's rows are in the experts' order
 // themselves, values between two products as fp16 with an exponent for each 64
-// columns (store_block).  A lane multiplies its operands by 2 to the difference from
+// columns (store_block; of MODE 2 one for a row, which its producer can know: without
+// the lanes' products 128 x 64 tiles take 57 us where they took 68).  A lane multiplies its operands by 2 to the difference from
 // the row's largest exponent, at most 1 and exact down to 2^-25 of the row's largest
 // value, and the sums are scaled by the latter.  One bf16 number for a value adds as
 // much to the result's error as the result's own rounding (2.3e-3 of the norm against
@@ -212,6 +213,7 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
     const unsigned ldss = lds_address(lds[kg]) + kSlice + wave * RG * 128;
 
     // GROUP 2: the tokens of this lane's operands, and the largest exponent of each
+    constexpr bool kBlocks = GROUP == 2 && MODE == 0;   // an exponent for each 64 columns
     constexpr int NE = GROUP == 2 ? TB / 2 : 1;
     const int *xexp[NE];
     int top[NE], ex[NE][2];
@@ -219,7 +221,7 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
     if constexpr (GROUP == 2) {
 #pragma unroll
         for (int t = 0; t < NE; ++t)
-            xexp[t] = p.xexp + (long long)min(tok0 + 32 * t + (lane & 31), tok1 - 1) * p.nexp;
+            xexp[t] = p.xexp + (long long)min(tok0 + 32 * t + (lane & 31), tok1 - 1) * (kBlocks ? p.nexp : 1);
     }
     // (lanes l and l + 32 take every other pair of a token's, eight loads at a time)
     auto find_tops = [&]() {
@@ -227,7 +229,9 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
 #pragma unroll
         for (int t = 0; t < NE; ++t)
             top[t] = kNoExponent;
-        for (int b0 = 2 * (lane >> 5); b0 < used; b0 += 32) {
+        for (int t = 0; !kBlocks && t < NE; ++t)
+            top[t] = *xexp[t];
+        for (int b0 = 2 * (lane >> 5); kBlocks && b0 < used; b0 += 32) {
             u32x2 v[NE][8];
 #pragma unroll
             for (int q = 0; q < 8; ++q)
@@ -245,7 +249,8 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
         }
 #pragma unroll
         for (int t = 0; t < NE; ++t) {
-            top[t] = max(top[t], __shfl_xor(top[t], 32));
+            if constexpr (kBlocks)
+                top[t] = max(top[t], __shfl_xor(top[t], 32));
             if (tid < 32)
                 tops[32 * t + tid] = top[t];
         }
@@ -270,7 +275,7 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
 #pragma unroll
         for (int r = 0; r < RG; ++r)
             cw[r] = buffer_load_b128(crsrc, (unsigned)((r * p.T + s) * 1024 + lane * 16));
-        if constexpr (GROUP == 2) {
+        if constexpr (kBlocks) {
 #pragma unroll
             for (int t = 0; t < NE; ++t) {
                 const u32x2 v = *reinterpret_cast<const u32x2 *>(xexp[t] + 2 * s);
@@ -284,7 +289,7 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
 #pragma unroll
         for (int r = 0; r < RG; ++r)
             asm volatile("" : "+v"(cw[r]));
-        if constexpr (GROUP == 2) {
+        if constexpr (kBlocks) {
 #pragma unroll
             for (int t = 0; t < NE; ++t)
                 asm volatile("" : "+v"(ex[t][0]), "+v"(ex[t][1]));
@@ -379,9 +384,13 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
                 const u32x4 a = *reinterpret_cast<const u32x4 *>(buf + x0 + t * 8 * kQuad + 64 * j);
                 const u32x4 d = *reinterpret_cast<const u32x4 *>(buf + x1 + t * 8 * kQuad + 64 * j);
                 if constexpr (GROUP == 2) {
-                    const f16x2 f = factor[t][j >> 1];
-                    const f16x8 f8 = {f[0], f[1], f[0], f[1], f[0], f[1], f[0], f[1]};
-                    const f16x8 af = __builtin_bit_cast(f16x8, a) * f8, df = __builtin_bit_cast(f16x8, d) * f8;
+                    f16x8 af = __builtin_bit_cast(f16x8, a), df = __builtin_bit_cast(f16x8, d);
+                    if constexpr (kBlocks) {
+                        const f16x2 f = factor[t][j >> 1];
+                        const f16x8 f8 = {f[0], f[1], f[0], f[1], f[0], f[1], f[0], f[1]};
+                        af *= f8;
+                        df *= f8;
+                    }
 #pragma unroll
                     for (int r = 0; r < RP; ++r)
                         acc[r][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, w[j & 1][r][0]), af,
@@ -418,7 +427,7 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
         for (int r = 0; r < RG; ++r)
             c[r] = cw[r];
         f16x2 factor[NE][2];
-        if constexpr (GROUP == 2) {
+        if constexpr (kBlocks) {
 #pragma unroll
             for (int t = 0; t < NE; ++t)
 #pragma unroll
@@ -546,7 +555,7 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
                         y[v] = in ? activate(z[v], decltype(act)::value) * u[v] : 0.f;
-                    const int exponent = block_exponent(row_max<16>(top_bits(y)));
+                    const int exponent = block_exponent(row_max(top_bits(y)));
                     if (in) {
                         store_block(static_cast<uint16_t *>(p.e.out) + (long long)tok * p.e.ldo + r, y, exponent);
                         if (r % 64 == 0)

@@ -493,14 +493,17 @@ __global__ __launch_bounds__(256) void nvfp4_moe_combine_kernel(nvfp4_epi_params
 
 // One workgroup a pair: with d = dY . Wd (for weight one), the weight's gradient
 // is the dot product of d with h = act(G) U, unrounded; dG = w d U act'(G) and dU
-// = w d act(G), times their tensor scales, become operands of the next product,
-// fp16 with an exponent for each 64 (as bf16, dX was off by 2.3e-3 of its norm, of
-// which its own rounding is 1.7e-3).  Memory bound: 2800 pairs of F = 1280 take 13 us
-// for 57 MB.
+// = w d act(G), times their tensor scales, become operands of the next product, fp16
+// with an exponent for the row (as bf16, dX was off by 2.3e-3 of its norm, of which
+// its own rounding is 1.7e-3).  They stay in registers until the row's largest is
+// known, kHeldTurns a thread; of longer rows the rest is computed again.  Memory
+// bound: 2800 pairs of F = 1280 take 13 us for 57 MB.
+constexpr int kHeldTurns = 4;
+
 __global__ __launch_bounds__(256) void nvfp4_moe_grad_kernel(const float *d, const float *preact, const int *position,
                                                              const int *experts, const float *weights, const float *gscale,
-                                                             float *dweights, uint16_t *dz, int *dzexp, int nexp, long long ldp,
-                                                             int E, int F, int act)
+                                                             float *dweights, uint16_t *dz, int *dzexp, long long ldp, int E,
+                                                             int F, int act)
 {
     const int q = blockIdx.x, tid = threadIdx.x;
     const int row = position[q];
@@ -514,36 +517,66 @@ __global__ __launch_bounds__(256) void nvfp4_moe_grad_kernel(const float *d, con
     const float *src = preact + (long long)row * ldp;
     uint16_t *dst = dz + (long long)row * 2 * F;
     float dot = 0.f;
-    for (int c = tid * 4; c < F; c += 1024) {
+    struct Grads {
+        f32x4 g, u;
+    };
+    auto grads = [&](int c) {
         const f32x4 dh = *reinterpret_cast<const f32x4 *>(d + (long long)row * F + c);
         const f32x4 g = *reinterpret_cast<const f32x4 *>(src + gated_row(c, 0));
         const f32x4 u = *reinterpret_cast<const f32x4 *>(src + gated_row(c, 1));
-        f32x4 dg, du;
+        Grads r;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float a = activate(g[j], act);
             dot = __builtin_fmaf(dh[j], a * u[j], dot);
-            dg[j] = w * dh[j] * u[j] * activate_grad(g[j], act) * gg;
-            du[j] = w * dh[j] * a * gu;
+            r.g[j] = w * dh[j] * u[j] * activate_grad(g[j], act) * gg;
+            r.u[j] = w * dh[j] * a * gu;
         }
-        if (dz) {
-            // eight lanes: 32 columns of both
-            const int exponent = block_exponent(row_max<8>(max(top_bits(dg), top_bits(du))));
-            store_block(dst + gated_row(c, 0), dg, exponent);
-            store_block(dst + gated_row(c, 1), du, exponent);
-            if (c % 32 == 0)
-                dzexp[(long long)row * nexp + c / 32] = exponent;
+        return r;
+    };
+    Grads held[kHeldTurns];
+    u32 top = 0;
+    static_for<kHeldTurns>([&](auto jc) {
+        constexpr int j = decltype(jc)::value;
+        const int c = tid * 4 + 1024 * j;
+        if (c < F) {
+            held[j] = grads(c);
+            top = max(top, max(top_bits(held[j].g), top_bits(held[j].u)));
         }
+    });
+    for (int c = tid * 4 + 1024 * kHeldTurns; c < F; c += 1024) {
+        const Grads r = grads(c);
+        top = max(top, max(top_bits(r.g), top_bits(r.u)));
     }
-    if (!dweights)
-        return;
     __shared__ float part[4];
+    __shared__ u32 tops[4];
     dot = wave_sum(dot);
-    if ((tid & 63) == 0)
+    top = wave_max(top);
+    if ((tid & 63) == 0) {
         part[tid >> 6] = dot;
+        tops[tid >> 6] = top;
+    }
     __syncthreads();
-    if (tid == 0)
+    if (tid == 0 && dweights)
         dweights[q] = (part[0] + part[1]) + (part[2] + part[3]);
+    if (!dz)
+        return;
+    const int exponent = block_exponent(max(max(tops[0], tops[1]), max(tops[2], tops[3])));
+    if (tid == 0)
+        dzexp[row] = exponent;
+    static_for<kHeldTurns>([&](auto jc) {
+        constexpr int j = decltype(jc)::value;
+        const int c = tid * 4 + 1024 * j;
+        if (c < F) {
+            store_block(dst + gated_row(c, 0), held[j].g, exponent);
+            store_block(dst + gated_row(c, 1), held[j].u, exponent);
+        }
+    });
+    for (int c = tid * 4 + 1024 * kHeldTurns; c < F; c += 1024) {
+        const Grads r = grads(c);
+        store_block(dst + gated_row(c, 0), r.g, exponent);
+        store_block(dst + gated_row(c, 1), r.u, exponent);
+    }
 }
 
 // bf16 rows of an fp32 or unaligned matrix, for the product.
@@ -649,15 +682,15 @@ Bytes expert_bytes(const nvfp4_experts *w, bool transposed)
                               nvfp4_packed_codes_bytes(w->K, w->F), nvfp4_packed_scales_bytes(w->K, w->F)};
 }
 
-// Exponents of a row of `cols` values between two products: one for 64, an even number.
-int exponents(int cols)
+// Exponents of a row of h: one for 64 columns, an even number.
+int exponents(int F)
 {
-    return (cols + 127) / 128 * 2;
+    return (F + 127) / 128 * 2;
 }
 
-size_t exponents_bytes(int rows, int cols)
+size_t exponents_bytes(int rows, int F)
 {
-    return round256((size_t)rows * exponents(cols) * 4);
+    return round256((size_t)rows * exponents(F) * 4);
 }
 
 // Workspace of a forward call of several tokens: the order, h with its exponents and
@@ -676,7 +709,7 @@ size_t backward_bytes(int n, int k, const nvfp4_experts *w, bool dx, bool copy)
     if (copy)
         b += round256((size_t)m * w->K * 2);
     if (dx)
-        b += round256((size_t)pairs * w->F * 4) + exponents_bytes(pairs, 2 * w->F) + round256((size_t)pairs * w->K * 4);
+        b += round256((size_t)pairs * w->F * 4) + round256((size_t)pairs * 4) + round256((size_t)pairs * w->K * 4);
     return b;
 }
 
@@ -1021,7 +1054,7 @@ int nvfp4_moe_backward(const nvfp4_experts *wt, const void *dY, int dy_dtype, in
         uint16_t *dz = dX ? reinterpret_cast<uint16_t *>(ws) : nullptr;
         ws += dX ? round256((size_t)pairs * F * 4) : 0;
         int *dzexp = reinterpret_cast<int *>(ws);
-        ws += dX ? exponents_bytes(pairs, 2 * F) : 0;
+        ws += dX ? round256((size_t)pairs * 4) : 0;
         float *rows = reinterpret_cast<float *>(ws);
         const int *ids = experts + (size_t)t0 * k;
         st = launch_sort(o, ids, pairs, E, tokens, s);
@@ -1051,8 +1084,7 @@ int nvfp4_moe_backward(const nvfp4_experts *wt, const void *dY, int dy_dtype, in
             break;
         hipLaunchKernelGGL(nvfp4_moe_grad_kernel, dim3((unsigned)pairs), dim3(256), 0, s, d, preact + (size_t)t0 * k * ldp,
                            o.position, ids, weights + (size_t)t0 * k, wt->gscale,
-                           dweights ? dweights + (size_t)t0 * k : nullptr, dz, dzexp, exponents(2 * F), (long long)ldp, E, F,
-                           activation);
+                           dweights ? dweights + (size_t)t0 * k : nullptr, dz, dzexp, (long long)ldp, E, F, activation);
         st = hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
         if (!dX || st != NVFP4_OK)
             continue;
@@ -1063,7 +1095,6 @@ int nvfp4_moe_backward(const nvfp4_experts *wt, const void *dY, int dy_dtype, in
         a.sstride = (long long)b.gu_scales;
         a.X = dz;
         a.xexp = dzexp;
-        a.nexp = exponents(2 * F);
         a.ldx = 2 * (long long)F;
         a.K = 2 * F;
         a.row_groups = K / kRowsPerGroup;
