@@ -98,15 +98,19 @@ __device__ __forceinline__ f32x2 scales2(u32 w)
 // rows of X are gathered through `pair`, by the vector offset of the LDS-direct
 // loads (no copy of X in the experts' order: 168 MB of it for 1500 tokens of
 // 5120 columns with 8 experts each); 2: X's rows are in the experts' order
-// themselves, values between two products as fp16 with an exponent for each 64
-// columns (store_block; of MODE 2 one for a row, which its producer can know: without
-// the lanes' products 128 x 64 tiles take 57 us where they took 68).  A lane multiplies its operands by 2 to the difference from
-// the row's largest exponent, at most 1 and exact down to 2^-25 of the row's largest
-// value, and the sums are scaled by the latter.  One bf16 number for a value adds as
-// much to the result's error as the result's own rounding (2.3e-3 of the norm against
+// themselves, values between two products as fp16 (store_block), of MODE 2 with an
+// exponent for a row, which its producer can know, of MODE 0 with one for each 64
+// columns.  There a lane multiplies its operands by 2 to the difference from the
+// row's largest exponent, at most 1 and exact down to 2^-24 of the row's largest
+// value; the sums are scaled by the latter.  One bf16 number for a value adds as much
+// to the result's error as the result's own rounding (2.3e-3 of the norm against
 // 1.7e-3); two bf16 parts, added by a second matrix instruction, take twice the
-// tokens' LDS: E = 64, F = 1408, K = 5120, n = 1500, k = 8: 833 us for the layer
-// against 711, 692 with one bf16 number.
+// tokens' LDS.  E = 64, F = 1408, K = 5120, n = 1500, k = 8, the down product: 237 us,
+// 220 from one bf16 number (without the lanes' products where a step's exponents are
+// alike, in a second copy of the loop's body: 275, it takes too many registers);
+// E = 32, F = 1280, K = 2048, n = 700, k = 4, the gradient's: 50, 68 with an exponent
+// for each 64, 55 from bf16.  (fp16 has a packed product, so that the weights'
+// dequantisation is shorter than to bf16.)
 //
 // LDS layout of the slice: token t's 16-byte chunk c (8 columns) at
 //     (t / 4) * kQuad + (t % 4) * 256 + (c ^ (t % 4)) * 16.
