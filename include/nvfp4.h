@@ -472,13 +472,13 @@ typedef struct nvfp4_experts {
  * counts twice.  X rows as nvfp4_linear's, ldx at most 2^18.  epilogue: activation,
  * residual (it may be Y itself), out_dtype, and preact: fp32 [n k][ldp >= 2 F]
  * receives the pre-activations for nvfp4_moe_backward, its rows in the order of
- * the experts (rows of slots without an expert are left as they were); biases
- * NULL.  h = act() * (), an operand of the matrix instructions, is held to 16
+ * the experts within each part (below; rows of slots without an expert are left as
+ * they were); biases NULL.  h = act() * (), an operand of the matrix instructions, is held to 16
  * significant bits up to 16 tokens, else to 11, down to 2^-24 of its row's largest
  * value; all sums are fp32.
  * Up to 16 tokens (K up to 8192, no preact) take two launches, and a token's
- * result does not depend on the others there; more are sorted by expert, 2^16
- * pairs at a time.  Workspace: nvfp4_moe_workspace_bytes, 16-byte aligned, with
+ * result does not depend on the others there; more are sorted by expert, in parts
+ * of 2^16 / k tokens (fewer where K is above about 16000 k).  Workspace: nvfp4_moe_workspace_bytes, 16-byte aligned, with
  * preact 1 where it is given.
  * Errors: NULL, RANGE, SHAPE, ALIGN, OVERLAP, WORKSPACE, DEVICE, LAUNCH. */
 int nvfp4_moe(const nvfp4_experts *w, const uint16_t *X, int64_t ldx, const int32_t *experts,

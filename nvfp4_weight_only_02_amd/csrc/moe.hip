@@ -579,7 +579,8 @@ __global__ __launch_bounds__(256) void nvfp4_moe_grad_kernel(const float *d, con
     }
 }
 
-// bf16 rows of an fp32 or unaligned matrix, for the product.
+// bf16 rows of an fp32 or unaligned matrix, or of one whose rows lie far apart, for the
+// product.
 __global__ __launch_bounds__(256) void nvfp4_moe_rows_kernel(const void *src, int f32, long long ld, int n, int cols,
                                                              uint16_t *dst)
 {
@@ -596,12 +597,22 @@ size_t round256(size_t bytes)
     return (bytes + 255) / 256 * 256;
 }
 
-// Tokens handled at a time: bounded work memory, and offsets of X (below the
-// 0x7FFFFFF0 that stands for "outside") within 32 bits.
-int chunk_tokens(int k, int64_t ldx)
+// Tokens handled at a time: bounded work memory, and offsets of their rows (below
+// the 0x7FFFFFF0 that stands for "outside") within 32 bits.  By k and K alone: the
+// pre-activations are in the experts' order within such a chunk, so the forward and
+// the backward call cut the tokens alike, whatever strides their rows have.
+constexpr int64_t kMaxOffset = 0x7FFF0000LL / 2 - kMaxLd;   // in elements
+
+int chunk_tokens(int k, int K)
 {
-    const int by_pairs = kChunkPairs / k, by_bytes = (int)((0x7FFF0000LL / 2 - kMaxLd) / (ldx < 1 ? 1 : ldx));
+    const int by_pairs = kChunkPairs / k, by_bytes = (int)(kMaxOffset / K);
     return by_pairs < by_bytes ? by_pairs : by_bytes;
+}
+
+// Whether a chunk's rows lie too far apart for 32 bits: they are copied next to each other.
+bool far_apart(int tokens, int64_t ld)
+{
+    return tokens > 1 && tokens * ld > kMaxOffset;
 }
 
 bool is_few(int n, int K)
@@ -631,6 +642,13 @@ int launch_sort(const Order &o, const int *experts, int pairs, int E, int tile_t
 {
     hipLaunchKernelGGL(nvfp4_moe_sort_kernel, dim3(1), dim3(1024), 0, stream, experts, pairs, E,
                        tile_tokens, o.position, o.pair, o.offset, o.tile);
+    return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
+}
+
+int launch_rows(const void *src, bool f32, long long ld, int n, int cols, uint16_t *dst, hipStream_t stream)
+{
+    hipLaunchKernelGGL(nvfp4_moe_rows_kernel, dim3((unsigned)(((long long)n * cols + 255) / 256)), dim3(256), 0, stream, src, f32,
+                       ld, n, cols, dst);
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
 }
 
@@ -702,14 +720,16 @@ size_t forward_bytes(int n, int k, const nvfp4_experts *w)
            round256((size_t)pairs * w->K * 4);
 }
 
+// (a copy of dY, which the first product reads, lies where the last one's rows will,
+// or without them in a place of its own)
 size_t backward_bytes(int n, int k, const nvfp4_experts *w, bool dx, bool copy)
 {
     const int by_pairs = kChunkPairs / k, m = n < by_pairs ? n : by_pairs, pairs = m * k;
     size_t b = order_bytes(pairs, w->E) + round256((size_t)pairs * w->F * 4);
-    if (copy)
-        b += round256((size_t)m * w->K * 2);
     if (dx)
         b += round256((size_t)pairs * w->F * 4) + round256((size_t)pairs * 4) + round256((size_t)pairs * w->K * 4);
+    else if (copy || far_apart(m, kMaxLd))
+        b += round256((size_t)m * w->K * 2);
     return b;
 }
 
@@ -903,7 +923,7 @@ int nvfp4_moe(const nvfp4_experts *w, const uint16_t *X, int64_t ldx, const int3
     }
     int cus = 0;
     st = nvfp4_device_cus(&cus);
-    const int step = chunk_tokens(k, n > 1 ? ldx : K);
+    const int step = chunk_tokens(k, K);
     for (int t0 = 0; t0 < n && st == NVFP4_OK; t0 += step) {
         const int m = n - t0 < step ? n - t0 : step, pairs = m * k, tokens = nvfp4_moe_tile_tokens(pairs, E, F);
         char *ws = static_cast<char *>(workspace);
@@ -913,6 +933,16 @@ int nvfp4_moe(const nvfp4_experts *w, const uint16_t *X, int64_t ldx, const int3
         ws += round256((size_t)pairs * F * 2);
         int *hexp = reinterpret_cast<int *>(ws);
         float *rows = reinterpret_cast<float *>(ws + exponents_bytes(pairs, F));
+        const uint16_t *x = X + (size_t)t0 * ldx;
+        long long ld = ldx;
+        if (far_apart(m, ldx)) {
+            uint16_t *near = reinterpret_cast<uint16_t *>(rows);   // (which the second product writes)
+            st = launch_rows(x, false, ldx, m, K, near, s);
+            if (st != NVFP4_OK)
+                break;
+            x = near;
+            ld = K;
+        }
         st = launch_sort(o, experts + (size_t)t0 * k, pairs, E, tokens, s);
         if (st != NVFP4_OK)
             break;
@@ -923,8 +953,8 @@ int nvfp4_moe(const nvfp4_experts *w, const uint16_t *X, int64_t ldx, const int3
         a.scales = w->gate_up_scales;
         a.cstride = (long long)b.gu_codes;
         a.sstride = (long long)b.gu_scales;
-        a.X = X + (size_t)t0 * ldx;
-        a.ldx = ldx;
+        a.X = x;
+        a.ldx = ld;
         a.xrows = m;
         a.k = k;
         a.rows = pairs;
@@ -1032,7 +1062,7 @@ int nvfp4_moe_backward(const nvfp4_experts *wt, const void *dY, int dy_dtype, in
     int cus = 0;
     st = nvfp4_device_cus(&cus);
     hipStream_t s = (hipStream_t)stream;
-    const int step = chunk_tokens(k, n > 1 ? ldy : K);
+    const int step = chunk_tokens(k, K);
     for (int t0 = 0; t0 < n && st == NVFP4_OK; t0 += step) {
         const int m = n - t0 < step ? n - t0 : step, pairs = m * k, tokens = nvfp4_moe_tile_tokens(pairs, E, F);
         char *ws = static_cast<char *>(workspace);
@@ -1040,22 +1070,22 @@ int nvfp4_moe_backward(const nvfp4_experts *wt, const void *dY, int dy_dtype, in
         ws += order_bytes(pairs, E);
         float *d = reinterpret_cast<float *>(ws);
         ws += round256((size_t)pairs * F * 4);
-        const uint16_t *dy = static_cast<const uint16_t *>(dY) + (size_t)t0 * ldy;
-        long long ld = ldy;
-        if (copy) {
-            const char *from = static_cast<const char *>(dY) + (size_t)t0 * ldy * ds;
-            uint16_t *to = reinterpret_cast<uint16_t *>(ws);
-            ws += round256((size_t)m * K * 2);
-            hipLaunchKernelGGL(nvfp4_moe_rows_kernel, dim3((unsigned)(((long long)m * K + 255) / 256)), dim3(256), 0, s, from,
-                               dy_dtype == NVFP4_DTYPE_F32, (long long)ldy, m, K, to);
-            dy = to;
-            ld = K;
-        }
         uint16_t *dz = dX ? reinterpret_cast<uint16_t *>(ws) : nullptr;
         ws += dX ? round256((size_t)pairs * F * 4) : 0;
         int *dzexp = reinterpret_cast<int *>(ws);
         ws += dX ? round256((size_t)pairs * 4) : 0;
         float *rows = reinterpret_cast<float *>(ws);
+        const char *from = static_cast<const char *>(dY) + (size_t)t0 * ldy * ds;
+        const uint16_t *dy = reinterpret_cast<const uint16_t *>(from);
+        long long ld = ldy;
+        if (copy || far_apart(m, ldy)) {
+            uint16_t *near = reinterpret_cast<uint16_t *>(ws);
+            st = launch_rows(from, dy_dtype == NVFP4_DTYPE_F32, ldy, m, K, near, s);
+            if (st != NVFP4_OK)
+                break;
+            dy = near;
+            ld = K;
+        }
         const int *ids = experts + (size_t)t0 * k;
         st = launch_sort(o, ids, pairs, E, tokens, s);
         if (st != NVFP4_OK)

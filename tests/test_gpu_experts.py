@@ -9,7 +9,7 @@ import experts_reference as X8
 import fused_reference as R
 import nvfp4_weight_only_02_amd as nv
 import oracle as O
-from nvfp4_weight_only_02_amd import inputs
+from nvfp4_weight_only_02_amd import experts, inputs
 
 pytestmark = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
@@ -525,6 +525,35 @@ def test_several_chunks():
         assert torch.equal(part, pre[a * k:b * k])
         x, d = nv.moe_backward(wt, dY[a:b], e[a:b], c[a:b], part)
         assert torch.equal(x, dX[a:b]) and torch.equal(d, dc[a:b])
+
+
+@pytest.mark.parametrize("wide", ["X", "dY", "both"])
+def test_chunks_do_not_depend_on_the_strides(wide):
+    """Rows so far apart that fewer of them than a chunk's fit 32-bit offsets, in
+    one direction or both: the bits of the same rows next to each other.  The
+    pre-activations are in the experts' order within a chunk, so that both
+    directions have to cut the tokens alike."""
+    say("moe chunk strides", wide)
+    E, F, K, k, n, ld = 4, 32, 48, 1, 5000, 1 << 18       # 4094 rows of this stride
+    w, Wg, Wu, Wd = weights(E, F, K, 300)
+    wt = w.transpose()
+    X, dY, (e, c) = randn((n, K), 301), randn((n, K), 302), choices(n, k, E, 303)
+
+    def apart(t):
+        rows = torch.empty(n, ld, device="cuda", dtype=BF16)[:, 64:64 + K]
+        rows.copy_(t)
+        return rows
+    Xs, dYs = apart(X) if wide != "dY" else X, apart(dY) if wide != "X" else dY
+    pre, pres = (torch.zeros(n * k, 2 * F, device="cuda") for _ in range(2))
+    Y, Ys = nv.moe(w, X, e, c, preact=pre), nv.moe(w, Xs, e, c, preact=pres)
+    assert torch.equal(Ys, Y) and torch.equal(pres, pre)
+    for need_x in (True, False):
+        got, want = (experts._moe_backward(wt, g, e, c, p, 2, need_x, True, None, None) for g, p in ((dYs, pres), (dY, pre)))
+        assert torch.equal(got[1], want[1]) and (not need_x or torch.equal(got[0], want[0]))
+    dX, dc = nv.moe_backward(wt, dYs, e, c, pres)
+    x, d = X8.moe_grads(f64(X), Wg, Wu, Wd, e.cpu().numpy(), f64(c), f64(dY))
+    check(dX, x, "dX")
+    check(dc, d, "dweights")
 
 
 # ---- together, streams, graphs -------------------------------------------------------------
