@@ -491,6 +491,11 @@ size_t nvfp4_moe_workspace_bytes(int n, int k, int E, int F, int K, int preact);
  * (NULL, RANGE, SHAPE). */
 int nvfp4_moe_geometry(int n, int k, int E, int F, int K, int *rows_per_workgroup, int *tokens_per_workgroup);
 
+/* Outputs of a workgroup in the down projection of up to 16 tokens on a device of
+ * so many compute units (any number: K / outputs workgroups).  Pure host function;
+ * returns a status (NULL, RANGE, SHAPE: K not a multiple of 16 up to 8192). */
+int nvfp4_moe_decode_geometry(int K, int compute_units, int *outputs_per_workgroup);
+
 /* The gradients of nvfp4_moe, on the transposed copies: dX bf16 [n][ldx] (NULL:
  * not wanted) and dweights fp32 [n][k] (NULL: not wanted; 0 where there is no
  * expert).  dY fp32 or bf16 [n][ldy], ldy at most 2^18; it is rounded to bf16, an

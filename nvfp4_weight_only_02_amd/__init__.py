@@ -417,5 +417,5 @@ def gemv_qkv(w: PackedWeight, X: torch.Tensor, rows, out_off, ldy: int,
 from .fused import (ACTIVATIONS, GatedWeight, TransposedWeight, fused_geometry, gated, gated_backward,  # noqa: E402
                     gated_rows, gemm_t, linear, linear_backward, preact_columns, transpose)
 from .experts import (ExpertWeights, TransposedExperts, moe, moe_backward, moe_route, moe_route_backward,  # noqa: E402
-                  moe_geometry, moe_workspace_bytes)
+                  moe_decode_geometry, moe_geometry, moe_workspace_bytes)
 from .int8 import Int8Weight, int8_geometry, int8_linear, int8_linear_workspace_bytes, int8_quantize  # noqa: E402

@@ -494,7 +494,8 @@ __global__ __launch_bounds__(kThreads, 4) void nvfp4_moe_down_kernel(MoeFewParam
     }
 }
 
-static_assert(kFewTokens * 32 <= kThreads, "a thread for each output of a workgroup");
+constexpr int kMaxDownRows = 32;   // two windows
+static_assert(kFewTokens * kMaxDownRows <= kThreads, "a thread for each output of a workgroup");
 
 typedef void (*FewKernel)(MoeFewParams);
 
@@ -504,6 +505,14 @@ FewKernel pick_up(int mt, std::integer_sequence<int, MT...>)
     FewKernel k = nullptr;
     ((mt == MT + 1 ? (void)(k = nvfp4_moe_up_kernel<MT + 1, NV>) : (void)0), ...);
     return k;
+}
+
+// Outputs of a workgroup of the down projection: in fours, so that every compute unit
+// has a workgroup; of few units some have several.
+int down_rows(int K, int cus)
+{
+    const long long each = 4LL * cus, rows = (K + each - 1) / each * 4;
+    return rows < kMaxDownRows ? (int)rows : kMaxDownRows;
 }
 
 // Waves that share an expert's down projection: a function of the layer's k, so
@@ -521,6 +530,18 @@ int down_split(int k, int Td)
 bool nvfp4_moe_is_few(int n, int K)
 {
     return n <= kFewTokens && K <= kWaves * kMaxTilesPerWave * kTileK;
+}
+
+int nvfp4_moe_decode_geometry(int K, int compute_units, int *outputs_per_workgroup)
+{
+    if (!outputs_per_workgroup)
+        return NVFP4_ERR_NULL;
+    if (K < 1 || compute_units < 1)
+        return NVFP4_ERR_RANGE;
+    if (K % 16 != 0 || !nvfp4_moe_is_few(1, K))
+        return NVFP4_ERR_SHAPE;
+    *outputs_per_workgroup = down_rows(K, compute_units);
+    return NVFP4_OK;
 }
 
 size_t nvfp4_moe_few_bytes(int n, int k, int F)
@@ -565,11 +586,8 @@ int nvfp4_launch_moe_few(const nvfp4_moe_few_args &a, hipStream_t stream)
     hipLaunchKernelGGL(up, dim3((unsigned)(most < cus ? most : cus)), dim3(kThreads), 0, stream, p);
     if (hipGetLastError() != hipSuccess)
         return NVFP4_ERR_LAUNCH;
-    // Rows in fours, so that every compute unit has a workgroup; up to K = 8192, 32 of them.
-    p.rows = (a.K + 4 * cus - 1) / (4 * cus) * 4;
+    p.rows = down_rows(a.K, cus);
     const int nk = a.n * a.k, nw = (p.rows + 15) / 16;
-    if (nw > 2)
-        return NVFP4_ERR_SHAPE;
     const dim3 grid((unsigned)((a.K + p.rows - 1) / p.rows));
     // Six tiles ahead where the sums leave the LDS for it (of 160 KiB, of which the
     // kernel's own arrays take less than 10), else four.

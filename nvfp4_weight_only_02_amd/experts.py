@@ -40,6 +40,7 @@ _SIGNATURES = {
     "nvfp4_moe": (_i32, [_vp, _vp, _i64, _vp, _vp, _i32, _i32, _vp, _i64, _vp, _vp, _SIZE, _vp]),
     "nvfp4_moe_workspace_bytes": (_SIZE, [_i32] * 6),
     "nvfp4_moe_geometry": (_i32, [_i32] * 5 + [ctypes.POINTER(_i32)] * 2),
+    "nvfp4_moe_decode_geometry": (_i32, [_i32, _i32, ctypes.POINTER(_i32)]),
     "nvfp4_moe_backward": (_i32, [_vp, _vp, _i32, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _SIZE, _vp]),
     "nvfp4_moe_backward_workspace_bytes": (_SIZE, [_i32] * 7),
 }
@@ -415,6 +416,14 @@ def moe_geometry(n: int, k: int, E: int, F: int, K: int) -> tuple:
     v = [_i32() for _ in range(2)]
     _run("nvfp4_moe_geometry", n, k, E, F, K, *(ctypes.byref(x) for x in v))
     return tuple(x.value for x in v)
+
+
+def moe_decode_geometry(K: int, compute_units: int) -> int:
+    """Outputs of a workgroup in the down projection of ``moe`` for up to 16 tokens on
+    a device of so many compute units (nvfp4_moe_decode_geometry)."""
+    v = _i32()
+    _run("nvfp4_moe_decode_geometry", K, compute_units, ctypes.byref(v))
+    return v.value
 
 
 def moe_workspace_bytes(n: int, k: int, w: ExpertWeights, preact: bool = False) -> int:

@@ -198,6 +198,22 @@ def test_geometry():
     assert experts._call("nvfp4_moe_geometry")(17, 1, 1, 64, 64, None, None) == NULL
 
 
+def test_decode_geometry():
+    """Any number of compute units serves every K of the decode form: a device may be
+    partitioned into 2, 4 or 8."""
+    assert [nv.moe_decode_geometry(5120, c) for c in (256, 128, 64)] == [20, 32, 32]
+    assert nv.moe_decode_geometry(8192, 256) == 32 and nv.moe_decode_geometry(16, 256) == 4
+    for units in list(range(1, 40)) + [64, 80, 128, 160, 256, 304, (1 << 31) - 1]:
+        for K in range(16, 8193, 16):
+            r = nv.moe_decode_geometry(K, units)
+            assert 4 <= r <= 32 and r % 4 == 0 and (r == 32 or -(-K // r) <= units)
+    for a, status in (((0, 256), RANGE), ((64, 0), RANGE), ((72, 256), SHAPE), ((8208, 256), SHAPE)):
+        with pytest.raises(nv.Nvfp4Error) as e:
+            nv.moe_decode_geometry(*a)
+        assert e.value.status == status
+    assert experts._call("nvfp4_moe_decode_geometry")(64, 256, None) == NULL
+
+
 @settings(max_examples=300, deadline=None)
 @given(n=st.integers(17, 1 << 20), N=st.integers(1, 1 << 17), T=st.integers(1, 1023), tail=st.sampled_from([0, 16, 112]))
 def test_int8_geometry_rule(n, N, T, tail):
