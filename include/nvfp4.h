@@ -526,8 +526,8 @@ int nvfp4_int8_pack(const int8_t *codes, int N, int K, int8_t *packed, void *str
  * q = 127 x / amax rounded to the nearest integer, halves to the even one (for
  * bf16 exactly; fp32 after one rounding of each operation), amax the row's largest
  * magnitude.  A row of zeros has scale 0; a row that holds a NaN or an infinity
- * scale NaN and q 0.  X and q rows are 16-byte aligned.  Errors: NULL, RANGE,
- * SHAPE (K % 16), ALIGN, OVERLAP, DEVICE, LAUNCH. */
+ * scale NaN and q 0.  K is any multiple of 16 here.  X and q rows are 16-byte
+ * aligned.  Errors: NULL, RANGE, SHAPE (K % 16), ALIGN, OVERLAP, DEVICE, LAUNCH. */
 int nvfp4_int8_quantize(const void *X, int dtype, int64_t ldx, int n, int K, int8_t *q, int64_t ldq,
                         float *scale, void *stream);
 

@@ -89,17 +89,18 @@ __global__ __launch_bounds__(kQuantThreads) void nvfp4_int8_quantize_kernel(cons
     struct Vec {
         u32 v[8];   // fp32 bits
     };
+    // (a row may be longer than 2^31 bytes)
     auto fetch = [&](int c) {
         Vec r;
         if constexpr (F32) {
-            const u32x4 a = *reinterpret_cast<const u32x4 *>(row + c * 32), b = *reinterpret_cast<const u32x4 *>(row + c * 32 + 16);
+            const u32x4 a = *reinterpret_cast<const u32x4 *>(row + c * 32LL), b = *reinterpret_cast<const u32x4 *>(row + c * 32LL + 16);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 r.v[j] = a[j];
                 r.v[4 + j] = b[j];
             }
         } else {
-            const u32x4 a = *reinterpret_cast<const u32x4 *>(row + c * 16);
+            const u32x4 a = *reinterpret_cast<const u32x4 *>(row + c * 16LL);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 r.v[2 * j] = a[j] << 16;
@@ -149,7 +150,7 @@ __global__ __launch_bounds__(kQuantThreads) void nvfp4_int8_quantize_kernel(cons
         for (int e = 0; e < 8; ++e) {
             w[e / 4] |= (u32)(row_scale.quantize<F32>(r.v[e]) & 255) << (8 * (e % 4));
         }
-        *reinterpret_cast<u32x2 *>(q + t * ldq + c * 8) = u32x2{w[0], w[1]};
+        *reinterpret_cast<u32x2 *>(q + t * ldq + c * 8LL) = u32x2{w[0], w[1]};
     };
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {

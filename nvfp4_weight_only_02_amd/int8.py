@@ -60,17 +60,27 @@ class Int8Weight:
             raise ValueError("codes must be [N, K], got %s" % list(codes.shape))
         N, K = codes.shape
         _vec(scale, (torch.float32,), "scale", N)
-        size = int(_call("nvfp4_int8_packed_bytes")(N, K)) if N < 1 << 31 and K < 1 << 31 else 0
-        if not size:
-            raise ValueError("N must be 1 to 2^30 and K a multiple of 16 from 16 to 131056, got %d x %d" % (N, K))
+        size = cls._sizes(N, K)
         at = _Launch(stream, codes, scale)
         packed = at.alloc(size, dtype=torch.int8)
         _run("nvfp4_int8_pack", codes.data_ptr(), N, K, packed.data_ptr(), at.handle)
         return cls(packed, scale, N, K)
 
+    @staticmethod
+    def _sizes(N, K) -> int:
+        """Bytes of the packed codes."""
+        size = int(_call("nvfp4_int8_packed_bytes")(N, K)) if N < 1 << 31 and K < 1 << 31 else 0
+        if not size:
+            raise ValueError("N must be 1 to 2^30 and K a multiple of 16 from 16 to 131056, got %d x %d" % (N, K))
+        return size
+
     @classmethod
     def from_float(cls, W: torch.Tensor, stream=None) -> "Int8Weight":
         """Quantise an fp32 or bf16 weight [N, K], each row as ``int8_quantize`` does."""
+        _typed(W, _FLOATS, "W")
+        if W.dim() != 2:
+            raise ValueError("W must be [N, K], got %s" % list(W.shape))
+        cls._sizes(*W.shape)
         q, scale = int8_quantize(W, stream=stream)
         return cls.from_int8(q, scale, stream)
 

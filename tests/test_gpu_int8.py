@@ -79,6 +79,27 @@ def test_quantize_halves_and_every_pair_of_mantissas():
     assert np.array_equal(q.cpu().numpy(), rq) and np.array_equal(f64(s), rs)
 
 
+@pytest.mark.parametrize("dtype,K", [(F32, (1 << 29) + 16), (BF16, (1 << 30) + 16)])
+def test_quantize_rows_of_more_than_2_31_bytes(dtype, K):
+    say("quantize long", dtype, K)
+    X = torch.zeros(1, K, device="cuda", dtype=dtype)
+    X[0, 5], X[0, K // 2 + 3], X[0, K - 9], X[0, K - 1] = 1.0, -0.5, -2.0, 0.25
+    q, s = nv.int8_quantize(X)
+    assert f64(s)[0] == np.float32(2) / np.float32(127)
+    # 63.5, 31.75, 127 and 15.875 steps: halves go to the even integer
+    assert [int(q[0, c]) for c in (5, K // 2 + 3, K - 9, K - 1)] == [64, -32, -127, 16]
+    assert int(torch.count_nonzero(q)) == 4
+
+
+def test_from_float_refuses_a_row_too_long_before_reading_it():
+    say("int8 from_float long")
+    for K in (131072, 131064, 8):
+        with pytest.raises(ValueError):
+            nv.Int8Weight.from_float(torch.ones(1, 1, device="cuda").expand(2, K))
+    with pytest.raises(ValueError):
+        nv.Int8Weight.from_float(torch.ones(64, device="cuda"))
+
+
 def test_quantize_extremes():
     say("quantize extremes")
     X = randn((8, 64), 3)
