@@ -473,13 +473,14 @@ typedef struct nvfp4_experts {
  * residual (it may be Y itself), out_dtype, and preact: fp32 [n k][ldp >= 2 F]
  * receives the pre-activations for nvfp4_moe_backward, its rows in the order of
  * the experts within each part (below; rows of slots without an expert are left as
- * they were); biases NULL.  h = act() * (), an operand of the matrix instructions, is held to 16
- * significant bits up to 16 tokens, else to 11, down to 2^-24 of its row's largest
- * value; all sums are fp32.
+ * they were); biases NULL.  h = act() * (), an operand of the matrix instructions,
+ * is held to 16 significant bits up to 16 tokens; beyond (or with preact) to 11
+ * where Y is bf16, whose own rounding is to 8, and to 22 where Y is fp32, down to
+ * 2^-24 of its row's largest value; all sums are fp32.
  * Up to 16 tokens (K up to 8192, no preact) take two launches, and a token's
  * result does not depend on the others there; more are sorted by expert, in parts
- * of 2^16 / k tokens (fewer where K is above about 16000 k).  Workspace: nvfp4_moe_workspace_bytes, 16-byte aligned, with
- * preact 1 where it is given.
+ * of 2^16 / k tokens (fewer where K is above about 16000 k).  Workspace:
+ * nvfp4_moe_workspace_bytes, 16-byte aligned, with preact 1 where it is given.
  * Errors: NULL, RANGE, SHAPE, ALIGN, OVERLAP, WORKSPACE, DEVICE, LAUNCH. */
 int nvfp4_moe(const nvfp4_experts *w, const uint16_t *X, int64_t ldx, const int32_t *experts,
               const float *weights, int n, int k, void *Y, int64_t ldy, const nvfp4_epilogue *epilogue,
@@ -499,7 +500,8 @@ int nvfp4_moe_decode_geometry(int K, int compute_units, int *outputs_per_workgro
 /* The gradients of nvfp4_moe, on the transposed copies: dX bf16 [n][ldx] (NULL:
  * not wanted) and dweights fp32 [n][k] (NULL: not wanted; 0 where there is no
  * expert).  dY fp32 or bf16 [n][ldy], ldy at most 2^18; it is rounded to bf16, an
- * operand of the products; the gradients of the pre-activations are held as h is.
+ * operand of the products.  The gradients of the pre-activations are held to 11
+ * bits, as h of a bf16 result (dX, which they are summed to, is one).
  * preact as nvfp4_moe stored it.  The residual's gradient is dY itself.
  * Workspace: nvfp4_moe_backward_workspace_bytes with dx as it is wanted, copy =
  * 0 only if dY is bf16, 16-byte aligned and ldy a multiple of 8. */

@@ -229,9 +229,9 @@ __device__ __forceinline__ float bf16_rest(float v, uint16_t high)
     return (high & 0x7F80) == 0x7F80 ? 0.f : v - bf16_bits_to_f32(high);
 }
 
-// The same for many rows, in half the matrix instructions: a block of values of a row
-// as fp16 with a common exponent, 11 significant bits of those not far below its
-// largest, whose fp16 is between 2^14 and 2^15.
+// For many rows, in half the matrix instructions: a block of values of a row as fp16
+// with a common exponent, 11 significant bits of those not far below its largest,
+// whose fp16 is between 2^14 and 2^15.  A bf16 result's own rounding is to 8.
 
 // Bits of the largest magnitude.
 __device__ __forceinline__ u32 top_bits(const f32x4 v)
@@ -268,6 +268,24 @@ __device__ __forceinline__ void store_block(uint16_t *p, const f32x4 v, int expo
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         h[j] = __builtin_bit_cast(uint16_t, (_Float16)__builtin_amdgcn_ldexpf(v[j], -exponent));
+    *reinterpret_cast<u16x4 *>(p) = h;
+}
+
+// What store_block's fp16 numbers leave of v, 2^kRestBits times it, as fp16 too: both
+// hold 22 significant bits, for a product whose result is fp32.  (At most half a step
+// of a number below 2^15: 2^3, and 2^14 then.  Infinities and NaN are in the first
+// part alone.)
+constexpr int kRestBits = 11;
+
+__device__ __forceinline__ void store_block_rest(uint16_t *p, const f32x4 v, int exponent)
+{
+    u16x4 h;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float t = __builtin_amdgcn_ldexpf(v[j], -exponent), first = (float)(_Float16)t;
+        const float rest = fabsf(first) <= 65504.f ? (t - first) * (1 << kRestBits) : 0.f;
+        h[j] = __builtin_bit_cast(uint16_t, (_Float16)rest);
+    }
     *reinterpret_cast<u16x4 *>(p) = h;
 }
 

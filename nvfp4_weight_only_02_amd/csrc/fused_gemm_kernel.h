@@ -30,6 +30,9 @@ struct GroupedGemmParams : FusedGemmParams {
     const float *gscale, *up_gscale;   // [E], or null (1)
     const int *xexp;              // GROUP 2: exponents of X's rows, [rows][nexp], or MODE 2: [rows]
     int *hexp;                    // MODE 1: of the rows it writes, likewise
+    uint16_t *hrest;              // MODE 1: second parts of the rows (store_block_rest), or null
+    int rest;                     // 0; else X holds second parts: 1, or GROUP 2 (bits below the first ones'
+                                  // exponent) kRestBits.  The sums are added to the rows that are there
     int nexp;                     // an even number
     long long cstride, sstride;   // bytes of an expert's codes and scales
 };
@@ -526,15 +529,18 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
                 if (tx * kOuts + o >= p.e.N)
                     continue;
                 f32x4 v = staged(t, o);
+                f32x4 *dst = reinterpret_cast<f32x4 *>(static_cast<float *>(p.e.out) + (long long)tok * p.e.ldo + tx * kOuts + o);
                 if constexpr (GROUP == 2) {
-                    const int top = tops[32 * b + t];
+                    const int top = tops[32 * b + t] - p.rest;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         v[j] = __builtin_amdgcn_ldexpf(p.e.gscale * v[j], top);
                 } else {
                     v = p.e.gscale * v;
                 }
-                *reinterpret_cast<f32x4 *>(static_cast<float *>(p.e.out) + (long long)tok * p.e.ldo + tx * kOuts + o) = v;
+                if (p.rest)
+                    v += *dst;
+                *dst = v;
             }
             continue;
         } else if constexpr (GROUP) {
@@ -562,6 +568,8 @@ __global__ __launch_bounds__(64 * RW * KG, RW * KG <= 4 ? 2 : 1) void nvfp4_fuse
                     const int exponent = block_exponent(row_max(top_bits(y)));
                     if (in) {
                         store_block(static_cast<uint16_t *>(p.e.out) + (long long)tok * p.e.ldo + r, y, exponent);
+                        if (p.hrest)
+                            store_block_rest(p.hrest + (long long)tok * p.e.ldo + r, y, exponent);
                         if (r % 64 == 0)
                             p.hexp[(long long)tok * p.nexp + r / 64] = exponent;
                     }

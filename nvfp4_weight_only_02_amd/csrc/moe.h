@@ -21,6 +21,8 @@ struct nvfp4_moe_gemm_args {
     const int *xexp;              // of X, and of the rows of mode 1's output
     int *hexp;
     int nexp;                     // of a row
+    uint16_t *hrest;              // as GroupedGemmParams
+    int rest;
     long long ldx;
     int xrows, k;                 // rows of X (gather), experts of a token
     int rows, E;                  // at most so many rows

@@ -711,12 +711,12 @@ size_t exponents_bytes(int rows, int F)
     return round256((size_t)rows * exponents(F) * 4);
 }
 
-// Workspace of a forward call of several tokens: the order, h with its exponents and
-// the rows.
+// Workspace of a forward call of several tokens: the order, h with its exponents, its
+// second parts (of a call whose result is fp32) and the rows.
 size_t forward_bytes(int n, int k, const nvfp4_experts *w)
 {
     const int by_pairs = kChunkPairs / k, m = n < by_pairs ? n : by_pairs, pairs = m * k;
-    return order_bytes(pairs, w->E) + round256((size_t)pairs * w->F * 2) + exponents_bytes(pairs, w->F) +
+    return order_bytes(pairs, w->E) + 2 * round256((size_t)pairs * w->F * 2) + exponents_bytes(pairs, w->F) +
            round256((size_t)pairs * w->K * 4);
 }
 
@@ -931,6 +931,8 @@ int nvfp4_moe(const nvfp4_experts *w, const uint16_t *X, int64_t ldx, const int3
         ws += order_bytes(pairs, E);
         uint16_t *h = reinterpret_cast<uint16_t *>(ws);
         ws += round256((size_t)pairs * F * 2);
+        uint16_t *hrest = reinterpret_cast<uint16_t *>(ws);
+        ws += round256((size_t)pairs * F * 2);
         int *hexp = reinterpret_cast<int *>(ws);
         float *rows = reinterpret_cast<float *>(ws + exponents_bytes(pairs, F));
         const uint16_t *x = X + (size_t)t0 * ldx;
@@ -966,6 +968,7 @@ int nvfp4_moe(const nvfp4_experts *w, const uint16_t *X, int64_t ldx, const int3
         a.up_gscale = w->gscale + E;
         a.order = {o.tile, o.offset, o.pair};
         a.hexp = hexp;
+        a.hrest = ep.out_dtype == NVFP4_DTYPE_F32 ? hrest : nullptr;
         a.nexp = exponents(F);
         a.epi = plain_out(h, F, false, F);
         a.epi.flags |= ep.activation;
@@ -993,6 +996,13 @@ int nvfp4_moe(const nvfp4_experts *w, const uint16_t *X, int64_t ldx, const int3
         st = nvfp4_launch_moe_gemm(a, s);
         if (st != NVFP4_OK)
             break;
+        if (a.hrest) {
+            a.X = hrest;
+            a.rest = kRestBits;
+            st = nvfp4_launch_moe_gemm(a, s);
+            if (st != NVFP4_OK)
+                break;
+        }
         nvfp4_epi_params c = e;
         c.out = static_cast<char *>(e.out) + (size_t)t0 * ldy * os;
         if (c.residual)
@@ -1078,9 +1088,10 @@ int nvfp4_moe_backward(const nvfp4_experts *wt, const void *dY, int dy_dtype, in
         const char *from = static_cast<const char *>(dY) + (size_t)t0 * ldy * ds;
         const uint16_t *dy = reinterpret_cast<const uint16_t *>(from);
         long long ld = ldy;
+        const bool f32 = dy_dtype == NVFP4_DTYPE_F32;
+        uint16_t *near = reinterpret_cast<uint16_t *>(ws);
         if (copy || far_apart(m, ldy)) {
-            uint16_t *near = reinterpret_cast<uint16_t *>(ws);
-            st = launch_rows(from, dy_dtype == NVFP4_DTYPE_F32, ldy, m, K, near, s);
+            st = launch_rows(from, f32, ldy, m, K, near, s);
             if (st != NVFP4_OK)
                 break;
             dy = near;

@@ -78,6 +78,8 @@ int nvfp4_launch_moe_gemm(const nvfp4_moe_gemm_args &a, hipStream_t stream)
     p.xexp = a.xexp;
     p.hexp = a.hexp;
     p.nexp = a.nexp;
+    p.hrest = a.hrest;
+    p.rest = a.rest;
     p.gscale = a.gscale;
     p.up_gscale = a.up_gscale;
     p.cstride = a.cstride;

@@ -97,10 +97,25 @@ def _kept(v, e):
     return e + 2.0 ** -11 * a + 2.0 ** -24 * a.max(1, keepdims=True)
 
 
-def moe(X, Wg, Wu, Wd, experts, weights, kind="silu", residual=None, out_f32=False):
-    """(Y, bound): h kept to 11 bits (_kept) and its down projection, k weighted terms
-    (a weight is multiplied by the tensor scale first: 3 steps), the residual, the
-    last rounding."""
+def kept_in_bf16_parts(v, e):
+    """Two bf16 parts of a value (16 bits): half a step, 2^-8 relative, of what half a
+    step of the value left."""
+    return e + 2.0 ** -16 * (np.abs(v) + e)
+
+
+def kept_in_fp16_parts(v, e):
+    """_kept, and a second fp16 number of what the first one left, 2^11 times it: 2^-11
+    of 2^-11 relative.  (Below fp16's normal numbers half a step is 2^-25, 2^-39 of
+    the block's largest, and the second part's 2^-36 2^-14; the row's last term covers
+    both, as it covers blocks that are lost.)"""
+    a = np.abs(v) + e
+    return e + 2.0 ** -22 * a + 2.0 ** -24 * a.max(1, keepdims=True)
+
+
+def moe(X, Wg, Wu, Wd, experts, weights, kind="silu", residual=None, out_f32=False, kept=_kept):
+    """(Y, bound): h kept to 11 bits (_kept) or as `kept` says and its down projection,
+    k weighted terms (a weight is multiplied by the tensor scale first: 3 steps), the
+    residual, the last rounding."""
     n, k = experts.shape
     F, K = Wg.shape[1:]
     y, b, m = np.zeros((n, K)), np.zeros((n, K)), np.zeros((n, K))
@@ -110,7 +125,7 @@ def moe(X, Wg, Wu, Wd, experts, weights, kind="silu", residual=None, out_f32=Fal
         if not len(t):
             continue
         h, eh = R.gated(X[t], Wg[e], Wu[e], kind=kind, out_f32=True)
-        eh = _kept(h, eh)
+        eh = kept(h, eh)
         o = h @ Wd[e].T
         eo = eh @ np.abs(Wd[e]).T + (F + 32) * STEP * ((np.abs(h) + eh) @ np.abs(Wd[e]).T)
         w = weights[t, s][:, None]

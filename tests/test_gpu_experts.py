@@ -252,6 +252,51 @@ def test_values_between_the_products_of_any_size(n):
     check(dc, d, "dweights")
 
 
+@pytest.mark.parametrize("E,F,K,k", [(5, 16, 32, 2), (13, 48, 144, 3), (70, 16, 80, 8)])
+@pytest.mark.parametrize("act", ["none", "relu"])
+@pytest.mark.parametrize("n", [1, 5, 16, 17, 40, 150, 900])
+def test_bits_of_fp32_results(n, E, F, K, k, act):
+    """Where the result is fp32, h is held to 16 bits up to 16 tokens and to 22
+    beyond (or with pre-activations): sums short enough to show a lost bit."""
+    say("moe bits", n, E, F, K, k, act)
+    w, Wg, Wu, Wd = weights(E, F, K, 320)
+    X = randn((n, K), 321)
+    e, c = choices(n, k, E, 322)
+    args = f64(X), Wg, Wu, Wd, e.cpu().numpy(), f64(c), act, None, True
+    Y = nv.moe(w, X, e, c, act, out_dtype=F32)
+    check(Y, X8.moe(*args, kept=X8.kept_in_bf16_parts if n <= 16 else X8.kept_in_fp16_parts), "Y")
+    Y = nv.moe(w, X, e, c, act, out_dtype=F32, preact=torch.empty(n * k, 2 * F, device="cuda"))
+    check(Y, X8.moe(*args, kept=X8.kept_in_fp16_parts), "Y with preact")
+
+
+def test_bits_of_values_of_any_size():
+    """Columns of h over 2^40, blocks of zeros, and beside them a token with an infinity:
+    the second parts have the first ones' exponents and change nothing there."""
+    say("moe bits, sizes")
+    E, F, K, k, n = 3, 208, 32, 2, 40
+    g = torch.Generator(device="cuda").manual_seed(330)
+    spread = 2.0 ** torch.randint(-10, 11, (E, F, 1), generator=g, device="cuda").float()
+    spread[:, 64:128] = 0
+    packed, dense = ([], [], []), ([], [], [])
+    for j, (N, C, m) in enumerate(((F, K, spread), (F, K, spread), (K, F, torch.ones(E, K, 1, device="cuda")))):
+        W = torch.randn(E, N, C, generator=g, device="cuda") * 0.1
+        for i in range(E):
+            codes, scales, t = O.quantize((W[i] * m[i]).cpu().numpy())
+            packed[j].append(nv.PackedWeight.from_canonical(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), t, N, C))
+            dense[j].append(np.asarray(O.dequant(codes, scales, t), dtype=np.float64))
+    w, (Wg, Wu, Wd) = nv.ExpertWeights.from_packed(*packed), (np.stack(d) for d in dense)
+    X = (randn((n, K), 331, F32) * 2.0 ** torch.linspace(-20, 20, n, device="cuda").round()[:, None]).to(BF16)
+    e, c = choices(n, k, E, 332)
+    Y = nv.moe(w, X, e, c, "none", out_dtype=F32)
+    check(Y, X8.moe(f64(X), Wg, Wu, Wd, e.cpu().numpy(), f64(c), "none", None, True, kept=X8.kept_in_fp16_parts), "Y")
+    X[3] = 2.0 ** 66                       # h is infinite in most columns
+    X[5] = 0
+    got, low = nv.moe(w, X, e, c, "none", out_dtype=F32), nv.moe(w, X, e, c, "none")
+    keep = [t for t in range(n) if t not in (3, 5)]
+    assert torch.equal(got[keep], Y[keep]) and (got[5] == 0).all()
+    assert torch.equal(torch.isnan(got[3]), torch.isnan(low[3])) and torch.equal(torch.isinf(got[3]), torch.isinf(low[3]))
+
+
 @pytest.mark.parametrize("K,F,n", [(8192, 32, 16), (8208, 32, 3), (7184, 128, 2), (32, 8208, 5), (1040, 144, 16)])
 def test_moe_long_rows(K, F, n):
     """Every wave's share of K up to 8192, the form beyond, long F."""
