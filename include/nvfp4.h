@@ -499,8 +499,8 @@ int nvfp4_moe_decode_geometry(int K, int compute_units, int *outputs_per_workgro
 
 /* The gradients of nvfp4_moe, on the transposed copies: dX bf16 [n][ldx] (NULL:
  * not wanted) and dweights fp32 [n][k] (NULL: not wanted; 0 where there is no
- * expert).  dY fp32 or bf16 [n][ldy], ldy at most 2^18; it is rounded to bf16, an
- * operand of the products.  The gradients of the pre-activations are held to 11
+ * expert).  dY fp32 or bf16 [n][ldy], ldy at most 2^18; fp32 enters the products
+ * with 16 significant bits.  The gradients of the pre-activations are held to 11
  * bits, as h of a bf16 result (dX, which they are summed to, is one).
  * preact as nvfp4_moe stored it.  The residual's gradient is dY itself.
  * Workspace: nvfp4_moe_backward_workspace_bytes with dx as it is wanted, copy =

@@ -580,14 +580,17 @@ __global__ __launch_bounds__(256) void nvfp4_moe_grad_kernel(const float *d, con
 }
 
 // bf16 rows of an fp32 or unaligned matrix, or of one whose rows lie far apart, for the
-// product.
-__global__ __launch_bounds__(256) void nvfp4_moe_rows_kernel(const void *src, int f32, long long ld, int n, int cols,
+// product; rest: the second parts of fp32 values (bf16_rest).
+__global__ __launch_bounds__(256) void nvfp4_moe_rows_kernel(const void *src, int f32, int rest, long long ld, int n, int cols,
                                                              uint16_t *dst)
 {
     const long long idx = (long long)blockIdx.x * 256 + threadIdx.x;
     const int t = (int)(idx / cols), c = (int)(idx % cols);
-    if (t < n)
-        dst[(long long)t * cols + c] = f32_to_bf16_bits(load_any(src, t * ld + c, f32));
+    if (t >= n)
+        return;
+    const float v = load_any(src, t * ld + c, f32);
+    const uint16_t high = f32_to_bf16_bits(v);
+    dst[(long long)t * cols + c] = rest ? f32_to_bf16_bits(bf16_rest(v, high)) : high;
 }
 
 // ---- host side --------------------------------------------------------------------------------
@@ -645,10 +648,10 @@ int launch_sort(const Order &o, const int *experts, int pairs, int E, int tile_t
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
 }
 
-int launch_rows(const void *src, bool f32, long long ld, int n, int cols, uint16_t *dst, hipStream_t stream)
+int launch_rows(const void *src, bool f32, bool rest, long long ld, int n, int cols, uint16_t *dst, hipStream_t stream)
 {
     hipLaunchKernelGGL(nvfp4_moe_rows_kernel, dim3((unsigned)(((long long)n * cols + 255) / 256)), dim3(256), 0, stream, src, f32,
-                       ld, n, cols, dst);
+                       rest, ld, n, cols, dst);
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
 }
 
@@ -939,7 +942,7 @@ int nvfp4_moe(const nvfp4_experts *w, const uint16_t *X, int64_t ldx, const int3
         long long ld = ldx;
         if (far_apart(m, ldx)) {
             uint16_t *near = reinterpret_cast<uint16_t *>(rows);   // (which the second product writes)
-            st = launch_rows(x, false, ldx, m, K, near, s);
+            st = launch_rows(x, false, false, ldx, m, K, near, s);
             if (st != NVFP4_OK)
                 break;
             x = near;
@@ -1091,7 +1094,7 @@ int nvfp4_moe_backward(const nvfp4_experts *wt, const void *dY, int dy_dtype, in
         const bool f32 = dy_dtype == NVFP4_DTYPE_F32;
         uint16_t *near = reinterpret_cast<uint16_t *>(ws);
         if (copy || far_apart(m, ldy)) {
-            st = launch_rows(from, f32, ldy, m, K, near, s);
+            st = launch_rows(from, f32, false, ldy, m, K, near, s);
             if (st != NVFP4_OK)
                 break;
             dy = near;
@@ -1123,6 +1126,15 @@ int nvfp4_moe_backward(const nvfp4_experts *wt, const void *dY, int dy_dtype, in
         st = nvfp4_launch_moe_gemm(a, s);
         if (st != NVFP4_OK)
             break;
+        if (f32) {
+            a.rest = 1;
+            st = launch_rows(from, true, true, ldy, m, K, near, s);
+            if (st == NVFP4_OK)
+                st = nvfp4_launch_moe_gemm(a, s);
+            if (st != NVFP4_OK)
+                break;
+            a.rest = 0;
+        }
         hipLaunchKernelGGL(nvfp4_moe_grad_kernel, dim3((unsigned)pairs), dim3(256), 0, s, d, preact + (size_t)t0 * k * ldp,
                            o.position, ids, weights + (size_t)t0 * k, wt->gscale,
                            dweights ? dweights + (size_t)t0 * k : nullptr, dz, dzexp, (long long)ldp, E, F, activation);

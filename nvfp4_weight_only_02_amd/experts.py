@@ -397,7 +397,8 @@ def moe(w: ExpertWeights, X: torch.Tensor, experts: torch.Tensor, weights: torch
 def moe_backward(wt: TransposedExperts, dY: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor, preact: torch.Tensor,
                  activation: str = "silu", *, out: torch.Tensor = None, stream=None):
     """(dX bf16 [n, K], dweights fp32 [n, k]) of ``moe``, with ``preact`` as it
-    filled it.  The residual's gradient is dY."""
+    filled it.  The residual's gradient is dY.  An fp32 dY has 16 significant bits
+    in the products, for which one of them is made twice."""
     act = _act(activation)
     _weight(wt, TransposedExperts, "wt")
     _typed(dY, _FLOATS, "dY")

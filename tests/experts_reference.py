@@ -139,8 +139,9 @@ def moe(X, Wg, Wu, Wd, experts, weights, kind="silu", residual=None, out_f32=Fal
     return y, b + R.half(out_f32) * (np.abs(y) + b) + 2.0 ** -133
 
 
-def moe_grads(X, Wg, Wu, Wd, experts, weights, dY, kind="silu", dy_f32=False):
-    """((dX, bound), (dweights, bound))"""
+def moe_grads(X, Wg, Wu, Wd, experts, weights, dY, kind="silu", dy_f32=False, dy_step=R.HALF_BF16):
+    """((dX, bound), (dweights, bound)); an fp32 dY is an operand within dy_step of its
+    value."""
     n, k = experts.shape
     F, K = Wg.shape[1:]
     dx, bx, mx = np.zeros((n, K)), np.zeros((n, K)), np.zeros((n, K))
@@ -157,7 +158,7 @@ def moe_grads(X, Wg, Wu, Wd, experts, weights, dY, kind="silu", dy_f32=False):
         d, ed = R._grad_parts(g, eg, kind)
         dh = dY[t] @ Wd[e]
         mag = np.abs(dY[t]) @ np.abs(Wd[e])
-        eh = (K + 33) * STEP * mag + (R.HALF_BF16 * mag if dy_f32 else 0.0)
+        eh = (K + 33) * STEP * mag + (dy_step * mag if dy_f32 else 0.0)
         h = a * u
         ehh = np.abs(a) * ru + np.abs(u) * ea + ea * ru + STEP * np.abs(h)
         dw[t, s] = (dh * h).sum(1)

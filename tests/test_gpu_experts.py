@@ -297,6 +297,32 @@ def test_bits_of_values_of_any_size():
     assert torch.equal(torch.isnan(got[3]), torch.isnan(low[3])) and torch.equal(torch.isinf(got[3]), torch.isinf(low[3]))
 
 
+@pytest.mark.parametrize("n", [3, 50, 300])
+def test_bits_of_fp32_dy(n):
+    """dweights of an fp32 dY, which enters the product in two bf16 parts."""
+    say("moe bits, dY", n)
+    E, F, K, k = 5, 48, 32, 2
+    w, Wg, Wu, Wd = weights(E, F, K, 340)
+    wt = w.transpose()
+    X, (e, c) = randn((n, K), 341), choices(n, k, E, 342, 0.2)
+    pre = torch.zeros(n * k, 2 * F, device="cuda")
+    nv.moe(w, X, e, c, "none", preact=pre)
+    dY = randn((n, K + 3), 343, F32)[:, 1:1 + K]
+    dX, dc = nv.moe_backward(wt, dY, e, c, pre, "none")
+    x, d = X8.moe_grads(f64(X), Wg, Wu, Wd, e.cpu().numpy(), f64(c), f64(dY), "none", True, 2.0 ** -16)
+    check(dX, x, "dX")
+    check(dc, d, "dweights")
+    only = experts._moe_backward(wt, dY, e, c, pre, 0, False, True, None, None)
+    assert only[0] is None and torch.equal(only[1], dc)
+    big = dY.clone()
+    big[1, 2], big[2, 0] = INF, NAN
+    got = nv.moe_backward(wt, big, e, c, pre, "none")
+    keep = [t for t in range(n) if t not in (1, 2)]
+    assert torch.equal(got[0][keep], dX[keep]) and torch.equal(got[1][keep], dc[keep])
+    live = (e[1] >= 0).tolist()
+    assert not torch.isfinite(got[1][1][live]).any() and torch.isnan(got[1][2][e[2] >= 0]).all()
+
+
 @pytest.mark.parametrize("K,F,n", [(8192, 32, 16), (8208, 32, 3), (7184, 128, 2), (32, 8208, 5), (1040, 144, 16)])
 def test_moe_long_rows(K, F, n):
     """Every wave's share of K up to 8192, the form beyond, long F."""
