@@ -280,8 +280,11 @@ class ExpertWeights:
 
 
 def _check_transposed(wt, w):
+    """wt is the transposed copy of w, as far as sizes, the codes it was made from and
+    the tensor scales tell, which it shares with the weights and so keeps alive."""
     source = None if wt._source is None else wt._source()
-    if (wt.E, wt.F, wt.K) != (w.E, w.F, w.K) or (source is not None and source.data_ptr() != w.gate_up_codes.data_ptr()):
+    if ((wt.E, wt.F, wt.K) != (w.E, w.F, w.K) or (source is not None and source.data_ptr() != w.gate_up_codes.data_ptr())
+            or (wt._source is not None and wt.gscale.data_ptr() != w.gscale.data_ptr())):
         raise ValueError("transposed is not the transposed copy of these experts (w.transpose())")
 
 

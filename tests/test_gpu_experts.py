@@ -1,6 +1,9 @@
 """GPU parity of the router and the expert layer, with their gradients, against
 64-bit arithmetic, through the Python entry points, within the bounds of
 experts_reference."""
+import copy
+import gc
+
 import numpy as np
 import pytest
 import torch
@@ -563,6 +566,23 @@ def test_reference_gradients_against_differences():
                 v = np.zeros_like(c)
                 v[i, j] = t
                 assert abs((f(X, c + v) - f(X, c - v)) / (2 * t) - dc[i, j]) < 1e-6 * (1 + abs(dc[i, j]))
+
+
+def test_transposed_copies_of_experts_that_are_gone():
+    say("moe transposed")
+    E, F, K, k, n = 2, 32, 48, 1, 5
+    X, (e, c) = randn((n, K), 351).requires_grad_(), choices(n, k, E, 352)
+    w = weights(E, F, K, 350)[0]
+    wt = w.transpose()
+    nv.moe(w, X, e, c, transposed=wt).sum().backward()
+    w = weights(E, F, K, 353)[0]          # the first ones are freed
+    gc.collect()
+    assert wt._source() is None
+    with pytest.raises(ValueError):
+        nv.moe(w, X, e, c, transposed=wt)
+    nv.moe(w, X, e, c, transposed=w.transpose()).sum().backward()
+    whole = copy.deepcopy((w, w.transpose()))      # both copied: nothing tells them apart
+    nv.moe(whole[0], X, e, c, transposed=whole[1]).sum().backward()
 
 
 def test_no_tokens():
