@@ -54,17 +54,22 @@ class Int8Weight:
 
     @classmethod
     def from_int8(cls, codes: torch.Tensor, scale: torch.Tensor, stream=None) -> "Int8Weight":
-        """From int8 codes [N, K] and fp32 scales [N]: the weight codes * scale."""
+        """From int8 codes [N, K] and fp32 scales [N]: the weight codes * scale.  Both
+        are copied."""
         _dev(codes, torch.int8, "codes")
         if codes.dim() != 2:
             raise ValueError("codes must be [N, K], got %s" % list(codes.shape))
         N, K = codes.shape
         _vec(scale, (torch.float32,), "scale", N)
+        _no_graph(scale)
         size = cls._sizes(N, K)
         at = _Launch(stream, codes, scale)
         packed = at.alloc(size, dtype=torch.int8)
         _run("nvfp4_int8_pack", codes.data_ptr(), N, K, packed.data_ptr(), at.handle)
-        return cls(packed, scale, N, K)
+        own = at.alloc(N, dtype=torch.float32)
+        with torch.cuda.stream(at.stream):       # (of None: the current one)
+            own.copy_(scale.detach())
+        return cls(packed, own, N, K)
 
     @staticmethod
     def _sizes(N, K) -> int:

@@ -100,6 +100,27 @@ def test_from_float_refuses_a_row_too_long_before_reading_it():
         nv.Int8Weight.from_float(torch.ones(64, device="cuda"))
 
 
+def test_the_weight_keeps_its_own_scales():
+    """The caller's buffers may be used again, for the next weight say."""
+    say("int8 own scales")
+    q, s, X = codes((40, 64), 50), randn((40,), 51, F32).abs(), randn((5, 64), 52)
+    w = nv.Int8Weight.from_int8(q, s)
+    want = nv.int8_linear(w, X)
+    q.zero_()
+    s.fill_(7.0)
+    assert torch.equal(nv.int8_linear(w, X), want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    q, s = codes((40, 64), 50), randn((40,), 51, F32).abs()
+    side.wait_stream(torch.cuda.current_stream())
+    w = nv.Int8Weight.from_int8(q, s, stream=side)
+    side.synchronize()
+    s.fill_(7.0)
+    assert torch.equal(nv.int8_linear(w, X), want)
+    with pytest.raises(ValueError):
+        nv.Int8Weight.from_int8(q, s.requires_grad_())
+
+
 def test_quantize_extremes():
     say("quantize extremes")
     X = randn((8, 64), 3)
