@@ -521,6 +521,26 @@ def test_moe_gradients(n, E, F, K, k, act, dtype, empty):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("F", [4096, 4112, 4400, 8208])
+@pytest.mark.parametrize("n", [2, 40])
+def test_gradients_of_rows_longer_than_the_registers_hold(F, n):
+    """From F = 4096 on, the rest of a row's gradients is computed again once the row's
+    largest is known; in some rows that lies in the rest."""
+    say("moe grad, long F", F, n)
+    E, K, k = 2, 48, 1
+    w, Wg, Wu, Wd = weights(E, F, K, 360)
+    wt = w.transpose()
+    X, (e, c) = randn((n, K), 361), choices(n, k, E, 362)
+    dY = randn((n, K), 363, BF16, 0.1)
+    pre = torch.zeros(n * k, 2 * F, device="cuda")
+    nv.moe(w, X, e, c, preact=pre)
+    args = f64(X), Wg, Wu, Wd, e.cpu().numpy(), f64(c)
+    dX, dc = nv.moe_backward(wt, dY, e, c, pre)
+    x, d = X8.moe_grads(*args, f64(dY))
+    check(dX, x, "dX")
+    check(dc, d, "dweights")
+
+
 def test_gradients_of_repeated_experts_and_expanded_dy():
     say("moe grad repeated")
     E, F, K, k, n = 4, 64, 96, 3, 21

@@ -79,6 +79,20 @@ def test_quantize_halves_and_every_pair_of_mantissas():
     assert np.array_equal(q.cpu().numpy(), rq) and np.array_equal(f64(s), rs)
 
 
+@pytest.mark.parametrize("n,K", [(3, 32784), (2, 131056), (1, 200000)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_quantize_rows_longer_than_the_registers_hold(n, K, dtype):
+    """The rest of a row is read again for the division; in one row the largest value
+    lies there, in another before."""
+    say("quantize again", n, K, dtype)
+    X = randn((n, K), K, dtype)
+    X[0, K - 5] = 9.0
+    X[n - 1, 11] = -8.5 if n > 1 else 1.0
+    q, s = nv.int8_quantize(X)
+    rq, rs = X8.int8_quantize(f64(X), dtype == F32)
+    assert np.array_equal(q.cpu().numpy(), rq) and np.array_equal(f64(s), rs)
+
+
 @pytest.mark.parametrize("dtype,K", [(F32, (1 << 29) + 16), (BF16, (1 << 30) + 16)])
 def test_quantize_rows_of_more_than_2_31_bytes(dtype, K):
     say("quantize long", dtype, K)
@@ -189,6 +203,19 @@ def test_every_tile(n, N, K, geometry):
     args = f64(q), f64(s), wq.astype(np.float64), ws, f64(b)
     check(nv.int8_linear(w, q, s, b, "silu", r), X8.int8_linear(*args, "silu", f64(r)), "Y")
     check(nv.int8_linear(w, q, s, b, "none", out_dtype=F32), X8.int8_linear(*args, "none", None, True), "Y")
+
+
+@pytest.mark.parametrize("n,K", [(8, 6144), (5, 4112), (7, 7008), (3, 16384), (2, 24576), (1, 49152), (1, 33040)])
+def test_rows_that_a_decode_launch_quantises_longer_than_its_registers_hold(n, K):
+    say("int8 decode, long rows", n, K)
+    assert nv.int8_linear_workspace_bytes(n, 70, K) == 0       # quantised in the launch
+    w, wq, ws = weight(70, K, 60)
+    X = randn((n, K), 61)
+    X[0, K - 3] = 12.0
+    q, s = X8.int8_quantize(f64(X))
+    Y = nv.int8_linear(w, X, out_dtype=F32)
+    check(Y, X8.int8_linear(q, s, wq, ws, out_f32=True), "Y")
+    assert torch.equal(nv.int8_linear(w, *nv.int8_quantize(X), out_dtype=F32), Y)
 
 
 @pytest.mark.parametrize("N,n", [(16384, 3), (9000, 16), (2000, 1), (16001, 5), (5120, 700)])
