@@ -174,7 +174,17 @@ struct Int8GemvParams {
     nvfp4_epi_params e;
 };
 
-constexpr int kQuantInside = 49152;   // most activations a decode launch quantises itself
+// Most activations a decode launch quantises itself, of eight tokens at most.  Both
+// ways, us, weights cold (inside / a launch of its own):
+//   n = 1   5120 x 6144 10.0 / 12.5    16384 x 8192 28.0 / 30.8    1024 x 17408 10.2 / 14.9
+//   n = 8   5120 x 4096  9.8 / 11.2    16384 x 4096 17.0 / 19.2    1024 x 4096   6.7 / 7.9
+//   n = 4   5120 x 8192 13.2 / 14.9    16384 x 12288 43.0 / 40.8   1024 x 12288 11.7 / 11.9
+//   n = 8   5120 x 6144 13.7 / 12.8    16384 x 6144 24.2 / 23.0    1024 x 6144   9.9 / 9.9
+//   n = 6   5120 x 8192 17.3 / 15.3    16384 x 8192 33.0 / 30.9    1024 x 8192  12.1 / 10.3
+//   beyond  n = 8  5120 x 8192 17.6 / 15.6    n = 4  16384 x 17408 58.5 / 54.6
+// What decides is a wave's share, whatever the rows: inside is faster up to the 4096
+// values that a wave holds, as fast to 2 us slower from 6144 on.
+constexpr int kQuantInside = 49152;
 
 // A workgroup has p.rows weight rows, in R windows of 16 (of which the last may use
 // fewer, and which need not begin with a row group); its eight waves take
@@ -186,7 +196,7 @@ constexpr int kQuantInside = 49152;   // most activations a decode launch quanti
 // units took 9.4 us).
 //
 // QUANT: every workgroup quantises the bf16 activations itself, into LDS, while
-// its first weights are under way; a launch for it costs 4.4 us more (5120 x 6144,
+// its first weights are under way; a launch for it costs 2.5 us more (5120 x 6144,
 // n = 1).  Up to eight tokens, a wave each, and kQuantInside values: beyond, the
 // arithmetic outlasts the loads that it hides behind.
 template <int R, int U, bool QUANT>
@@ -428,8 +438,8 @@ int check_shape(int n, int N, int K)
 
 int launch_quantize(const void *X, int dtype, long long ldx, int n, int K, int8_t *q, long long ldq, float *scale, hipStream_t s)
 {
-    // (a row of 8192 stays in the registers of 256 threads; n = 300, K = 17408: 7.7 us
-    // with 256, LONG with 1024)
+    // (a row of 8192 stays in the registers of 256 threads; n = 300, K = 17408: 9.1 us
+    // with 256, 7.8 with 1024)
     const bool f32 = dtype == NVFP4_DTYPE_F32;
     if (K <= 8192) {
         auto k = f32 ? nvfp4_int8_quantize_kernel<true, 256> : nvfp4_int8_quantize_kernel<false, 256>;

@@ -10,7 +10,7 @@ namespace {
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxSlots = 32;           // experts of a token
 constexpr int kMaxF = 1 << 18;
-constexpr int kMaxLd = 1 << 18;         // row strides of X and dY: see chunk_tokens
+constexpr int kMaxLd = 1 << 18;         // row strides of X and dY
 constexpr int kChunkPairs = 1 << 16;
 
 // ---- router --------------------------------------------------------------------------
@@ -31,7 +31,7 @@ struct RouteParams {
 // Dword v of another lane: STEP 0 and 1 of the lane 1 and 2 away, 2 and 3 of the
 // mirror of its eight and sixteen, 4 and 5 of the other sixteen and half of the wave.
 // Without LDS: the router's rounds wait for one reduction after another (16 x 64,
-// k = 4: 3.9 us, 5.4 through __shfl_xor).
+// k = 8: 3.9 us, 5.4 through __shfl_xor; k = 4: 3.4).
 template <int STEP>
 __device__ __forceinline__ int other_lane(int v)
 {
