@@ -474,7 +474,7 @@ typedef struct nvfp4_experts {
  * receives the pre-activations for nvfp4_moe_backward, its rows in the order of
  * the experts within each part (below; rows of slots without an expert are left as
  * they were); biases NULL.  h = act() * (), an operand of the matrix instructions,
- * is held to 16 significant bits up to 16 tokens; beyond (or with preact) to 11
+ * is held to 16 significant bits in the form for up to 16 tokens; in the other to 11
  * where Y is bf16, whose own rounding is to 8, and to 22 where Y is fp32, down to
  * 2^-24 of its row's largest value; all sums are fp32.
  * Up to 16 tokens (K up to 8192, no preact) take two launches, and a token's

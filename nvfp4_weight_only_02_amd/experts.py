@@ -359,8 +359,9 @@ def moe(w: ExpertWeights, X: torch.Tensor, experts: torch.Tensor, weights: torch
     ``preact`` (fp32 [n k, 2 F]) receives what ``moe_backward`` needs.
 
     Between the two products act() * () is held to 16 significant bits up to 16
-    tokens; beyond, or where pre-activations are kept (``preact``, gradients), to 11
-    for a bf16 Y, and to 22, in a second down projection, for an fp32 one.
+    tokens; beyond, where K is above 8192 or pre-activations are kept (``preact``,
+    gradients), to 11 for a bf16 Y, and to 22, in a second down projection, for an
+    fp32 one.
 
     ``workspace``: uint8, nvfp4_moe_workspace_bytes (allocated otherwise).
     Differentiable in X and weights (given ``transposed``) and the residual."""
