@@ -113,7 +113,9 @@ __device__ __forceinline__ f32x2 scales2(u32 w)
 // alike, in a second copy of the loop's body: 275, it takes too many registers);
 // E = 32, F = 1280, K = 2048, n = 700, k = 4, the gradient's: 50, 68 with an exponent
 // for each 64, 55 from bf16.  (fp16 has a packed product, so that the weights'
-// dequantisation is shorter than to bf16.)
+// dequantisation is shorter than to bf16.)  Of an fp32 result a second launch multiplies
+// the values' second parts and adds its sums: the whole layer 1040 us for 740, 3.9e-7
+// of the norm for 2.1e-4.
 //
 // LDS layout of the slice: token t's 16-byte chunk c (8 columns) at
 //     (t / 4) * kQuad + (t % 4) * 256 + (c ^ (t % 4)) * 16.
